@@ -529,6 +529,176 @@ int dlrm_interaction_fwd(const float* d_dense, const float* d_pooled, int64_t ba
 int dlrm_interaction_bwd(const float* d_dense, const float* d_pooled, const float* d_dout, int64_t batch,
                          int32_t n_tables, int32_t dim, float* d_ddense, float* d_dpooled, void* stream);
 
+/* ------------------------------- attention over behaviour sequences --- */
+/*
+ * The behaviour-sequence lookup ("the item-ID sequence of the last 100
+ * clicks": variable-length bags, CSR offsets) pools a user's events by a sum
+ * or a mean.  These calls attend over them instead: multi-head attention
+ * within each sequence of a jagged batch, with a learned bias for the
+ * distance (in time or index) between two events.
+ *
+ * For the events i, j of one sequence, query head h and its key/value head
+ * g = h / (n_heads / n_kv_heads):
+ *   dist_ij = pos_i - pos_j, saturated to int32
+ *   b_ij    = number of boundaries <= dist_ij (the Bucketize of the feature
+ *             transforms), 0 .. n_boundaries
+ *   s_ij    = scale q_ih . k_jg + bias[h, b_ij]
+ *   p_ij    = exp(s_ij - lse_ih), lse_ih = log sum_j exp(s_ij), over the j
+ *             that i may see: those whose key_off is not negative and, when
+ *             causal, that do not come after i
+ *   out_ih  = sum_j p_ij v_jg
+ * An event that may see none gets out = 0 and lse = -infinity, and no
+ * gradient.  Keys and values that no event may see (a negative key_off: a
+ * lookup that found no row) are never used, whatever they hold; a value that
+ * is not finite in a visible place may reach every event of its sequence.
+ *
+ * q, k, v, out and their gradients are [n_events, heads, dim] in the
+ * handle's type (RSE_F32 or RSE_BF16), given as rse_seq_rows: the elements
+ * of a head are adjacent, the distances between events and between heads are
+ * free (views of one joint projection, for example).  Addresses and both
+ * strides are multiples of 16 bytes, else RSE_ERR_INVALID_ARG.  Products are
+ * accumulated and the softmax is held in fp32.  With RSE_BF16 the
+ * probabilities (and their gradients) are rounded to bf16 where they enter
+ * a matrix product, outputs once at the end; the bias gradient is summed
+ * from the unrounded fp32 values.  No floating-point atomics are shared
+ * between lanes: results are run-to-run identical.
+ */
+#define RSE_SEQ_MAX_BOUNDARIES 127
+#define RSE_SEQ_MAX_HEADS 256
+
+typedef struct rse_seqattn rse_seqattn;
+
+/* Device bytes of a handle's memory (status, bucket boundaries). */
+int rse_seqattn_mem_size(size_t* bytes_out);
+
+/* Create a handle over caller memory d_mem (256-byte aligned).  n_heads is a
+ * multiple of n_kv_heads (at most RSE_SEQ_MAX_HEADS); dim is 32, 64 or 128,
+ * else RSE_ERR_UNSUPPORTED; the
+ * boundaries (host array, at most RSE_SEQ_MAX_BOUNDARIES) ascend, the lowest
+ * above INT32_MIN; scale is finite.  No synchronisation. */
+int rse_seqattn_create(rse_seqattn** out, void* d_mem, size_t mem_bytes, int32_t n_heads, int32_t n_kv_heads,
+                       int32_t dim, int32_t dtype, int32_t causal, float scale, const int32_t* boundaries,
+                       int32_t n_boundaries, void* stream);
+int rse_seqattn_destroy(rse_seqattn* attn);
+
+/* Sticky status (synchronises `stream`): RSE_ERR_BAD_INPUT after a call whose
+ * offsets were malformed or whose sequences exceeded max_len.  The sequences
+ * concerned are skipped; nothing is read or written out of bounds. */
+int rse_seqattn_status(rse_seqattn* attn, int32_t* status_out, void* stream);
+int rse_seqattn_clear_status(rse_seqattn* attn, void* stream);
+
+typedef struct rse_seq_rows {
+    void* data;          /* element (0, 0, 0); only written through for outputs */
+    int64_t row_stride;  /* elements from one event to the next */
+    int64_t head_stride; /* elements from one head to the next */
+} rse_seq_rows;
+
+typedef struct rse_seq_batch {
+    const int64_t* d_offsets; /* [batch + 1]: sequence b is events offsets[b] .. offsets[b+1] */
+    int64_t batch;
+    int64_t n_events;         /* offsets[batch] */
+    int64_t max_len;          /* no sequence is longer */
+    const int32_t* d_pos;     /* [n_events] time or index of each event */
+    const int64_t* d_key_off; /* [n_events] row offsets, negative: not to be seen; or NULL */
+    const float* d_bias;      /* [n_heads, n_boundaries + 1] */
+} rse_seq_batch;
+
+/* Bytes of what a forward leaves for its backward (fp32 statistics of every
+ * event and head), for the same n_events and max_len. */
+int rse_seqattn_saved_size(const rse_seqattn* attn, int64_t n_events, int64_t max_len, size_t* bytes_out);
+
+/* Forward.  d_saved: rse_seqattn_saved_size bytes (256-byte aligned) written
+ * for the backward, or NULL when there will be none. */
+int seq_attention_fwd(const rse_seqattn* attn, const rse_seq_batch* batch, const rse_seq_rows* q,
+                      const rse_seq_rows* k, const rse_seq_rows* v, const rse_seq_rows* out, void* d_saved,
+                      size_t saved_bytes, void* stream);
+
+/* Workspace bytes of one seq_attention_bwd. */
+int rse_seqattn_bwd_workspace_size(const rse_seqattn* attn, int64_t n_events, int64_t batch, int64_t max_len,
+                                   size_t* bytes_out);
+
+/*
+ * Backward: recomputes the probabilities from q, k and the saved lse.
+ *   dp_ij = dout_ih . v_jg,  ds_ij = p_ij (dp_ij - sum_j p_ij dp_ij)
+ *   dq_ih = scale sum_j ds_ij k_jg
+ *   dk_jg = scale sum_{h of g} sum_i ds_ij q_ih
+ *   dv_jg = sum_{h of g} sum_i p_ij dout_ih
+ *   dbias[h, b] = sum of ds_ij over all pairs with b_ij = b   (fp32
+ *                 [n_heads, n_boundaries + 1], overwritten)
+ * All gradients are overwritten.  Nothing is kept between calls.
+ */
+int seq_attention_bwd(const rse_seqattn* attn, const rse_seq_batch* batch, const rse_seq_rows* q,
+                      const rse_seq_rows* k, const rse_seq_rows* v, const void* d_saved, size_t saved_bytes,
+                      const rse_seq_rows* dout, const rse_seq_rows* dq, const rse_seq_rows* dk,
+                      const rse_seq_rows* dv, float* d_dbias, void* d_ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------- history cache and single events -- */
+/*
+ * For serving, each user's keys, values and times stay in pages of page_size
+ * events in one pool: k, v [n_pages, page_size, n_kv_heads, dim], pos
+ * [n_pages, page_size].  Event e of user b is at slot
+ *   page_table[b, e / page_size] * page_size + e % page_size
+ * so a history grows without moving, like the embedding blocks.
+ */
+typedef struct rse_seqcache rse_seqcache;
+
+/* Device bytes of a cache's metadata (its status). */
+int rse_seqcache_meta_size(size_t* bytes_out);
+
+/* Create over caller memory.  page_size is a power of two in [8, 1024];
+ * n_pages * page_size may not exceed 2^40.  k, v and pos are 16-byte aligned. */
+int rse_seqcache_create(rse_seqcache** out, void* d_meta, size_t meta_bytes, void* d_k, void* d_v, int32_t* d_pos,
+                        int64_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t dim, int32_t dtype,
+                        void* stream);
+int rse_seqcache_destroy(rse_seqcache* cache);
+
+/* Sticky status (synchronises `stream`): RSE_ERR_NEED_GROW (an assign ran out
+ * of free pages) or RSE_ERR_BAD_INPUT. */
+int rse_seqcache_status(rse_seqcache* cache, int32_t* status_out, void* stream);
+int rse_seqcache_clear_status(rse_seqcache* cache, void* stream);
+
+/*
+ * Page tables and slots of d_counts[b] new events after the d_lens[b] that
+ * user b has cached.  Pages ceil(len / page_size) ..
+ * ceil((len + count) / page_size) - 1 of each user are taken from d_free in
+ * user order and entered in d_page_table [batch, max_pages].  Written:
+ * d_offsets [batch + 1] (the new events' CSR offsets), d_slots [n_events]
+ * (each new event's slot), *d_taken (pages taken; the caller moves its free
+ * list on by that).  If the free list is too short (RSE_ERR_NEED_GROW) or a
+ * length is negative, a history exceeds max_pages or the counts do not sum to
+ * n_events (RSE_ERR_BAD_INPUT), the page table is unchanged, *d_taken is 0
+ * and every slot is -1.  d_ws: rse_seqcache_assign_workspace_size bytes.
+ */
+int rse_seqcache_assign_workspace_size(int64_t batch, size_t* bytes_out);
+int seq_cache_assign(rse_seqcache* cache, const int64_t* d_counts, const int64_t* d_lens, int64_t batch,
+                     int32_t* d_page_table, int32_t max_pages, const int32_t* d_free, int64_t n_free,
+                     int64_t n_events, int64_t* d_slots, int64_t* d_offsets, int64_t* d_taken, void* d_ws,
+                     size_t ws_bytes, void* stream);
+
+/* Write the events' k, v rows and times at their slots.  A negative slot is
+ * skipped; one past the pool is skipped with RSE_ERR_BAD_INPUT. */
+int seq_cache_write(rse_seqcache* cache, const int64_t* d_slots, int64_t n_events, const rse_seq_rows* k,
+                    const rse_seq_rows* v, const int32_t* d_pos, void* stream);
+
+/* Workspace bytes of one seq_attention_step. */
+int rse_seqattn_step_workspace_size(const rse_seqattn* attn, int64_t batch, int64_t max_len, size_t* bytes_out);
+
+/*
+ * One new event for each user: its k, v, pos are stored at event number
+ * d_lens[b] of user b (whose page must be in the table), and out[b] =
+ * attention of q[b] over the d_lens[b] + 1 events, itself included, by the
+ * formulas above (key_off aside; the event is the last, so causal or not is
+ * the same).  d_lens[b] < 0: the user is idle, out[b] = 0 and nothing is
+ * stored.  d_lens[b] + 1 > max_len or past the table, or a page out of the
+ * pool: RSE_ERR_BAD_INPUT in the cache's status and out[b] = 0 (a bad page's
+ * events left out).  Slots behind a history are not used, whatever they
+ * hold.  The lengths are not changed: the caller adds 1.
+ */
+int seq_attention_step(const rse_seqattn* attn, rse_seqcache* cache, const rse_seq_rows* q, const rse_seq_rows* k,
+                       const rse_seq_rows* v, const int32_t* d_pos, const float* d_bias,
+                       const int32_t* d_page_table, int32_t max_pages, const int64_t* d_lens, int64_t batch,
+                       int64_t max_len, const rse_seq_rows* out, void* d_ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------- kernel trace -- */
 /*
  * Per-kernel timing with HIP events, for measurement: while a trace is

@@ -10,6 +10,9 @@ seen by torch as tensors).  The functions keep the C ABI's names:
 and embedding_bag_bwd_update's two halves, embedding_bag_bwd_prepare (sort;
 may overlap the forward on another stream) and embedding_bag_bwd_apply.
 
+Attention over behaviour sequences (``SeqAttention``, ``SeqCache`` and the
+``seq_*`` calls) is in ``sequence.py``.
+
 ``IdMap`` and ``EmbeddingBlocks`` own the caller-side device memory of the two
 library objects.  Importing this package loads librse.so and fails if it is
 missing (there is no CPU fallback).
@@ -695,7 +698,11 @@ __all__ = [
     "embedding_bag_bwd_prepare", "embedding_bag_bwd_apply",
     "bwd_workspace", "row_bytes", "status_str", "lib", "trace_start", "trace_stop", "K_PROBE", "K_FWD",
     "K_SORT_SCATTER", "K_SEG_UPDATE", "K_COMBINE", "K_INTERACT", "save", "load", "dlrm_interaction_fwd",
-    "dlrm_interaction_bwd",
+    "dlrm_interaction_bwd", "SeqAttention", "SeqCache", "seq_attention_fwd", "seq_attention_bwd",
+    "seq_attention_step", "seq_cache_assign", "seq_cache_write",
 ]
 
 from .saver import load, save  # noqa: E402  (the Saver uses the classes above)
+from .sequence import (  # noqa: E402
+    SeqAttention, SeqCache, seq_attention_bwd, seq_attention_fwd, seq_attention_step, seq_cache_assign, seq_cache_write,
+)

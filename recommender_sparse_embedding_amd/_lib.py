@@ -42,6 +42,16 @@ class RseOptim(ctypes.Structure):
                 ("step", ctypes.c_int64)]
 
 
+class RseSeqRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class RseSeqBatch(ctypes.Structure):
+    _fields_ = [("d_offsets", ctypes.c_void_p), ("batch", ctypes.c_int64), ("n_events", ctypes.c_int64),
+                ("max_len", ctypes.c_int64), ("d_pos", ctypes.c_void_p), ("d_key_off", ctypes.c_void_p),
+                ("d_bias", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I32, _I64, _U64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
 _SZ = ctypes.c_size_t
@@ -97,6 +107,26 @@ SIGNATURES = {
                                  ctypes.POINTER(RseOptim), _P, _P, _SZ, _P], ctypes.c_int),
     "dlrm_interaction_fwd": ([_P, _P, _I64, _I32, _I32, _P, _P], ctypes.c_int),
     "dlrm_interaction_bwd": ([_P, _P, _P, _I64, _I32, _I32, _P, _P, _P], ctypes.c_int),
+    "rse_seqattn_mem_size": ([_PSZ], ctypes.c_int),
+    "rse_seqattn_create": ([ctypes.POINTER(_P), _P, _SZ, _I32, _I32, _I32, _I32, _I32, ctypes.c_float, _PI32, _I32, _P],
+                           ctypes.c_int),
+    "rse_seqattn_destroy": ([_P], ctypes.c_int),
+    "rse_seqattn_status": ([_P, _PI32, _P], ctypes.c_int),
+    "rse_seqattn_clear_status": ([_P, _P], ctypes.c_int),
+    "rse_seqattn_saved_size": ([_P, _I64, _I64, _PSZ], ctypes.c_int),
+    "seq_attention_fwd": ([_P, _P, _P, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
+    "rse_seqattn_bwd_workspace_size": ([_P, _I64, _I64, _I64, _PSZ], ctypes.c_int),
+    "seq_attention_bwd": ([_P, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
+    "rse_seqcache_meta_size": ([_PSZ], ctypes.c_int),
+    "rse_seqcache_create": ([ctypes.POINTER(_P), _P, _SZ, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _P], ctypes.c_int),
+    "rse_seqcache_destroy": ([_P], ctypes.c_int),
+    "rse_seqcache_status": ([_P, _PI32, _P], ctypes.c_int),
+    "rse_seqcache_clear_status": ([_P, _P], ctypes.c_int),
+    "rse_seqcache_assign_workspace_size": ([_I64, _PSZ], ctypes.c_int),
+    "seq_cache_assign": ([_P, _P, _P, _I64, _P, _I32, _P, _I64, _I64, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
+    "seq_cache_write": ([_P, _P, _I64, _P, _P, _P, _P], ctypes.c_int),
+    "rse_seqattn_step_workspace_size": ([_P, _I64, _I64, _PSZ], ctypes.c_int),
+    "seq_attention_step": ([_P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _I64, _P, _P, _SZ, _P], ctypes.c_int),
     "rse_trace_start": ([_I32], ctypes.c_int),
     "rse_trace_stop": ([_PI64, ctypes.POINTER(ctypes.c_double)], ctypes.c_int),
 }

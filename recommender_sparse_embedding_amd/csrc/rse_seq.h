@@ -1,0 +1,128 @@
+// rse_seq.h -- shared by the sequence operators' translation units: the
+// handles, the views passed to kernels, the bucket lookup (not part of the
+// public ABI).
+#pragma once
+
+#include "rse_host.h"
+
+namespace rse {
+
+// Device memory of an attention handle.
+struct SeqHeader {
+    int32_t status;
+    int32_t n_bounds;
+    int32_t pad[62];
+    int32_t bounds[RSE_SEQ_MAX_BOUNDARIES + 1];   // unused entries: INT32_MAX
+};
+static_assert(sizeof(SeqHeader) == 256 + 512, "SeqHeader size");
+
+struct SeqCacheHeader {
+    int32_t status;
+    int32_t pad[63];
+};
+static_assert(sizeof(SeqCacheHeader) == 256, "SeqCacheHeader size");
+
+// rse_seq_rows as a kernel sees them.
+template <typename T>
+struct Rows {
+    T* p;
+    int64_t row, head;
+    __device__ __forceinline__ T* at(int64_t i, int64_t h) const { return p + i * row + h * head; }
+};
+
+// What every attention kernel is given about the batch and the layer.
+struct SeqArgs {
+    const int64_t* offsets;
+    int64_t batch, n_events, max_len;
+    const int32_t* pos;
+    const int64_t* key_off;
+    const float* bias;
+    SeqHeader* hdr;
+    int32_t n_heads, group;      // query heads, query heads per key/value head
+    int32_t n_bounds, causal;
+    float scale;
+};
+
+// pos_i - pos_j saturated to int32 (one instruction).
+__device__ __forceinline__ int32_t seq_dist(int32_t a, int32_t b) { return __builtin_elementwise_sub_sat(a, b); }
+
+// Number of boundaries <= d: binary search over a table padded to 128 entries
+// with INT32_MAX (a distance of INT32_MAX would count the padding: capped).
+__device__ __forceinline__ int seq_bucket(const int32_t* bounds, int n_bounds, int32_t d) {
+    int b = 0;
+#pragma unroll
+    for (int step = 64; step > 0; step >>= 1)
+        if (bounds[b + step - 1] <= d) b += step;
+    return b < n_bounds ? b : n_bounds;
+}
+
+// Wave-level ordering of a wave's own LDS writes before its other lanes read them.
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Elements of the two storage types as fp32, and back.
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(uint16_t x) { return bf16_to_f32(x); }
+__device__ __forceinline__ uint16_t f32_to_bf16(float x) {   // to nearest even; NaN stays NaN
+    uint32_t u = __float_as_uint(x);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
+    u += 0x7FFFu + ((u >> 16) & 1u);
+    return (uint16_t)(u >> 16);
+}
+__device__ __forceinline__ void from_f32(float& y, float x) { y = x; }
+__device__ __forceinline__ void from_f32(uint16_t& y, float x) { y = f32_to_bf16(x); }
+
+// The largest b in [0, batch) whose key f(b) <= x, for f ascending with
+// f(0) <= x: 64 probes at a time, all lanes of the wave together.
+template <typename F>
+__device__ __forceinline__ int64_t wave_last_le(int64_t n, F f, int64_t x) {
+    int64_t lo = 0, len = n;                 // the answer is in [lo, lo + len)
+    const int lane = lane_id();
+    while (len > 1) {
+        const int64_t step = (len + WAVE - 1) / WAVE;
+        const int64_t at = lo + lane * step;
+        const bool le = lane * step < len && f(at) <= x;
+        const int k = __popcll(__ballot(le));   // lanes 0 .. k-1 hold; k >= 1 for ascending f
+        const int64_t first = lo + (int64_t)(k > 0 ? k - 1 : 0) * step;
+        const int64_t end = lo + len;
+        lo = first;
+        len = end - first < step ? end - first : step;
+    }
+    return lo;
+}
+
+}  // namespace rse
+
+struct rse_seqattn {
+    int32_t n_heads, n_kv_heads, dim, dtype, causal, n_bounds;
+    float scale;
+    rse::SeqHeader* hdr;
+};
+
+struct rse_seqcache {
+    rse::SeqCacheHeader* hdr;
+    void* k;
+    void* v;
+    int32_t* pos;
+    int64_t n_pages;
+    int32_t page_size, page_shift, n_kv_heads, dim, dtype;
+};
+
+namespace rse_host {
+
+// Rows of the handle's type: present, 16-byte aligned, strides in 16 bytes.
+inline bool rows_ok(const rse_seq_rows* r, int32_t dtype) {
+    const int64_t e = dtype == RSE_F32 ? 4 : 2;
+    return r && r->data && reinterpret_cast<uintptr_t>(r->data) % 16 == 0 && r->row_stride % (16 / e) == 0 &&
+           r->head_stride % (16 / e) == 0;
+}
+
+template <typename T>
+inline rse::Rows<T> rows_view(const rse_seq_rows* r) {
+    return {static_cast<T*>(r->data), r->row_stride, r->head_stride};
+}
+
+}  // namespace rse_host

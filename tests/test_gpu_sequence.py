@@ -1,0 +1,537 @@
+"""Attention over behaviour sequences on the GPU against the float64 oracle:
+forward, every gradient, the single-event step over the paged history, page
+tables and slots.  An element may be off by the oracle's bound for it (sums in
+fp32, bf16 products where the type is bf16), no more."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import sequence as oseq
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = 0, 1
+KIND = {F32: "f32", BF16: "bf16"}
+DT = {F32: torch.float32, BF16: torch.bfloat16}
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _check(got, ref, what):
+    value, bound = ref
+    got = _np(got)
+    assert np.all(np.isfinite(got)), f"{what}: not finite"
+    off = np.abs(got - value)
+    at = np.unravel_index(np.argmax(off / bound), off.shape) if off.size else ()
+    assert np.all(off <= bound), f"{what} at {at}: {got[at]} for {value[at]}, bound {bound[at]:.3g}"
+
+
+class Case:
+    """Inputs of one jagged batch, as views of a joint [N, H + 2 Hk, D] tensor."""
+
+    def __init__(self, lens, H, Hk, D, dtype, causal=True, bounds=(0, 1, 2, 4, 8, 16, 32, 64), times=True, missing=0.0,
+                 seed=0, size=1.0):
+        import recommender_sparse_embedding_amd as rse
+
+        self.rse, self.causal, self.bounds, self.dtype = rse, causal, list(bounds), dtype
+        g = torch.Generator().manual_seed(seed + 1000 * len(lens) + sum(lens))
+        N = sum(lens)
+        qkv = (torch.randn((N, H + 2 * Hk, D), generator=g) * size).to(DT[dtype]).cuda()
+        self.q, self.k, self.v = qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:]
+        self.dout = torch.randn((N, H, D), generator=g).to(DT[dtype]).cuda()
+        gaps = torch.randint(0, 30, (N,), generator=g) if times else torch.ones(N, dtype=torch.int64)
+        self.pos = gaps.cumsum(0).to(torch.int32).cuda()
+        self.bias = torch.randn((H, len(bounds) + 1), generator=g).cuda()
+        self.off = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int64).cuda()
+        self.key_off = None
+        if missing:
+            self.key_off = torch.where(torch.rand(N, generator=g) < missing, -1, 5).cuda()
+        self.max_len = max(lens, default=0)
+        self.attn = rse.SeqAttention(H, Hk, D, dtype, bounds, causal=causal)
+
+    def oracle(self, dout=True):
+        return oseq.attention(_np(self.q), _np(self.k), _np(self.v), self.pos.cpu().numpy(), _np(self.bias),
+                              self.off.cpu().numpy(), self.bounds, self.causal, self.attn.scale,
+                              None if self.key_off is None else self.key_off.cpu().numpy(),
+                              _np(self.dout) if dout else None, KIND[self.dtype])
+
+    def run(self, **kw):
+        kw = {"key_off": self.key_off, "max_len": self.max_len, **kw}
+        where = (self.attn, self.q, self.k, self.v, self.pos, self.bias, self.off)
+        out, saved = self.rse.seq_attention_fwd(*where, for_backward=True, **kw)
+        dq, dk, dv, db = self.rse.seq_attention_bwd(*where, saved, self.dout, **kw)
+        assert self.attn.status() == 0
+        return {"out": out, "dq": dq, "dk": dk, "dv": dv, "dbias": db}
+
+    def forward(self, **kw):
+        kw = {"key_off": self.key_off, "max_len": self.max_len, **kw}
+        return self.rse.seq_attention_fwd(self.attn, self.q, self.k, self.v, self.pos, self.bias, self.off, **kw)
+
+    def check(self):
+        got, ref = self.run(), self.oracle()
+        for name in got:
+            _check(got[name], ref[name], name)
+        assert torch.equal(self.forward(), got["out"])
+        return got
+
+
+LENS = {"one": [1], "empties": [0, 1, 0, 0, 2, 0], "tile edges": [31, 32, 33, 63, 64, 65], "blocks": [127, 128, 129],
+        "long": [300, 5], "longer": [513], "none": [0, 0], "many": [(7 * i) % 41 for i in range(60)]}
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("lens", LENS)
+def test_attention_lengths(lens, D, dtype):
+    Case(LENS[lens], 4, 2, D, dtype).check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (3, 1), (4, 4), (6, 2), (8, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_heads_and_directions(H, Hk, causal, dtype):
+    Case([40, 3, 77, 150], H, Hk, 64, dtype, causal=causal, missing=0.3).check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bounds", [(), (5,), tuple(range(-63, 64)), tuple(2**m for m in range(31)),
+                                    (0, 0, 3, 3, 3, 2**31 - 1)])
+def test_attention_boundaries(bounds, dtype):
+    if not bounds:
+        # one bucket: its gradient is the sum of all ds, 0 but for rounding
+        got, ref = (c := Case([50, 140], 2, 1, 32, dtype, bounds=bounds)).run(), c.oracle()
+        assert np.all(np.abs(_np(got["dbias"])) <= ref["dbias"][1])
+    Case([50, 140], 2, 1, 32, dtype, bounds=bounds, causal=False).check()
+    Case([50, 140], 2, 1, 32, dtype, bounds=bounds, times=False).check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_attention_any_order_of_times(dtype):
+    c = Case([60, 130], 2, 2, 32, dtype, bounds=(-100, -1, 0, 7, 2**20, 2**30, 2**31 - 1), causal=False)
+    g = torch.Generator().manual_seed(1)
+    c.pos = torch.randint(-2**31, 2**31, c.pos.shape, generator=g).to(torch.int32).cuda()
+    c.pos[::7] = -2**31
+    c.pos[1::7] = 2**31 - 1
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_that_see_nothing_and_what_they_hide(causal, dtype):
+    """Every key of one sequence and the first keys of the others have no row;
+    their keys and values hold NaN and infinities, which nothing may see."""
+    c = Case([70, 33, 1, 140, 64], 4, 2, 64, dtype, causal=causal)
+    off = torch.zeros(c.pos.numel(), dtype=torch.int64)
+    off[70:103] = -1                  # the whole second sequence
+    off[103] = -9
+    off[104:110] = -1                 # its first events see nothing when causal
+    off[150:170] = -(2**62)
+    c.key_off = off.cuda()
+    hide = c.key_off < 0
+    c.k[hide] = float("nan")
+    c.v[hide] = torch.tensor(float("inf")).to(c.v.dtype)
+    got = c.check()
+    assert torch.all(got["out"][70:104] == 0) and torch.all(got["dq"][70:104] == 0)
+    assert torch.all(got["dk"][hide] == 0) and torch.all(got["dv"][hide] == 0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_neighbours_do_not_leak(dtype):
+    """A sequence of NaN between two others, and rows before and after the batch."""
+    c = Case([37, 20, 45], 2, 1, 64, dtype)
+    ref = c.oracle()
+    for t in (c.q, c.k, c.v, c.dout):
+        t[37:57] = float("nan")
+    got = c.run()
+    keep = torch.ones(102, dtype=torch.bool)
+    keep[37:57] = False
+    for name in ("out", "dq", "dk", "dv"):
+        _check(got[name][keep.cuda()], tuple(x[keep.numpy()] for x in ref[name]), name)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_large_scores(dtype):
+    """Scores of some hundreds: probabilities of 0 and 1, no overflow."""
+    Case([90, 150], 2, 1, 64, dtype, size=6.0).check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_bias_of_the_lowest_value(dtype):
+    """A bucket's bias at the type's lowest value acts as a mask; a row with
+    nothing else takes the plain average of equal scores."""
+    c = Case([40, 90], 2, 2, 32, dtype, bounds=(1, 2, 4))
+    c.bias[:, 2] = torch.finfo(torch.float32).min
+    c.bias[0, 0] = -1e30
+    got = c.run()
+    off, lo = c.oracle(), c.bias[:, 2].cpu().numpy()
+    assert np.all(lo < -3e38)
+    # the bounds hold wherever the row has a finite-scale score; those rows
+    # are the ones whose best score is ordinary
+    ordinary = off["lse"].T > -1e4
+    out = _np(got["out"])
+    assert np.all(np.isfinite(out))
+    err = np.abs(out - off["out"][0])
+    scale = np.abs(_np(c.v)).max() * (4e-3 if dtype == F32 else 2e-2)
+    assert np.all(err[ordinary] <= scale)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_repeat_runs_are_identical(dtype):
+    c = Case([200, 31, 129, 64], 4, 2, 64, dtype, missing=0.1)
+    a, b = c.run(), c.run()
+    for name in a:
+        assert torch.equal(a[name], b[name]), name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradients_match_differences(dtype):
+    """The directional derivative of sum(out * dout) along random directions,
+    by central differences of the float64 oracle."""
+    c = Case([20, 140], 2, 1, 32, dtype, bounds=(1, 2, 4, 8, 40))
+    got, ref = c.run(), c.oracle()
+    rng = np.random.default_rng(3)
+    base = [_np(c.q), _np(c.k), _np(c.v), _np(c.bias)]
+    do = _np(c.dout)
+
+    def loss(x):
+        o = oseq.attention(*x[:3], c.pos.cpu().numpy(), x[3], c.off.cpu().numpy(), c.bounds, True, c.attn.scale)
+        return float((o["out"][0] * do).sum())
+
+    for at, name in enumerate(("dq", "dk", "dv", "dbias")):
+        way = rng.choice([-1.0, 1.0], base[at].shape)
+        hi, lo = list(base), list(base)
+        hi[at], lo[at] = base[at] + 1e-5 * way, base[at] - 1e-5 * way
+        slope = (loss(hi) - loss(lo)) / 2e-5
+        # every element may be off by its bound; differences by 1e-6
+        assert abs((_np(got[name]) * way).sum() - slope) <= ref[name][1].sum() + 1e-6 * (1 + abs(slope)), name
+
+
+def test_strides_past_32_bits():
+    """Events 2^28 elements apart: byte offsets far past 2^32."""
+    c = Case([3, 9], 2, 1, 32, BF16)
+    far = torch.empty((12, 1 << 28), dtype=torch.bfloat16, device="cuda")
+    q, k, v = (far[:, a:a + h * 32].view(12, h, 32) for a, h in ((0, 2), (64, 1), (96, 1)))
+    for t, x in ((q, c.q), (k, c.k), (v, c.v)):
+        t.copy_(x)
+    ref, want = c.oracle(), c.run()
+    c.q, c.k, c.v = q, k, v
+    got = c.run()
+    for name in got:
+        assert torch.equal(got[name], want[name])
+        _check(got[name], ref[name], name)
+
+
+def test_joint_gradient_views_and_another_stream():
+    c = Case([30, 80], 4, 2, 64, BF16)
+    want = c.run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        joint = torch.full((110, 8, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    where = (c.attn, c.q, c.k, c.v, c.pos, c.bias, c.off)
+    out, saved = c.rse.seq_attention_fwd(*where, max_len=80, for_backward=True, stream=side)
+    views = (joint[:, :4], joint[:, 4:6], joint[:, 6:])
+    got = c.rse.seq_attention_bwd(*where, saved, c.dout, max_len=80, grads=views, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want["out"]) and torch.equal(got[3], want["dbias"])
+    for x, name in zip(views, ("dq", "dk", "dv")):
+        assert torch.equal(x, want[name]), name
+
+
+def test_max_len_is_only_a_bound():
+    """A looser max_len may take other kernels: the results keep their bounds."""
+    for dtype in (F32, BF16):
+        c = Case([20, 100, 3], 4, 2, 64, dtype)
+        ref = c.oracle()
+        for most in (100, 123, None, 10**12):
+            got = c.run(max_len=most)
+            for name in got:
+                _check(got[name], ref[name], f"{name} at max_len {most}")
+
+
+def test_malformed_offsets_are_reported():
+    c = Case([20, 30], 2, 1, 64, BF16)
+    for bad in ([0, 20, 49], [0, 60, 50], [1, 20, 50], [0, -5, 50]):
+        c.off = torch.tensor(bad, dtype=torch.int64).cuda()
+        c.forward(max_len=50)
+        assert c.attn.status() == -9, bad
+        c.attn.clear_status()
+    c.off = torch.tensor([0, 20, 50], dtype=torch.int64).cuda()
+    c.forward(max_len=29)                        # the second sequence is longer
+    assert c.attn.status() == -9
+    c.attn.clear_status()
+    _check(c.forward(max_len=30), c.oracle(False)["out"], "after the status was cleared")
+
+
+def test_refusals_of_tensors():
+    c = Case([20, 30], 2, 1, 64, BF16)
+    rse = c.rse
+    where = [c.attn, c.q, c.k, c.v, c.pos, c.bias, c.off]
+
+    def call(at, x):
+        return rse.seq_attention_fwd(*where[:at], x, *where[at + 1:])
+
+    with pytest.raises(TypeError):
+        call(1, c.q.float())
+    with pytest.raises(ValueError):
+        call(1, c.q[:, :1])
+    with pytest.raises(ValueError, match="16 bytes"):
+        call(2, torch.zeros((50, 1, 68), dtype=torch.bfloat16, device="cuda")[:, :, 1:65])
+    with pytest.raises(ValueError, match="16 bytes"):
+        call(2, torch.zeros((50, 64, 2), dtype=torch.bfloat16, device="cuda")[:, :, :1].transpose(1, 2))
+    with pytest.raises(TypeError):
+        call(4, c.pos.long())
+    with pytest.raises(ValueError):
+        call(5, c.bias[:, 1:].contiguous())
+    with pytest.raises(TypeError):
+        call(6, c.off.int())
+    with pytest.raises(ValueError):
+        call(6, c.off[:1])
+    with pytest.raises(rse.RseError) as e:
+        rse.seq_attention_fwd(*where, max_len=-1)
+    assert e.value.code == -1
+    out, saved = rse.seq_attention_fwd(*where, for_backward=True)
+    with pytest.raises(rse.RseError) as e:
+        rse.seq_attention_bwd(*where, saved[:8].contiguous(), c.dout)
+    assert e.value.code == -3
+
+
+# ------------------------------------------------------------------- serving --
+class Serving:
+    def __init__(self, lens, H, Hk, D, dtype, page=16, bounds=(1, 2, 4, 8, 16, 32, 64, 128), extra=0, seed=0):
+        import recommender_sparse_embedding_amd as rse
+
+        self.rse, self.lens, self.page, self.dtype, self.bounds = rse, lens, page, dtype, list(bounds)
+        g = torch.Generator().manual_seed(seed + sum(lens))
+        B, most = len(lens), max(max(lens) // page + 1, 1)
+        n_pages = B * most + 2 + extra
+        self.table = (torch.randperm(B * most, generator=g) + 2 + extra).view(B, most).to(torch.int32)
+        norm = lambda *s: torch.randn(s, generator=g).to(DT[dtype]).cuda()  # noqa: E731
+        self.cache = rse.SeqCache.empty(n_pages, page, Hk, D, dtype)
+        if extra < 1000:                         # what nobody cached is NaN
+            self.cache.k.fill_(float("nan"))
+            self.cache.v.fill_(float("nan"))
+            self.cache.pos.fill_(-2**31)
+        self.q, self.nk, self.nv = norm(B, H, D), norm(B, Hk, D), norm(B, Hk, D)
+        self.hist = []
+        for b, n in enumerate(lens):
+            if n < 0:
+                self.hist.append(None)
+                continue
+            k, v = norm(n, Hk, D), norm(n, Hk, D)
+            t = torch.randint(0, 40, (n + 1,), generator=g).cumsum(0).to(torch.int32).cuda()
+            slot = self.table[b].long()[torch.arange(n) // page] * page + torch.arange(n) % page
+            at = slot.cuda()
+            self.cache.k.view(-1, Hk, D)[at] = k
+            self.cache.v.view(-1, Hk, D)[at] = v
+            self.cache.pos.view(-1)[at] = t[:n]
+            self.hist.append((torch.cat([k, self.nk[b:b + 1]]), torch.cat([v, self.nv[b:b + 1]]), t))
+        self.pos = torch.tensor([0 if h is None else int(h[2][-1]) for h in self.hist], dtype=torch.int32).cuda()
+        self.bias = torch.randn((H, len(bounds) + 1), generator=g).cuda()
+        self.attn = rse.SeqAttention(H, Hk, D, dtype, bounds)
+        self.t_lens = torch.tensor(lens, dtype=torch.int64).cuda()
+        self.table = self.table.cuda()
+
+    def run(self, **kw):
+        kw = {"max_len": max(self.lens) + 1, **kw}
+        return self.rse.seq_attention_step(self.attn, self.cache, self.q, self.nk, self.nv, self.pos, self.bias,
+                                           self.table, self.t_lens, **kw)
+
+    def oracle(self):
+        hist = [None if h is None else (_np(h[0]), _np(h[1]), h[2].cpu().numpy()) for h in self.hist]
+        return oseq.step(hist, _np(self.q), _np(self.bias), self.bounds, self.attn.scale, KIND[self.dtype])
+
+    def check(self):
+        out = self.run()
+        _check(out, self.oracle(), "step")
+        assert self.cache.status() == 0
+        for b, n in enumerate(self.lens):
+            if n >= 0:
+                p = int(self.table[b, n // self.page])
+                assert torch.equal(self.cache.k[p, n % self.page], self.nk[b])
+                assert torch.equal(self.cache.v[p, n % self.page], self.nv[b])
+                assert int(self.cache.pos[p, n % self.page]) == int(self.pos[b])
+            else:
+                assert torch.all(out[b] == 0)
+        assert torch.equal(self.run(), out)      # the lengths did not move: the same again
+        return out
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("lens,page", [([0], 16), ([0, -1, 1, 15, 16, 17], 16), ([31, 32, 33, 63, 64, 65, -1], 8),
+                                       ([300], 64), ([1500, 3, 700], 32), ([5], 1024)])
+def test_step_lengths(lens, page, D, dtype):
+    Serving(lens, 4, 2, D, dtype, page).check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (3, 3), (8, 1), (12, 4), (16, 1), (40, 2)])
+def test_step_heads(H, Hk, dtype):
+    Serving([100, 37, 0], H, Hk, 64, dtype).check()
+
+
+@pytest.mark.parametrize("bounds", [(), tuple(range(-60, 67)), tuple(2**m for m in range(31))])
+def test_step_boundaries(bounds):
+    Serving([100, 260], 4, 2, 32, BF16, bounds=bounds).check()
+
+
+def test_step_pool_past_32_bits():
+    """Pages past 2^32 bytes and 2^31 elements of the pool."""
+    extra = (1 << 31) // (64 * 2 * 128) + 100
+    Serving([70, 10], 4, 2, 128, BF16, 64, extra=extra).check()
+
+
+def test_step_bad_input_is_reported():
+    s = Serving([20, 40], 4, 2, 64, BF16)
+    good = s.run()
+    s.run(max_len=30)                            # the second history is longer
+    assert s.cache.status() == -9
+    s.cache.clear_status()
+    table = s.table.clone()
+    s.table[1, 0] = 10**6
+    out = s.run()
+    assert s.cache.status() == -9 and torch.equal(out[0], good[0]) and torch.all(torch.isfinite(out))
+    s.cache.clear_status()
+    s.table = table
+    s.t_lens = torch.tensor([20, 10**9], dtype=torch.int64).cuda()
+    out = s.run()
+    assert s.cache.status() == -9 and torch.equal(out[0], good[0]) and torch.all(out[1] == 0)
+
+
+def test_step_in_a_graph():
+    s = Serving([20, 400, -1, 0], 4, 2, 64, BF16)
+    want = s.check().clone()
+    out = torch.empty_like(want)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        s.run(out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.run(out=out)
+    for _ in range(4):
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert torch.equal(s.run(), want)
+
+
+def test_training_in_a_graph():
+    c = Case([20, 130, 0, 64], 4, 2, 64, BF16)
+    want = c.run()
+    torch.cuda.synchronize()
+    where = (c.attn, c.q, c.k, c.v, c.pos, c.bias, c.off)
+
+    def once():
+        out, saved = c.rse.seq_attention_fwd(*where, max_len=c.max_len, for_backward=True)
+        return (out, *c.rse.seq_attention_bwd(*where, saved, c.dout, max_len=c.max_len))
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = once()
+    for _ in range(4):
+        for t in got:
+            t.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, name in zip(got, ("out", "dq", "dk", "dv", "dbias")):
+            assert torch.equal(t, want[name]), name
+        c.run()
+
+
+@pytest.mark.parametrize("page", [8, 64])
+@pytest.mark.parametrize("B", [1, 7, 1500])
+def test_assign_and_write(B, page):
+    import recommender_sparse_embedding_amd as rse
+
+    rng = np.random.default_rng(B + page)
+    lens = rng.integers(0, 40, B)
+    counts = np.where(rng.random(B) < 0.2, 0, rng.integers(0, 90, B))
+    most = int((lens + counts).max()) // page + 1
+    n_pages = B * most + 5
+    ids = rng.permutation(n_pages).astype(np.int32)
+    held = np.arange(most)[None, :] < -(-lens[:, None] // page)
+    table = np.where(held, ids[:B * most].reshape(B, most), -1).astype(np.int32)
+    free = np.setdiff1d(ids, table[held])
+    rng.shuffle(free)
+    ref = oseq.assign(counts, lens, table, free, page)
+    cache = rse.SeqCache.empty(n_pages, page, 2, 32)
+    for t in (cache.k, cache.v, cache.pos):
+        t.zero_()
+    cuda = lambda x, dt: torch.tensor(x, dtype=dt).cuda()  # noqa: E731
+    t_table, N = cuda(table, torch.int32), int(counts.sum())
+    args = (cache, cuda(counts, torch.int64), cuda(lens, torch.int64), t_table)
+    slots, off, taken = rse.seq_cache_assign(*args, cuda(free, torch.int32), N)
+    assert slots.tolist() == ref[0] and off.tolist() == ref[1] and taken.item() == ref[2]
+    assert t_table.tolist() == ref[3] and cache.status() == 0
+    joint = torch.randn((N, 4, 32), device="cuda").bfloat16()
+    pos = torch.arange(N, dtype=torch.int32, device="cuda")
+    rse.seq_cache_write(cache, slots, joint[:, :2], joint[:, 2:], pos)
+    assert torch.equal(cache.k.view(-1, 2, 32)[slots], joint[:, :2])
+    assert torch.equal(cache.v.view(-1, 2, 32)[slots], joint[:, 2:])
+    assert torch.equal(cache.pos.view(-1)[slots], pos)
+    rest = torch.ones(n_pages * page, dtype=torch.bool, device="cuda")
+    rest[slots] = False
+    assert torch.all(cache.k.view(-1, 64)[rest] == 0) and torch.all(cache.pos.view(-1)[rest] == 0)
+    if ref[2] == 0:
+        return
+    # a free list one page short: nothing is assigned
+    before = cuda(table, torch.int32)
+    again = before.clone()
+    slots, _, taken = rse.seq_cache_assign(*args[:3], again, cuda(free[:ref[2] - 1], torch.int32), N)
+    assert cache.status() == -5 and torch.all(slots == -1) and taken.item() == 0 and torch.equal(again, before)
+    cache.clear_status()
+    # a count that does not fit the table, a negative one, a wrong sum
+    for bad in ((0, most * page + 1), (0, -1), (0, int(counts[0]) + 1)):
+        c = counts.copy()
+        c[bad[0]] = bad[1]
+        _, _, taken = rse.seq_cache_assign(cache, cuda(c, torch.int64), args[2], again, cuda(free, torch.int32), N)
+        assert cache.status() == -9 and taken.item() == 0 and torch.equal(again, before)
+        cache.clear_status()
+    # slots: negative ones are skipped, one past the pool is reported
+    kept = cache.k.clone()
+    odd = torch.tensor([-1, n_pages * page], dtype=torch.int64, device="cuda")
+    two = torch.ones((2, 2, 32), dtype=torch.bfloat16, device="cuda")
+    rse.seq_cache_write(cache, odd, two, two, torch.zeros(2, dtype=torch.int32, device="cuda"))
+    assert cache.status() == -9 and torch.equal(cache.k, kept)
+
+
+def test_prompt_then_steps_equal_one_pass():
+    """A session's events through the forward, their keys stored, then events
+    one by one: each step's output is the causal forward's row."""
+    import recommender_sparse_embedding_amd as rse
+
+    g = torch.Generator().manual_seed(4)
+    lens, more, H, Hk, D, P = [5, 40, 0, 33], 3, 4, 2, 64, 16
+    B, full = len(lens), [n + more for n in lens]
+    N = sum(full)
+    q, k, v = (torch.randn((N, h, D), generator=g).bfloat16().cuda() for h in (H, Hk, Hk))
+    pos = torch.randint(0, 20, (N,), generator=g).cumsum(0).to(torch.int32).cuda()
+    bias = torch.randn((H, 6), generator=g).cuda()
+    attn = rse.SeqAttention(H, Hk, D, rse.BF16, [1, 5, 25, 125, 625])
+    off = torch.tensor(np.concatenate([[0], np.cumsum(full)]), dtype=torch.int64).cuda()
+    want = rse.seq_attention_fwd(attn, q, k, v, pos, bias, off)
+    cache = rse.SeqCache.empty(64, P, Hk, D)
+    table = torch.full((B, 4), -1, dtype=torch.int32, device="cuda")
+    free = torch.randperm(64, generator=g).to(torch.int32).cuda()
+    first = torch.cat([torch.arange(int(off[b]), int(off[b]) + n) for b, n in enumerate(lens)]).cuda()
+    held = torch.zeros(B, dtype=torch.int64, device="cuda")
+    counts = torch.tensor(lens, dtype=torch.int64).cuda()
+    slots, _, taken = rse.seq_cache_assign(cache, counts, held, table, free, len(first))
+    rse.seq_cache_write(cache, slots, k[first], v[first], pos[first])
+    held, free = counts.clone(), free[int(taken):].contiguous()
+    one = torch.ones(B, dtype=torch.int64, device="cuda")
+    for _ in range(more):
+        _, _, taken = rse.seq_cache_assign(cache, one, held, table, free, B)
+        at = off[:-1] + held
+        out = rse.seq_attention_step(attn, cache, q[at], k[at], v[at], pos[at], bias, table, held)
+        # both round the same sums in another order
+        assert torch.allclose(out.float(), want[at].float(), rtol=2**-6, atol=2**-8)
+        held += 1
+        free = free[int(taken):].contiguous()
+    assert cache.status() == 0 and attn.status() == 0
