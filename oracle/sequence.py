@@ -13,8 +13,9 @@ from __future__ import annotations
 import numpy as np
 
 U = 2.0 ** -24          # unit roundoff of fp32
-R = {"f32": 0.0, "bf16": 2.0 ** -9}      # rounding of a factor before a product
-OUT = {"f32": 2.0 ** -24, "bf16": 2.0 ** -9}
+UB = 2.0 ** -8          # unit roundoff of bf16: 8 significant bits, to nearest
+R = {"f32": 0.0, "bf16": UB}             # rounding of a factor before a product
+OUT = {"f32": U, "bf16": UB}
 
 
 def bucket(pos_i, pos_j, boundaries):

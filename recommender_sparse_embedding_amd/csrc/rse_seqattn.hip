@@ -4,7 +4,7 @@
 #include <cmath>
 #include <new>
 
-#include "rse_seq.h"
+#include "rse_seqmma.h"
 
 using namespace rse;
 using namespace rse_host;
@@ -64,55 +64,217 @@ __device__ __forceinline__ bool visible(const SeqArgs& a, int64_t i, int64_t j) 
     return (!a.causal || j <= i) && (!a.key_off || a.key_off[j] >= 0);
 }
 
-// One wave per event and query head, 64 keys at a time.
-template <typename T, int D>
-__global__ __launch_bounds__(AB) void k_attn_fwd(SeqArgs a, Rows<const T> q, Rows<const T> k, Rows<const T> v,
-                                                 Rows<T> out, float* lse) {
-    __shared__ int32_t bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
-    __shared__ float sq[AW][D];
-    for (int t = threadIdx.x; t <= RSE_SEQ_MAX_BOUNDARIES; t += AB) bounds[t] = a.hdr->bounds[t];
-    __syncthreads();
-    constexpr int E = (D + WAVE - 1) / WAVE;
-    const int lane = lane_id(), w = threadIdx.x / WAVE;
-    const int64_t items = a.n_events * a.n_heads;
-    for (int64_t it = (int64_t)blockIdx.x * AW + w; it < items; it += (int64_t)gridDim.x * AW) {
-        const int64_t i = it / a.n_heads;
-        const int h = (int)(it % a.n_heads), g = h / a.group;
-        int64_t s, e;
-        if (!find_seq(a, i, s, e)) continue;
-        for (int d = lane; d < D; d += WAVE) sq[w][d] = to_f32(q.at(i, h)[d]);
-        wave_lds_sync();
-        float m = -INFINITY, l = 0.f, acc[E] = {};
-        const int64_t end = a.causal ? i + 1 : e;
-        for (int64_t c = s; c < end; c += WAVE) {
-            const int64_t j = c + lane;
-            float x = -INFINITY;
-            if (j < end && visible(a, i, j))
-                x = dot_row<T, D>(sq[w], k.at(j, g)) * a.scale +
-                    a.bias[h * (a.n_bounds + 1) + seq_bucket(bounds, a.n_bounds, seq_dist(a.pos[i], a.pos[j]))];
-            const float top = fmaxf(m, wave_max(x));
-            if (top == -INFINITY) continue;
-            const float p = expf(x - top), r = expf(m - top);
-            l = l * r + wave_sum(p);
-            m = top;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+// More distinct buckets than this in a tile: looked up event by event.
+constexpr int CHAIN = 6;
+
+// Bias (base 2) of the lane's column for the 16 rows of a 32 x 32 tile that
+// may span buckets lo .. hi, added to s times c.  row_pos: positions of the
+// tile's rows in LDS.  A tile of few buckets compares each distance with the
+// boundaries between them; with many, each distance is searched in the LDS
+// copy of the boundaries.
+// `column_first`: the column event is the query (distance = column - row).
+template <bool column_first>
+__device__ __forceinline__ f32x16 add_bias(f32x16 s, float c, const WaveBuckets& wb, int lo, int hi, const int32_t* row_pos,
+                                           int32_t col_pos, const int32_t* s_bounds, const float* s_bias) {
+    const int h = lane_id() >> 5;
+    int32_t dist[16];
 #pragma unroll
-            for (int u = 0; u < E; ++u) acc[u] *= r;
-            const unsigned long long used = __ballot(x > -INFINITY);
-            for (int t = 0; t < WAVE; ++t) {
-                if (!((used >> t) & 1)) continue;
-                const float pt = __shfl(p, t, WAVE);
+    for (int j = 0; j < 4; ++j) {
+        const i32x4 p = *reinterpret_cast<const i32x4*>(row_pos + 8 * j + 4 * h);
 #pragma unroll
-                for (int u = 0; u < E; ++u)
-                    if (u * WAVE + lane < D)
-                        acc[u] = __fmaf_rn(pt, to_f32(v.at(c + t, g)[u * WAVE + lane]), acc[u]);
+        for (int i = 0; i < 4; ++i) dist[4 * j + i] = column_first ? seq_dist(col_pos, p[i]) : seq_dist(p[i], col_pos);
+    }
+    f32x16 b;
+    if (hi - lo <= CHAIN) {
+        const float b0 = wb.value(lo);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) b[r] = b0;
+        for (int m = lo; m < hi; ++m) {
+            const int32_t edge = wb.boundary(m);
+            const float bm = wb.value(m + 1);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) b[r] = dist[r] >= edge ? bm : b[r];
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) b[r] = s_bias[seq_bucket(s_bounds, wb.n, dist[r])];
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], c, b[r]);
+    return s;
+}
+
+// Forward.  A block of W waves takes 32 W queries of one sequence and head; a
+// wave has 32 of them as columns.  Keys go by in tiles of KT, staged in LDS
+// row-major (the next tile's loads are in flight meanwhile): S^T = K Q^T,
+// online softmax down the registers of a lane (a row's maximum needs one
+// exchange between the wave's halves, its sum none until the end), and
+// O^T += V^T P^T with the same registers as operand.
+template <typename T, int D, int W, int KT>
+__global__ __launch_bounds__(W * 64) void k_attn_fwd(SeqArgs a, Rows<const T> q, Rows<const T> k, Rows<const T> v,
+                                                     Rows<T> out, float* lse) {
+    using TL = Tile<T, D>;
+    constexpr int NT = W * 64, CH = TL::CH, PER = KT * CH / NT, NS = KT / 32, ND = D / 32;
+    static_assert(KT * CH % NT == 0 && KT <= 64, "tile shape");
+    __shared__ u32x4 s_k[2][KT * CH], s_v[2][KT * CH];
+    __shared__ float s_mask[2][KT];
+    __shared__ int32_t s_pos[2][KT];
+    __shared__ int32_t s_range[2][3];           // lowest and highest position, any key hidden
+    __shared__ int32_t s_bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
+    __shared__ float s_bias[RSE_SEQ_MAX_BOUNDARIES + 1];
+    const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5;
+    const int head = blockIdx.y, g = head / a.group, nb = a.n_bounds + 1;
+    int64_t s;
+    int len, tile;
+    if (!find_tile(a, blockIdx.x, 32 * W, s, len, tile, head == 0)) return;
+    const int n_tiles = (len + 32 * W - 1) / (32 * W);
+    if (a.causal) tile = n_tiles - 1 - tile;    // the longest first
+    const int q0 = tile * 32 * W, my_q = q0 + 32 * w + (lane & 31), row = my_q < len ? my_q : len - 1;
+    const int end = a.causal ? (q0 + 32 * W < len ? q0 + 32 * W : len) : len;      // keys of the block
+    const int my_end = a.causal && q0 + 32 * w + 32 < end ? q0 + 32 * w + 32 : end;  // and of the wave
+
+    WaveBuckets wb;
+    wb.load(a.hdr, a.bias + head * nb, a.n_bounds, LOG2E);
+    for (int t = threadIdx.x; t <= RSE_SEQ_MAX_BOUNDARIES; t += NT) {
+        s_bounds[t] = a.hdr->bounds[t];
+        s_bias[t] = t < nb ? a.bias[head * nb + t] * LOG2E : 0.f;
+    }
+    ColFrag<T, D> qf;
+    qf.load(q.at(s + row, head), half);
+    if (a.scale < 0.f) qf.negate();
+    const float c2 = fabsf(a.scale) * LOG2E;
+    const int32_t my_pos = a.pos[s + row];
+    const int32_t q_lo = wave_min(my_pos), q_hi = wave_max(my_pos);
+
+    // staging: thread t holds chunk t % CH of rows t / CH, + NT / CH, ...
+    const int srow = threadIdx.x / CH, sch = threadIdx.x % CH;
+    u32x4 rk[PER], rv[PER];
+    int32_t rp = 0;
+    bool rs = false;
+    bool hid[PER];
+    auto load_tile = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int kk = k0 + srow + i * (NT / CH);
+            const int64_t j = s + (kk < end ? kk : end - 1);
+            rk[i] = gload_u4(k.at(j, g) + sch * TL::EPC);
+            rv[i] = gload_u4(v.at(j, g) + sch * TL::EPC);
+            hid[i] = kk >= end || (a.key_off && a.key_off[j] < 0);
+        }
+        if (threadIdx.x < KT) {
+            const int kk = k0 + (int)threadIdx.x;
+            const int64_t j = s + (kk < end ? kk : end - 1);
+            rp = a.pos[j];
+            rs = kk < end && !(a.key_off && a.key_off[j] < 0);
+        }
+    };
+    auto store_tile = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int at = TL::chunk_at(srow + i * (NT / CH), sch);
+            s_k[b][at] = hid[i] ? u32x4{0, 0, 0, 0} : rk[i];
+            s_v[b][at] = hid[i] ? u32x4{0, 0, 0, 0} : rv[i];
+        }
+        if (w == 0) {
+            const bool mine = lane < KT;
+            const int32_t lo = wave_min(mine ? rp : INT32_MAX), hi = wave_max(mine ? rp : INT32_MIN);
+            const bool any = __ballot(mine && !rs) != 0;
+            if (mine) {
+                s_mask[b][lane] = rs ? 0.f : -INFINITY;
+                s_pos[b][lane] = rp;
+            }
+            if (lane == 0) {
+                s_range[b][0] = lo;
+                s_range[b][1] = hi;
+                s_range[b][2] = any;
             }
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+    };
+
+    f32x16 o[ND] = {};
+    float m = -INFINITY, l = 0.f;
+    load_tile(0);
+    store_tile(0);
+    __syncthreads();
+    for (int k0 = 0, b = 0; k0 < end; k0 += KT, b ^= 1) {
+        if (k0 + KT < end) load_tile(k0 + KT);
+        if (k0 < my_end) {
+            f32x16 x[NS];
 #pragma unroll
-        for (int u = 0; u < E; ++u)
-            if (u * WAVE + lane < D) from_f32(out.at(i, h)[u * WAVE + lane], acc[u] * inv);
-        if (lse && lane == 0) lse[(int64_t)h * a.n_events + i] = l > 0.f ? m + logf(l) : -INFINITY;
-        wave_lds_sync();
+            for (int u = 0; u < NS; ++u) x[u] = mma_rows<T, D>(s_k[b], 32 * u, qf, f32x16{});
+            const int lo = wb.bucket(seq_dist(q_lo, s_range[b][1])), hi = wb.bucket(seq_dist(q_hi, s_range[b][0]));
+            const bool hidden = __builtin_amdgcn_readfirstlane(s_range[b][2]);
+            const bool diagonal = a.causal && k0 + KT - 1 > q0 + 32 * w;
+            float c = c2, bias = 0.f;           // p = exp2(x c + bias - m)
+            if (lo == hi && !hidden && !diagonal) {
+                bias = wb.value(lo);
+            } else {
+                c = 1.f;
+#pragma unroll
+                for (int u = 0; u < NS; ++u) {
+                    x[u] = add_bias<true>(x[u], c2, wb, lo, hi, s_pos[b] + 32 * u, my_pos, s_bounds, s_bias);
+                    if (hidden) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const f32x4 mk = *reinterpret_cast<const f32x4*>(&s_mask[b][32 * u + 8 * j + 4 * half]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[u][4 * j + i] += mk[i];
+                        }
+                    }
+                    if (diagonal) {
+                        const int lim = my_q - k0 - 32 * u - 4 * half;
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) x[u][r] = tile_row(r, 0) <= lim ? x[u][r] : -INFINITY;
+                    }
+                }
+            }
+            float top = x[0][0];
+#pragma unroll
+            for (int u = 0; u < NS; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) top = fmaxf(top, x[u][r]);
+            top = fmaxf(top, other_half(top));
+            top = __builtin_fmaf(top, c, bias);
+            // the reference of the exponents follows the maximum only when it
+            // has grown by more than 8 (p up to 2^8, exact in a float), so
+            // that most tiles leave the sums as they are
+            if (__any(top > m + 8.f || (m == -INFINITY && top > -INFINITY))) {
+                const float ref = fmaxf(m, top);
+                const float r = ref == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - ref);
+                m = ref;
+                l *= r;
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) o[dt] *= r;
+            }
+            const float shift = m == -INFINITY ? 0.f : bias - m;
+            RowOperand<T> p[NS];
+#pragma unroll
+            for (int u = 0; u < NS; ++u) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    x[u][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][r], c, shift));
+                    l += x[u][r];
+                }
+                p[u].set(x[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < NS; ++u)
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) o[dt] = mma_over_rows<D>(s_v[b], 32 * u, dt, p[u], o[dt]);
+        }
+        if (k0 + KT < end) {
+            store_tile(b ^ 1);
+            __syncthreads();
+        }
+    }
+    l += other_half(l);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    if (my_q < len) {
+        T* dst = out.at(s + my_q, head);
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) store_column(dst + 32 * dt, o[dt], inv);
+        if (lse && half == 0) lse[(int64_t)head * a.n_events + s + my_q] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
     }
 }
 
@@ -265,7 +427,7 @@ SeqArgs seq_args(const rse_seqattn* a, const rse_seq_batch* b) {
     s.offsets = b->d_offsets;
     s.batch = b->batch;
     s.n_events = b->n_events;
-    s.max_len = b->max_len;
+    s.max_len = b->max_len < INT32_MAX / 2 ? b->max_len : INT32_MAX / 2;   // tiles count events in 32 bits
     s.pos = b->d_pos;
     s.key_off = b->d_key_off;
     s.bias = b->d_bias;
@@ -296,12 +458,26 @@ BwdWs bwd_ws(const rse_seqattn* a, int64_t n, void* base) {
     return w;
 }
 
-template <typename T, int D>
-int run_fwd(const rse_seqattn* at, const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k,
-            const rse_seq_rows* v, const rse_seq_rows* out, float* lse, hipStream_t s) {
-    hipLaunchKernelGGL((k_attn_fwd<T, D>), dim3(fill_blocks(a.n_events * a.n_heads, AW, 1 << 16)), dim3(AB), 0, s, a,
+template <typename T, int D, int W>
+int run_fwd_w(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v,
+              const rse_seq_rows* out, float* lse, hipStream_t s) {
+    // keys of a tile: 64 where two buffers of them take at most 64 KiB and
+    // there are several waves to stage them
+    constexpr int KT = W > 1 && D * sizeof(T) <= 256 ? 64 : 32;
+    const int64_t slots = tile_slots(a.n_events, a.batch, 32 * W);
+    if (slots > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((k_attn_fwd<T, D, W, KT>), dim3((unsigned)slots, a.n_heads), dim3(W * WAVE), 0, s, a,
                        rows_view<const T>(q), rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), lse);
     return launch_status();
+}
+
+// Waves of a block: as many groups of 32 queries as a sequence can have, up to 4.
+template <typename T, int D>
+int run_fwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v,
+            const rse_seq_rows* out, float* lse, hipStream_t s) {
+    if (a.max_len <= 32) return run_fwd_w<T, D, 1>(a, q, k, v, out, lse, s);
+    if (a.max_len <= 64) return run_fwd_w<T, D, 2>(a, q, k, v, out, lse, s);
+    return run_fwd_w<T, D, 4>(a, q, k, v, out, lse, s);
 }
 
 template <typename T, int D>
@@ -422,7 +598,7 @@ int seq_attention_fwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
     if (d_saved && saved_bytes < saved_bytes_of(attn, batch->n_events)) return RSE_ERR_WORKSPACE;
     const SeqArgs a = seq_args(attn, batch);
     return by_type(attn, [&](auto t, auto d) {
-        return run_fwd<decltype(t), decltype(d)::value>(attn, a, q, k, v, out, static_cast<float*>(d_saved),
+        return run_fwd<decltype(t), decltype(d)::value>(a, q, k, v, out, static_cast<float*>(d_saved),
                                                         as_stream(stream));
     });
 }
