@@ -3,6 +3,8 @@
 // public ABI).
 #pragma once
 
+#include <type_traits>
+
 #include "rse_host.h"
 
 namespace rse {
@@ -123,6 +125,60 @@ inline bool rows_ok(const rse_seq_rows* r, int32_t dtype) {
 template <typename T>
 inline rse::Rows<T> rows_view(const rse_seq_rows* r) {
     return {static_cast<T*>(r->data), r->row_stride, r->head_stride};
+}
+
+inline int batch_ok(const rse_seqattn* a, const rse_seq_batch* b) {
+    if (!a || !b || !b->d_offsets || !b->d_bias) return RSE_ERR_INVALID_ARG;
+    if (b->batch < 0 || b->n_events < 0 || b->max_len < 0) return RSE_ERR_INVALID_ARG;
+    if (b->n_events > 0 && (!b->d_pos || b->batch == 0 || b->max_len == 0)) return RSE_ERR_INVALID_ARG;
+    return RSE_OK;
+}
+
+inline rse::SeqArgs seq_args(const rse_seqattn* a, const rse_seq_batch* b) {
+    rse::SeqArgs s;
+    s.offsets = b->d_offsets;
+    s.batch = b->batch;
+    s.n_events = b->n_events;
+    s.max_len = b->max_len < INT32_MAX / 2 ? b->max_len : INT32_MAX / 2;   // tiles count events in 32 bits
+    s.pos = b->d_pos;
+    s.key_off = b->d_key_off;
+    s.bias = b->d_bias;
+    s.hdr = a->hdr;
+    s.n_heads = a->n_heads;
+    s.group = a->n_heads / a->n_kv_heads;
+    s.n_bounds = a->n_bounds;
+    s.causal = a->causal;
+    s.scale = a->scale;
+    return s;
+}
+
+// What a forward leaves for its backward: base-2 log-sums [n_heads][n_events]
+// and, unrounded, the outputs [n_events][n_heads][dim].
+struct Saved {
+    float* lse2;
+    float* out32;
+    size_t bytes;
+};
+inline Saved saved_view(const rse_seqattn* a, int64_t n, void* base) {
+    Carver c(base);
+    Saved v;
+    v.lse2 = c.take<float>((size_t)a->n_heads * n);
+    v.out32 = c.take<float>((size_t)n * a->n_heads * a->dim);
+    v.bytes = c.size();
+    return v;
+}
+
+// f(T(), integral_constant<dim>) for the handle's type and dim.
+template <typename F>
+inline int by_type(const rse_seqattn* a, F f) {
+    if (a->dtype == RSE_F32) {
+        if (a->dim == 32) return f(float(), std::integral_constant<int, 32>());
+        if (a->dim == 64) return f(float(), std::integral_constant<int, 64>());
+        return f(float(), std::integral_constant<int, 128>());
+    }
+    if (a->dim == 32) return f(uint16_t(), std::integral_constant<int, 32>());
+    if (a->dim == 64) return f(uint16_t(), std::integral_constant<int, 64>());
+    return f(uint16_t(), std::integral_constant<int, 128>());
 }
 
 }  // namespace rse_host

@@ -69,6 +69,15 @@ struct ColFrag {
     }
 };
 
+// Elements e .. e + 3 of a chunk as fp32.
+template <typename T>
+__device__ __forceinline__ f32x4 chunk_f32(u32x4 v, int e) {
+    if (sizeof(T) == 4) return __builtin_bit_cast(f32x4, v);
+    const uint32_t a = v[e / 2], b = v[e / 2 + 1];
+    return f32x4{__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u), __uint_as_float(b << 16),
+                 __uint_as_float(b & 0xFFFF0000u)};
+}
+
 template <typename T>
 __device__ __forceinline__ f32x16 mma_chunk(u32x4 a, u32x4 b, f32x16 c);
 template <>
@@ -100,6 +109,7 @@ template <>
 struct RowOperand<float> {
     f32x16 v;
     __device__ __forceinline__ void set(const f32x16& x) { v = x; }
+    __device__ __forceinline__ void set_rest(const f32x16&, const RowOperand&) { v = f32x16{}; }
 };
 template <>
 struct RowOperand<uint16_t> {
@@ -109,6 +119,15 @@ struct RowOperand<uint16_t> {
         for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[s][i] = pack_bf16(x[8 * s + 2 * i], x[8 * s + 2 * i + 1]);
+    }
+    // what hi's rounding left of x (exact), rounded in turn
+    __device__ __forceinline__ void set_rest(const f32x16& x, const RowOperand& hi) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[s][i] = pack_bf16(x[8 * s + 2 * i] - __uint_as_float(hi.v[s][i] << 16),
+                                    x[8 * s + 2 * i + 1] - __uint_as_float(hi.v[s][i] & 0xFFFF0000u));
     }
 };
 
@@ -220,6 +239,74 @@ __device__ __forceinline__ int32_t wave_max(int32_t x) {
         x = y > x ? y : x;
     }
     return x;
+}
+
+constexpr float LOG2E = 1.4426950408889634f;
+// More distinct buckets than this in a tile: looked up event by event.
+constexpr int CHAIN = 6;
+
+// Buckets of the lane's column and the 16 rows of a tile that spans buckets
+// lo .. hi: compared with the boundaries between them, or searched.
+template <bool column_first>
+__device__ __forceinline__ void bucket_index(int (&idx)[16], const WaveBuckets& wb, int lo, int hi, const int32_t* row_pos,
+                                             int32_t col_pos, const int32_t* s_bounds) {
+    const int h = lane_id() >> 5;
+    int32_t dist[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const i32x4 p = *reinterpret_cast<const i32x4*>(row_pos + 8 * j + 4 * h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dist[4 * j + i] = column_first ? seq_dist(col_pos, p[i]) : seq_dist(p[i], col_pos);
+    }
+    if (hi - lo <= 2 * CHAIN) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) idx[r] = lo;
+        for (int m = lo; m < hi; ++m) {
+            const int32_t edge = wb.boundary(m);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) idx[r] += dist[r] >= edge;
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) idx[r] = seq_bucket(s_bounds, wb.n, dist[r]);
+    }
+}
+
+// Bias (base 2) of the lane's column for the 16 rows of a 32 x 32 tile that
+// may span buckets lo .. hi, added to s times c.  row_pos: positions of the
+// tile's rows in LDS.  A tile of few buckets compares each distance with the
+// boundaries between them; with many, each distance is searched in the LDS
+// copy of the boundaries.
+// `column_first`: the column event is the query (distance = column - row).
+template <bool column_first>
+__device__ __forceinline__ f32x16 add_bias(f32x16 s, float c, const WaveBuckets& wb, int lo, int hi, const int32_t* row_pos,
+                                           int32_t col_pos, const int32_t* s_bounds, const float* s_bias) {
+    const int h = lane_id() >> 5;
+    int32_t dist[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const i32x4 p = *reinterpret_cast<const i32x4*>(row_pos + 8 * j + 4 * h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dist[4 * j + i] = column_first ? seq_dist(col_pos, p[i]) : seq_dist(p[i], col_pos);
+    }
+    f32x16 b;
+    if (hi - lo <= CHAIN) {
+        const float b0 = wb.value(lo);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) b[r] = b0;
+        for (int m = lo; m < hi; ++m) {
+            const int32_t edge = wb.boundary(m);
+            const float bm = wb.value(m + 1);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) b[r] = dist[r] >= edge ? bm : b[r];
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) b[r] = s_bias[seq_bucket(s_bounds, wb.n, dist[r])];
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], c, b[r]);
+    return s;
 }
 
 // ------------------------------------------------------------- tile finder --
