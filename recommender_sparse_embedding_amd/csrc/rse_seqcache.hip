@@ -3,7 +3,7 @@
 // attention of one new event per user over its cached history.
 #include <new>
 
-#include "rse_seq.h"
+#include "rse_seqmma.h"
 
 using namespace rse;
 using namespace rse_host;
@@ -161,86 +161,279 @@ __device__ __forceinline__ bool step_ok(const StepArgs& a, int64_t n) {
     return true;
 }
 
-template <typename T>
-__global__ __launch_bounds__(CB) void k_step_append(StepArgs a, Rows<const T> k, Rows<const T> v, T* kp, T* vp, int n_kv,
-                                                    int dim) {
-    const int64_t b = blockIdx.x, n = a.lens[b];
-    if (!step_ok(a, n)) return;
-    const int64_t s = slot_of(a, b, n);
-    if (s < 0) return;
-    for (int x = threadIdx.x; x < n_kv * dim; x += CB) {
-        kp[s * n_kv * dim + x] = k.at(b, x / dim)[x % dim];
-        vp[s * n_kv * dim + x] = v.at(b, x / dim)[x % dim];
-    }
-    if (threadIdx.x == 0) a.tp[s] = a.pos[b];
-}
+// One new event per user.  A block of SW waves takes the heads that share one
+// key/value head (at most 32, as columns; column c is head h0 + c) and one of
+// `splits` equal parts of a user's tiles of 32 events; its waves take tiles in
+// turn, each from memory to its own registers and LDS, so that no wave waits
+// for another: K rows are read as matrix operands straight from the page, V
+// rows pass through the wave's LDS tile.  The waves' softmax sums are joined
+// in LDS at the end; with more than one part, k_step_join joins the parts.
+// The new event's own key and value are read from the call's arguments (no
+// other block waits for the store that the first part makes).
+constexpr int SW = 4;
 
-// One wave per user and query head, 64 events at a time.
 template <typename T, int D>
-__global__ __launch_bounds__(CB) void k_step(StepArgs a, Rows<const T> q, const T* kp, const T* vp, Rows<T> out) {
-    __shared__ int32_t bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
-    __shared__ float sq[CW][D];
-    for (int t = threadIdx.x; t <= RSE_SEQ_MAX_BOUNDARIES; t += CB) bounds[t] = a.hdr->bounds[t];
-    __syncthreads();
-    constexpr int E = (D + WAVE - 1) / WAVE;
-    const int lane = lane_id(), w = threadIdx.x / WAVE, n_kv = a.n_heads / a.group;
-    const int64_t it = (int64_t)blockIdx.x * CW + w;
-    if (it >= a.batch * a.n_heads) return;
-    const int64_t b = it / a.n_heads;
-    const int h = (int)(it % a.n_heads), g = h / a.group;
-    const int64_t n = a.lens[b];
-    float m = -INFINITY, l = 0.f, acc[E] = {};
-    if (step_ok(a, n)) {
-        for (int d = lane; d < D; d += WAVE) sq[w][d] = to_f32(q.at(b, h)[d]);
-        wave_lds_sync();
-        for (int64_t c = 0; c <= n; c += WAVE) {
-            const int64_t e = c + lane;
-            float x = -INFINITY;
-            const int64_t s = e <= n ? slot_of(a, b, e) : -1;
-            if (s >= 0) {
-                const T* row = kp + (s * n_kv + g) * D;
-                float dot = 0.f;
-                for (int d = 0; d < D; ++d) dot = __fmaf_rn(sq[w][d], to_f32(row[d]), dot);
-                x = dot * a.scale +
-                    a.bias[h * (a.n_bounds + 1) + seq_bucket(bounds, a.n_bounds, seq_dist(a.pos[b], a.tp[s]))];
+__global__ __launch_bounds__(SW * 64) void k_step(StepArgs a, Rows<const T> q, Rows<const T> k, Rows<const T> v, T* kp,
+                                                  T* vp, Rows<T> out, int splits, int cols, float* part_o, float* part_ml) {
+    using TL = Tile<T, D>;
+    constexpr int CH = TL::CH, ND = D / 32, NC = CH / 2;
+    extern __shared__ u32x4 s_mem[];            // SW tiles of V, then the waves' sums; s_bias [nb][cols]
+    __shared__ int32_t s_bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
+    __shared__ int32_t s_idx[SW][32];
+    __shared__ float s_ml[SW][2][32];
+    const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5, col = lane & 31;
+    const int n_kv = a.n_heads / a.group, nb = a.n_bounds + 1, blocks = (a.group + cols - 1) / cols;
+    int64_t x = blockIdx.x;
+    const int split = (int)(x % splits);
+    x /= splits;
+    const int cb = (int)(x % blocks);
+    x /= blocks;
+    const int g = (int)(x % n_kv);
+    const int64_t b = x / n_kv;
+    const int h0 = g * a.group + cb * cols, nc = a.group - cb * cols < cols ? a.group - cb * cols : cols;
+    const int head = h0 + (col < nc ? col : nc - 1);
+    u32x4* tile = s_mem + w * 32 * CH;
+    const int tiles_bytes = SW * 32 * CH * 16, sums_bytes = SW * cols * D * 4;
+    float* s_sum = reinterpret_cast<float*>(s_mem);
+    float* s_bias = reinterpret_cast<float*>(reinterpret_cast<char*>(s_mem) + (tiles_bytes > sums_bytes ? tiles_bytes : sums_bytes));
+
+    for (int t = threadIdx.x; t <= RSE_SEQ_MAX_BOUNDARIES; t += SW * 64) s_bounds[t] = a.hdr->bounds[t];
+    for (int t = threadIdx.x; t < nb * cols; t += SW * 64) {
+        const int c = t % cols;
+        s_bias[t] = a.bias[(h0 + (c < nc ? c : nc - 1)) * nb + t / cols] * LOG2E;
+    }
+    int64_t n = a.lens[b];
+    if (!step_ok(a, n)) n = -1;
+    const int64_t nt = (n + 32) / 32, t0 = nt * split / splits, t1 = nt * (split + 1) / splits;
+    const int32_t my_pos = a.pos[b];
+    const int64_t row_elems = (int64_t)n_kv * D;
+    if (n >= 0 && split == 0 && cb == 0 && w == 0) {                // the new event into its page
+        const int64_t s = slot_of(a, b, n);
+        if (s >= 0) {
+            const int c = lane < CH ? lane : 0;
+            const u32x4 kv = gload_u4(k.at(b, g) + c * TL::EPC), vv = gload_u4(v.at(b, g) + c * TL::EPC);
+            if (lane < CH) {
+                gstore_u4(kp + s * row_elems + g * D + c * TL::EPC, kv);
+                gstore_u4(vp + s * row_elems + g * D + c * TL::EPC, vv);
             }
-            float top = x;
-            for (int k = 32; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor(top, k, WAVE));
-            top = fmaxf(top, m);
-            if (top == -INFINITY) continue;
-            const float p = expf(x - top), r = expf(m - top);
-            float sum = p;
-            for (int k = 32; k > 0; k >>= 1) sum += __shfl_xor(sum, k, WAVE);
-            l = l * r + sum;
-            m = top;
+            if (g == 0 && lane == 0) a.tp[s] = my_pos;
+        }
+    }
+    __syncthreads();
+
+    ColFrag<T, D> qf;
+    qf.load(q.at(b, head), half);
+    if (a.scale < 0.f) qf.negate();
+    const float c2 = fabsf(a.scale) * LOG2E;
+
+    // the lane's event of a tile: its page, then its rows and time
+    auto page_of = [&](int64_t t) -> int64_t {
+        const int64_t e = t * 32 + col;
+        return t < t1 && e < n ? (int64_t)a.table[b * a.max_pages + (e >> a.shift)] : 0;
+    };
+    u32x4 rk[NC], rv[NC];
+    int32_t rp = 0;
+    bool see = false;
+    auto load_rows = [&](int64_t t, int64_t page) {
+        const int64_t e = t * 32 + col;
+        const T *kr = k.at(b, g), *vr = v.at(b, g);     // the new event's, also for lanes that may not look
+        rp = my_pos;
+        see = e <= n;
+        if (e < n) {
+            if (page < 0 || page >= a.n_pages) {
+                set_status(&a.status->status, RSE_ERR_BAD_INPUT);
+                see = false;
+            } else {
+                const int64_t s = (page << a.shift) + (e & ((1ll << a.shift) - 1));
+                kr = kp + s * row_elems + g * D;
+                vr = vp + s * row_elems + g * D;
+                rp = a.tp[s];
+            }
+        }
 #pragma unroll
-            for (int u = 0; u < E; ++u) acc[u] *= r;
-            for (int t = 0; t < WAVE; ++t) {
-                const int64_t st = __shfl(s, t, WAVE);
-                if (st < 0) continue;
-                const float pt = __shfl(p, t, WAVE);
+        for (int i = 0; i < NC; ++i) {
+            rk[i] = gload_u4(kr + (2 * i + half) * TL::EPC);
+            rv[i] = gload_u4(vr + (2 * i + half) * TL::EPC);
+        }
+    };
+
+    f32x16 o[ND] = {};
+    float m = -INFINITY, l = 0.f;
+    int64_t t = t0 + w;
+    int64_t page = page_of(t);
+    if (t < t1) load_rows(t, page);
+    page = page_of(t + SW);
+    for (; t < t1; t += SW) {
+        f32x16 s = {};
 #pragma unroll
-                for (int u = 0; u < E; ++u)
-                    if (u * WAVE + lane < D)
-                        acc[u] = __fmaf_rn(pt, to_f32(vp[(st * n_kv + g) * D + u * WAVE + lane]), acc[u]);
+        for (int i = 0; i < NC; ++i) s = mma_chunk<T>(rk[i], qf.v[i], s);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) tile[TL::chunk_at(col, 2 * i + half)] = see ? rv[i] : u32x4{0, 0, 0, 0};
+        const bool hidden = __ballot(!see) != 0;
+        const uint32_t seen = (uint32_t)__ballot(see);
+        // the 32 events' buckets; all in one is the common case far back
+        const int idx = seq_bucket(s_bounds, a.n_bounds, seq_dist(my_pos, rp));
+        const int lo = __builtin_amdgcn_readfirstlane(idx);
+        const bool one = __all(idx == lo);
+        s_idx[w][col] = idx * cols;
+        wave_lds_sync();
+        if (t + SW < t1) load_rows(t + SW, page);
+        page = page_of(t + 2 * SW);
+        const int cc = col < nc ? col : nc - 1;
+        if (one) {
+            const float b0 = s_bias[lo * cols + cc];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], c2, b0);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const i32x4 at = *reinterpret_cast<const i32x4*>(&s_idx[w][8 * j + 4 * half]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[4 * j + i] = __builtin_fmaf(s[4 * j + i], c2, s_bias[at[i] + cc]);
+            }
+        }
+        if (hidden) {
+            const uint32_t bits = seen >> (4 * half);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = (bits >> tile_row(r, 0)) & 1 ? s[r] : -INFINITY;
+        }
+        float top = s[0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) top = fmaxf(top, s[r]);
+        top = fmaxf(top, other_half(top));
+        const float ref = fmaxf(m, top);
+        if (__any(ref > m)) {
+            const float r = ref == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - ref);
+            m = ref;
+            l *= r;
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt) o[dt] *= r;
+        }
+        const float shift = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            s[r] = __builtin_amdgcn_exp2f(s[r] - shift);
+            l += s[r];
+        }
+        RowOperand<T> p;
+        p.set(s);
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) o[dt] = mma_over_rows<D>(tile, 0, dt, p, o[dt]);
+        wave_lds_sync();
+    }
+    l += other_half(l);
+    if (half == 0) {
+        s_ml[w][0][col] = m;
+        s_ml[w][1][col] = l;
+    }
+    __syncthreads();                            // the V tiles are done with: their place takes the sums
+    if (col < nc) {
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<f32x4*>(s_sum + (w * cols + col) * D + 32 * dt + 8 * j + 4 * half) =
+                    f32x4{o[dt][4 * j], o[dt][4 * j + 1], o[dt][4 * j + 2], o[dt][4 * j + 3]};
+    }
+    __syncthreads();
+    for (int y = threadIdx.x; y < nc * D; y += SW * 64) {
+        const int c = y / D, d = y % D;
+        float M = -INFINITY, L = 0.f, O = 0.f;
+        for (int u = 0; u < SW; ++u) M = fmaxf(M, s_ml[u][0][c]);
+        for (int u = 0; u < SW; ++u) {
+            const float r = M == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(s_ml[u][0][c] - M);
+            L = __builtin_fmaf(s_ml[u][1][c], r, L);
+            O = __builtin_fmaf(s_sum[(u * cols + c) * D + d], r, O);
+        }
+        if (splits == 1) {
+            from_f32(out.at(b, h0 + c)[d], L > 0.f ? O / L : 0.f);
+        } else {
+            const int64_t at = (b * a.n_heads + h0 + c) * splits + split;
+            part_o[at * D + d] = O;
+            if (d == 0) {
+                part_ml[2 * at] = M;
+                part_ml[2 * at + 1] = L;
             }
         }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+}
+
+// Joins a head's parts: one wave per user and head.
+template <typename T, int D>
+__global__ __launch_bounds__(CB) void k_step_join(const float* part_o, const float* part_ml, int64_t rows, int n_heads,
+                                                  int splits, Rows<T> out) {
+    const int lane = lane_id();
+    const int64_t at = (int64_t)blockIdx.x * CW + threadIdx.x / WAVE;
+    if (at >= rows) return;
+    const float m = lane < splits ? part_ml[2 * (at * splits + lane)] : -INFINITY;
+    float M = m;
+    for (int s = 32; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor(M, s, WAVE));
+    const float r = M == -INFINITY || lane >= splits ? 0.f : __builtin_amdgcn_exp2f(m - M);
+    float L = lane < splits ? r * part_ml[2 * (at * splits + lane) + 1] : 0.f;
+    for (int s = 32; s > 0; s >>= 1) L += __shfl_xor(L, s, WAVE);
+    constexpr int E = (D + WAVE - 1) / WAVE;
+    float O[E] = {};
+    for (int s = 0; s < splits; ++s) {
+        const float rs = __shfl(r, s, WAVE);
+#pragma unroll
+        for (int u = 0; u < E; ++u)
+            if (u * WAVE + lane < D) O[u] = __builtin_fmaf(rs, part_o[(at * splits + s) * D + u * WAVE + lane], O[u]);
+    }
 #pragma unroll
     for (int u = 0; u < E; ++u)
-        if (u * WAVE + lane < D) from_f32(out.at(b, h)[u * WAVE + lane], acc[u] * inv);
+        if (u * WAVE + lane < D) from_f32(out.at(at / n_heads, at % n_heads)[u * WAVE + lane], L > 0.f ? O[u] / L : 0.f);
+}
+
+// Parts of a history: enough blocks to fill the GPU four times over, each
+// wave with two tiles at least; k_step_join reads at most 64.
+constexpr int64_t STEP_BLOCKS = 1024;
+
+struct StepPlan {
+    int cols, blocks, splits;
+};
+StepPlan step_plan(const rse_seqattn* at, int64_t batch, int64_t max_len) {
+    StepPlan p;
+    const int group = at->n_heads / at->n_kv_heads;
+    p.cols = group < 32 ? group : 32;
+    p.blocks = (group + p.cols - 1) / p.cols;
+    const int64_t units = batch * at->n_kv_heads * p.blocks;
+    int64_t s = units > 0 ? (STEP_BLOCKS + units - 1) / units : 1;
+    const int64_t most = max_len / (32 * SW * 2);
+    if (s > most) s = most;
+    p.splits = (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
+    return p;
+}
+
+struct StepWs {
+    float* o;
+    float* ml;
+    size_t bytes;
+};
+StepWs step_ws(const rse_seqattn* at, int64_t batch, const StepPlan& p, void* base) {
+    Carver c(base);
+    const size_t n = p.splits > 1 ? (size_t)batch * at->n_heads * p.splits : 0;
+    StepWs w;
+    w.o = c.take<float>(n * at->dim);
+    w.ml = c.take<float>(2 * n);
+    w.bytes = c.size();
+    return w;
 }
 
 template <typename T, int D>
-int run_step(const rse_seqcache* c, const StepArgs& a, const rse_seq_rows* q, const rse_seq_rows* k,
-             const rse_seq_rows* v, const rse_seq_rows* out, hipStream_t s) {
-    T* kp = static_cast<T*>(c->k);
-    T* vp = static_cast<T*>(c->v);
-    hipLaunchKernelGGL(k_step_append<T>, dim3((unsigned)a.batch), dim3(CB), 0, s, a, rows_view<const T>(k),
-                       rows_view<const T>(v), kp, vp, c->n_kv_heads, c->dim);
-    hipLaunchKernelGGL((k_step<T, D>), dim3((unsigned)((a.batch * a.n_heads + CW - 1) / CW)), dim3(CB), 0, s, a,
-                       rows_view<const T>(q), kp, vp, rows_view<T>(out));
+int run_step(const rse_seqattn* at, const rse_seqcache* c, const StepArgs& a, const StepPlan& p, const StepWs& ws,
+             const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v, const rse_seq_rows* out, hipStream_t s) {
+    const size_t tiles = SW * 32 * D * sizeof(T), sums = (size_t)SW * p.cols * D * sizeof(float);
+    const size_t lds = (tiles > sums ? tiles : sums) + (size_t)(a.n_bounds + 1) * p.cols * sizeof(float);
+    const int64_t grid = a.batch * at->n_kv_heads * p.blocks * p.splits;
+    if (grid > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((k_step<T, D>), dim3((unsigned)grid), dim3(SW * WAVE), lds, s, a, rows_view<const T>(q),
+                       rows_view<const T>(k), rows_view<const T>(v), static_cast<T*>(c->k), static_cast<T*>(c->v),
+                       rows_view<T>(out), p.splits, p.cols, ws.o, ws.ml);
+    if (p.splits > 1) {
+        const int64_t rows = a.batch * a.n_heads;
+        hipLaunchKernelGGL((k_step_join<T, D>), dim3((unsigned)((rows + CW - 1) / CW)), dim3(CB), 0, s, ws.o, ws.ml,
+                           rows, a.n_heads, p.splits, rows_view<T>(out));
+    }
     return launch_status();
 }
 
@@ -359,7 +552,7 @@ int seq_cache_write(rse_seqcache* cache, const int64_t* d_slots, int64_t n_event
 
 int rse_seqattn_step_workspace_size(const rse_seqattn* attn, int64_t batch, int64_t max_len, size_t* bytes_out) {
     if (!attn || !bytes_out || batch < 0 || max_len < 0) return RSE_ERR_INVALID_ARG;
-    *bytes_out = 256;
+    *bytes_out = step_ws(attn, batch, step_plan(attn, batch, max_len), nullptr).bytes;
     return RSE_OK;
 }
 
@@ -372,12 +565,13 @@ int seq_attention_step(const rse_seqattn* attn, rse_seqcache* cache, const rse_s
     if (attn->dim != cache->dim || attn->dtype != cache->dtype || attn->n_kv_heads != cache->n_kv_heads)
         return RSE_ERR_INVALID_ARG;
     if (batch == 0) return RSE_OK;
-    if (!d_pos || !d_bias || !d_page_table || !d_lens || !d_ws) return RSE_ERR_INVALID_ARG;
+    if (!d_pos || !d_bias || !d_page_table || !d_lens || !d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256)
+        return RSE_ERR_INVALID_ARG;
     for (const rse_seq_rows* r : {q, k, v, out})
         if (!rows_ok(r, attn->dtype)) return RSE_ERR_INVALID_ARG;
-    size_t need = 0;
-    rse_seqattn_step_workspace_size(attn, batch, max_len, &need);
-    if (ws_bytes < need) return RSE_ERR_WORKSPACE;
+    const StepPlan plan = step_plan(attn, batch, max_len);
+    const StepWs ws = step_ws(attn, batch, plan, d_ws);
+    if (ws_bytes < ws.bytes) return RSE_ERR_WORKSPACE;
     StepArgs a;
     a.hdr = attn->hdr;
     a.status = cache->hdr;
@@ -396,12 +590,9 @@ int seq_attention_step(const rse_seqattn* attn, rse_seqcache* cache, const rse_s
     a.batch = batch;
     a.scale = attn->scale;
     hipStream_t s = as_stream(stream);
-    const bool f = attn->dtype == RSE_F32;
-    switch (attn->dim) {
-        case 32: return f ? run_step<float, 32>(cache, a, q, k, v, out, s) : run_step<uint16_t, 32>(cache, a, q, k, v, out, s);
-        case 64: return f ? run_step<float, 64>(cache, a, q, k, v, out, s) : run_step<uint16_t, 64>(cache, a, q, k, v, out, s);
-        default: return f ? run_step<float, 128>(cache, a, q, k, v, out, s) : run_step<uint16_t, 128>(cache, a, q, k, v, out, s);
-    }
+    return by_type(attn, [&](auto t, auto d) {
+        return run_step<decltype(t), decltype(d)::value>(attn, cache, a, plan, ws, q, k, v, out, s);
+    });
 }
 
 }  // extern "C"
