@@ -15,8 +15,18 @@ struct SeqHeader {
     int32_t n_bounds;
     int32_t pad[62];
     int32_t bounds[RSE_SEQ_MAX_BOUNDARIES + 1];   // unused entries: INT32_MAX
+    uint8_t cell[512];                            // by seq_cell: boundaries <= every distance of the cell
 };
-static_assert(sizeof(SeqHeader) == 256 + 512, "SeqHeader size");
+static_assert(sizeof(SeqHeader) == 256 + 512 + 512, "SeqHeader size");
+
+// Distances in cells of an eighth of a power of two (positive and negative
+// apart): sign, exponent and three more bits of the distance as a float.
+__host__ __device__ __forceinline__ int seq_cell(int32_t d) {
+    const float f = (float)d;
+    const uint32_t u = __builtin_bit_cast(uint32_t, f);
+    const int c = (int)((u >> 20) & 0x7FF) - 1015;      // 1 for a distance of 1, 249 for 2^31
+    return (c > 0 ? c : 0) | (int)((u >> 31) << 8);
+}
 
 struct SeqCacheHeader {
     int32_t status;
@@ -42,6 +52,7 @@ struct SeqArgs {
     SeqHeader* hdr;
     int32_t n_heads, group;      // query heads, query heads per key/value head
     int32_t n_bounds, causal;
+    int32_t cells;               // no cell holds two boundaries: seq_bucket_cell may be used
     float scale;
 };
 
@@ -56,6 +67,13 @@ __device__ __forceinline__ int seq_bucket(const int32_t* bounds, int n_bounds, i
     for (int step = 64; step > 0; step >>= 1)
         if (bounds[b + step - 1] <= d) b += step;
     return b < n_bounds ? b : n_bounds;
+}
+
+// The same by the distance's cell, where no cell holds two boundaries: all
+// boundaries <= the whole cell, and perhaps the next one.
+__device__ __forceinline__ int seq_bucket_cell(const uint8_t* cell, const int32_t* bounds, int n_bounds, int32_t d) {
+    const int b = cell[seq_cell(d)];
+    return b + (b < n_bounds && bounds[b] <= d);
 }
 
 // Wave-level ordering of a wave's own LDS writes before its other lanes read them.
@@ -99,7 +117,7 @@ __device__ __forceinline__ int64_t wave_last_le(int64_t n, F f, int64_t x) {
 }  // namespace rse
 
 struct rse_seqattn {
-    int32_t n_heads, n_kv_heads, dim, dtype, causal, n_bounds;
+    int32_t n_heads, n_kv_heads, dim, dtype, causal, n_bounds, cells;
     float scale;
     rse::SeqHeader* hdr;
 };
@@ -148,6 +166,7 @@ inline rse::SeqArgs seq_args(const rse_seqattn* a, const rse_seq_batch* b) {
     s.group = a->n_heads / a->n_kv_heads;
     s.n_bounds = a->n_bounds;
     s.causal = a->causal;
+    s.cells = a->cells;
     s.scale = a->scale;
     return s;
 }

@@ -14,6 +14,7 @@ namespace {
 struct InitArgs {
     int32_t n_bounds;
     int32_t bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
+    uint8_t cell[512];
 };
 
 __global__ void k_attn_init(SeqHeader* h, InitArgs a) {
@@ -22,6 +23,38 @@ __global__ void k_attn_init(SeqHeader* h, InitArgs a) {
         h->n_bounds = a.n_bounds;
     }
     if (threadIdx.x <= RSE_SEQ_MAX_BOUNDARIES) h->bounds[threadIdx.x] = a.bounds[threadIdx.x];
+    for (int t = threadIdx.x; t < 512; t += blockDim.x) h->cell[t] = a.cell[t];
+}
+
+// Fills a.cell; true if no cell holds two boundaries past its first distance.
+// A cell's distances are consecutive (the conversion to float is monotonic):
+// its first is found by bisection.
+bool fill_cells(InitArgs& a) {
+    bool single = true;
+    for (int sign = 0; sign < 2; ++sign)
+        for (int c = 0; c < 256; ++c) {
+            // smallest magnitude of code c or more, and of c + 1 or more
+            int64_t at[2];
+            for (int u = 0; u < 2; ++u) {
+                int64_t lo = 0, hi = (1ll << 31) + 1;
+                while (lo < hi) {
+                    const int64_t mid = (lo + hi) / 2;
+                    const int64_t d = sign ? -mid : (mid < INT32_MAX ? mid : INT32_MAX);
+                    if (mid > (1ll << 31) || (seq_cell((int32_t)d) & 255) >= c + u) hi = mid;
+                    else lo = mid + 1;
+                }
+                at[u] = lo;
+            }
+            const int64_t first = sign ? -(at[1] - 1) : at[0], last = sign ? -at[0] : at[1] - 1;
+            int base = 0, inside = 0;
+            for (int m = 0; m < a.n_bounds; ++m) {
+                base += a.bounds[m] <= first;
+                inside += a.bounds[m] > first && a.bounds[m] <= last;
+            }
+            a.cell[sign * 256 + c] = (uint8_t)base;
+            if (inside > 1 && first <= last) single = false;
+        }
+    return single;
 }
 
 __global__ void k_attn_clear(SeqHeader* h) { h->status = 0; }
@@ -48,6 +81,7 @@ __global__ __launch_bounds__(W * 64) void k_attn_fwd(SeqArgs a, Rows<const T> q,
     __shared__ int32_t s_range[2][3];           // lowest and highest position, any key hidden
     __shared__ int32_t s_bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
     __shared__ float s_bias[RSE_SEQ_MAX_BOUNDARIES + 1];
+    __shared__ uint32_t s_cell[128];
     const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5;
     const int head = blockIdx.y, g = head / a.group, nb = a.n_bounds + 1;
     int64_t s;
@@ -63,6 +97,7 @@ __global__ __launch_bounds__(W * 64) void k_attn_fwd(SeqArgs a, Rows<const T> q,
     wb.load(a.hdr, a.bias + head * nb, a.n_bounds, LOG2E);
     for (int t = threadIdx.x; t <= RSE_SEQ_MAX_BOUNDARIES; t += NT) {
         s_bounds[t] = a.hdr->bounds[t];
+        s_cell[t] = reinterpret_cast<const uint32_t*>(a.hdr->cell)[t];
         s_bias[t] = t < nb ? a.bias[head * nb + t] * LOG2E : 0.f;
     }
     ColFrag<T, D> qf;
@@ -139,7 +174,8 @@ __global__ __launch_bounds__(W * 64) void k_attn_fwd(SeqArgs a, Rows<const T> q,
                 c = 1.f;
 #pragma unroll
                 for (int u = 0; u < NS; ++u) {
-                    x[u] = add_bias<true>(x[u], c2, wb, lo, hi, s_pos[b] + 32 * u, my_pos, s_bounds, s_bias);
+                    x[u] = add_bias<true>(x[u], c2, wb, lo, hi, s_pos[b] + 32 * u, my_pos, a.cells, s_cell,
+                                          s_bounds, s_bias);
                     if (hidden) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -245,8 +281,7 @@ int run_fwd_w(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, co
 template <typename T, int D>
 int run_fwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v,
             const rse_seq_rows* out, const Saved& sv, hipStream_t s) {
-    if (a.max_len <= 32) return run_fwd_w<T, D, 1>(a, q, k, v, out, sv, s);
-    if (a.max_len <= 64) return run_fwd_w<T, D, 2>(a, q, k, v, out, sv, s);
+    if (a.max_len <= 128) return run_fwd_w<T, D, 1>(a, q, k, v, out, sv, s);
     return run_fwd_w<T, D, 4>(a, q, k, v, out, sv, s);
 }
 
@@ -280,6 +315,7 @@ int rse_seqattn_create(rse_seqattn** out, void* d_mem, size_t mem_bytes, int32_t
     }
     rse_seqattn* h = new (std::nothrow) rse_seqattn();
     if (!h) return RSE_ERR_INVALID_ARG;
+    h->cells = fill_cells(a);
     h->n_heads = n_heads;
     h->n_kv_heads = n_kv_heads;
     h->dim = dim;

@@ -70,6 +70,7 @@ __global__ __launch_bounds__(W * 64) void k_attn_dq(SeqArgs a, int64_t slots, Ro
     __shared__ int32_t s_range[2][3];
     __shared__ int32_t s_bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
     __shared__ float s_bias[RSE_SEQ_MAX_BOUNDARIES + 1];
+    __shared__ uint32_t s_cell[128];
     extern __shared__ float s_hist[];           // [W][n_bounds + 1][HC]
     const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5;
     const int head = blockIdx.y, g = head / a.group, nb = a.n_bounds + 1;
@@ -79,6 +80,7 @@ __global__ __launch_bounds__(W * 64) void k_attn_dq(SeqArgs a, int64_t slots, Ro
     wb.load(a.hdr, a.bias + head * nb, a.n_bounds, LOG2E);
     for (int t = threadIdx.x; t <= RSE_SEQ_MAX_BOUNDARIES; t += NT) {
         s_bounds[t] = a.hdr->bounds[t];
+        s_cell[t] = reinterpret_cast<const uint32_t*>(a.hdr->cell)[t];
         s_bias[t] = t < nb ? a.bias[head * nb + t] * LOG2E : 0.f;
     }
     for (int t = threadIdx.x; t < W * nb * HC; t += NT) s_hist[t] = 0.f;
@@ -162,6 +164,7 @@ __global__ __launch_bounds__(W * 64) void k_attn_dq(SeqArgs a, int64_t slots, Ro
                 float sum = 0.f;
 #pragma unroll
                 for (int u = 0; u < NS; ++u) {
+                    if (k0 + 32 * u >= my_end) continue;
                     f32x16 x = mma_rows<T, D>(s_k[b], 32 * u, qf, f32x16{});
                     const f32x16 dp = mma_rows<T, D>(s_v[b], 32 * u, df, f32x16{});
                     int idx[16];
@@ -170,7 +173,7 @@ __global__ __launch_bounds__(W * 64) void k_attn_dq(SeqArgs a, int64_t slots, Ro
 #pragma unroll
                         for (int r = 0; r < 16; ++r) x[r] = __builtin_fmaf(x[r], c2, b0);
                     } else {
-                        bucket_index<true>(idx, wb, lo, hi, s_pos[b] + 32 * u, my_pos, s_bounds);
+                        bucket_index<true>(idx, wb, lo, hi, s_pos[b] + 32 * u, my_pos, a.cells, s_cell, s_bounds);
 #pragma unroll
                         for (int r = 0; r < 16; ++r) x[r] = __builtin_fmaf(x[r], c2, s_bias[idx[r]]);
                     }
@@ -262,6 +265,7 @@ __global__ __launch_bounds__(W * 64) void k_attn_dkv(SeqArgs a, Rows<const T> q,
     __shared__ int32_t s_range[2][2];
     __shared__ int32_t s_bounds[NBP];
     __shared__ float s_bias[2][NBP];
+    __shared__ uint32_t s_cell[128];
     const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5;
     const int g = blockIdx.y, nb = a.n_bounds + 1;
     int64_t s;
@@ -272,7 +276,10 @@ __global__ __launch_bounds__(W * 64) void k_attn_dkv(SeqArgs a, Rows<const T> q,
     const int first = a.causal ? j0 / KT * KT : 0;                  // queries of the block: first .. len
     const int per_head = (len - first + KT - 1) / KT, total = per_head * a.group;
 
-    for (int t = threadIdx.x; t < NBP; t += NT) s_bounds[t] = a.hdr->bounds[t];
+    for (int t = threadIdx.x; t < NBP; t += NT) {
+        s_bounds[t] = a.hdr->bounds[t];
+        s_cell[t] = reinterpret_cast<const uint32_t*>(a.hdr->cell)[t];
+    }
     ColFrag<T, D> kf, vf;
     kf.load(k.at(s + row, g), half);
     vf.load(v.at(s + row, g), half);
@@ -339,6 +346,7 @@ __global__ __launch_bounds__(W * 64) void k_attn_dkv(SeqArgs a, Rows<const T> q,
             const bool diagonal = a.causal && i0 < j0 + 32 * w + 31;
 #pragma unroll
             for (int u = 0; u < NS; ++u) {
+                if (i0 + 32 * u >= len || (a.causal && i0 + 32 * u + 31 < j0 + 32 * w)) continue;
                 f32x16 x = mma_rows<T, D>(s_q[b], 32 * u, kf, f32x16{});
                 f32x16 dp = mma_rows<T, D>(s_d[b], 32 * u, vf, f32x16{});
                 if (lo == hi) {
@@ -346,7 +354,7 @@ __global__ __launch_bounds__(W * 64) void k_attn_dkv(SeqArgs a, Rows<const T> q,
 #pragma unroll
                     for (int r = 0; r < 16; ++r) x[r] = __builtin_fmaf(x[r], c2, b0);
                 } else {
-                    x = add_bias<false>(x, c2, wb, lo, hi, s_pos[b] + 32 * u, my_pos, s_bounds, s_bias[b]);
+                    x = add_bias<false>(x, c2, wb, lo, hi, s_pos[b] + 32 * u, my_pos, a.cells, s_cell, s_bounds, s_bias[b]);
                 }
                 if (diagonal) {
                     const int lim = my_k - i0 - 32 * u - 4 * half;
@@ -402,7 +410,7 @@ struct BwdWs {
     int64_t blocks;              // of k_attn_dq, per head
 };
 
-int waves_for(int64_t max_len) { return max_len <= 32 ? 1 : (max_len <= 64 ? 2 : 4); }
+int waves_for(int64_t max_len) { return max_len <= 128 ? 1 : 4; }
 
 BwdWs bwd_ws(const rse_seqattn* a, int64_t n, int64_t batch, int64_t max_len, void* base) {
     BwdWs w;
@@ -472,7 +480,6 @@ int seq_attention_bwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
         constexpr int D = decltype(d)::value;
         switch (waves_for(a.max_len)) {
             case 1: return run_bwd_w<T, D, 1>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
-            case 2: return run_bwd_w<T, D, 2>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
             default: return run_bwd_w<T, D, 4>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
         }
     });

@@ -249,7 +249,8 @@ constexpr int CHAIN = 6;
 // lo .. hi: compared with the boundaries between them, or searched.
 template <bool column_first>
 __device__ __forceinline__ void bucket_index(int (&idx)[16], const WaveBuckets& wb, int lo, int hi, const int32_t* row_pos,
-                                             int32_t col_pos, const int32_t* s_bounds) {
+                                             int32_t col_pos, bool cells, const uint32_t* s_cell,
+                                             const int32_t* s_bounds) {
     const int h = lane_id() >> 5;
     int32_t dist[16];
 #pragma unroll
@@ -266,6 +267,10 @@ __device__ __forceinline__ void bucket_index(int (&idx)[16], const WaveBuckets& 
 #pragma unroll
             for (int r = 0; r < 16; ++r) idx[r] += dist[r] >= edge;
         }
+    } else if (cells) {
+        const uint8_t* cell = reinterpret_cast<const uint8_t*>(s_cell);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) idx[r] = seq_bucket_cell(cell, s_bounds, wb.n, dist[r]);
     } else {
 #pragma unroll
         for (int r = 0; r < 16; ++r) idx[r] = seq_bucket(s_bounds, wb.n, dist[r]);
@@ -280,7 +285,8 @@ __device__ __forceinline__ void bucket_index(int (&idx)[16], const WaveBuckets& 
 // `column_first`: the column event is the query (distance = column - row).
 template <bool column_first>
 __device__ __forceinline__ f32x16 add_bias(f32x16 s, float c, const WaveBuckets& wb, int lo, int hi, const int32_t* row_pos,
-                                           int32_t col_pos, const int32_t* s_bounds, const float* s_bias) {
+                                           int32_t col_pos, bool cells, const uint32_t* s_cell,
+                                           const int32_t* s_bounds, const float* s_bias) {
     const int h = lane_id() >> 5;
     int32_t dist[16];
 #pragma unroll
@@ -300,6 +306,10 @@ __device__ __forceinline__ f32x16 add_bias(f32x16 s, float c, const WaveBuckets&
 #pragma unroll
             for (int r = 0; r < 16; ++r) b[r] = dist[r] >= edge ? bm : b[r];
         }
+    } else if (cells) {
+        const uint8_t* cell = reinterpret_cast<const uint8_t*>(s_cell);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) b[r] = s_bias[seq_bucket_cell(cell, s_bounds, wb.n, dist[r])];
     } else {
 #pragma unroll
         for (int r = 0; r < 16; ++r) b[r] = s_bias[seq_bucket(s_bounds, wb.n, dist[r])];
