@@ -61,38 +61,50 @@ __global__ void k_attn_clear(SeqHeader* h) { h->status = 0; }
 
 // Forward.  A block of W waves takes 32 W queries of one sequence and head; a
 // wave has 32 of them as columns.  Keys go by in tiles of KT, staged in LDS
-// row-major (the next tile's loads are in flight meanwhile): S^T = K Q^T,
-// online softmax down the registers of a lane (a row's maximum needs one
-// exchange between the wave's halves, its sum none until the end), and
-// O^T += V^T P^T with the same registers as operand.
+// row-major (the next tile's loads are in flight meanwhile), 32 at a time:
+// S^T = K Q^T, online softmax down the registers of a lane (a row's maximum
+// needs one exchange between the wave's halves, its sum none until the end),
+// and O^T += V^T P^T with the same registers as operand.
+//
+// The logits are formed relative to a reference m of the row, in base 2:
+// y = s c + (bias - m), p = exp2(y).  m follows the row's maximum only when
+// that has grown by more than 8 (p up to 2^8, exact in a float), so most
+// tiles need neither a second pass over y nor a rescaling of the sums.
+//
 // SAVE: also leaves the log-sums and outputs for the backward, whose
 // dO . out has to equal sum_j p dp to fp32 accuracy (the bias gradient sums
 // differences from it): what bf16 rounds off the probabilities goes through
 // a second product into those outputs.
+// Registers are held to what lets FWD_WAVES waves share a SIMD.
+template <typename T, int D, bool SAVE>
+constexpr int FWD_WAVES = Shape<T, D>::RB == 64 ? 4 : (Shape<T, D>::RB == 128 ? 3 : 2);
+
 template <typename T, int D, int W, int KT, bool SAVE>
-__global__ __launch_bounds__(W * 64) void k_attn_fwd(SeqArgs a, Rows<const T> q, Rows<const T> k, Rows<const T> v,
-                                                     Rows<T> out, float* lse2, float* out32) {
-    using TL = Tile<T, D>;
-    constexpr int NT = W * 64, CH = TL::CH, PER = KT * CH / NT, NS = KT / 32, ND = D / 32;
-    static_assert(KT * CH % NT == 0 && KT <= 64, "tile shape");
+__global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(FWD_WAVES<T, D, SAVE>))) void k_attn_fwd(SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k,
+                                                     Rows<const T> v, Rows<T> out, float* lse2, float* out32) {
+    constexpr int NT = W * 64, CH = Tile<T, D>::CH, NS = KT / 32, ND = D / 32;
+    constexpr bool REST = SAVE && sizeof(T) == 2;
     __shared__ u32x4 s_k[2][KT * CH], s_v[2][KT * CH];
-    __shared__ float s_mask[2][KT];
-    __shared__ int32_t s_pos[2][KT];
-    __shared__ int32_t s_range[2][3];           // lowest and highest position, any key hidden
+    __shared__ KeySide<KT> s_side;
     __shared__ int32_t s_bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
     __shared__ float s_bias[RSE_SEQ_MAX_BOUNDARIES + 1];
     __shared__ uint32_t s_cell[128];
     const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5;
-    const int head = blockIdx.y, g = head / a.group, nb = a.n_bounds + 1;
+    const int head = blockIdx.x % a.n_heads, g = head / a.group, nb = a.n_bounds + 1;
     int64_t s;
     int len, tile;
-    if (!find_tile(a, blockIdx.x, 32 * W, s, len, tile, head == 0)) return;
-    const int n_tiles = (len + 32 * W - 1) / (32 * W);
-    if (a.causal) tile = n_tiles - 1 - tile;    // the longest first
-    const int q0 = tile * 32 * W, my_q = q0 + 32 * w + (lane & 31), row = my_q < len ? my_q : len - 1;
-    const int end = a.causal ? (q0 + 32 * W < len ? q0 + 32 * W : len) : len;      // keys of the block
-    const int my_end = a.causal && q0 + 32 * w + 32 < end ? q0 + 32 * w + 32 : end;  // and of the wave
+    if (!find_tile(a, grid, blockIdx.x / a.n_heads, 32 * W, a.causal, s, len, tile, head == 0)) return;
+    const int q0 = tile * 32 * W, w0 = q0 + 32 * w, my_q = w0 + (lane & 31), row = my_q < len ? my_q : len - 1;
+    const int end = a.causal ? (q0 + 32 * W < len ? q0 + 32 * W : len) : len;       // keys of the block
+    const int my_end = w0 >= len ? 0 : (a.causal && w0 + 32 < end ? w0 + 32 : end);  // and of the wave
 
+    RowStage<T, D, NT, KT> st;
+    KeySideStage side;
+    st.load(k, g, v, g, s, 0, end, a.key_off);
+    side.load(a, s, 0, end, KT);
+    ColFrag<T, D> qf;
+    qf.load(q.at(s + row, head), half);
+    const int32_t my_pos = a.pos[s + row];
     WaveBuckets wb;
     wb.load(a.hdr, a.bias + head * nb, a.n_bounds, LOG2E);
     for (int t = threadIdx.x; t <= RSE_SEQ_MAX_BOUNDARIES; t += NT) {
@@ -100,144 +112,82 @@ __global__ __launch_bounds__(W * 64) void k_attn_fwd(SeqArgs a, Rows<const T> q,
         s_cell[t] = reinterpret_cast<const uint32_t*>(a.hdr->cell)[t];
         s_bias[t] = t < nb ? a.bias[head * nb + t] * LOG2E : 0.f;
     }
-    ColFrag<T, D> qf;
-    qf.load(q.at(s + row, head), half);
+    const LdsBuckets lb = {s_bounds, s_cell, a.cells != 0, a.n_bounds};
     if (a.scale < 0.f) qf.negate();
     const float c2 = fabsf(a.scale) * LOG2E;
-    const int32_t my_pos = a.pos[s + row];
-    const int32_t q_lo = wave_min(my_pos), q_hi = wave_max(my_pos);
+    const int32_t q_lo = half_min(my_pos), q_hi = half_max(my_pos);
 
-    // staging: thread t holds chunk t % CH of rows t / CH, + NT / CH, ...
-    const int srow = threadIdx.x / CH, sch = threadIdx.x % CH;
-    u32x4 rk[PER], rv[PER];
-    int32_t rp = 0;
-    bool rs = false;
-    bool hid[PER];
-    auto load_tile = [&](int k0) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int kk = k0 + srow + i * (NT / CH);
-            const int64_t j = s + (kk < end ? kk : end - 1);
-            rk[i] = gload_u4(k.at(j, g) + sch * TL::EPC);
-            rv[i] = gload_u4(v.at(j, g) + sch * TL::EPC);
-            hid[i] = kk >= end || (a.key_off && a.key_off[j] < 0);
-        }
-        if (threadIdx.x < KT) {
-            const int kk = k0 + (int)threadIdx.x;
-            const int64_t j = s + (kk < end ? kk : end - 1);
-            rp = a.pos[j];
-            rs = kk < end && !(a.key_off && a.key_off[j] < 0);
-        }
-    };
-    auto store_tile = [&](int b) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int at = TL::chunk_at(srow + i * (NT / CH), sch);
-            s_k[b][at] = hid[i] ? u32x4{0, 0, 0, 0} : rk[i];
-            s_v[b][at] = hid[i] ? u32x4{0, 0, 0, 0} : rv[i];
-        }
-        if (w == 0) {
-            const bool mine = lane < KT;
-            const int32_t lo = wave_min(mine ? rp : INT32_MAX), hi = wave_max(mine ? rp : INT32_MIN);
-            const bool any = __ballot(mine && !rs) != 0;
-            if (mine) {
-                s_mask[b][lane] = rs ? 0.f : -INFINITY;
-                s_pos[b][lane] = rp;
-            }
-            if (lane == 0) {
-                s_range[b][0] = lo;
-                s_range[b][1] = hi;
-                s_range[b][2] = any;
-            }
-        }
-    };
-
-    constexpr bool REST = SAVE && sizeof(T) == 2;
     f32x16 o[ND] = {}, rest[REST ? ND : 1] = {};
-    float m = -INFINITY, l = 0.f;
-    load_tile(0);
-    store_tile(0);
+    float m = 0.f, l = 0.f;
+    bool set = false;                           // m has been taken from a visible key
+    st.store(s_k[0], s_v[0]);
+    side.store(s_side, 0);
     __syncthreads();
     for (int k0 = 0, b = 0; k0 < end; k0 += KT, b ^= 1) {
-        if (k0 + KT < end) load_tile(k0 + KT);
-        if (k0 < my_end) {
-            f32x16 x[NS];
+        if (k0 + KT < end) {
+            st.load(k, g, v, g, s, k0 + KT, end, a.key_off);
+            side.load(a, s, k0 + KT, end, KT);
+        }
 #pragma unroll
-            for (int u = 0; u < NS; ++u) x[u] = mma_rows<T, D>(s_k[b], 32 * u, qf, f32x16{});
-            const int lo = wb.bucket(seq_dist(q_lo, s_range[b][1])), hi = wb.bucket(seq_dist(q_hi, s_range[b][0]));
-            const bool hidden = __builtin_amdgcn_readfirstlane(s_range[b][2]);
-            const bool diagonal = a.causal && k0 + KT - 1 > q0 + 32 * w;
-            float c = c2, bias = 0.f;           // p = exp2(x c + bias - m)
-            if (lo == hi && !hidden && !diagonal) {
-                bias = wb.value(lo);
-            } else {
-                c = 1.f;
+        for (int u = 0; u < NS; ++u) {
+            const int k1 = k0 + 32 * u;
+            if (k1 >= my_end) continue;
+            f32x16 x = mma_rows<T, D>(s_k[b], 32 * u, qf, f32x16{});
+            TileBuckets<true> tb;
+            tb.set(wb, q_lo, q_hi, s_side.range[b][u]);
+            x = tb.logits(x, c2, -m, wb, lb, s_bias, s_side.pos[b] + 32 * u, my_pos);
+            if (__builtin_amdgcn_readfirstlane((uint32_t)(s_side.hidden[b] >> (32 * u)))) {
 #pragma unroll
-                for (int u = 0; u < NS; ++u) {
-                    x[u] = add_bias<true>(x[u], c2, wb, lo, hi, s_pos[b] + 32 * u, my_pos, a.cells, s_cell,
-                                          s_bounds, s_bias);
-                    if (hidden) {
+                for (int j = 0; j < 4; ++j) {
+                    const f32x4 mk = *reinterpret_cast<const f32x4*>(&s_side.mask[b][32 * u + 8 * j + 4 * half]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const f32x4 mk = *reinterpret_cast<const f32x4*>(&s_mask[b][32 * u + 8 * j + 4 * half]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) x[u][4 * j + i] += mk[i];
-                        }
-                    }
-                    if (diagonal) {
-                        const int lim = my_q - k0 - 32 * u - 4 * half;
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) x[u][r] = tile_row(r, 0) <= lim ? x[u][r] : -INFINITY;
-                    }
+                    for (int i = 0; i < 4; ++i) x[4 * j + i] += mk[i];
                 }
             }
-            float top = x[0][0];
+            if (a.causal && k1 + 31 > w0) {
+                const int lim = my_q - k1 - 4 * half;
 #pragma unroll
-            for (int u = 0; u < NS; ++u)
+                for (int r = 0; r < 16; ++r) x[r] = tile_row(r, 0) <= lim ? x[r] : -INFINITY;
+            }
+            float top = x[0];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, x[u][r]);
+            for (int r = 1; r < 16; ++r) top = fmaxf(top, x[r]);
             top = fmaxf(top, other_half(top));
-            top = __builtin_fmaf(top, c, bias);
-            // the reference of the exponents follows the maximum only when it
-            // has grown by more than 8 (p up to 2^8, exact in a float), so
-            // that most tiles leave the sums as they are
-            if (__any(top > m + 8.f || (m == -INFINITY && top > -INFINITY))) {
-                const float ref = fmaxf(m, top);
-                const float r = ref == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - ref);
-                m = ref;
-                l *= r;
+            const bool move = top > 8.f || (!set && top > -INFINITY);
+            set |= top > -INFINITY;
+            if (__any(move)) {
+                const float by = move ? top : 0.f, r = __builtin_amdgcn_exp2f(-by);
+                m += by;
+                // nothing summed yet: 0, also where exp2 overflows
+                l = l > 0.f ? l * r : 0.f;
 #pragma unroll
-                for (int dt = 0; dt < ND; ++dt) o[dt] *= r;
-                if (REST)
+                for (int i = 0; i < 16; ++i) x[i] -= by;
+                const float ro = r < INFINITY ? r : 0.f;
 #pragma unroll
-                    for (int dt = 0; dt < ND; ++dt) rest[dt] *= r;
-            }
-            const float shift = m == -INFINITY ? 0.f : bias - m;
-            RowOperand<T> p[NS];
-#pragma unroll
-            for (int u = 0; u < NS; ++u) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    x[u][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][r], c, shift));
-                    l += x[u][r];
+                for (int dt = 0; dt < ND; ++dt) {
+                    o[dt] *= ro;
+                    if (REST) rest[dt] *= ro;
                 }
-                p[u].set(x[u]);
             }
 #pragma unroll
-            for (int u = 0; u < NS; ++u)
+            for (int r = 0; r < 16; ++r) {
+                x[r] = __builtin_amdgcn_exp2f(x[r]);
+                l += x[r];
+            }
+            RowOperand<T> p;
+            p.set(x);
 #pragma unroll
-                for (int dt = 0; dt < ND; ++dt) o[dt] = mma_over_rows<D>(s_v[b], 32 * u, dt, p[u], o[dt]);
-            if (REST)
+            for (int dt = 0; dt < ND; ++dt) o[dt] = mma_over_rows<D>(s_v[b], 32 * u, dt, p, o[dt]);
+            if (REST) {
+                RowOperand<T> lo;
+                lo.set_rest(x, p);
 #pragma unroll
-                for (int u = 0; u < NS; ++u) {
-                    RowOperand<T> lo;
-                    lo.set_rest(x[u], p[u]);
-#pragma unroll
-                    for (int dt = 0; dt < ND; ++dt) rest[dt] = mma_over_rows<D>(s_v[b], 32 * u, dt, lo, rest[dt]);
-                }
+                for (int dt = 0; dt < ND; ++dt) rest[dt] = mma_over_rows<D>(s_v[b], 32 * u, dt, lo, rest[dt]);
+            }
         }
         if (k0 + KT < end) {
-            store_tile(b ^ 1);
+            st.store(s_k[b ^ 1], s_v[b ^ 1]);
+            side.store(s_side, b ^ 1);
             __syncthreads();
         }
     }
@@ -259,30 +209,19 @@ __global__ __launch_bounds__(W * 64) void k_attn_fwd(SeqArgs a, Rows<const T> q,
 }
 
 // ------------------------------------------------------------------ host --
-template <typename T, int D, int W>
-int run_fwd_w(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v,
-              const rse_seq_rows* out, const Saved& sv, hipStream_t s) {
-    // keys of a tile: 64 where two buffers of them take at most 64 KiB and
-    // there are several waves to stage them
-    constexpr int KT = W > 1 && D * sizeof(T) <= 256 ? 64 : 32;
-    const int64_t slots = tile_slots(a.n_events, a.batch, 32 * W);
-    if (slots > INT32_MAX) return RSE_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)slots, a.n_heads), block(W * WAVE);
-    if (sv.lse2)
-        hipLaunchKernelGGL((k_attn_fwd<T, D, W, KT, true>), grid, block, 0, s, a, rows_view<const T>(q),
-                           rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), sv.lse2, sv.out32);
-    else
-        hipLaunchKernelGGL((k_attn_fwd<T, D, W, KT, false>), grid, block, 0, s, a, rows_view<const T>(q),
-                           rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), nullptr, nullptr);
-    return launch_status();
-}
-
-// Waves of a block: as many groups of 32 queries as a sequence can have, up to 4.
-template <typename T, int D>
+template <typename T, int D, int W, int KT>
 int run_fwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v,
             const rse_seq_rows* out, const Saved& sv, hipStream_t s) {
-    if (a.max_len <= 128) return run_fwd_w<T, D, 1>(a, q, k, v, out, sv, s);
-    return run_fwd_w<T, D, 4>(a, q, k, v, out, sv, s);
+    const TileGrid tg = tile_grid(a.n_events, a.batch, a.max_len, 32 * W);
+    if (tg.items * a.n_heads > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)(tg.items * a.n_heads)), block(W * WAVE);
+    if (sv.lse2)
+        hipLaunchKernelGGL((k_attn_fwd<T, D, W, KT, true>), grid, block, 0, s, a, tg, rows_view<const T>(q),
+                           rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), sv.lse2, sv.out32);
+    else
+        hipLaunchKernelGGL((k_attn_fwd<T, D, W, KT, false>), grid, block, 0, s, a, tg, rows_view<const T>(q),
+                           rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), nullptr, nullptr);
+    return launch_status();
 }
 
 }  // namespace
@@ -375,7 +314,11 @@ int seq_attention_fwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
     if (!d_saved) sv.lse2 = sv.out32 = nullptr;
     const SeqArgs a = seq_args(attn, batch);
     return by_type(attn, [&](auto t, auto d) {
-        return run_fwd<decltype(t), decltype(d)::value>(a, q, k, v, out, sv, as_stream(stream));
+        using T = decltype(t);
+        constexpr int D = decltype(d)::value;
+        using S = Shape<T, D>;
+        if (a.max_len <= SHORT) return run_fwd<T, D, S::W_SHORT, S::KT_SHORT>(a, q, k, v, out, sv, as_stream(stream));
+        return run_fwd<T, D, S::W_LONG, S::KT_LONG>(a, q, k, v, out, sv, as_stream(stream));
     });
 }
 

@@ -10,40 +10,6 @@ using namespace rse_host;
 
 namespace {
 
-// Rows k0 .. k0 + KT - 1 of two tensors on their way to LDS: loaded into
-// registers (thread t: chunk t % CH of rows t / CH, + NT / CH, ...), stored
-// after the current tile's work.  Hidden rows and rows past the end are
-// stored as zeros, whatever they hold.
-template <typename T, int D, int NT, int KT>
-struct RowStage {
-    using TL = Tile<T, D>;
-    static constexpr int CH = TL::CH, PER = KT * CH / NT, STEP = NT / CH;
-    static_assert(KT * CH % NT == 0, "tile shape");
-    u32x4 x[PER], y[PER];
-    bool hid[PER];
-    __device__ __forceinline__ void load(const Rows<const T>& X, int hx, const Rows<const T>& Y, int hy, int64_t s, int k0,
-                                         int end, const int64_t* key_off) {
-        const int row = threadIdx.x / CH, c = threadIdx.x % CH;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int kk = k0 + row + i * STEP;
-            const int64_t j = s + (kk < end ? kk : end - 1);
-            x[i] = gload_u4(X.at(j, hx) + c * TL::EPC);
-            y[i] = gload_u4(Y.at(j, hy) + c * TL::EPC);
-            hid[i] = kk >= end || (key_off && key_off[j] < 0);
-        }
-    }
-    __device__ __forceinline__ void store(u32x4* sx, u32x4* sy) const {
-        const int row = threadIdx.x / CH, c = threadIdx.x % CH;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int at = TL::chunk_at(row + i * STEP, c);
-            sx[at] = hid[i] ? u32x4{0, 0, 0, 0} : x[i];
-            sy[at] = hid[i] ? u32x4{0, 0, 0, 0} : y[i];
-        }
-    }
-};
-
 // Columns of a wave's bucket sums: the two halves of the wave add in turn to
 // the same 32, so each entry is added to in program order.
 constexpr int HC = 32;
@@ -58,16 +24,20 @@ __device__ __forceinline__ void lds_add(float* p, float x) {
 // one bucket is summed in registers, else scattered into the wave's LDS
 // columns of bucket sums.  A block stays with its head and takes tiles of
 // queries blockIdx.x, + gridDim.x, ...; its sums go to part.
+// Registers are held to what lets DQ_WAVES (DKV_WAVES) waves share a SIMD.
+template <typename T, int D>
+constexpr int DQ_WAVES = Shape<T, D>::RB <= 64 ? 3 : (Shape<T, D>::RB <= 256 ? 2 : 1);
+template <typename T, int D>
+constexpr int DKV_WAVES = Shape<T, D>::RB <= 64 ? 3 : (Shape<T, D>::RB <= 128 || sizeof(T) == 4 && D == 64 ? 2 : 1);
+
 template <typename T, int D, int W, int KT>
-__global__ __launch_bounds__(W * 64) void k_attn_dq(SeqArgs a, int64_t slots, Rows<const T> q, Rows<const T> k,
+__global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(DQ_WAVES<T, D>))) void k_attn_dq(SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k,
                                                     Rows<const T> v, const float* lse2, const float* out32,
                                                     Rows<const T> dout, Rows<T> dq, float* delta, float* part) {
     using TL = Tile<T, D>;
     constexpr int NT = W * 64, CH = TL::CH, NS = KT / 32, ND = D / 32;
     __shared__ u32x4 s_k[2][KT * CH], s_v[2][KT * CH];
-    __shared__ float s_mask[2][KT];
-    __shared__ int32_t s_pos[2][KT];
-    __shared__ int32_t s_range[2][3];
+    __shared__ KeySide<KT> s_side;
     __shared__ int32_t s_bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
     __shared__ float s_bias[RSE_SEQ_MAX_BOUNDARIES + 1];
     __shared__ uint32_t s_cell[128];
@@ -86,13 +56,18 @@ __global__ __launch_bounds__(W * 64) void k_attn_dq(SeqArgs a, int64_t slots, Ro
     for (int t = threadIdx.x; t < W * nb * HC; t += NT) s_hist[t] = 0.f;
     const float c2 = fabsf(a.scale) * LOG2E;
 
-    for (int64_t slot = blockIdx.x; slot < slots; slot += gridDim.x) {
+    const LdsBuckets lb = {s_bounds, s_cell, a.cells != 0, a.n_bounds};
+    for (int64_t item = blockIdx.x; item < grid.items; item += gridDim.x) {
         int64_t s;
         int len, tile;
-        if (!find_tile(a, slot, 32 * W, s, len, tile, head == 0)) continue;
-        const int q0 = tile * 32 * W, my_q = q0 + 32 * w + (lane & 31), row = my_q < len ? my_q : len - 1;
+        if (!find_tile(a, grid, item, 32 * W, a.causal, s, len, tile, head == 0)) continue;
+        const int q0 = tile * 32 * W, w0 = q0 + 32 * w, my_q = w0 + (lane & 31), row = my_q < len ? my_q : len - 1;
         const int end = a.causal ? (q0 + 32 * W < len ? q0 + 32 * W : len) : len;
-        const int my_end = a.causal && q0 + 32 * w + 32 < end ? q0 + 32 * w + 32 : end;
+        const int my_end = w0 >= len ? 0 : (a.causal && w0 + 32 < end ? w0 + 32 : end);
+        RowStage<T, D, NT, KT> st;
+        KeySideStage side;
+        st.load(k, g, v, g, s, 0, end, a.key_off);
+        side.load(a, s, 0, end, KT);
         ColFrag<T, D> qf, df;
         qf.load(q.at(s + row, head), half);
         df.load(dout.at(s + row, head), half);
@@ -115,108 +90,71 @@ __global__ __launch_bounds__(W * 64) void k_attn_dq(SeqArgs a, int64_t slots, Ro
         if (my_q < len && half == 0) delta[(int64_t)head * a.n_events + s + my_q] = del;
         if (a.scale < 0.f) qf.negate();
         const int32_t my_pos = a.pos[s + row];
-        const int32_t q_lo = wave_min(my_pos), q_hi = wave_max(my_pos);
-
-        RowStage<T, D, NT, KT> st;
-        int32_t rp = 0;
-        bool rs = false;
-        auto load_side = [&](int k0) {
-            if (threadIdx.x < KT) {
-                const int kk = k0 + (int)threadIdx.x;
-                const int64_t j = s + (kk < end ? kk : end - 1);
-                rp = a.pos[j];
-                rs = kk < end && !(a.key_off && a.key_off[j] < 0);
-            }
-        };
-        auto store_side = [&](int b) {
-            if (w == 0) {
-                const bool mine = lane < KT;
-                const int32_t lo = wave_min(mine ? rp : INT32_MAX), hi = wave_max(mine ? rp : INT32_MIN);
-                const bool any = __ballot(mine && !rs) != 0;
-                if (mine) {
-                    s_mask[b][lane] = rs ? 0.f : -INFINITY;
-                    s_pos[b][lane] = rp;
-                }
-                if (lane == 0) {
-                    s_range[b][0] = lo;
-                    s_range[b][1] = hi;
-                    s_range[b][2] = any;
-                }
-            }
-        };
-
+        const int32_t q_lo = half_min(my_pos), q_hi = half_max(my_pos);
         f32x16 acc[ND] = {};
-        st.load(k, g, v, g, s, 0, end, a.key_off);
-        load_side(0);
         __syncthreads();                        // the previous tile's LDS is no longer read
         st.store(s_k[0], s_v[0]);
-        store_side(0);
+        side.store(s_side, 0);
         __syncthreads();
         for (int k0 = 0, b = 0; k0 < end; k0 += KT, b ^= 1) {
             if (k0 + KT < end) {
                 st.load(k, g, v, g, s, k0 + KT, end, a.key_off);
-                load_side(k0 + KT);
+                side.load(a, s, k0 + KT, end, KT);
             }
-            if (k0 < my_end) {
-                const int lo = wb.bucket(seq_dist(q_lo, s_range[b][1])), hi = wb.bucket(seq_dist(q_hi, s_range[b][0]));
-                const bool hidden = __builtin_amdgcn_readfirstlane(s_range[b][2]);
-                const bool diagonal = a.causal && k0 + KT - 1 > q0 + 32 * w;
-                float sum = 0.f;
 #pragma unroll
-                for (int u = 0; u < NS; ++u) {
-                    if (k0 + 32 * u >= my_end) continue;
-                    f32x16 x = mma_rows<T, D>(s_k[b], 32 * u, qf, f32x16{});
-                    const f32x16 dp = mma_rows<T, D>(s_v[b], 32 * u, df, f32x16{});
-                    int idx[16];
-                    if (lo == hi) {
-                        const float b0 = wb.value(lo);
+            for (int u = 0; u < NS; ++u) {
+                const int k1 = k0 + 32 * u;
+                if (k1 >= my_end) continue;
+                f32x16 x = mma_rows<T, D>(s_k[b], 32 * u, qf, f32x16{});
+                const f32x16 dp = mma_rows<T, D>(s_v[b], 32 * u, df, f32x16{});
+                TileBuckets<true> tb;
+                tb.set(wb, q_lo, q_hi, s_side.range[b][u]);
+                int idx[16];
+                if (tb.lo == tb.hi) {
+                    const float b0 = wb.value(tb.lo) - L;
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) x[r] = __builtin_fmaf(x[r], c2, b0);
-                    } else {
-                        bucket_index<true>(idx, wb, lo, hi, s_pos[b] + 32 * u, my_pos, a.cells, s_cell, s_bounds);
+                    for (int r = 0; r < 16; ++r) x[r] = __builtin_fmaf(x[r], c2, b0);
+                } else {
+                    tb.index(idx, wb, lb, s_side.pos[b] + 32 * u, my_pos);
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) x[r] = __builtin_fmaf(x[r], c2, s_bias[idx[r]]);
-                    }
-                    if (hidden) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const f32x4 mk = *reinterpret_cast<const f32x4*>(&s_mask[b][32 * u + 8 * j + 4 * half]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) x[4 * j + i] += mk[i];
-                        }
-                    }
-                    if (diagonal) {
-                        const int lim = my_q - k0 - 32 * u - 4 * half;
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) x[r] = tile_row(r, 0) <= lim ? x[r] : -INFINITY;
-                    }
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(x[r] - L) * (dp[r] - del);
-                    if (lo == hi) {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) sum += x[r];
-                    } else {
-                        if (half == 0) {
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) lds_add(hist + idx[r] * HC, x[r]);
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) lds_add(hist + idx[r] * HC, x[r]);
-                        }
-                    }
-                    RowOperand<T> ds;
-                    ds.set(x);
-#pragma unroll
-                    for (int dt = 0; dt < ND; ++dt) acc[dt] = mma_over_rows<D>(s_k[b], 32 * u, dt, ds, acc[dt]);
+                    for (int r = 0; r < 16; ++r) x[r] = __builtin_fmaf(x[r], c2, -L) + s_bias[idx[r]];
                 }
-                if (lo == hi) {
+                if (__builtin_amdgcn_readfirstlane((uint32_t)(s_side.hidden[b] >> (32 * u)))) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const f32x4 mk = *reinterpret_cast<const f32x4*>(&s_side.mask[b][32 * u + 8 * j + 4 * half]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[4 * j + i] += mk[i];
+                    }
+                }
+                if (a.causal && k1 + 31 > w0) {
+                    const int lim = my_q - k1 - 4 * half;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) x[r] = tile_row(r, 0) <= lim ? x[r] : -INFINITY;
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(x[r]) * (dp[r] - del);
+                if (tb.lo == tb.hi) {
+                    float sum = x[0];
+#pragma unroll
+                    for (int r = 1; r < 16; ++r) sum += x[r];
                     sum += other_half(sum);
-                    if (half == 0) lds_add(hist + lo * HC, sum);
+                    if (half == 0) lds_add(hist + tb.lo * HC, sum);
+                } else if (half == 0) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) lds_add(hist + idx[r] * HC, x[r]);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) lds_add(hist + idx[r] * HC, x[r]);
                 }
+                RowOperand<T> ds;
+                ds.set(x);
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) acc[dt] = mma_over_rows<D>(s_k[b], 32 * u, dt, ds, acc[dt]);
             }
             if (k0 + KT < end) {
                 st.store(s_k[b ^ 1], s_v[b ^ 1]);
-                store_side(b ^ 1);
+                side.store(s_side, b ^ 1);
                 __syncthreads();
             }
         }
@@ -254,7 +192,7 @@ __global__ __launch_bounds__(1024) void k_attn_dbias(const float* part, int bloc
 // dk and dv, keys as columns: per tile of queries of each head of the group
 // S = Q K^T and dP = dO V^T, dV^T += dO^T P, dK^T += Q^T dS.
 template <typename T, int D, int W, int KT>
-__global__ __launch_bounds__(W * 64) void k_attn_dkv(SeqArgs a, Rows<const T> q, Rows<const T> k, Rows<const T> v,
+__global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(DKV_WAVES<T, D>))) void k_attn_dkv(SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k, Rows<const T> v,
                                                      const float* lse2, const float* delta, Rows<const T> dout,
                                                      Rows<T> dk, Rows<T> dv) {
     using TL = Tile<T, D>;
@@ -262,16 +200,16 @@ __global__ __launch_bounds__(W * 64) void k_attn_dkv(SeqArgs a, Rows<const T> q,
     __shared__ u32x4 s_q[2][KT * CH], s_d[2][KT * CH];
     __shared__ float s_lse[2][KT], s_del[2][KT];
     __shared__ int32_t s_pos[2][KT];
-    __shared__ int32_t s_range[2][2];
+    __shared__ int32_t s_range[2][NS][2];
     __shared__ int32_t s_bounds[NBP];
     __shared__ float s_bias[2][NBP];
     __shared__ uint32_t s_cell[128];
     const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5;
-    const int g = blockIdx.y, nb = a.n_bounds + 1;
+    const int n_kv = a.n_heads / a.group, g = blockIdx.x % n_kv, nb = a.n_bounds + 1;
     int64_t s;
     int len, tile;
-    if (!find_tile(a, blockIdx.x, 32 * W, s, len, tile, false)) return;
-    const int j0 = tile * 32 * W, my_k = j0 + 32 * w + (lane & 31), row = my_k < len ? my_k : len - 1;
+    if (!find_tile(a, grid, blockIdx.x / n_kv, 32 * W, false, s, len, tile, false)) return;
+    const int j0 = tile * 32 * W, w0 = j0 + 32 * w, my_k = w0 + (lane & 31), row = my_k < len ? my_k : len - 1;
     const bool seen = !(a.key_off && a.key_off[s + row] < 0);
     const int first = a.causal ? j0 / KT * KT : 0;                  // queries of the block: first .. len
     const int per_head = (len - first + KT - 1) / KT, total = per_head * a.group;
@@ -286,7 +224,8 @@ __global__ __launch_bounds__(W * 64) void k_attn_dkv(SeqArgs a, Rows<const T> q,
     if (a.scale < 0.f) kf.negate();
     const float c2 = fabsf(a.scale) * LOG2E;
     const int32_t my_pos = a.pos[s + row];
-    const int32_t k_lo = wave_min(my_pos), k_hi = wave_max(my_pos);
+    const int32_t k_lo = half_min(my_pos), k_hi = half_max(my_pos);
+    const LdsBuckets lb = {s_bounds, s_cell, a.cells != 0, a.n_bounds};
     WaveBuckets wb;
     wb.load(a.hdr, a.bias, a.n_bounds, LOG2E);
 
@@ -313,16 +252,15 @@ __global__ __launch_bounds__(W * 64) void k_attn_dkv(SeqArgs a, Rows<const T> q,
     auto store = [&](int b) {
         st.store(s_q[b], s_d[b]);
         if (w == 0) {
-            const bool mine = lane < KT;
-            const int32_t lo = wave_min(mine ? rp : INT32_MAX), hi = wave_max(mine ? rp : INT32_MIN);
-            if (mine) {
+            const int32_t lo = half_min(rp), hi = half_max(rp);
+            if (lane < KT) {
                 s_pos[b][lane] = rp;
                 s_lse[b][lane] = rl;
                 s_del[b][lane] = rd;
-            }
-            if (lane == 0) {
-                s_range[b][0] = lo;
-                s_range[b][1] = hi;
+                if ((lane & 31) == 0) {
+                    s_range[b][lane / 32][0] = lo;
+                    s_range[b][lane / 32][1] = hi;
+                }
             }
         }
 #pragma unroll
@@ -339,25 +277,20 @@ __global__ __launch_bounds__(W * 64) void k_attn_dkv(SeqArgs a, Rows<const T> q,
     for (int it = 0, b = 0; it < total; ++it, b ^= 1) {
         const int i0 = first + it % per_head * KT;
         if (it + 1 < total) load(it + 1);
-        if (!a.causal || i0 + KT - 1 >= j0 + 32 * w) {
+        if (w0 < len && (!a.causal || i0 + KT - 1 >= w0)) {
             wb.bias[0] = s_bias[b][lane];
             wb.bias[1] = s_bias[b][64 + lane];
-            const int lo = wb.bucket(seq_dist(s_range[b][0], k_hi)), hi = wb.bucket(seq_dist(s_range[b][1], k_lo));
-            const bool diagonal = a.causal && i0 < j0 + 32 * w + 31;
 #pragma unroll
             for (int u = 0; u < NS; ++u) {
-                if (i0 + 32 * u >= len || (a.causal && i0 + 32 * u + 31 < j0 + 32 * w)) continue;
+                const int i1 = i0 + 32 * u;
+                if (i1 >= len || (a.causal && i1 + 31 < w0)) continue;
                 f32x16 x = mma_rows<T, D>(s_q[b], 32 * u, kf, f32x16{});
                 f32x16 dp = mma_rows<T, D>(s_d[b], 32 * u, vf, f32x16{});
-                if (lo == hi) {
-                    const float b0 = wb.value(lo);
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) x[r] = __builtin_fmaf(x[r], c2, b0);
-                } else {
-                    x = add_bias<false>(x, c2, wb, lo, hi, s_pos[b] + 32 * u, my_pos, a.cells, s_cell, s_bounds, s_bias[b]);
-                }
-                if (diagonal) {
-                    const int lim = my_k - i0 - 32 * u - 4 * half;
+                TileBuckets<false> tb;
+                tb.set(wb, k_lo, k_hi, s_range[b][u]);
+                x = tb.logits(x, c2, 0.f, wb, lb, s_bias[b], s_pos[b] + 32 * u, my_pos);
+                if (a.causal && i1 < w0 + 31) {
+                    const int lim = my_k - i1 - 4 * half;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) x[r] = tile_row(r, 0) >= lim ? x[r] : -INFINITY;
                 }
@@ -410,12 +343,18 @@ struct BwdWs {
     int64_t blocks;              // of k_attn_dq, per head
 };
 
-int waves_for(int64_t max_len) { return max_len <= 128 ? 1 : 4; }
+// Events of a block's tile.
+int tile_events(const rse_seqattn* a, int64_t max_len) {
+    return by_type(a, [&](auto t, auto d) {
+        using S = Shape<decltype(t), decltype(d)::value>;
+        return 32 * (max_len <= SHORT ? S::W_SHORT : S::W_LONG);
+    });
+}
 
 BwdWs bwd_ws(const rse_seqattn* a, int64_t n, int64_t batch, int64_t max_len, void* base) {
     BwdWs w;
     const int64_t most = DQ_BLOCKS / a->n_heads > 16 ? DQ_BLOCKS / a->n_heads : 16;
-    w.blocks = tile_slots(n, batch, 32 * waves_for(max_len));
+    w.blocks = tile_grid(n, batch, max_len, tile_events(a, max_len)).items;
     if (w.blocks > most) w.blocks = most;
     Carver c(base);
     w.delta = c.take<float>((size_t)a->n_heads * n);
@@ -424,21 +363,21 @@ BwdWs bwd_ws(const rse_seqattn* a, int64_t n, int64_t batch, int64_t max_len, vo
     return w;
 }
 
-template <typename T, int D, int W>
-int run_bwd_w(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v, const Saved& sv,
+template <typename T, int D, int W, int KT>
+int run_bwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v, const Saved& sv,
               const rse_seq_rows* dout, const rse_seq_rows* dq, const rse_seq_rows* dk, const rse_seq_rows* dv,
               float* dbias, const BwdWs& w, hipStream_t s) {
-    constexpr int KT = W > 1 && D * sizeof(T) <= 256 ? 64 : 32;
     const int nb = a.n_bounds + 1;
-    const int64_t slots = tile_slots(a.n_events, a.batch, 32 * W);
-    if (slots > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+    const TileGrid tg = tile_grid(a.n_events, a.batch, a.max_len, 32 * W);
+    const int64_t dkv = tg.items * (a.n_heads / a.group);
+    if (dkv > INT32_MAX) return RSE_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((k_attn_dq<T, D, W, KT>), dim3((unsigned)w.blocks, a.n_heads), dim3(W * WAVE),
-                       W * nb * HC * sizeof(float), s, a, slots, rows_view<const T>(q), rows_view<const T>(k),
+                       W * nb * HC * sizeof(float), s, a, tg, rows_view<const T>(q), rows_view<const T>(k),
                        rows_view<const T>(v), sv.lse2, sv.out32, rows_view<const T>(dout), rows_view<T>(dq), w.delta, w.part);
     int rc = launch_status();
     if (rc) return rc;
     hipLaunchKernelGGL(k_attn_dbias, dim3(a.n_heads), dim3(1024), 0, s, w.part, (int)w.blocks, nb, dbias);
-    hipLaunchKernelGGL((k_attn_dkv<T, D, W, KT>), dim3((unsigned)slots, a.n_heads / a.group), dim3(W * WAVE), 0, s, a,
+    hipLaunchKernelGGL((k_attn_dkv<T, D, W, KT>), dim3((unsigned)dkv), dim3(W * WAVE), 0, s, a, tg,
                        rows_view<const T>(q), rows_view<const T>(k), rows_view<const T>(v), sv.lse2, w.delta,
                        rows_view<const T>(dout), rows_view<T>(dk), rows_view<T>(dv));
     return launch_status();
@@ -478,10 +417,10 @@ int seq_attention_bwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
     return by_type(attn, [&](auto t, auto d) {
         using T = decltype(t);
         constexpr int D = decltype(d)::value;
-        switch (waves_for(a.max_len)) {
-            case 1: return run_bwd_w<T, D, 1>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
-            default: return run_bwd_w<T, D, 4>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
-        }
+        using S = Shape<T, D>;
+        if (a.max_len <= SHORT)
+            return run_bwd<T, D, S::W_SHORT, S::KT_SHORT>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
+        return run_bwd<T, D, S::W_LONG, S::KT_LONG>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
     });
 }
 

@@ -224,122 +224,180 @@ struct WaveBuckets {
     }
 };
 
-__device__ __forceinline__ int32_t wave_min(int32_t x) {
+// Lowest and highest of each half of the wave.
+__device__ __forceinline__ int32_t half_min(int32_t x) {
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) {
+    for (int m = 16; m > 0; m >>= 1) {
         const int32_t y = __shfl_xor(x, m, WAVE);
         x = y < x ? y : x;
     }
     return x;
 }
-__device__ __forceinline__ int32_t wave_max(int32_t x) {
+__device__ __forceinline__ int32_t half_max(int32_t x) {
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) {
+    for (int m = 16; m > 0; m >>= 1) {
         const int32_t y = __shfl_xor(x, m, WAVE);
         x = y > x ? y : x;
     }
     return x;
 }
-
 constexpr float LOG2E = 1.4426950408889634f;
-// More distinct buckets than this in a tile: looked up event by event.
+// More boundaries than this inside a tile: looked up event by event.
 constexpr int CHAIN = 6;
 
-// Buckets of the lane's column and the 16 rows of a tile that spans buckets
-// lo .. hi: compared with the boundaries between them, or searched.
-template <bool column_first>
-__device__ __forceinline__ void bucket_index(int (&idx)[16], const WaveBuckets& wb, int lo, int hi, const int32_t* row_pos,
-                                             int32_t col_pos, bool cells, const uint32_t* s_cell,
-                                             const int32_t* s_bounds) {
+__device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) { return __builtin_elementwise_add_sat(a, b); }
+
+// What a kernel holds in LDS to look buckets up event by event.
+struct LdsBuckets {
+    const int32_t* bounds;
+    const uint32_t* cell;
+    bool cells;
+    int n;
+    __device__ __forceinline__ int find(int32_t d) const {
+        return cells ? seq_bucket_cell(reinterpret_cast<const uint8_t*>(cell), bounds, n, d) : seq_bucket(bounds, n, d);
+    }
+};
+
+// Positions of the 16 rows of a lane's half.
+__device__ __forceinline__ void row_positions(int32_t (&p)[16], const int32_t* row_pos) {
     const int h = lane_id() >> 5;
-    int32_t dist[16];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const i32x4 p = *reinterpret_cast<const i32x4*>(row_pos + 8 * j + 4 * h);
+        const i32x4 v = *reinterpret_cast<const i32x4*>(row_pos + 8 * j + 4 * h);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dist[4 * j + i] = column_first ? seq_dist(col_pos, p[i]) : seq_dist(p[i], col_pos);
-    }
-    if (hi - lo <= 2 * CHAIN) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) idx[r] = lo;
-        for (int m = lo; m < hi; ++m) {
-            const int32_t edge = wb.boundary(m);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) idx[r] += dist[r] >= edge;
-        }
-    } else if (cells) {
-        const uint8_t* cell = reinterpret_cast<const uint8_t*>(s_cell);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) idx[r] = seq_bucket_cell(cell, s_bounds, wb.n, dist[r]);
-    } else {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) idx[r] = seq_bucket(s_bounds, wb.n, dist[r]);
+        for (int i = 0; i < 4; ++i) p[4 * j + i] = v[i];
     }
 }
 
-// Bias (base 2) of the lane's column for the 16 rows of a 32 x 32 tile that
-// may span buckets lo .. hi, added to s times c.  row_pos: positions of the
-// tile's rows in LDS.  A tile of few buckets compares each distance with the
-// boundaries between them; with many, each distance is searched in the LDS
-// copy of the boundaries.
-// `column_first`: the column event is the query (distance = column - row).
+// The rows of a 32 x 32 tile span positions range[0] .. range[1]; its pairs'
+// distances the buckets lo .. hi.  column_first: distance = column - row.
+//
+// A boundary is passed by the rows on one side of a position that is the
+// lane's own (col_pos -/+ the boundary, saturated): one comparison per pair
+// and boundary.  A saturated threshold is met wrongly only by a row at the
+// very end of int32, so such tiles are looked up pair by pair.
 template <bool column_first>
-__device__ __forceinline__ f32x16 add_bias(f32x16 s, float c, const WaveBuckets& wb, int lo, int hi, const int32_t* row_pos,
-                                           int32_t col_pos, bool cells, const uint32_t* s_cell,
-                                           const int32_t* s_bounds, const float* s_bias) {
-    const int h = lane_id() >> 5;
-    int32_t dist[16];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const i32x4 p = *reinterpret_cast<const i32x4*>(row_pos + 8 * j + 4 * h);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dist[4 * j + i] = column_first ? seq_dist(col_pos, p[i]) : seq_dist(p[i], col_pos);
+struct TileBuckets {
+    int lo, hi;
+    bool chain;
+    __device__ __forceinline__ void set(const WaveBuckets& wb, int32_t col_lo, int32_t col_hi, const int32_t* range) {
+        const int32_t r_lo = __builtin_amdgcn_readfirstlane(range[0]), r_hi = __builtin_amdgcn_readfirstlane(range[1]);
+        lo = wb.bucket(column_first ? seq_dist(col_lo, r_hi) : seq_dist(r_lo, col_hi));
+        hi = wb.bucket(column_first ? seq_dist(col_hi, r_lo) : seq_dist(r_hi, col_lo));
+        chain = hi - lo <= CHAIN && (column_first ? r_lo > INT32_MIN : r_hi < INT32_MAX);
     }
-    f32x16 b;
-    if (hi - lo <= CHAIN) {
-        const float b0 = wb.value(lo);
+    __device__ __forceinline__ int32_t threshold(const WaveBuckets& wb, int m, int32_t col_pos) const {
+        const int32_t edge = wb.boundary(m);
+        return column_first ? seq_dist(col_pos, edge) : sat_add(col_pos, edge);
+    }
+    static __device__ __forceinline__ bool passed(int32_t row, int32_t threshold) {
+        return column_first ? row <= threshold : row >= threshold;
+    }
+    static __device__ __forceinline__ int32_t dist(int32_t row, int32_t col) {
+        return column_first ? seq_dist(col, row) : seq_dist(row, col);
+    }
+    // s c + bias + shift of every pair
+    __device__ __forceinline__ f32x16 logits(f32x16 s, float c, float shift, const WaveBuckets& wb, const LdsBuckets& lb,
+                                             const float* s_bias, const int32_t* row_pos, int32_t col_pos) const {
+        if (lo == hi) {
+            const float b = wb.value(lo) + shift;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) b[r] = b0;
-        for (int m = lo; m < hi; ++m) {
-            const int32_t edge = wb.boundary(m);
-            const float bm = wb.value(m + 1);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) b[r] = dist[r] >= edge ? bm : b[r];
+            for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], c, b);
+            return s;
         }
-    } else if (cells) {
-        const uint8_t* cell = reinterpret_cast<const uint8_t*>(s_cell);
+        int32_t p[16];
+        row_positions(p, row_pos);
+        if (chain) {
+            float b[16];
+            const float b0 = wb.value(lo) + shift;
+            {
+                const int32_t th = threshold(wb, lo, col_pos);
+                const float bm = wb.value(lo + 1) + shift;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) b[r] = s_bias[seq_bucket_cell(cell, s_bounds, wb.n, dist[r])];
-    } else {
+                for (int r = 0; r < 16; ++r) b[r] = passed(p[r], th) ? bm : b0;
+            }
+            for (int m = lo + 1; m < hi; ++m) {
+                const int32_t th = threshold(wb, m, col_pos);
+                const float bm = wb.value(m + 1) + shift;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) b[r] = s_bias[seq_bucket(s_bounds, wb.n, dist[r])];
+                for (int r = 0; r < 16; ++r) b[r] = passed(p[r], th) ? bm : b[r];
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], c, b[r]);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[r] = __builtin_fmaf(s[r], c, shift) + s_bias[lb.find(dist(p[r], col_pos))];
+                if ((r & 3) == 3) __builtin_amdgcn_sched_barrier(0);    // four lookups in flight, for the registers
+            }
+        }
+        return s;
     }
+    // bucket of every pair (lo < hi)
+    __device__ __forceinline__ void index(int (&idx)[16], const WaveBuckets& wb, const LdsBuckets& lb, const int32_t* row_pos,
+                                          int32_t col_pos) const {
+        int32_t p[16];
+        row_positions(p, row_pos);
+        if (chain) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], c, b[r]);
-    return s;
-}
+            for (int r = 0; r < 16; ++r) idx[r] = lo;
+            for (int m = lo; m < hi; ++m) {
+                const int32_t th = threshold(wb, m, col_pos);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) idx[r] += passed(p[r], th);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                idx[r] = lb.find(dist(p[r], col_pos));
+                if ((r & 3) == 3) __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+};
 
 // ------------------------------------------------------------- tile finder --
-// Tiles of TQ events of every sequence, numbered without a table: sequence b
-// has the numbers offsets[b] / TQ + b and on, at least as many as its tiles
-// (a number past its last tile is idle).  True with the sequence's range and
-// the tile's index; also checks all offsets, a part in each block.
-__host__ __device__ __forceinline__ int64_t tile_slots(int64_t n_events, int64_t batch, int tq) { return n_events / tq + batch; }
+// Tiles of tq events of every sequence, numbered in one of two ways.
+//  - per_seq > 0 (no sequence has more tiles): item t * batch + b is tile t of
+//    sequence b; idle where the sequence is shorter.  No search, and tiles of
+//    equal index stand together, so that long work can start first.
+//  - per_seq = 0, where that would leave most items idle: sequence b has the
+//    numbers offsets[b] / tq + b and on, at least as many as its tiles, found
+//    by a search.
+// Every call checks a part of the offsets.
+struct TileGrid {
+    int64_t items;
+    int64_t per_seq;
+};
+inline TileGrid tile_grid(int64_t n_events, int64_t batch, int64_t max_len, int tq) {
+    const int64_t slots = n_events / tq + batch, longest = max_len < n_events ? max_len : n_events;
+    const int64_t per_seq = (longest + tq - 1) / tq;
+    if (per_seq <= 4 * slots / (batch > 0 ? batch : 1)) return {per_seq * batch, per_seq};
+    return {slots, 0};
+}
 
-__device__ __forceinline__ bool find_tile(const SeqArgs& a, int64_t slot, int tq, int64_t& s, int& len, int& tile,
-                                          bool check) {
+// The item's sequence (first event, length) and tile; false if it is idle.
+// backwards: items of a grid by tile index start from the last tile.
+__device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, int64_t item, int tq, bool backwards,
+                                          int64_t& s, int& len, int& tile, bool check) {
     if (check) {
-        const int64_t i = slot * blockDim.x + threadIdx.x;
-        if (i < a.batch) {
+        for (int64_t i = item * blockDim.x + threadIdx.x; i < a.batch; i += g.items * blockDim.x) {
             const int64_t x = a.offsets[i], y = a.offsets[i + 1];
             if (x > y || (i == 0 && x != 0) || (i == a.batch - 1 && y != a.n_events))
                 set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
         }
     }
-    const int64_t b = wave_last_le(a.batch, [&](int64_t x) { return a.offsets[x] / tq + x; }, slot);
+    int64_t b, t;
+    if (g.per_seq) {
+        t = item / a.batch;
+        b = item - t * a.batch;
+        if (backwards) t = g.per_seq - 1 - t;
+    } else {
+        b = wave_last_le(a.batch, [&](int64_t x) { return a.offsets[x] / tq + x; }, item);
+        t = item - (a.offsets[b] / tq + b);
+    }
     s = a.offsets[b];
     const int64_t e = a.offsets[b + 1];
-    const int64_t t = slot - (s / tq + b);
     if (s < 0 || e < s || e > a.n_events || e - s > a.max_len) {
         if (lane_id() == 0) set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
         return false;
@@ -349,5 +407,91 @@ __device__ __forceinline__ bool find_tile(const SeqArgs& a, int64_t slot, int tq
     tile = (int)t;
     return true;
 }
+
+// ------------------------------------------------------------------ shapes --
+// Long sequences: blocks of 4 waves share tiles of 64 keys (two buffers of
+// two tensors: at most 64 KiB).  Up to SHORT events, where such a block would
+// mostly idle: as few waves as can hold the next tile's loads in registers.
+constexpr int64_t SHORT = 128;
+template <typename T, int D>
+struct Shape {
+    static constexpr int RB = D * (int)sizeof(T);       // bytes of a row
+    static constexpr int W_LONG = 4, KT_LONG = RB <= 256 ? 64 : 32;
+    static constexpr int W_SHORT = RB <= 128 ? 1 : (RB == 256 ? 2 : 4), KT_SHORT = 32;
+};
+
+// ----------------------------------------------------------------- staging --
+// Rows k0 .. k0 + KT - 1 of two tensors on their way to LDS: loaded into
+// registers (thread t: chunk t % CH of rows t / CH, + NT / CH, ...), stored
+// after the current tile's work.  Hidden rows and rows past the end are
+// stored as zeros, whatever they hold.
+template <typename T, int D, int NT, int KT>
+struct RowStage {
+    using TL = Tile<T, D>;
+    static constexpr int CH = TL::CH, PER = KT * CH / NT, STEP = NT / CH;
+    static_assert(KT * CH % NT == 0, "tile shape");
+    u32x4 x[PER], y[PER];
+    bool hid[PER];
+    __device__ __forceinline__ void load(const Rows<const T>& X, int hx, const Rows<const T>& Y, int hy, int64_t s, int k0,
+                                         int end, const int64_t* key_off) {
+        const int row = threadIdx.x / CH, c = threadIdx.x % CH;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int kk = k0 + row + i * STEP;
+            const int64_t j = s + (kk < end ? kk : end - 1);
+            x[i] = gload_u4(X.at(j, hx) + c * TL::EPC);
+            y[i] = gload_u4(Y.at(j, hy) + c * TL::EPC);
+            hid[i] = kk >= end || (key_off && key_off[j] < 0);
+        }
+    }
+    __device__ __forceinline__ void store(u32x4* sx, u32x4* sy) const {
+        const int row = threadIdx.x / CH, c = threadIdx.x % CH;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int at = TL::chunk_at(row + i * STEP, c);
+            sx[at] = hid[i] ? u32x4{0, 0, 0, 0} : x[i];
+            sy[at] = hid[i] ? u32x4{0, 0, 0, 0} : y[i];
+        }
+    }
+};
+
+// The events of a tile of keys on their way to LDS beside its rows (threads
+// 0 .. KT - 1): positions, which may be seen, and of each 32 of them the
+// lowest and highest position and whether any may not be seen.
+template <int KT>
+struct KeySide {
+    float mask[2][KT];
+    int32_t pos[2][KT];
+    int32_t range[2][KT / 32][2];
+    uint64_t hidden[2];                         // bit per event
+};
+struct KeySideStage {
+    int32_t p;
+    bool see;
+    __device__ __forceinline__ void load(const SeqArgs& a, int64_t s, int k0, int end, int kt) {
+        if ((int)threadIdx.x < kt) {
+            const int kk = k0 + (int)threadIdx.x;
+            const int64_t j = s + (kk < end ? kk : end - 1);
+            p = a.pos[j];
+            see = kk < end && !(a.key_off && a.key_off[j] < 0);
+        }
+    }
+    template <int KT>
+    __device__ __forceinline__ void store(KeySide<KT>& ks, int b) const {
+        if (threadIdx.x >= WAVE) return;
+        const int lane = lane_id();
+        const int32_t lo = half_min(p), hi = half_max(p);
+        const uint64_t hid = __ballot(lane < KT && !see);
+        if (lane < KT) {
+            ks.mask[b][lane] = see ? 0.f : -INFINITY;
+            ks.pos[b][lane] = p;
+            if ((lane & 31) == 0) {
+                ks.range[b][lane / 32][0] = lo;
+                ks.range[b][lane / 32][1] = hi;
+            }
+            if (lane == 0) ks.hidden[b] = hid;
+        }
+    }
+};
 
 }  // namespace rse
