@@ -73,7 +73,8 @@ __device__ __forceinline__ int seq_bucket(const int32_t* bounds, int n_bounds, i
 // boundaries <= the whole cell, and perhaps the next one.
 __device__ __forceinline__ int seq_bucket_cell(const uint8_t* cell, const int32_t* bounds, int n_bounds, int32_t d) {
     const int b = cell[seq_cell(d)];
-    return b + (b < n_bounds && bounds[b] <= d);
+    const int e = b + (bounds[b] <= d);         // the padding at n_bounds counts where d is INT32_MAX
+    return e < n_bounds ? e : n_bounds;
 }
 
 // Wave-level ordering of a wave's own LDS writes before its other lanes read them.

@@ -59,12 +59,12 @@ bool fill_cells(InitArgs& a) {
 
 __global__ void k_attn_clear(SeqHeader* h) { h->status = 0; }
 
-// Forward.  A block of W waves takes 32 W queries of one sequence and head; a
-// wave has 32 of them as columns.  Keys go by in tiles of KT, staged in LDS
-// row-major (the next tile's loads are in flight meanwhile), 32 at a time:
-// S^T = K Q^T, online softmax down the registers of a lane (a row's maximum
-// needs one exchange between the wave's halves, its sum none until the end),
-// and O^T += V^T P^T with the same registers as operand.
+// Forward.  A wave has 32 queries of one sequence and head as columns.  Keys
+// go by in tiles staged in LDS row-major (the next tile's loads are in flight
+// meanwhile), 32 at a time: S^T = K Q^T, online softmax down the registers of
+// a lane (a row's maximum needs one exchange between the wave's halves, its
+// sum none until the end), and O^T += V^T P^T with the same registers as
+// operand.
 //
 // The logits are formed relative to a reference m of the row, in base 2:
 // y = s c + (bias - m), p = exp2(y).  m follows the row's maximum only when
@@ -75,44 +75,47 @@ __global__ void k_attn_clear(SeqHeader* h) { h->status = 0; }
 // dO . out has to equal sum_j p dp to fp32 accuracy (the bias gradient sums
 // differences from it): what bf16 rounds off the probabilities goes through
 // a second product into those outputs.
+//
 // Registers are held to what lets FWD_WAVES waves share a SIMD.
 template <typename T, int D, bool SAVE>
-constexpr int FWD_WAVES = Shape<T, D>::RB == 64 ? 4 : (Shape<T, D>::RB == 128 ? 3 : 2);
+constexpr int FWD_WAVES = D * sizeof(T) <= 64 ? 4 : (D * sizeof(T) == 128 ? 3 : 2);
 
-template <typename T, int D, int W, int KT, bool SAVE>
-__global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(FWD_WAVES<T, D, SAVE>))) void k_attn_fwd(SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k,
-                                                     Rows<const T> v, Rows<T> out, float* lse2, float* out32) {
-    constexpr int NT = W * 64, CH = Tile<T, D>::CH, NS = KT / 32, ND = D / 32;
+template <typename T, int D, typename SH, bool SAVE>
+__global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(FWD_WAVES<T, D, SAVE>))) void k_attn_fwd(
+    SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k, Rows<const T> v, Rows<T> out, float* lse2, float* out32) {
+    constexpr int CH = SH::CH, KT = SH::KT, NS = SH::NS, NB = SH::NB, NT = SH::NT, WH = SH::WH, WQ = SH::WQ, ND = D / 32;
     constexpr bool REST = SAVE && sizeof(T) == 2;
-    __shared__ u32x4 s_k[2][KT * CH], s_v[2][KT * CH];
-    __shared__ KeySide<KT> s_side;
-    __shared__ int32_t s_bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
-    __shared__ float s_bias[RSE_SEQ_MAX_BOUNDARIES + 1];
-    __shared__ uint32_t s_cell[128];
-    const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5;
-    const int head = blockIdx.x % a.n_heads, g = head / a.group, nb = a.n_bounds + 1;
+    __shared__ u32x4 s_k[SH::TEAMS][NB][KT * CH], s_v[SH::TEAMS][NB][KT * CH];
+    __shared__ u32x4 s_pairs[WQ][NS][WAVE];
+    __shared__ KeySide<KT> s_side[SH::TEAMS][NB];
+    __shared__ LdsBuckets s_buckets;
+    __shared__ float s_bias[WH][RSE_SEQ_MAX_BOUNDARIES + 1];
+    const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5, wh = w % WH, wq = w / WH;
+    const int team = w / SH::TEAM, t = threadIdx.x % NT;
+    const int hblocks = (a.n_heads + WH - 1) / WH, h0 = blockIdx.x % hblocks * WH, nb = a.n_bounds + 1;
+    const bool live = h0 + wh < a.n_heads;
+    const int head = live ? h0 + wh : a.n_heads - 1, g = head / a.group;
     int64_t s;
     int len, tile;
-    if (!find_tile(a, grid, blockIdx.x / a.n_heads, 32 * W, a.causal, s, len, tile, head == 0)) return;
-    const int q0 = tile * 32 * W, w0 = q0 + 32 * w, my_q = w0 + (lane & 31), row = my_q < len ? my_q : len - 1;
-    const int end = a.causal ? (q0 + 32 * W < len ? q0 + 32 * W : len) : len;       // keys of the block
+    if (!find_tile(a, grid, blockIdx.x / hblocks, 32 * WQ, a.causal, s, len, tile, h0 == 0)) return;
+    const int q0 = tile * 32 * WQ, w0 = q0 + 32 * wq, my_q = w0 + (lane & 31), row = my_q < len ? my_q : len - 1;
+    const int end = a.causal ? (q0 + 32 * WQ < len ? q0 + 32 * WQ : len) : len;     // keys of the block
     const int my_end = w0 >= len ? 0 : (a.causal && w0 + 32 < end ? w0 + 32 : end);  // and of the wave
 
     RowStage<T, D, NT, KT> st;
     KeySideStage side;
-    st.load(k, g, v, g, s, 0, end, a.key_off);
-    side.load(a, s, 0, end, KT);
+    st.load(k, g, v, g, s, 0, end, a.key_off, t);
+    side.load(a, s, 0, end, KT, t);
     ColFrag<T, D> qf;
     qf.load(q.at(s + row, head), half);
     const int32_t my_pos = a.pos[s + row];
     WaveBuckets wb;
     wb.load(a.hdr, a.bias + head * nb, a.n_bounds, LOG2E);
-    for (int t = threadIdx.x; t <= RSE_SEQ_MAX_BOUNDARIES; t += NT) {
-        s_bounds[t] = a.hdr->bounds[t];
-        s_cell[t] = reinterpret_cast<const uint32_t*>(a.hdr->cell)[t];
-        s_bias[t] = t < nb ? a.bias[head * nb + t] * LOG2E : 0.f;
+    s_buckets.load(a.hdr);
+    if (wq == 0) {
+        s_bias[wh][lane] = wb.bias[0];
+        s_bias[wh][64 + lane] = wb.bias[1];
     }
-    const LdsBuckets lb = {s_bounds, s_cell, a.cells != 0, a.n_bounds};
     if (a.scale < 0.f) qf.negate();
     const float c2 = fabsf(a.scale) * LOG2E;
     const int32_t q_lo = half_min(my_pos), q_hi = half_max(my_pos);
@@ -120,30 +123,31 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(FWD_WAVE
     f32x16 o[ND] = {}, rest[REST ? ND : 1] = {};
     float m = 0.f, l = 0.f;
     bool set = false;                           // m has been taken from a visible key
-    st.store(s_k[0], s_v[0]);
-    side.store(s_side, 0);
+    st.store(s_k[team][0], s_v[team][0], t);
+    side.store(s_side[team][0], t);
     __syncthreads();
-    for (int k0 = 0, b = 0; k0 < end; k0 += KT, b ^= 1) {
+    for (int k0 = 0, b = 0; k0 < end; k0 += KT, b ^= NB - 1) {
         if (k0 + KT < end) {
-            st.load(k, g, v, g, s, k0 + KT, end, a.key_off);
-            side.load(a, s, k0 + KT, end, KT);
+            st.load(k, g, v, g, s, k0 + KT, end, a.key_off, t);
+            side.load(a, s, k0 + KT, end, KT, t);
         }
-#pragma unroll
+        const KeySide<KT>& ks = s_side[team][b];
+#pragma unroll 1
         for (int u = 0; u < NS; ++u) {
             const int k1 = k0 + 32 * u;
-            if (k1 >= my_end) continue;
-            f32x16 x = mma_rows<T, D>(s_k[b], 32 * u, qf, f32x16{});
+            if (k1 >= my_end) break;
             TileBuckets<true> tb;
-            tb.set(wb, q_lo, q_hi, s_side.range[b][u]);
-            x = tb.logits(x, c2, -m, wb, lb, s_bias, s_side.pos[b] + 32 * u, my_pos);
-            if (__builtin_amdgcn_readfirstlane((uint32_t)(s_side.hidden[b] >> (32 * u)))) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f32x4 mk = *reinterpret_cast<const f32x4*>(&s_side.mask[b][32 * u + 8 * j + 4 * half]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[4 * j + i] += mk[i];
-                }
+            tb.set(wb, q_lo, q_hi, ks.range[u]);
+            if (tb.many) {
+                // all waves of a column tile are here, and share the lookups
+                if (SH::TEAM == 1 && WH > 1) __syncthreads();   // the last tile's are no longer read
+                tb.find_pairs(s_pairs[wq][u], wh, WH, s_buckets, a.n_bounds, a.cells, ks.pos + 32 * u, my_pos);
+                if (WH > 1) __syncthreads();
+                else wave_lds_sync();
             }
+            f32x16 x = mma_rows<T, D>(s_k[team][b], 32 * u, qf, f32x16{});
+            x = tb.logits(x, c2, -m, wb, s_pairs[wq][u], s_bias[wh], ks.pos + 32 * u, my_pos);
+            hide(x, ks.hidden[u], ks.mask + 32 * u);
             if (a.causal && k1 + 31 > w0) {
                 const int lim = my_q - k1 - 4 * half;
 #pragma unroll
@@ -177,23 +181,24 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(FWD_WAVE
             RowOperand<T> p;
             p.set(x);
 #pragma unroll
-            for (int dt = 0; dt < ND; ++dt) o[dt] = mma_over_rows<D>(s_v[b], 32 * u, dt, p, o[dt]);
+            for (int dt = 0; dt < ND; ++dt) o[dt] = mma_over_rows<D>(s_v[team][b], 32 * u, dt, p, o[dt]);
             if (REST) {
                 RowOperand<T> lo;
                 lo.set_rest(x, p);
 #pragma unroll
-                for (int dt = 0; dt < ND; ++dt) rest[dt] = mma_over_rows<D>(s_v[b], 32 * u, dt, lo, rest[dt]);
+                for (int dt = 0; dt < ND; ++dt) rest[dt] = mma_over_rows<D>(s_v[team][b], 32 * u, dt, lo, rest[dt]);
             }
         }
         if (k0 + KT < end) {
-            st.store(s_k[b ^ 1], s_v[b ^ 1]);
-            side.store(s_side, b ^ 1);
-            __syncthreads();
+            if (SH::TEAM == 1) wave_lds_sync();
+            st.store(s_k[team][b ^ (NB - 1)], s_v[team][b ^ (NB - 1)], t);
+            side.store(s_side[team][b ^ (NB - 1)], t);
+            team_sync<SH::TEAM>();
         }
     }
     l += other_half(l);
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    if (my_q < len) {
+    if (my_q < len && live) {
         T* dst = out.at(s + my_q, head);
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) store_column(dst + 32 * dt, o[dt], inv);
@@ -209,17 +214,19 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(FWD_WAVE
 }
 
 // ------------------------------------------------------------------ host --
-template <typename T, int D, int W, int KT>
+template <typename T, int D, int TEAM, int WH, int WQ>
 int run_fwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v,
             const rse_seq_rows* out, const Saved& sv, hipStream_t s) {
-    const TileGrid tg = tile_grid(a.n_events, a.batch, a.max_len, 32 * W);
-    if (tg.items * a.n_heads > INT32_MAX) return RSE_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)(tg.items * a.n_heads)), block(W * WAVE);
+    using SH = Shape<T, D, TEAM, WH, WQ>;
+    const TileGrid tg = tile_grid(a.n_events, a.batch, a.max_len, 32 * WQ);
+    const int64_t blocks = tg.items * ((a.n_heads + WH - 1) / WH);
+    if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks), block(SH::WAVES * WAVE);
     if (sv.lse2)
-        hipLaunchKernelGGL((k_attn_fwd<T, D, W, KT, true>), grid, block, 0, s, a, tg, rows_view<const T>(q),
+        hipLaunchKernelGGL((k_attn_fwd<T, D, SH, true>), grid, block, 0, s, a, tg, rows_view<const T>(q),
                            rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), sv.lse2, sv.out32);
     else
-        hipLaunchKernelGGL((k_attn_fwd<T, D, W, KT, false>), grid, block, 0, s, a, tg, rows_view<const T>(q),
+        hipLaunchKernelGGL((k_attn_fwd<T, D, SH, false>), grid, block, 0, s, a, tg, rows_view<const T>(q),
                            rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), nullptr, nullptr);
     return launch_status();
 }
@@ -316,9 +323,14 @@ int seq_attention_fwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
     return by_type(attn, [&](auto t, auto d) {
         using T = decltype(t);
         constexpr int D = decltype(d)::value;
-        using S = Shape<T, D>;
-        if (a.max_len <= SHORT) return run_fwd<T, D, S::W_SHORT, S::KT_SHORT>(a, q, k, v, out, sv, as_stream(stream));
-        return run_fwd<T, D, S::W_LONG, S::KT_LONG>(a, q, k, v, out, sv, as_stream(stream));
+        const hipStream_t st = as_stream(stream);
+        if constexpr (short_form<T, D>(0))
+            if (short_form<T, D>(a.max_len)) {
+                if (a.n_heads > 1) return run_fwd<T, D, 1, 4, 1>(a, q, k, v, out, sv, st);
+                return run_fwd<T, D, 1, 1, 1>(a, q, k, v, out, sv, st);
+            }
+        if (a.group % 4 == 0) return run_fwd<T, D, 4, 4, 1>(a, q, k, v, out, sv, st);
+        return run_fwd<T, D, 4, 1, 4>(a, q, k, v, out, sv, st);
     });
 }
 

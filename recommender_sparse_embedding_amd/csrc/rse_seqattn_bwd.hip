@@ -10,67 +10,90 @@ using namespace rse_host;
 
 namespace {
 
-// Columns of a wave's bucket sums: the two halves of the wave add in turn to
-// the same 32, so each entry is added to in program order.
-constexpr int HC = 32;
-
-__device__ __forceinline__ void lds_add(float* p, float x) {
-    __builtin_amdgcn_ds_faddf((RSE_LDS float*)p, x, 0, 0, false);
+// A wave's bucket sums in LDS, [bucket][cols]: lane l adds in column l % cols
+// by a plain read, addition and write, so every entry has a fixed order of
+// additions.  (An LDS atomic addition of floats took 93 LDS cycles here, a
+// read and a write together some ten.)  With 32 columns the two halves of the
+// wave take turns.
+__device__ __forceinline__ void add_pairs(float* hist, int cols, const int (&idx)[16], const f32x16& x) {
+    const int lane = lane_id();
+    float* mine = hist + (lane & (cols - 1));
+    if (cols == WAVE || lane < 32)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mine[idx[r] * cols] += x[r];
+    wave_lds_sync();
+    if (cols < WAVE && lane >= 32)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mine[idx[r] * cols] += x[r];
+    wave_lds_sync();
 }
+// One lane's sum per column pair into one bucket.
+__device__ __forceinline__ void add_bucket(float* hist, int cols, int bucket, float sum) {
+    sum += other_half(sum);
+    if (lane_id() < 32) hist[bucket * cols + lane_id()] += sum;
+    wave_lds_sync();
+}
+// Up to so many buckets of a tile are summed in registers.
+constexpr int SUMS = 3;
 
 // dq and the bias gradient, queries as columns: per tile of keys
 // S^T = K Q^T and dP^T = V dO^T, ds = p (dp - delta), dQ^T += K^T dS^T.
 // delta = sum_j p dp = dO . out, from the unrounded outputs.  ds of a tile in
 // one bucket is summed in registers, else scattered into the wave's LDS
-// columns of bucket sums.  A block stays with its head and takes tiles of
+// columns of bucket sums.  A block stays with its heads and takes tiles of
 // queries blockIdx.x, + gridDim.x, ...; its sums go to part.
 // Registers are held to what lets DQ_WAVES (DKV_WAVES) waves share a SIMD.
 template <typename T, int D>
-constexpr int DQ_WAVES = Shape<T, D>::RB <= 64 ? 3 : (Shape<T, D>::RB <= 256 ? 2 : 1);
+constexpr int DQ_WAVES = D * sizeof(T) <= 64 ? 3 : (D * sizeof(T) <= 256 ? 2 : 1);
 template <typename T, int D>
-constexpr int DKV_WAVES = Shape<T, D>::RB <= 64 ? 3 : (Shape<T, D>::RB <= 128 || sizeof(T) == 4 && D == 64 ? 2 : 1);
+constexpr int DKV_WAVES = D * sizeof(T) <= 64 ? 3 : (D * sizeof(T) <= 128 || D == 64 ? 2 : 1);
 
-template <typename T, int D, int W, int KT>
-__global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(DQ_WAVES<T, D>))) void k_attn_dq(SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k,
-                                                    Rows<const T> v, const float* lse2, const float* out32,
-                                                    Rows<const T> dout, Rows<T> dq, float* delta, float* part) {
+template <typename T, int D, typename SH>
+__global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(DQ_WAVES<T, D>))) void k_attn_dq(
+    SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k, Rows<const T> v, const float* lse2, const float* out32,
+    Rows<const T> dout, Rows<T> dq, float* delta, float* part, int cols) {
     using TL = Tile<T, D>;
-    constexpr int NT = W * 64, CH = TL::CH, NS = KT / 32, ND = D / 32;
-    __shared__ u32x4 s_k[2][KT * CH], s_v[2][KT * CH];
-    __shared__ KeySide<KT> s_side;
-    __shared__ int32_t s_bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
-    __shared__ float s_bias[RSE_SEQ_MAX_BOUNDARIES + 1];
-    __shared__ uint32_t s_cell[128];
-    extern __shared__ float s_hist[];           // [W][n_bounds + 1][HC]
-    const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5;
-    const int head = blockIdx.y, g = head / a.group, nb = a.n_bounds + 1;
-    float* hist = s_hist + w * nb * HC + (lane & 31);
+    constexpr int CH = SH::CH, KT = SH::KT, NS = SH::NS, NB = SH::NB, NT = SH::NT, WH = SH::WH, WQ = SH::WQ, ND = D / 32;
+    __shared__ u32x4 s_k[SH::TEAMS][NB][KT * CH], s_v[SH::TEAMS][NB][KT * CH];
+    __shared__ u32x4 s_pairs[WQ][NS][WAVE];
+    __shared__ KeySide<KT> s_side[SH::TEAMS][NB];
+    __shared__ LdsBuckets s_buckets;
+    __shared__ float s_bias[WH][RSE_SEQ_MAX_BOUNDARIES + 1];
+    extern __shared__ float s_hist[];           // [waves][n_bounds + 1][cols]
+    const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5, wh = w % WH, wq = w / WH;
+    const int team = w / SH::TEAM, t = threadIdx.x % NT;
+    const int h0 = blockIdx.y * WH, nb = a.n_bounds + 1;
+    const bool live = h0 + wh < a.n_heads;
+    const int head = live ? h0 + wh : a.n_heads - 1, g = head / a.group;
+    float* hist = s_hist + w * nb * cols;
 
     WaveBuckets wb;
     wb.load(a.hdr, a.bias + head * nb, a.n_bounds, LOG2E);
-    for (int t = threadIdx.x; t <= RSE_SEQ_MAX_BOUNDARIES; t += NT) {
-        s_bounds[t] = a.hdr->bounds[t];
-        s_cell[t] = reinterpret_cast<const uint32_t*>(a.hdr->cell)[t];
-        s_bias[t] = t < nb ? a.bias[head * nb + t] * LOG2E : 0.f;
+    s_buckets.load(a.hdr);
+    if (wq == 0) {
+        s_bias[wh][lane] = wb.bias[0];
+        s_bias[wh][64 + lane] = wb.bias[1];
     }
-    for (int t = threadIdx.x; t < W * nb * HC; t += NT) s_hist[t] = 0.f;
+    for (int x = threadIdx.x; x < SH::WAVES * nb * cols; x += SH::WAVES * WAVE) s_hist[x] = 0.f;
     const float c2 = fabsf(a.scale) * LOG2E;
 
-    const LdsBuckets lb = {s_bounds, s_cell, a.cells != 0, a.n_bounds};
     for (int64_t item = blockIdx.x; item < grid.items; item += gridDim.x) {
         int64_t s;
         int len, tile;
-        if (!find_tile(a, grid, item, 32 * W, a.causal, s, len, tile, head == 0)) continue;
-        const int q0 = tile * 32 * W, w0 = q0 + 32 * w, my_q = w0 + (lane & 31), row = my_q < len ? my_q : len - 1;
-        const int end = a.causal ? (q0 + 32 * W < len ? q0 + 32 * W : len) : len;
+        if (!find_tile(a, grid, item, 32 * WQ, a.causal, s, len, tile, h0 == 0)) continue;
+        const int q0 = tile * 32 * WQ, w0 = q0 + 32 * wq, my_q = w0 + (lane & 31), row = my_q < len ? my_q : len - 1;
+        const int end = a.causal ? (q0 + 32 * WQ < len ? q0 + 32 * WQ : len) : len;
         const int my_end = w0 >= len ? 0 : (a.causal && w0 + 32 < end ? w0 + 32 : end);
         RowStage<T, D, NT, KT> st;
         KeySideStage side;
-        st.load(k, g, v, g, s, 0, end, a.key_off);
-        side.load(a, s, 0, end, KT);
+        st.load(k, g, v, g, s, 0, end, a.key_off, t);
+        side.load(a, s, 0, end, KT, t);
         ColFrag<T, D> qf, df;
         qf.load(q.at(s + row, head), half);
         df.load(dout.at(s + row, head), half);
+        const int32_t my_pos = a.pos[s + row];
+        float L = lse2[(int64_t)head * a.n_events + s + row];
+        if (my_q >= len || L == -INFINITY) L = INFINITY;        // p = 0
         float del = 0.f;
         {
             const float* o = out32 + ((s + row) * a.n_heads + head) * D;
@@ -85,48 +108,45 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(DQ_WAVES
                 }
             del += other_half(del);
         }
-        float L = lse2[(int64_t)head * a.n_events + s + row];
-        if (my_q >= len || L == -INFINITY) L = INFINITY;        // p = 0
-        if (my_q < len && half == 0) delta[(int64_t)head * a.n_events + s + my_q] = del;
+        if (my_q < len && half == 0 && live) delta[(int64_t)head * a.n_events + s + my_q] = del;
         if (a.scale < 0.f) qf.negate();
-        const int32_t my_pos = a.pos[s + row];
         const int32_t q_lo = half_min(my_pos), q_hi = half_max(my_pos);
         f32x16 acc[ND] = {};
-        __syncthreads();                        // the previous tile's LDS is no longer read
-        st.store(s_k[0], s_v[0]);
-        side.store(s_side, 0);
+        __syncthreads();                        // the previous item's LDS is no longer read
+        st.store(s_k[team][0], s_v[team][0], t);
+        side.store(s_side[team][0], t);
         __syncthreads();
-        for (int k0 = 0, b = 0; k0 < end; k0 += KT, b ^= 1) {
+        for (int k0 = 0, b = 0; k0 < end; k0 += KT, b ^= NB - 1) {
             if (k0 + KT < end) {
-                st.load(k, g, v, g, s, k0 + KT, end, a.key_off);
-                side.load(a, s, k0 + KT, end, KT);
+                st.load(k, g, v, g, s, k0 + KT, end, a.key_off, t);
+                side.load(a, s, k0 + KT, end, KT, t);
             }
-#pragma unroll
+            const KeySide<KT>& ks = s_side[team][b];
+#pragma unroll 1
             for (int u = 0; u < NS; ++u) {
                 const int k1 = k0 + 32 * u;
-                if (k1 >= my_end) continue;
-                f32x16 x = mma_rows<T, D>(s_k[b], 32 * u, qf, f32x16{});
-                const f32x16 dp = mma_rows<T, D>(s_v[b], 32 * u, df, f32x16{});
+                if (k1 >= my_end) break;
                 TileBuckets<true> tb;
-                tb.set(wb, q_lo, q_hi, s_side.range[b][u]);
+                tb.set(wb, q_lo, q_hi, ks.range[u]);
+                if (tb.many) {
+                    if (SH::TEAM == 1 && WH > 1) __syncthreads();
+                    tb.find_pairs(s_pairs[wq][u], wh, WH, s_buckets, a.n_bounds, a.cells, ks.pos + 32 * u, my_pos);
+                    if (WH > 1) __syncthreads();
+                    else wave_lds_sync();
+                }
+                f32x16 x = mma_rows<T, D>(s_k[team][b], 32 * u, qf, f32x16{});
+                const f32x16 dp = mma_rows<T, D>(s_v[team][b], 32 * u, df, f32x16{});
                 int idx[16];
                 if (tb.lo == tb.hi) {
                     const float b0 = wb.value(tb.lo) - L;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) x[r] = __builtin_fmaf(x[r], c2, b0);
                 } else {
-                    tb.index(idx, wb, lb, s_side.pos[b] + 32 * u, my_pos);
+                    tb.index(idx, wb, s_pairs[wq][u], ks.pos + 32 * u, my_pos);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) x[r] = __builtin_fmaf(x[r], c2, -L) + s_bias[idx[r]];
+                    for (int r = 0; r < 16; ++r) x[r] = __builtin_fmaf(x[r], c2, s_bias[wh][idx[r]] - L);
                 }
-                if (__builtin_amdgcn_readfirstlane((uint32_t)(s_side.hidden[b] >> (32 * u)))) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const f32x4 mk = *reinterpret_cast<const f32x4*>(&s_side.mask[b][32 * u + 8 * j + 4 * half]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[4 * j + i] += mk[i];
-                    }
-                }
+                hide(x, ks.hidden[u], ks.mask + 32 * u);
                 if (a.causal && k1 + 31 > w0) {
                     const int lim = my_q - k1 - 4 * half;
 #pragma unroll
@@ -138,157 +158,166 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(DQ_WAVES
                     float sum = x[0];
 #pragma unroll
                     for (int r = 1; r < 16; ++r) sum += x[r];
-                    sum += other_half(sum);
-                    if (half == 0) lds_add(hist + tb.lo * HC, sum);
-                } else if (half == 0) {
+                    add_bucket(hist, cols, tb.lo, sum);
+                } else if (tb.hi - tb.lo < SUMS) {
+#pragma unroll 1
+                    for (int bk = tb.lo; bk <= tb.hi; ++bk) {
+                        float sum = 0.f;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) lds_add(hist + idx[r] * HC, x[r]);
+                        for (int r = 0; r < 16; ++r) sum += idx[r] == bk ? x[r] : 0.f;
+                        add_bucket(hist, cols, bk, sum);
+                    }
                 } else {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) lds_add(hist + idx[r] * HC, x[r]);
+                    add_pairs(hist, cols, idx, x);
                 }
                 RowOperand<T> ds;
                 ds.set(x);
 #pragma unroll
-                for (int dt = 0; dt < ND; ++dt) acc[dt] = mma_over_rows<D>(s_k[b], 32 * u, dt, ds, acc[dt]);
+                for (int dt = 0; dt < ND; ++dt) acc[dt] = mma_over_rows<D>(s_k[team][b], 32 * u, dt, ds, acc[dt]);
             }
             if (k0 + KT < end) {
-                st.store(s_k[b ^ 1], s_v[b ^ 1]);
-                side.store(s_side, b ^ 1);
-                __syncthreads();
+                if (SH::TEAM == 1) wave_lds_sync();
+                st.store(s_k[team][b ^ (NB - 1)], s_v[team][b ^ (NB - 1)], t);
+                side.store(s_side[team][b ^ (NB - 1)], t);
+                team_sync<SH::TEAM>();
             }
         }
-        if (my_q < len) {
+        if (my_q < len && live) {
             T* dst = dq.at(s + my_q, head);
 #pragma unroll
             for (int dt = 0; dt < ND; ++dt) store_column(dst + 32 * dt, acc[dt], a.scale);
         }
     }
     __syncthreads();
-    for (int t = threadIdx.x; t < nb; t += NT) {
+    // a head's sums: over its WQ waves and their columns, in a fixed order
+    for (int x = threadIdx.x; x < WH * nb; x += SH::WAVES * WAVE) {
+        const int hh = x / nb, bk = x % nb;
+        if (h0 + hh >= a.n_heads) break;
         float sum = 0.f;
-        for (int x = 0; x < W; ++x)
-            for (int c = 0; c < HC; ++c) sum += s_hist[(x * nb + t) * HC + ((c + t) & (HC - 1))];
-        part[((int64_t)head * gridDim.x + blockIdx.x) * nb + t] = sum;
+        for (int y = 0; y < WQ; ++y)
+            for (int c = 0; c < cols; ++c) sum += s_hist[((y * WH + hh) * nb + bk) * cols + ((c + bk) & (cols - 1))];
+        part[((int64_t)(h0 + hh) * nb + bk) * gridDim.x + blockIdx.x] = sum;
     }
 }
 
 // The blocks' bucket sums, added in 64 bits in a fixed order: one block per
-// head, 8 threads per bucket.
-__global__ __launch_bounds__(1024) void k_attn_dbias(const float* part, int blocks, int nb, float* dbias) {
-    __shared__ double s[8][RSE_SEQ_MAX_BOUNDARIES + 1];
-    const int h = blockIdx.x, b = threadIdx.x & 127, p = threadIdx.x >> 7;
+// head and bucket.
+__global__ __launch_bounds__(256) void k_attn_dbias(const float* part, int blocks, float* dbias) {
+    __shared__ double s[4];
+    const float* p = part + (int64_t)blockIdx.x * blocks;
     double t = 0.0;
-    if (b < nb)
-        for (int x = p; x < blocks; x += 8) t += part[((int64_t)h * blocks + x) * nb + b];
-    s[p][b] = t;
+    for (int x = threadIdx.x; x < blocks; x += 256) t += p[x];
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) t += shfl_xor_f64(t, m);
+    if (lane_id() == 0) s[threadIdx.x / WAVE] = t;
     __syncthreads();
-    if (p == 0 && b < nb) {
-        for (int x = 1; x < 8; ++x) t += s[x][b];
-        dbias[h * nb + b] = (float)t;
-    }
+    if (threadIdx.x == 0) dbias[blockIdx.x] = (float)(s[0] + s[1] + s[2] + s[3]);
 }
 
-// dk and dv, keys as columns: per tile of queries of each head of the group
-// S = Q K^T and dP = dO V^T, dV^T += dO^T P, dK^T += Q^T dS.
-template <typename T, int D, int W, int KT>
-__global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(DKV_WAVES<T, D>))) void k_attn_dkv(SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k, Rows<const T> v,
-                                                     const float* lse2, const float* delta, Rows<const T> dout,
-                                                     Rows<T> dk, Rows<T> dv) {
-    using TL = Tile<T, D>;
-    constexpr int NT = W * 64, CH = TL::CH, NS = KT / 32, ND = D / 32, NBP = RSE_SEQ_MAX_BOUNDARIES + 1;
-    __shared__ u32x4 s_q[2][KT * CH], s_d[2][KT * CH];
-    __shared__ float s_lse[2][KT], s_del[2][KT];
-    __shared__ int32_t s_pos[2][KT];
-    __shared__ int32_t s_range[2][NS][2];
-    __shared__ int32_t s_bounds[NBP];
-    __shared__ float s_bias[2][NBP];
-    __shared__ uint32_t s_cell[128];
-    const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5;
-    const int n_kv = a.n_heads / a.group, g = blockIdx.x % n_kv, nb = a.n_bounds + 1;
+// dk and dv, keys as columns: per tile of queries and head of the group
+// S = Q K^T and dP = dO V^T, dV^T += dO^T P, dK^T += Q^T dS.  WQ waves take
+// tiles of keys, WH waves key heads; the buckets of a tile are looked up once
+// for the heads of the group.
+template <typename T, int D, typename SH>
+__global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(DKV_WAVES<T, D>))) void k_attn_dkv(
+    SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k, Rows<const T> v, const float* lse2, const float* delta,
+    Rows<const T> dout, Rows<T> dk, Rows<T> dv) {
+    constexpr int CH = SH::CH, KT = SH::KT, NS = SH::NS, NB = SH::NB, NT = SH::NT, WH = SH::WH, WQ = SH::WQ, ND = D / 32,
+                  NBP = RSE_SEQ_MAX_BOUNDARIES + 1;
+    __shared__ u32x4 s_q[SH::TEAMS][NB][KT * CH], s_d[SH::TEAMS][NB][KT * CH];
+    __shared__ u32x4 s_pairs[WQ][NS][WAVE];
+    __shared__ float s_lse[SH::TEAMS][NB][KT], s_del[SH::TEAMS][NB][KT];
+    __shared__ int32_t s_pos[SH::TEAMS][NB][KT];
+    __shared__ int32_t s_range[SH::TEAMS][NB][NS][2];
+    __shared__ LdsBuckets s_buckets;
+    __shared__ float s_bias[SH::TEAMS][NB][NBP];
+    const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5, wh = w % WH, wq = w / WH;
+    const int team = w / SH::TEAM, t = threadIdx.x % NT;
+    const int n_kv = a.n_heads / a.group, gblocks = (n_kv + WH - 1) / WH, g0 = blockIdx.x % gblocks * WH, nb = a.n_bounds + 1;
+    const bool live = g0 + wh < n_kv;
+    const int g = live ? g0 + wh : n_kv - 1;
     int64_t s;
     int len, tile;
-    if (!find_tile(a, grid, blockIdx.x / n_kv, 32 * W, false, s, len, tile, false)) return;
-    const int j0 = tile * 32 * W, w0 = j0 + 32 * w, my_k = w0 + (lane & 31), row = my_k < len ? my_k : len - 1;
-    const bool seen = !(a.key_off && a.key_off[s + row] < 0);
+    if (!find_tile(a, grid, blockIdx.x / gblocks, 32 * WQ, false, s, len, tile, false)) return;
+    const int j0 = tile * 32 * WQ, w0 = j0 + 32 * wq, my_k = w0 + (lane & 31), row = my_k < len ? my_k : len - 1;
     const int first = a.causal ? j0 / KT * KT : 0;                  // queries of the block: first .. len
-    const int per_head = (len - first + KT - 1) / KT, total = per_head * a.group;
-
-    for (int t = threadIdx.x; t < NBP; t += NT) {
-        s_bounds[t] = a.hdr->bounds[t];
-        s_cell[t] = reinterpret_cast<const uint32_t*>(a.hdr->cell)[t];
-    }
-    ColFrag<T, D> kf, vf;
-    kf.load(k.at(s + row, g), half);
-    vf.load(v.at(s + row, g), half);
-    if (a.scale < 0.f) kf.negate();
-    const float c2 = fabsf(a.scale) * LOG2E;
-    const int32_t my_pos = a.pos[s + row];
-    const int32_t k_lo = half_min(my_pos), k_hi = half_max(my_pos);
-    const LdsBuckets lb = {s_bounds, s_cell, a.cells != 0, a.n_bounds};
-    WaveBuckets wb;
-    wb.load(a.hdr, a.bias, a.n_bounds, LOG2E);
+    const int total = (len - first + KT - 1) / KT * a.group;       // tiles of them, each for every head
 
     RowStage<T, D, NT, KT> st;
     int32_t rp = 0;
-    float rl = 0.f, rd = 0.f, rb[NBP / NT + 1];
+    float rl = 0.f, rd = 0.f, rb[(NBP + NT - 1) / NT];
+    bool rin = false;
     auto load = [&](int it) {
-        const int h = g * a.group + it / per_head, i0 = first + it % per_head * KT;
-        st.load(q, h, dout, h, s, i0, len, nullptr);
-        if (threadIdx.x < KT) {
-            const int kk = i0 + (int)threadIdx.x;
+        const int h = g * a.group + it % a.group, i0 = first + it / a.group * KT;
+        st.load(q, h, dout, h, s, i0, len, nullptr, t);
+        if (t < KT) {
+            const int kk = i0 + t;
             const int64_t j = s + (kk < len ? kk : len - 1);
             rp = a.pos[j];
             rl = lse2[(int64_t)h * a.n_events + j];
-            rd = kk < len ? delta[(int64_t)h * a.n_events + j] : 0.f;
-            if (kk >= len || rl == -INFINITY) rl = INFINITY;        // p = 0
+            rd = delta[(int64_t)h * a.n_events + j];
+            rin = kk < len;
         }
+        if (it == 0 || a.group > 1)
 #pragma unroll
-        for (int i = 0; i * NT < NBP; ++i) {
-            const int t = i * NT + (int)threadIdx.x;
-            rb[i] = t < nb ? a.bias[h * nb + t] * LOG2E : 0.f;
-        }
+            for (int i = 0; i * NT < NBP; ++i) rb[i] = i * NT + t < nb ? a.bias[h * nb + i * NT + t] : 0.f;
     };
     auto store = [&](int b) {
-        st.store(s_q[b], s_d[b]);
-        if (w == 0) {
+        st.store(s_q[team][b], s_d[team][b], t);
+        if (t < WAVE) {
             const int32_t lo = half_min(rp), hi = half_max(rp);
-            if (lane < KT) {
-                s_pos[b][lane] = rp;
-                s_lse[b][lane] = rl;
-                s_del[b][lane] = rd;
-                if ((lane & 31) == 0) {
-                    s_range[b][lane / 32][0] = lo;
-                    s_range[b][lane / 32][1] = hi;
+            if (t < KT) {
+                s_pos[team][b][t] = rp;
+                s_lse[team][b][t] = rin && rl > -INFINITY ? rl : INFINITY;      // else p = 0
+                s_del[team][b][t] = rin ? rd : 0.f;
+                if ((t & 31) == 0) {
+                    s_range[team][b][t / 32][0] = lo;
+                    s_range[team][b][t / 32][1] = hi;
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i * NT < NBP; ++i) {
-            const int t = i * NT + (int)threadIdx.x;
-            if (t < NBP) s_bias[b][t] = rb[i];
-        }
+        for (int i = 0; i * NT < NBP; ++i)
+            if (i * NT + t < NBP) s_bias[team][b][i * NT + t] = rb[i] * LOG2E;
     };
 
-    f32x16 ak[ND] = {}, av[ND] = {};
     load(0);
+    ColFrag<T, D> kf, vf;
+    kf.load(k.at(s + row, g), half);
+    vf.load(v.at(s + row, g), half);
+    const bool seen = !(a.key_off && a.key_off[s + row] < 0);
+    const int32_t my_pos = a.pos[s + row];
+    s_buckets.load(a.hdr);
+    WaveBuckets wb;
+    wb.load(a.hdr, a.bias, a.n_bounds, LOG2E);
+    if (a.scale < 0.f) kf.negate();
+    const float c2 = fabsf(a.scale) * LOG2E;
+    const int32_t k_lo = half_min(my_pos), k_hi = half_max(my_pos);
+    f32x16 ak[ND] = {}, av[ND] = {};
     store(0);
     __syncthreads();
-    for (int it = 0, b = 0; it < total; ++it, b ^= 1) {
-        const int i0 = first + it % per_head * KT;
+    for (int it = 0, b = 0; it < total; ++it, b ^= NB - 1) {
+        const int i0 = first + it / a.group * KT;
         if (it + 1 < total) load(it + 1);
-        if (w0 < len && (!a.causal || i0 + KT - 1 >= w0)) {
-            wb.bias[0] = s_bias[b][lane];
-            wb.bias[1] = s_bias[b][64 + lane];
-#pragma unroll
+        if (w0 < len) {
+            wb.bias[0] = s_bias[team][b][lane];
+            wb.bias[1] = s_bias[team][b][64 + lane];
+#pragma unroll 1
             for (int u = 0; u < NS; ++u) {
                 const int i1 = i0 + 32 * u;
-                if (i1 >= len || (a.causal && i1 + 31 < w0)) continue;
-                f32x16 x = mma_rows<T, D>(s_q[b], 32 * u, kf, f32x16{});
-                f32x16 dp = mma_rows<T, D>(s_d[b], 32 * u, vf, f32x16{});
+                if (i1 >= len) break;
+                if (a.causal && i1 + 31 < w0) continue;
                 TileBuckets<false> tb;
-                tb.set(wb, k_lo, k_hi, s_range[b][u]);
-                x = tb.logits(x, c2, 0.f, wb, lb, s_bias[b], s_pos[b] + 32 * u, my_pos);
+                tb.set(wb, k_lo, k_hi, s_range[team][b][u]);
+                if (tb.many && it % a.group == 0) {
+                    if (WH > 1) __syncthreads();
+                    tb.find_pairs(s_pairs[wq][u], wh, WH, s_buckets, a.n_bounds, a.cells, s_pos[team][b] + 32 * u, my_pos);
+                    if (WH > 1) __syncthreads();
+                    else wave_lds_sync();
+                }
+                f32x16 x = mma_rows<T, D>(s_q[team][b], 32 * u, kf, f32x16{});
+                f32x16 dp = mma_rows<T, D>(s_d[team][b], 32 * u, vf, f32x16{});
+                x = tb.logits(x, c2, 0.f, wb, s_pairs[wq][u], s_bias[team][b], s_pos[team][b] + 32 * u, my_pos);
                 if (a.causal && i1 < w0 + 31) {
                     const int lim = my_k - i1 - 4 * half;
 #pragma unroll
@@ -296,8 +325,8 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(DKV_WAVE
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const f32x4 L = *reinterpret_cast<const f32x4*>(&s_lse[b][32 * u + 8 * j + 4 * half]);
-                    const f32x4 de = *reinterpret_cast<const f32x4*>(&s_del[b][32 * u + 8 * j + 4 * half]);
+                    const f32x4 L = *reinterpret_cast<const f32x4*>(&s_lse[team][b][32 * u + 8 * j + 4 * half]);
+                    const f32x4 de = *reinterpret_cast<const f32x4*>(&s_del[team][b][32 * u + 8 * j + 4 * half]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         x[4 * j + i] = __builtin_amdgcn_exp2f(x[4 * j + i] - L[i]);
@@ -309,17 +338,18 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(DKV_WAVE
                 ds.set(dp);
 #pragma unroll
                 for (int dt = 0; dt < ND; ++dt) {
-                    av[dt] = mma_over_rows<D>(s_d[b], 32 * u, dt, p, av[dt]);
-                    ak[dt] = mma_over_rows<D>(s_q[b], 32 * u, dt, ds, ak[dt]);
+                    av[dt] = mma_over_rows<D>(s_d[team][b], 32 * u, dt, p, av[dt]);
+                    ak[dt] = mma_over_rows<D>(s_q[team][b], 32 * u, dt, ds, ak[dt]);
                 }
             }
         }
         if (it + 1 < total) {
-            store(b ^ 1);
-            __syncthreads();
+            if (SH::TEAM == 1) wave_lds_sync();
+            store(b ^ (NB - 1));
+            team_sync<SH::TEAM>();
         }
     }
-    if (my_k < len) {
+    if (my_k < len && live) {
         T* pk = dk.at(s + my_k, g);
         T* pv = dv.at(s + my_k, g);
 #pragma unroll
@@ -334,7 +364,7 @@ __global__ __launch_bounds__(W * 64) __attribute__((amdgpu_waves_per_eu(DKV_WAVE
 // ------------------------------------------------------------------ host --
 // Blocks of k_attn_dq over all heads: enough to fill the GPU several times
 // over; more would only add partial bucket sums.
-constexpr int64_t DQ_BLOCKS = 4096;
+constexpr int64_t DQ_BLOCKS = 2048;
 
 struct BwdWs {
     float* delta;
@@ -343,19 +373,22 @@ struct BwdWs {
     int64_t blocks;              // of k_attn_dq, per head
 };
 
-// Events of a block's tile.
-int tile_events(const rse_seqattn* a, int64_t max_len) {
-    return by_type(a, [&](auto t, auto d) {
-        using S = Shape<decltype(t), decltype(d)::value>;
-        return 32 * (max_len <= SHORT ? S::W_SHORT : S::W_LONG);
-    });
+// The blocks of k_attn_dq, by the rules of the forward.
+struct DqForm {
+    int wh, wq;
+};
+DqForm dq_form(const rse_seqattn* a, int64_t max_len) {
+    const bool brief = by_type(a, [&](auto t, auto d) { return (int)short_form<decltype(t), decltype(d)::value>(max_len); });
+    if (brief) return {a->n_heads > 1 ? 4 : 1, 1};
+    return a->n_heads / a->n_kv_heads % 4 == 0 ? DqForm{4, 1} : DqForm{1, 4};
 }
 
 BwdWs bwd_ws(const rse_seqattn* a, int64_t n, int64_t batch, int64_t max_len, void* base) {
     BwdWs w;
-    const int64_t most = DQ_BLOCKS / a->n_heads > 16 ? DQ_BLOCKS / a->n_heads : 16;
-    w.blocks = tile_grid(n, batch, max_len, tile_events(a, max_len)).items;
-    if (w.blocks > most) w.blocks = most;
+    const DqForm f = dq_form(a, max_len);
+    w.blocks = tile_grid(n, batch, max_len, 32 * f.wq).items;
+    const int64_t most = DQ_BLOCKS * f.wh / a->n_heads;
+    if (w.blocks > most) w.blocks = most > 16 ? most : 16;
     Carver c(base);
     w.delta = c.take<float>((size_t)a->n_heads * n);
     w.part = c.take<float>((size_t)a->n_heads * w.blocks * (a->n_bounds + 1));
@@ -363,21 +396,25 @@ BwdWs bwd_ws(const rse_seqattn* a, int64_t n, int64_t batch, int64_t max_len, vo
     return w;
 }
 
-template <typename T, int D, int W, int KT>
+template <typename T, int D, int TEAM, int WH, int WQ, int KH, int KQ>
 int run_bwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v, const Saved& sv,
-              const rse_seq_rows* dout, const rse_seq_rows* dq, const rse_seq_rows* dk, const rse_seq_rows* dv,
-              float* dbias, const BwdWs& w, hipStream_t s) {
-    const int nb = a.n_bounds + 1;
-    const TileGrid tg = tile_grid(a.n_events, a.batch, a.max_len, 32 * W);
-    const int64_t dkv = tg.items * (a.n_heads / a.group);
-    if (dkv > INT32_MAX) return RSE_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((k_attn_dq<T, D, W, KT>), dim3((unsigned)w.blocks, a.n_heads), dim3(W * WAVE),
-                       W * nb * HC * sizeof(float), s, a, tg, rows_view<const T>(q), rows_view<const T>(k),
-                       rows_view<const T>(v), sv.lse2, sv.out32, rows_view<const T>(dout), rows_view<T>(dq), w.delta, w.part);
+            const rse_seq_rows* dout, const rse_seq_rows* dq, const rse_seq_rows* dk, const rse_seq_rows* dv,
+            float* dbias, const BwdWs& w, hipStream_t s) {
+    using QS = Shape<T, D, TEAM, WH, WQ>;
+    using KS = Shape<T, D, TEAM, KH, KQ>;
+    const int nb = a.n_bounds + 1, n_kv = a.n_heads / a.group;
+    const int cols = nb <= 32 ? 64 : 32;        // at most 32 KiB a block of 4 waves up to 64 buckets, 64 KiB past that
+    const TileGrid tq = tile_grid(a.n_events, a.batch, a.max_len, 32 * WQ);
+    const TileGrid tk = tile_grid(a.n_events, a.batch, a.max_len, 32 * KQ);
+    const int64_t blocks = tk.items * ((n_kv + KH - 1) / KH);
+    if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL((k_attn_dq<T, D, QS>), dim3((unsigned)w.blocks, (a.n_heads + WH - 1) / WH), dim3(QS::WAVES * WAVE),
+                       QS::WAVES * nb * cols * sizeof(float), s, a, tq, rows_view<const T>(q), rows_view<const T>(k),
+                       rows_view<const T>(v), sv.lse2, sv.out32, rows_view<const T>(dout), rows_view<T>(dq), w.delta, w.part, cols);
     int rc = launch_status();
     if (rc) return rc;
-    hipLaunchKernelGGL(k_attn_dbias, dim3(a.n_heads), dim3(1024), 0, s, w.part, (int)w.blocks, nb, dbias);
-    hipLaunchKernelGGL((k_attn_dkv<T, D, W, KT>), dim3((unsigned)dkv), dim3(W * WAVE), 0, s, a, tg,
+    hipLaunchKernelGGL(k_attn_dbias, dim3(a.n_heads * nb), dim3(256), 0, s, w.part, (int)w.blocks, dbias);
+    hipLaunchKernelGGL((k_attn_dkv<T, D, KS>), dim3((unsigned)blocks), dim3(KS::WAVES * WAVE), 0, s, a, tk,
                        rows_view<const T>(q), rows_view<const T>(k), rows_view<const T>(v), sv.lse2, w.delta,
                        rows_view<const T>(dout), rows_view<T>(dk), rows_view<T>(dv));
     return launch_status();
@@ -405,7 +442,7 @@ int seq_attention_bwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
     if (ws_bytes < w.bytes) return RSE_ERR_WORKSPACE;
     hipStream_t s = as_stream(stream);
     if (batch->n_events == 0) {
-        hipLaunchKernelGGL(k_attn_dbias, dim3(attn->n_heads), dim3(1024), 0, s, w.part, 0, attn->n_bounds + 1, d_dbias);
+        hipLaunchKernelGGL(k_attn_dbias, dim3(attn->n_heads * (attn->n_bounds + 1)), dim3(256), 0, s, w.part, 0, d_dbias);
         return launch_status();
     }
     for (const rse_seq_rows* r : {q, k, v, dout, dq, dk, dv})
@@ -417,10 +454,14 @@ int seq_attention_bwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
     return by_type(attn, [&](auto t, auto d) {
         using T = decltype(t);
         constexpr int D = decltype(d)::value;
-        using S = Shape<T, D>;
-        if (a.max_len <= SHORT)
-            return run_bwd<T, D, S::W_SHORT, S::KT_SHORT>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
-        return run_bwd<T, D, S::W_LONG, S::KT_LONG>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
+        if constexpr (short_form<T, D>(0))
+            if (short_form<T, D>(a.max_len)) {
+                if (a.n_heads == 1) return run_bwd<T, D, 1, 1, 1, 1, 1>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
+                if (attn->n_kv_heads == 1) return run_bwd<T, D, 1, 4, 1, 1, 1>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
+                return run_bwd<T, D, 1, 4, 1, 4, 1>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
+            }
+        if (a.group % 4 == 0) return run_bwd<T, D, 4, 4, 1, 1, 4>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
+        return run_bwd<T, D, 4, 1, 4, 1, 4>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
     });
 }
 

@@ -247,44 +247,36 @@ constexpr int CHAIN = 6;
 
 __device__ __forceinline__ int32_t sat_add(int32_t a, int32_t b) { return __builtin_elementwise_add_sat(a, b); }
 
-// What a kernel holds in LDS to look buckets up event by event.
+// What a kernel holds in LDS to look buckets up pair by pair.
 struct LdsBuckets {
-    const int32_t* bounds;
-    const uint32_t* cell;
-    bool cells;
-    int n;
-    __device__ __forceinline__ int find(int32_t d) const {
-        return cells ? seq_bucket_cell(reinterpret_cast<const uint8_t*>(cell), bounds, n, d) : seq_bucket(bounds, n, d);
+    int32_t bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
+    uint32_t cell[128];
+    __device__ __forceinline__ void load(const SeqHeader* h) {
+        for (int t = threadIdx.x; t <= RSE_SEQ_MAX_BOUNDARIES; t += blockDim.x) {
+            bounds[t] = h->bounds[t];
+            cell[t] = reinterpret_cast<const uint32_t*>(h->cell)[t];
+        }
     }
 };
 
-// Positions of the 16 rows of a lane's half.
-__device__ __forceinline__ void row_positions(int32_t (&p)[16], const int32_t* row_pos) {
-    const int h = lane_id() >> 5;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const i32x4 v = *reinterpret_cast<const i32x4*>(row_pos + 8 * j + 4 * h);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[4 * j + i] = v[i];
-    }
-}
-
 // The rows of a 32 x 32 tile span positions range[0] .. range[1]; its pairs'
 // distances the buckets lo .. hi.  column_first: distance = column - row.
-//
-// A boundary is passed by the rows on one side of a position that is the
-// lane's own (col_pos -/+ the boundary, saturated): one comparison per pair
-// and boundary.  A saturated threshold is met wrongly only by a row at the
-// very end of int32, so such tiles are looked up pair by pair.
+//  - one bucket (most tiles of a long history): the bias is a constant;
+//  - up to CHAIN boundaries: each is passed by the rows on one side of a
+//    position that is the lane's own (col_pos -/+ the boundary, saturated),
+//    one comparison per pair and boundary.  A saturated threshold is met
+//    wrongly only by a row at the very end of int32: such tiles go with
+//  - many: every pair is looked up (find_pairs), into LDS as bytes in the
+//    order of the registers, so that the heads share the work.
 template <bool column_first>
 struct TileBuckets {
     int lo, hi;
-    bool chain;
+    bool many;
     __device__ __forceinline__ void set(const WaveBuckets& wb, int32_t col_lo, int32_t col_hi, const int32_t* range) {
         const int32_t r_lo = __builtin_amdgcn_readfirstlane(range[0]), r_hi = __builtin_amdgcn_readfirstlane(range[1]);
         lo = wb.bucket(column_first ? seq_dist(col_lo, r_hi) : seq_dist(r_lo, col_hi));
         hi = wb.bucket(column_first ? seq_dist(col_hi, r_lo) : seq_dist(r_hi, col_lo));
-        chain = hi - lo <= CHAIN && (column_first ? r_lo > INT32_MIN : r_hi < INT32_MAX);
+        many = lo != hi && (hi - lo > CHAIN || (column_first ? r_lo == INT32_MIN : r_hi == INT32_MAX));
     }
     __device__ __forceinline__ int32_t threshold(const WaveBuckets& wb, int m, int32_t col_pos) const {
         const int32_t edge = wb.boundary(m);
@@ -293,21 +285,48 @@ struct TileBuckets {
     static __device__ __forceinline__ bool passed(int32_t row, int32_t threshold) {
         return column_first ? row <= threshold : row >= threshold;
     }
-    static __device__ __forceinline__ int32_t dist(int32_t row, int32_t col) {
-        return column_first ? seq_dist(col, row) : seq_dist(row, col);
+    // Of `many` tiles: registers 4 j .. 4 j + 3 for j = first, + step, ... < 4.
+    static __device__ __forceinline__ void find_pairs(u32x4* bytes, int first, int step, const LdsBuckets& lb, int n, bool cells,
+                                                      const int32_t* row_pos, int32_t col_pos) {
+        const int lane = lane_id(), h = lane >> 5;
+        uint32_t* mine = reinterpret_cast<uint32_t*>(bytes + lane);
+#pragma unroll 1
+        for (int j = first; j < 4; j += step) {
+            const i32x4 p = *reinterpret_cast<const i32x4*>(row_pos + 8 * j + 4 * h);
+            uint32_t packed = 0;
+            if (cells) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    packed |= seq_bucket_cell(reinterpret_cast<const uint8_t*>(lb.cell), lb.bounds, n,
+                                              column_first ? seq_dist(col_pos, p[i]) : seq_dist(p[i], col_pos)) << (8 * i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    packed |= seq_bucket(lb.bounds, n, column_first ? seq_dist(col_pos, p[i]) : seq_dist(p[i], col_pos)) << (8 * i);
+            }
+            mine[j] = packed;
+        }
+    }
+    static __device__ __forceinline__ int pair(const u32x4& bytes, int r) { return (bytes[r >> 2] >> (8 * (r & 3))) & 255; }
+    static __device__ __forceinline__ void positions(int32_t (&p)[16], const int32_t* row_pos) {
+        const int h = lane_id() >> 5;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const i32x4 v = *reinterpret_cast<const i32x4*>(row_pos + 8 * j + 4 * h);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[4 * j + i] = v[i];
+        }
     }
     // s c + bias + shift of every pair
-    __device__ __forceinline__ f32x16 logits(f32x16 s, float c, float shift, const WaveBuckets& wb, const LdsBuckets& lb,
+    __device__ __forceinline__ f32x16 logits(f32x16 s, float c, float shift, const WaveBuckets& wb, const u32x4* bytes,
                                              const float* s_bias, const int32_t* row_pos, int32_t col_pos) const {
         if (lo == hi) {
             const float b = wb.value(lo) + shift;
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], c, b);
-            return s;
-        }
-        int32_t p[16];
-        row_positions(p, row_pos);
-        if (chain) {
+        } else if (!many) {
+            int32_t p[16];
+            positions(p, row_pos);
             float b[16];
             const float b0 = wb.value(lo) + shift;
             {
@@ -316,6 +335,7 @@ struct TileBuckets {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) b[r] = passed(p[r], th) ? bm : b0;
             }
+#pragma unroll 1
             for (int m = lo + 1; m < hi; ++m) {
                 const int32_t th = threshold(wb, m, col_pos);
                 const float bm = wb.value(m + 1) + shift;
@@ -325,41 +345,38 @@ struct TileBuckets {
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], c, b[r]);
         } else {
+            const u32x4 at = bytes[lane_id()];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                s[r] = __builtin_fmaf(s[r], c, shift) + s_bias[lb.find(dist(p[r], col_pos))];
-                if ((r & 3) == 3) __builtin_amdgcn_sched_barrier(0);    // four lookups in flight, for the registers
-            }
+            for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], c, s_bias[pair(at, r)] + shift);
         }
         return s;
     }
     // bucket of every pair (lo < hi)
-    __device__ __forceinline__ void index(int (&idx)[16], const WaveBuckets& wb, const LdsBuckets& lb, const int32_t* row_pos,
+    __device__ __forceinline__ void index(int (&idx)[16], const WaveBuckets& wb, const u32x4* bytes, const int32_t* row_pos,
                                           int32_t col_pos) const {
-        int32_t p[16];
-        row_positions(p, row_pos);
-        if (chain) {
+        if (!many) {
+            int32_t p[16];
+            positions(p, row_pos);
 #pragma unroll
             for (int r = 0; r < 16; ++r) idx[r] = lo;
+#pragma unroll 1
             for (int m = lo; m < hi; ++m) {
                 const int32_t th = threshold(wb, m, col_pos);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) idx[r] += passed(p[r], th);
             }
         } else {
+            const u32x4 at = bytes[lane_id()];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                idx[r] = lb.find(dist(p[r], col_pos));
-                if ((r & 3) == 3) __builtin_amdgcn_sched_barrier(0);
-            }
+            for (int r = 0; r < 16; ++r) idx[r] = pair(at, r);
         }
     }
 };
 
 // ------------------------------------------------------------- tile finder --
 // Tiles of tq events of every sequence, numbered in one of two ways.
-//  - per_seq > 0 (no sequence has more tiles): item t * batch + b is tile t of
-//    sequence b; idle where the sequence is shorter.  No search, and tiles of
+//  - per_seq > 0 (no sequence has more tiles): items t * batch and on are the
+//    tiles t of the sequences; idle where the sequence is shorter.  No search, and tiles of
 //    equal index stand together, so that long work can start first.
 //  - per_seq = 0, where that would leave most items idle: sequence b has the
 //    numbers offsets[b] / tq + b and on, at least as many as its tiles, found
@@ -390,7 +407,8 @@ __device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, i
     int64_t b, t;
     if (g.per_seq) {
         t = item / a.batch;
-        b = item - t * a.batch;
+        b = item - t * a.batch + t % a.batch;           // a sequence's tiles on different XCDs
+        if (b >= a.batch) b -= a.batch;
         if (backwards) t = g.per_seq - 1 - t;
     } else {
         b = wave_last_le(a.batch, [&](int64_t x) { return a.offsets[x] / tq + x; }, item);
@@ -409,89 +427,123 @@ __device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, i
 }
 
 // ------------------------------------------------------------------ shapes --
-// Long sequences: blocks of 4 waves share tiles of 64 keys (two buffers of
-// two tensors: at most 64 KiB).  Up to SHORT events, where such a block would
-// mostly idle: as few waves as can hold the next tile's loads in registers.
+// A block's waves and what they share.  A team of waves stages tiles of rows
+// together; WH waves take heads side by side, WQ waves tiles of 32 columns.
+//  - long sequences: one team of 4, tiles of 64 rows (two buffers of two
+//    tensors: at most 64 KiB), either 4 column tiles of one head, or one
+//    column tile of 4 heads that share keys (equal work for every wave, and
+//    the buckets of a tile looked up once for the 4);
+//  - up to SHORT events, where such a block would mostly idle: every wave a
+//    team of its own with one buffer, 4 heads of one column tile side by side.
+//    Rows past 128 bytes do not pass through one wave's registers: long form.
 constexpr int64_t SHORT = 128;
-template <typename T, int D>
+template <typename T, int D, int TEAM_, int WH_, int WQ_>
 struct Shape {
+    static constexpr int TEAM = TEAM_, WH = WH_, WQ = WQ_, WAVES = WH * WQ, TEAMS = WAVES / TEAM;
     static constexpr int RB = D * (int)sizeof(T);       // bytes of a row
-    static constexpr int W_LONG = 4, KT_LONG = RB <= 256 ? 64 : 32;
-    static constexpr int W_SHORT = RB <= 128 ? 1 : (RB == 256 ? 2 : 4), KT_SHORT = 32;
+    static constexpr int KT = TEAM > 1 && RB <= 256 ? 64 : 32, NS = KT / 32, NB = TEAM > 1 ? 2 : 1;
+    static constexpr int CH = Tile<T, D>::CH, NT = TEAM * WAVE;
 };
+template <typename T, int D>
+constexpr bool short_form(int64_t max_len) { return max_len <= SHORT && D * sizeof(T) <= 128; }
+
+// Orders a team's LDS writes before its reads.
+template <int TEAM>
+__device__ __forceinline__ void team_sync() {
+    if (TEAM > 1) __syncthreads();
+    else wave_lds_sync();
+}
 
 // ----------------------------------------------------------------- staging --
 // Rows k0 .. k0 + KT - 1 of two tensors on their way to LDS: loaded into
-// registers (thread t: chunk t % CH of rows t / CH, + NT / CH, ...), stored
-// after the current tile's work.  Hidden rows and rows past the end are
-// stored as zeros, whatever they hold.
+// registers (thread t of the team: chunk t % CH of rows t / CH, + NT / CH,
+// ...), stored after the current tile's work.  Hidden rows and rows past the
+// end are stored as zeros, whatever they hold.  Nothing loaded is looked at
+// before the store: a wait there would end the overlap.
 template <typename T, int D, int NT, int KT>
 struct RowStage {
     using TL = Tile<T, D>;
     static constexpr int CH = TL::CH, PER = KT * CH / NT, STEP = NT / CH;
-    static_assert(KT * CH % NT == 0, "tile shape");
+    static_assert(KT * CH % NT == 0 && NT % CH == 0, "tile shape");
     u32x4 x[PER], y[PER];
-    bool hid[PER];
+    int32_t off[PER];                           // high half of the row's key_off, 0 without one
+    int left;                                   // rows from the thread's first to the end
     __device__ __forceinline__ void load(const Rows<const T>& X, int hx, const Rows<const T>& Y, int hy, int64_t s, int k0,
-                                         int end, const int64_t* key_off) {
-        const int row = threadIdx.x / CH, c = threadIdx.x % CH;
+                                         int end, const int64_t* key_off, int t) {
+        const int row = t / CH, c = t % CH;
+        left = end - k0 - row;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int kk = k0 + row + i * STEP;
             const int64_t j = s + (kk < end ? kk : end - 1);
             x[i] = gload_u4(X.at(j, hx) + c * TL::EPC);
             y[i] = gload_u4(Y.at(j, hy) + c * TL::EPC);
-            hid[i] = kk >= end || (key_off && key_off[j] < 0);
+            off[i] = key_off ? reinterpret_cast<const int32_t*>(key_off + j)[1] : 0;
         }
     }
-    __device__ __forceinline__ void store(u32x4* sx, u32x4* sy) const {
-        const int row = threadIdx.x / CH, c = threadIdx.x % CH;
+    __device__ __forceinline__ void store(u32x4* sx, u32x4* sy, int t) const {
+        const int row = t / CH, c = t % CH;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int at = TL::chunk_at(row + i * STEP, c);
-            sx[at] = hid[i] ? u32x4{0, 0, 0, 0} : x[i];
-            sy[at] = hid[i] ? u32x4{0, 0, 0, 0} : y[i];
+            const bool z = i * STEP >= left || off[i] < 0;
+            sx[at] = z ? u32x4{0, 0, 0, 0} : x[i];
+            sy[at] = z ? u32x4{0, 0, 0, 0} : y[i];
         }
     }
 };
 
-// The events of a tile of keys on their way to LDS beside its rows (threads
-// 0 .. KT - 1): positions, which may be seen, and of each 32 of them the
-// lowest and highest position and whether any may not be seen.
+// The events of a tile of keys beside its rows (the team's first KT threads):
+// positions, which may be seen, and of each 32 of them the lowest and highest
+// position and whether any may not be seen.
 template <int KT>
 struct KeySide {
-    float mask[2][KT];
-    int32_t pos[2][KT];
-    int32_t range[2][KT / 32][2];
-    uint64_t hidden[2];                         // bit per event
+    float mask[KT];
+    int32_t pos[KT];
+    int32_t range[KT / 32][2];
+    uint32_t hidden[KT / 32];                   // bit per event
 };
 struct KeySideStage {
-    int32_t p;
-    bool see;
-    __device__ __forceinline__ void load(const SeqArgs& a, int64_t s, int k0, int end, int kt) {
-        if ((int)threadIdx.x < kt) {
-            const int kk = k0 + (int)threadIdx.x;
+    int32_t p, off;
+    bool in;
+    __device__ __forceinline__ void load(const SeqArgs& a, int64_t s, int k0, int end, int kt, int t) {
+        if (t < kt) {
+            const int kk = k0 + t;
             const int64_t j = s + (kk < end ? kk : end - 1);
             p = a.pos[j];
-            see = kk < end && !(a.key_off && a.key_off[j] < 0);
+            off = a.key_off ? reinterpret_cast<const int32_t*>(a.key_off + j)[1] : 0;
+            in = kk < end;
         }
     }
     template <int KT>
-    __device__ __forceinline__ void store(KeySide<KT>& ks, int b) const {
-        if (threadIdx.x >= WAVE) return;
-        const int lane = lane_id();
+    __device__ __forceinline__ void store(KeySide<KT>& ks, int t) const {
+        if (t >= WAVE) return;
+        const bool see = in && off >= 0;
         const int32_t lo = half_min(p), hi = half_max(p);
-        const uint64_t hid = __ballot(lane < KT && !see);
-        if (lane < KT) {
-            ks.mask[b][lane] = see ? 0.f : -INFINITY;
-            ks.pos[b][lane] = p;
-            if ((lane & 31) == 0) {
-                ks.range[b][lane / 32][0] = lo;
-                ks.range[b][lane / 32][1] = hi;
+        const uint64_t hid = __ballot(t < KT && !see);
+        if (t < KT) {
+            ks.mask[t] = see ? 0.f : -INFINITY;
+            ks.pos[t] = p;
+            if ((t & 31) == 0) {
+                ks.range[t / 32][0] = lo;
+                ks.range[t / 32][1] = hi;
+                ks.hidden[t / 32] = (uint32_t)(hid >> t);
             }
-            if (lane == 0) ks.hidden[b] = hid;
         }
     }
 };
+
+// -infinity where a key may not be seen: hidden ones, and those after the
+// lane's query (lim: the last row the lane's half may see).
+__device__ __forceinline__ void hide(f32x16& x, uint32_t hidden, const float* mask) {
+    if (!__builtin_amdgcn_readfirstlane(hidden)) return;
+    const int h = lane_id() >> 5;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const f32x4 mk = *reinterpret_cast<const f32x4*>(mask + 8 * j + 4 * h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[4 * j + i] += mk[i];
+    }
+}
 
 }  // namespace rse
