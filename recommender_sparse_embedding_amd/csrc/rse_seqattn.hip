@@ -78,7 +78,7 @@ __global__ void k_attn_clear(SeqHeader* h) { h->status = 0; }
 //
 // Registers are held to what lets FWD_WAVES waves share a SIMD.
 template <typename T, int D, bool SAVE>
-constexpr int FWD_WAVES = D * sizeof(T) <= 64 ? 4 : (D * sizeof(T) == 128 ? 3 : 2);
+constexpr int FWD_WAVES = D * sizeof(T) <= 64 ? 3 : (D * sizeof(T) == 128 || (D * sizeof(T) == 256 && !(SAVE && D == 128)) ? 2 : 1);
 
 template <typename T, int D, typename SH, bool SAVE>
 __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(FWD_WAVES<T, D, SAVE>))) void k_attn_fwd(
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     __shared__ KeySide<KT> s_side[SH::TEAMS][NB];
     __shared__ LdsBuckets s_buckets;
     __shared__ float s_bias[WH][RSE_SEQ_MAX_BOUNDARIES + 1];
-    const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5, wh = w % WH, wq = w / WH;
+    const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), half = lane >> 5, wh = w % WH, wq = w / WH;
     const int team = w / SH::TEAM, t = threadIdx.x % NT;
     const int hblocks = (a.n_heads + WH - 1) / WH, h0 = blockIdx.x % hblocks * WH, nb = a.n_bounds + 1;
     const bool live = h0 + wh < a.n_heads;

@@ -44,9 +44,9 @@ constexpr int SUMS = 3;
 // queries blockIdx.x, + gridDim.x, ...; its sums go to part.
 // Registers are held to what lets DQ_WAVES (DKV_WAVES) waves share a SIMD.
 template <typename T, int D>
-constexpr int DQ_WAVES = D * sizeof(T) <= 64 ? 3 : (D * sizeof(T) <= 256 ? 2 : 1);
+constexpr int DQ_WAVES = D * sizeof(T) <= 128 ? 2 : 1;
 template <typename T, int D>
-constexpr int DKV_WAVES = D * sizeof(T) <= 64 ? 3 : (D * sizeof(T) <= 128 || D == 64 ? 2 : 1);
+constexpr int DKV_WAVES = D * sizeof(T) <= 128 ? 2 : 1;
 
 template <typename T, int D, typename SH>
 __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(DQ_WAVES<T, D>))) void k_attn_dq(
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     __shared__ LdsBuckets s_buckets;
     __shared__ float s_bias[WH][RSE_SEQ_MAX_BOUNDARIES + 1];
     extern __shared__ float s_hist[];           // [waves][n_bounds + 1][cols]
-    const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5, wh = w % WH, wq = w / WH;
+    const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), half = lane >> 5, wh = w % WH, wq = w / WH;
     const int team = w / SH::TEAM, t = threadIdx.x % NT;
     const int h0 = blockIdx.y * WH, nb = a.n_bounds + 1;
     const bool live = h0 + wh < a.n_heads;
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     __shared__ int32_t s_range[SH::TEAMS][NB][NS][2];
     __shared__ LdsBuckets s_buckets;
     __shared__ float s_bias[SH::TEAMS][NB][NBP];
-    const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5, wh = w % WH, wq = w / WH;
+    const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), half = lane >> 5, wh = w % WH, wq = w / WH;
     const int team = w / SH::TEAM, t = threadIdx.x % NT;
     const int n_kv = a.n_heads / a.group, gblocks = (n_kv + WH - 1) / WH, g0 = blockIdx.x % gblocks * WH, nb = a.n_bounds + 1;
     const bool live = g0 + wh < n_kv;

@@ -181,7 +181,7 @@ __global__ __launch_bounds__(SW * 64) void k_step(StepArgs a, Rows<const T> q, R
     __shared__ int32_t s_bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
     __shared__ int32_t s_idx[SW][32];
     __shared__ float s_ml[SW][2][32];
-    const int lane = lane_id(), w = threadIdx.x / WAVE, half = lane >> 5, col = lane & 31;
+    const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), half = lane >> 5, col = lane & 31;
     const int n_kv = a.n_heads / a.group, nb = a.n_bounds + 1, blocks = (a.group + cols - 1) / cols;
     int64_t x = blockIdx.x;
     const int split = (int)(x % splits);
@@ -202,7 +202,7 @@ __global__ __launch_bounds__(SW * 64) void k_step(StepArgs a, Rows<const T> q, R
         const int c = t % cols;
         s_bias[t] = a.bias[(h0 + (c < nc ? c : nc - 1)) * nb + t / cols] * LOG2E;
     }
-    int64_t n = a.lens[b];
+    int64_t n = uniform(a.lens[b]);
     if (!step_ok(a, n)) n = -1;
     const int64_t nt = (n + 32) / 32, t0 = nt * split / splits, t1 = nt * (split + 1) / splits;
     const int32_t my_pos = a.pos[b];

@@ -414,8 +414,9 @@ __device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, i
         b = wave_last_le(a.batch, [&](int64_t x) { return a.offsets[x] / tq + x; }, item);
         t = item - (a.offsets[b] / tq + b);
     }
-    s = a.offsets[b];
-    const int64_t e = a.offsets[b + 1];
+    s = uniform(a.offsets[b]);
+    const int64_t e = uniform(a.offsets[b + 1]);
+    t = uniform(t);
     if (s < 0 || e < s || e > a.n_events || e - s > a.max_len) {
         if (lane_id() == 0) set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
         return false;
