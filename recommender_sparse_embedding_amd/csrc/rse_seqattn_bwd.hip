@@ -216,15 +216,20 @@ __global__ __launch_bounds__(256) void k_attn_dbias(const float* part, int block
 
 // dk and dv, keys as columns: per tile of queries and head of the group
 // S = Q K^T and dP = dO V^T, dV^T += dO^T P, dK^T += Q^T dS.  WQ waves take
-// tiles of keys, WH waves key heads; the buckets of a tile are looked up once
-// for the heads of the group.
-template <typename T, int D, typename SH>
+// tiles of keys, WH waves key heads or (IN_GROUP) query heads of one key head,
+// whose sums are then added over the waves in LDS; the buckets of a tile are
+// looked up once for the heads of the group.
+// (12 sequences of up to 2048 events, 8 heads on 2: 402 us with 4 tiles of
+// keys a block and its heads in turn, which leaves 384 blocks.)
+template <typename T, int D, typename SH, bool IN_GROUP>
 __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(DKV_WAVES<T, D>))) void k_attn_dkv(
     SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k, Rows<const T> v, const float* lse2, const float* delta,
     Rows<const T> dout, Rows<T> dk, Rows<T> dv) {
     constexpr int CH = SH::CH, KT = SH::KT, NS = SH::NS, NB = SH::NB, NT = SH::NT, WH = SH::WH, WQ = SH::WQ, ND = D / 32,
                   NBP = RSE_SEQ_MAX_BOUNDARIES + 1;
-    __shared__ u32x4 s_q[SH::TEAMS][NB][KT * CH], s_d[SH::TEAMS][NB][KT * CH];
+    __shared__ u32x4 s_rows[2][SH::TEAMS][NB][KT * CH];
+    auto& s_q = s_rows[0];
+    auto& s_d = s_rows[1];
     __shared__ u32x4 s_pairs[WQ][NS][WAVE];
     __shared__ float s_lse[SH::TEAMS][NB][KT], s_del[SH::TEAMS][NB][KT];
     __shared__ int32_t s_pos[SH::TEAMS][NB][KT];
@@ -233,22 +238,24 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     __shared__ float s_bias[SH::TEAMS][NB][NBP];
     const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), half = lane >> 5, wh = w % WH, wq = w / WH;
     const int team = w / SH::TEAM, t = threadIdx.x % NT;
-    const int n_kv = a.n_heads / a.group, gblocks = (n_kv + WH - 1) / WH, g0 = blockIdx.x % gblocks * WH, nb = a.n_bounds + 1;
-    const bool live = g0 + wh < n_kv;
-    const int g = live ? g0 + wh : n_kv - 1;
+    const int n_kv = a.n_heads / a.group, gblocks = IN_GROUP ? n_kv : (n_kv + WH - 1) / WH,
+              g0 = blockIdx.x % gblocks * (IN_GROUP ? 1 : WH), nb = a.n_bounds + 1;
+    const bool live = IN_GROUP || g0 + wh < n_kv;
+    const int g = IN_GROUP ? g0 : (live ? g0 + wh : n_kv - 1);
+    const int turns = IN_GROUP ? a.group / WH : a.group;            // heads one after the other
     int64_t s;
     int len, tile;
     if (!find_tile(a, grid, blockIdx.x / gblocks, 32 * WQ, false, s, len, tile, false)) return;
     const int j0 = tile * 32 * WQ, w0 = j0 + 32 * wq, my_k = w0 + (lane & 31), row = my_k < len ? my_k : len - 1;
     const int first = a.causal ? j0 / KT * KT : 0;                  // queries of the block: first .. len
-    const int total = (len - first + KT - 1) / KT * a.group;       // tiles of them, each for every head
+    const int total = (len - first + KT - 1) / KT * turns;         // tiles of them, each in all turns
 
     RowStage<T, D, NT, KT> st;
     int32_t rp = 0;
     float rl = 0.f, rd = 0.f, rb[(NBP + NT - 1) / NT];
     bool rin = false;
     auto load = [&](int it) {
-        const int h = g * a.group + it % a.group, i0 = first + it / a.group * KT;
+        const int h = g * a.group + (IN_GROUP ? it % turns * WH + wh : it % turns), i0 = first + it / turns * KT;
         st.load(q, h, dout, h, s, i0, len, nullptr, t);
         if (t < KT) {
             const int kk = i0 + t;
@@ -258,7 +265,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
             rd = delta[(int64_t)h * a.n_events + j];
             rin = kk < len;
         }
-        if (it == 0 || a.group > 1)
+        if (it == 0 || turns > 1)
 #pragma unroll
             for (int i = 0; i * NT < NBP; ++i) rb[i] = i * NT + t < nb ? a.bias[h * nb + i * NT + t] : 0.f;
     };
@@ -297,7 +304,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     store(0);
     __syncthreads();
     for (int it = 0, b = 0; it < total; ++it, b ^= NB - 1) {
-        const int i0 = first + it / a.group * KT;
+        const int i0 = first + it / turns * KT;
         if (it + 1 < total) load(it + 1);
         if (w0 < len) {
             wb.bias[0] = s_bias[team][b][lane];
@@ -309,7 +316,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                 if (a.causal && i1 + 31 < w0) continue;
                 TileBuckets<false> tb;
                 tb.set(wb, k_lo, k_hi, s_range[team][b][u]);
-                if (tb.many && it % a.group == 0) {
+                if (tb.many && it % turns == 0) {
                     if (WH > 1) __syncthreads();
                     tb.find_pairs(s_pairs[wq][u], wh, WH, s_buckets, a.n_bounds, a.cells, s_pos[team][b] + 32 * u, my_pos);
                     if (WH > 1) __syncthreads();
@@ -349,14 +356,38 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
             team_sync<SH::TEAM>();
         }
     }
-    if (my_k < len && live) {
-        T* pk = dk.at(s + my_k, g);
-        T* pv = dv.at(s + my_k, g);
+    if (!IN_GROUP) {
+        if (my_k < len && live) {
+            T* pk = dk.at(s + my_k, g);
+            T* pv = dv.at(s + my_k, g);
 #pragma unroll
-        for (int dt = 0; dt < ND; ++dt) {
-            if (!seen) ak[dt] = av[dt] = f32x16{};      // hidden: whatever the key held
-            store_column(pk + 32 * dt, ak[dt], a.scale);
-            store_column(pv + 32 * dt, av[dt], 1.f);
+            for (int dt = 0; dt < ND; ++dt) {
+                if (!seen) ak[dt] = av[dt] = f32x16{};      // hidden: whatever the key held
+                store_column(pk + 32 * dt, ak[dt], a.scale);
+                store_column(pv + 32 * dt, av[dt], 1.f);
+            }
+        }
+        return;
+    }
+    // wave w adds and stores the w-th quarter of each 32 elements
+    f32x4* s_sum = reinterpret_cast<f32x4*>(s_rows);
+    static_assert(!IN_GROUP || sizeof(s_rows) >= 4 * 4 * WAVE * 16, "room for the sums");
+#pragma unroll
+    for (int x = 0; x < 2 * ND; ++x) {
+        const f32x16& mine = x < ND ? ak[x % ND] : av[x % ND];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            s_sum[(w * 4 + j) * WAVE + lane] = f32x4{mine[4 * j], mine[4 * j + 1], mine[4 * j + 2], mine[4 * j + 3]};
+        __syncthreads();
+        f32x4 sum = s_sum[w * WAVE + lane];
+#pragma unroll
+        for (int y = 1; y < 4; ++y) sum += s_sum[(y * 4 + w) * WAVE + lane];
+        if (my_k < len) {
+            if (x < ND) sum *= a.scale;
+            if (!seen) sum = f32x4{0.f, 0.f, 0.f, 0.f};
+            T* p = (x < ND ? dk.at(s + my_k, g) : dv.at(s + my_k, g)) + 32 * (x % ND) + 8 * w + 4 * half;
+            store_four(p, sum);
         }
     }
 }
@@ -396,17 +427,17 @@ BwdWs bwd_ws(const rse_seqattn* a, int64_t n, int64_t batch, int64_t max_len, vo
     return w;
 }
 
-template <typename T, int D, int TEAM, int WH, int WQ, int KH, int KQ>
+template <typename T, int D, int TEAM, int WH, int WQ, int KTEAM, int KH, int KQ, bool IN_GROUP>
 int run_bwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v, const Saved& sv,
             const rse_seq_rows* dout, const rse_seq_rows* dq, const rse_seq_rows* dk, const rse_seq_rows* dv,
             float* dbias, const BwdWs& w, hipStream_t s) {
     using QS = Shape<T, D, TEAM, WH, WQ>;
-    using KS = Shape<T, D, TEAM, KH, KQ>;
+    using KS = Shape<T, D, KTEAM, KH, KQ>;
     const int nb = a.n_bounds + 1, n_kv = a.n_heads / a.group;
     const int cols = nb <= 32 ? 64 : 32;        // at most 32 KiB a block of 4 waves up to 64 buckets, 64 KiB past that
     const TileGrid tq = tile_grid(a.n_events, a.batch, a.max_len, 32 * WQ);
     const TileGrid tk = tile_grid(a.n_events, a.batch, a.max_len, 32 * KQ);
-    const int64_t blocks = tk.items * ((n_kv + KH - 1) / KH);
+    const int64_t blocks = tk.items * (IN_GROUP ? n_kv : (n_kv + KH - 1) / KH);
     if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
     hipLaunchKernelGGL((k_attn_dq<T, D, QS>), dim3((unsigned)w.blocks, (a.n_heads + WH - 1) / WH), dim3(QS::WAVES * WAVE),
                        QS::WAVES * nb * cols * sizeof(float), s, a, tq, rows_view<const T>(q), rows_view<const T>(k),
@@ -414,7 +445,7 @@ int run_bwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, cons
     int rc = launch_status();
     if (rc) return rc;
     hipLaunchKernelGGL(k_attn_dbias, dim3(a.n_heads * nb), dim3(256), 0, s, w.part, (int)w.blocks, dbias);
-    hipLaunchKernelGGL((k_attn_dkv<T, D, KS>), dim3((unsigned)blocks), dim3(KS::WAVES * WAVE), 0, s, a, tk,
+    hipLaunchKernelGGL((k_attn_dkv<T, D, KS, IN_GROUP>), dim3((unsigned)blocks), dim3(KS::WAVES * WAVE), 0, s, a, tk,
                        rows_view<const T>(q), rows_view<const T>(k), rows_view<const T>(v), sv.lse2, w.delta,
                        rows_view<const T>(dout), rows_view<T>(dk), rows_view<T>(dv));
     return launch_status();
@@ -454,14 +485,26 @@ int seq_attention_bwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
     return by_type(attn, [&](auto t, auto d) {
         using T = decltype(t);
         constexpr int D = decltype(d)::value;
+        auto run = [&](auto team, auto wh, auto wq, auto kteam, auto kh, auto kq, auto in_group) {
+            return run_bwd<T, D, team.value, wh.value, wq.value, kteam.value, kh.value, kq.value, in_group.value>(
+                a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
+        };
+        using I1 = std::integral_constant<int, 1>;
+        using I4 = std::integral_constant<int, 4>;
+        std::true_type in_group;
+        std::false_type apart;
+        const bool fours = a.group % 4 == 0;
+        // (dq's team, heads, tiles; dkv's)
         if constexpr (short_form<T, D>(0))
             if (short_form<T, D>(a.max_len)) {
-                if (a.n_heads == 1) return run_bwd<T, D, 1, 1, 1, 1, 1>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
-                if (attn->n_kv_heads == 1) return run_bwd<T, D, 1, 4, 1, 1, 1>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
-                return run_bwd<T, D, 1, 4, 1, 4, 1>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
+                if (a.n_heads == 1) return run(I1(), I1(), I1(), I1(), I1(), I1(), apart);
+                if (fours) return run(I1(), I4(), I1(), I1(), I4(), I1(), in_group);
+                return run(I1(), I4(), I1(), I1(), I4(), I1(), apart);
             }
-        if (a.group % 4 == 0) return run_bwd<T, D, 4, 4, 1, 1, 4>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
-        return run_bwd<T, D, 4, 1, 4, 1, 4>(a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
+        if constexpr (sizeof(T) * D <= 256)
+            if (fours) return run(I4(), I4(), I1(), I1(), I4(), I1(), in_group);
+        if (fours) return run(I4(), I4(), I1(), I4(), I1(), I4(), apart);
+        return run(I4(), I1(), I4(), I4(), I1(), I4(), apart);
     });
 }
 

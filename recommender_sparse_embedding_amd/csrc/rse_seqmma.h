@@ -195,6 +195,11 @@ __device__ __forceinline__ void store_column(uint16_t* p, const f32x16& acc, flo
     }
 }
 
+__device__ __forceinline__ void store_four(float* p, f32x4 x) { gstore_f4(p, x); }
+__device__ __forceinline__ void store_four(uint16_t* p, f32x4 x) {
+    *(RSE_GLOBAL u32x2*)p = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+}
+
 // ---------------------------------------------------------------- buckets --
 // A wave's copy of one head's boundaries and bias (lane l: entries l and
 // 64 + l): a wave-uniform distance finds its bucket by two comparisons and
