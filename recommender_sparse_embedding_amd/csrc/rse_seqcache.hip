@@ -172,8 +172,12 @@ __device__ __forceinline__ bool step_ok(const StepArgs& a, int64_t n) {
 // other block waits for the store that the first part makes).
 constexpr int SW = 4;
 
+// Registers are held to what lets STEP_WAVES waves share a SIMD.
 template <typename T, int D>
-__global__ __launch_bounds__(SW * 64) void k_step(StepArgs a, Rows<const T> q, Rows<const T> k, Rows<const T> v, T* kp,
+constexpr int STEP_WAVES = D * sizeof(T) <= 128 ? 3 : (D * sizeof(T) == 256 ? 2 : 1);
+
+template <typename T, int D>
+__global__ __launch_bounds__(SW * 64) __attribute__((amdgpu_waves_per_eu(STEP_WAVES<T, D>))) void k_step(StepArgs a, Rows<const T> q, Rows<const T> k, Rows<const T> v, T* kp,
                                                   T* vp, Rows<T> out, int splits, int cols, float* part_o, float* part_ml) {
     using TL = Tile<T, D>;
     constexpr int CH = TL::CH, ND = D / 32, NC = CH / 2;
@@ -358,30 +362,46 @@ __global__ __launch_bounds__(SW * 64) void k_step(StepArgs a, Rows<const T> q, R
     }
 }
 
-// Joins a head's parts: one wave per user and head.
+// Joins a head's parts: one block per user and head, CB / D groups of threads
+// taking parts in turn, their sums added in order.
 template <typename T, int D>
-__global__ __launch_bounds__(CB) void k_step_join(const float* part_o, const float* part_ml, int64_t rows, int n_heads,
-                                                  int splits, Rows<T> out) {
-    const int lane = lane_id();
-    const int64_t at = (int64_t)blockIdx.x * CW + threadIdx.x / WAVE;
-    if (at >= rows) return;
-    const float m = lane < splits ? part_ml[2 * (at * splits + lane)] : -INFINITY;
-    float M = m;
-    for (int s = 32; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor(M, s, WAVE));
-    const float r = M == -INFINITY || lane >= splits ? 0.f : __builtin_amdgcn_exp2f(m - M);
-    float L = lane < splits ? r * part_ml[2 * (at * splits + lane) + 1] : 0.f;
-    for (int s = 32; s > 0; s >>= 1) L += __shfl_xor(L, s, WAVE);
-    constexpr int E = (D + WAVE - 1) / WAVE;
-    float O[E] = {};
-    for (int s = 0; s < splits; ++s) {
-        const float rs = __shfl(r, s, WAVE);
+__global__ __launch_bounds__(CB) void k_step_join(const float* part_o, const float* part_ml, int n_heads, int splits,
+                                                  Rows<T> out) {
+    constexpr int G = CB / D;
+    __shared__ float s_r[64], s_o[G][D];
+    __shared__ float s_l;
+    const int lane = lane_id(), d = threadIdx.x % D, grp = threadIdx.x / D;
+    const int64_t at = blockIdx.x;
+    float o = 0.f, v[4];
 #pragma unroll
-        for (int u = 0; u < E; ++u)
-            if (u * WAVE + lane < D) O[u] = __builtin_fmaf(rs, part_o[(at * splits + s) * D + u * WAVE + lane], O[u]);
+    for (int i = 0; i < 4; ++i) {               // the first loads fly while the weights are formed
+        const int s = grp + i * G;
+        v[i] = s < splits ? part_o[(at * splits + s) * D + d] : 0.f;
     }
+    if (threadIdx.x < WAVE) {
+        const float m = lane < splits ? part_ml[2 * (at * splits + lane)] : -INFINITY;
+        const float l = lane < splits ? part_ml[2 * (at * splits + lane) + 1] : 0.f;
+        float M = m;
+        for (int s = 32; s > 0; s >>= 1) M = fmaxf(M, __shfl_xor(M, s, WAVE));
+        const float r = M == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - M);
+        float L = r * l;
+        for (int s = 32; s > 0; s >>= 1) L += __shfl_xor(L, s, WAVE);
+        s_r[lane] = r;
+        if (lane == 0) s_l = L;
+    }
+    __syncthreads();
 #pragma unroll
-    for (int u = 0; u < E; ++u)
-        if (u * WAVE + lane < D) from_f32(out.at(at / n_heads, at % n_heads)[u * WAVE + lane], L > 0.f ? O[u] / L : 0.f);
+    for (int i = 0; i < 4; ++i)
+        if (grp + i * G < splits) o = __builtin_fmaf(s_r[grp + i * G], v[i], o);
+#pragma unroll 4
+    for (int s = grp + 4 * G; s < splits; s += G) o = __builtin_fmaf(s_r[s], part_o[(at * splits + s) * D + d], o);
+    s_o[grp][d] = o;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+        for (int x = 1; x < G; ++x) o += s_o[x][d];
+        from_f32(out.at(at / n_heads, at % n_heads)[d], s_l > 0.f ? o / s_l : 0.f);
+    }
 }
 
 // Parts of a history: enough blocks to fill the GPU four times over, each
@@ -430,9 +450,8 @@ int run_step(const rse_seqattn* at, const rse_seqcache* c, const StepArgs& a, co
                        rows_view<const T>(k), rows_view<const T>(v), static_cast<T*>(c->k), static_cast<T*>(c->v),
                        rows_view<T>(out), p.splits, p.cols, ws.o, ws.ml);
     if (p.splits > 1) {
-        const int64_t rows = a.batch * a.n_heads;
-        hipLaunchKernelGGL((k_step_join<T, D>), dim3((unsigned)((rows + CW - 1) / CW)), dim3(CB), 0, s, ws.o, ws.ml,
-                           rows, a.n_heads, p.splits, rows_view<T>(out));
+        hipLaunchKernelGGL((k_step_join<T, D>), dim3((unsigned)(a.batch * a.n_heads)), dim3(CB), 0, s, ws.o, ws.ml,
+                           a.n_heads, p.splits, rows_view<T>(out));
     }
     return launch_status();
 }
