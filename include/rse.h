@@ -680,7 +680,7 @@ int seq_cache_assign(rse_seqcache* cache, const int64_t* d_counts, const int64_t
 int seq_cache_write(rse_seqcache* cache, const int64_t* d_slots, int64_t n_events, const rse_seq_rows* k,
                     const rse_seq_rows* v, const int32_t* d_pos, void* stream);
 
-/* Workspace bytes of one seq_attention_step. */
+/* Workspace bytes of one seq_attention_step; may be 0 (d_ws may be NULL then). */
 int rse_seqattn_step_workspace_size(const rse_seqattn* attn, int64_t batch, int64_t max_len, size_t* bytes_out);
 
 /*

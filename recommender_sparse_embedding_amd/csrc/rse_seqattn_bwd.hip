@@ -189,14 +189,17 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
         }
     }
     __syncthreads();
-    // a head's sums: over its WQ waves and their columns, in a fixed order
-    for (int x = threadIdx.x; x < WH * nb; x += SH::WAVES * WAVE) {
-        const int hh = x / nb, bk = x % nb;
-        if (h0 + hh >= a.n_heads) break;
+    // a head's sums, over its WQ waves and their columns: 8 lanes each, in a
+    // fixed order
+    for (int x = threadIdx.x / 8; x < WH * nb; x += SH::WAVES * 8) {
+        const int hh = x / nb, bk = x % nb, part8 = threadIdx.x % 8;
         float sum = 0.f;
         for (int y = 0; y < WQ; ++y)
-            for (int c = 0; c < cols; ++c) sum += s_hist[((y * WH + hh) * nb + bk) * cols + ((c + bk) & (cols - 1))];
-        part[((int64_t)(h0 + hh) * nb + bk) * gridDim.x + blockIdx.x] = sum;
+            for (int c = part8; c < cols; c += 8) sum += s_hist[((y * WH + hh) * nb + bk) * cols + c];
+        sum += __shfl_xor(sum, 1, 8);
+        sum += __shfl_xor(sum, 2, 8);
+        sum += __shfl_xor(sum, 4, 8);
+        if (part8 == 0 && h0 + hh < a.n_heads) part[((int64_t)(h0 + hh) * nb + bk) * gridDim.x + blockIdx.x] = sum;
     }
 }
 

@@ -29,19 +29,26 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+_PER16 = {torch.float32: 4, torch.bfloat16: 8}
+
+
 def _rows(t: torch.Tensor, dtype, n: int, heads: int, dim: int, name: str) -> RseSeqRows:
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name}: expected a {dtype} CUDA tensor, got {t.dtype} on {t.device}")
     if t.shape != (n, heads, dim):
         raise ValueError(f"{name}: expected shape ({n}, {heads}, {dim}), got {tuple(t.shape)}")
     row, head, one = t.stride()
-    per16 = 16 // t.element_size()
+    per16 = _PER16[dtype]
     # the stride of a dimension of one element is never used
-    row, head = (row if n > 1 else per16), (head if heads > 1 else per16)
-    if n and (one != 1 or row % per16 or head % per16 or t.data_ptr() % 16):
+    if n <= 1:
+        row = per16
+    if heads == 1:
+        head = per16
+    p = t.data_ptr()
+    if n and (one != 1 or row % per16 or head % per16 or p % 16):
         raise ValueError(f"{name}: the last dimension must be contiguous, and the address and the other strides "
                          f"multiples of 16 bytes (strides {t.stride()})")
-    return RseSeqRows(t.data_ptr(), row, head)
+    return RseSeqRows(p, row, head)
 
 
 def _vector(t: torch.Tensor, dtype, n: int, name: str):
@@ -78,6 +85,7 @@ class SeqAttention:
                                      self.dim, dtype, int(self.causal), self.scale, arr, n, _stream(stream)),
               "rse_seqattn_create")
         self.handle = h
+        self.step_bytes: dict[tuple[int, int], int] = {}     # workspace sizes of steps, by (batch, max_len)
         self._finalizer = weakref.finalize(self, lib.rse_seqattn_destroy, h)
 
     @property
@@ -98,6 +106,13 @@ def _size(fn, what: str, *args) -> int:
     sz = ctypes.c_size_t()
     check(fn(*args, ctypes.byref(sz)), what)
     return sz.value
+
+
+def _on_empty(stream, shape, dtype, device):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _batch(attn: SeqAttention, n: int, pos, bias, seq_offsets, key_off, max_len) -> RseSeqBatch:
@@ -273,13 +288,16 @@ def seq_attention_step(attn: SeqAttention, cache: SeqCache, q: torch.Tensor, k: 
     pos_p = _vector(pos, torch.int32, batch, "pos")
     bias_p = _vector(bias, torch.float32, H * attn.n_buckets, "bias")
     lens_p = _vector(lens, torch.int64, batch, "lens")
-    size = _size(lib.rse_seqattn_step_workspace_size, "rse_seqattn_step_workspace_size", attn.handle, batch, most)
-    with _on(stream):
-        if out is None:
-            out = torch.empty((batch, H, D), dtype=dt, device=q.device)
-        ws = _bytes(size, q.device)
+    size = attn.step_bytes.get((batch, most))
+    if size is None:
+        size = _size(lib.rse_seqattn_step_workspace_size, "rse_seqattn_step_workspace_size", attn.handle, batch, most)
+        attn.step_bytes[(batch, most)] = size
+    if out is None:
+        out = _on_empty(stream, (batch, H, D), dt, q.device)
+    ws = _on_empty(stream, size, torch.uint8, q.device) if size else None
     o = _rows(out, dt, batch, H, D, "out")
-    check(lib.seq_attention_step(attn.handle, cache.handle, *map(ctypes.byref, args), pos_p, bias_p,
-                                 _ptr(page_table), max_pages, lens_p, batch, most, ctypes.byref(o), _ptr(ws),
-                                 ws.numel(), _stream(stream)), "seq_attention_step")
+    byref = ctypes.byref
+    check(lib.seq_attention_step(attn.handle, cache.handle, byref(args[0]), byref(args[1]), byref(args[2]), pos_p,
+                                 bias_p, page_table.data_ptr(), max_pages, lens_p, batch, most, byref(o), _ptr(ws),
+                                 size, _stream(stream)), "seq_attention_step")
     return out
