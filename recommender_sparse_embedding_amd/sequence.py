@@ -18,10 +18,23 @@ import weakref
 
 import torch
 
-from . import BF16, F32, _bytes, _need, _ptr, _stream, lib
+from . import BF16, F32, _bytes, _need, _ptr, lib
 from ._lib import RseSeqBatch, RseSeqRows, check
 
 _DTYPE = {F32: torch.float32, BF16: torch.bfloat16}
+
+
+# the current stream's handle without building a stream object (several
+# microseconds of a call), where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream=None) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _on(stream):
