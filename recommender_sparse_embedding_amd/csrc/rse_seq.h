@@ -180,18 +180,26 @@ inline rse::SeqArgs seq_args(const rse_seqattn* a, const rse_seq_batch* b) {
     return s;
 }
 
+// Sequences short enough (and rows narrow enough) for the kernels whose waves
+// work apart: see SHORT.
+constexpr int64_t SHORT = 128;
+inline bool short_form(const rse_seqattn* a, int64_t max_len) {
+    return max_len <= SHORT && a->dim * (a->dtype == RSE_F32 ? 4 : 2) <= 128;
+}
+
 // What a forward leaves for its backward: base-2 log-sums [n_heads][n_events]
-// and, unrounded, the outputs [n_events][n_heads][dim].
+// and, unless the sequences are short, the unrounded outputs
+// [n_events][n_heads][dim].
 struct Saved {
     float* lse2;
     float* out32;
     size_t bytes;
 };
-inline Saved saved_view(const rse_seqattn* a, int64_t n, void* base) {
+inline Saved saved_view(const rse_seqattn* a, int64_t n, int64_t max_len, void* base) {
     Carver c(base);
     Saved v;
     v.lse2 = c.take<float>((size_t)a->n_heads * n);
-    v.out32 = c.take<float>((size_t)n * a->n_heads * a->dim);
+    v.out32 = c.take<float>(short_form(a, max_len) ? 0 : (size_t)n * a->n_heads * a->dim);
     v.bytes = c.size();
     return v;
 }

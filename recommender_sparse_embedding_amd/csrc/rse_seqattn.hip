@@ -71,20 +71,26 @@ __global__ void k_attn_clear(SeqHeader* h) { h->status = 0; }
 // that has grown by more than 8 (p up to 2^8, exact in a float), so most
 // tiles need neither a second pass over y nor a rescaling of the sums.
 //
-// SAVE: also leaves the log-sums and outputs for the backward, whose
-// dO . out has to equal sum_j p dp to fp32 accuracy (the bias gradient sums
-// differences from it): what bf16 rounds off the probabilities goes through
-// a second product into those outputs.
+// SAVE: also leaves the log-sums for the backward, and SAVE_OUT the outputs:
+// its dO . out has to equal sum_j p dp to fp32 accuracy (the bias gradient
+// sums differences from it), so what bf16 rounds off the probabilities goes
+// through a second product into those outputs.
+enum { SAVE_NONE = 0, SAVE = 1, SAVE_OUT = 2 };
+//
+// Short sequences: a block goes on through its sequences' tiles of queries,
+// and the next tile's first loads are in flight during the last step of the
+// current one.  (8192 sequences of 1..100 events, 4 heads of 64: 454 us with a
+// block per tile, most of it waiting for the first loads of each.)
 //
 // Registers are held to what lets FWD_WAVES waves share a SIMD.
-template <typename T, int D, bool SAVE>
-constexpr int FWD_WAVES = D * sizeof(T) <= 64 ? 3 : (D * sizeof(T) == 128 || (D * sizeof(T) == 256 && !(SAVE && D == 128)) ? 2 : 1);
+template <typename T, int D, int S>
+constexpr int FWD_WAVES = D * sizeof(T) <= 64 ? 3 : (D * sizeof(T) == 128 || (D * sizeof(T) == 256 && !(S == SAVE_OUT && D == 128)) ? 2 : 1);
 
-template <typename T, int D, typename SH, bool SAVE>
-__global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(FWD_WAVES<T, D, SAVE>))) void k_attn_fwd(
+template <typename T, int D, typename SH, int S>
+__global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(FWD_WAVES<T, D, S>))) void k_attn_fwd(
     SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k, Rows<const T> v, Rows<T> out, float* lse2, float* out32) {
     constexpr int CH = SH::CH, KT = SH::KT, NS = SH::NS, NB = SH::NB, NT = SH::NT, WH = SH::WH, WQ = SH::WQ, ND = D / 32;
-    constexpr bool REST = SAVE && sizeof(T) == 2;
+    constexpr bool REST = S == SAVE_OUT && sizeof(T) == 2, BRIEF = SH::TEAM == 1;
     __shared__ u32x4 s_k[SH::TEAMS][NB][KT * CH], s_v[SH::TEAMS][NB][KT * CH];
     __shared__ u32x4 s_pairs[WQ][NS][WAVE];
     __shared__ KeySide<KT> s_side[SH::TEAMS][NB];
@@ -95,20 +101,32 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     const int hblocks = (a.n_heads + WH - 1) / WH, h0 = blockIdx.x % hblocks * WH, nb = a.n_bounds + 1;
     const bool live = h0 + wh < a.n_heads;
     const int head = live ? h0 + wh : a.n_heads - 1, g = head / a.group;
-    int64_t s;
-    int len, tile;
-    if (!find_tile(a, grid, blockIdx.x / hblocks, 32 * WQ, a.causal, s, len, tile, h0 == 0)) return;
-    const int q0 = tile * 32 * WQ, w0 = q0 + 32 * wq, my_q = w0 + (lane & 31), row = my_q < len ? my_q : len - 1;
-    const int end = a.causal ? (q0 + 32 * WQ < len ? q0 + 32 * WQ : len) : len;     // keys of the block
-    const int my_end = w0 >= len ? 0 : (a.causal && w0 + 32 < end ? w0 + 32 : end);  // and of the wave
+    SeqTiles at;
+    if (BRIEF) {
+        at.begin(a, blockIdx.x / hblocks, gridDim.x / hblocks, h0 == 0);
+        if (!at.valid) return;
+    } else if (!find_tile(a, grid, blockIdx.x / hblocks, 32 * WQ, a.causal, at.s, at.len, at.tile, h0 == 0)) {
+        return;
+    }
 
     RowStage<T, D, NT, KT> st;
     KeySideStage side;
-    st.load(k, g, v, g, s, 0, end, a.key_off, t);
-    side.load(a, s, 0, end, KT, t);
-    ColFrag<T, D> qf;
-    qf.load(q.at(s + row, head), half);
-    const int32_t my_pos = a.pos[s + row];
+    ColFrag<T, D> qn;
+    int32_t pn;
+    // keys of a block's tile end here
+    auto end_of = [&](const SeqTiles& x) {
+        const int past = (x.tile + 1) * 32 * WQ;
+        return a.causal && past < x.len ? past : x.len;
+    };
+    auto load_first = [&](const SeqTiles& x) {
+        st.load(k, g, v, g, x.s, 0, end_of(x), a.key_off, t);
+        side.load(a, x.s, 0, end_of(x), KT, t);
+        const int i = x.tile * 32 * WQ + 32 * wq + (lane & 31);
+        const int64_t row = x.s + (i < x.len ? i : x.len - 1);
+        qn.load(q.at(row, head), half);
+        pn = a.pos[row];
+    };
+    load_first(at);
     WaveBuckets wb;
     wb.load(a.hdr, a.bias + head * nb, a.n_bounds, LOG2E);
     s_buckets.load(a.hdr);
@@ -116,117 +134,128 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
         s_bias[wh][lane] = wb.bias[0];
         s_bias[wh][64 + lane] = wb.bias[1];
     }
-    if (a.scale < 0.f) qf.negate();
     const float c2 = fabsf(a.scale) * LOG2E;
-    const int32_t q_lo = half_min(my_pos), q_hi = half_max(my_pos);
-
-    f32x16 o[ND] = {}, rest[REST ? ND : 1] = {};
-    float m = 0.f, l = 0.f;
-    bool set = false;                           // m has been taken from a visible key
-    st.store(s_k[team][0], s_v[team][0], t);
-    side.store(s_side[team][0], t);
     __syncthreads();
-    for (int k0 = 0, b = 0; k0 < end; k0 += KT, b ^= NB - 1) {
-        if (k0 + KT < end) {
-            st.load(k, g, v, g, s, k0 + KT, end, a.key_off, t);
-            side.load(a, s, k0 + KT, end, KT, t);
-        }
-        const KeySide<KT>& ks = s_side[team][b];
+    for (;;) {
+        const int64_t s = at.s;
+        const int len = at.len, w0 = at.tile * 32 * WQ + 32 * wq, my_q = w0 + (lane & 31), end = end_of(at);
+        const int my_end = w0 >= len ? 0 : (a.causal && w0 + 32 < end ? w0 + 32 : end);     // keys of the wave
+        ColFrag<T, D> qf = qn;
+        if (a.scale < 0.f) qf.negate();
+        const int32_t my_pos = pn, q_lo = half_min(my_pos), q_hi = half_max(my_pos);
+        f32x16 o[ND] = {}, rest[REST ? ND : 1] = {};
+        float m = 0.f, l = 0.f;
+        bool set = false;                       // m has been taken from a visible key
+        for (int k0 = 0, b = 0; k0 < end; k0 += KT, b ^= NB - 1) {
+            st.store(s_k[team][b], s_v[team][b], t);
+            side.store(s_side[team][b], t);
+            team_sync<SH::TEAM>();
+            if (k0 + KT < end) {
+                st.load(k, g, v, g, s, k0 + KT, end, a.key_off, t);
+                side.load(a, s, k0 + KT, end, KT, t);
+            } else if (BRIEF) {
+                at.advance(a);
+                if (at.valid) load_first(at);
+            }
+            const KeySide<KT>& ks = s_side[team][b];
 #pragma unroll 1
-        for (int u = 0; u < NS; ++u) {
-            const int k1 = k0 + 32 * u;
-            if (k1 >= my_end) break;
-            TileBuckets<true> tb;
-            tb.set(wb, q_lo, q_hi, ks.range[u]);
-            if (tb.many) {
-                // all waves of a column tile are here, and share the lookups
-                if (SH::TEAM == 1 && WH > 1) __syncthreads();   // the last tile's are no longer read
-                tb.find_pairs(s_pairs[wq][u], wh, WH, s_buckets, a.n_bounds, a.cells, ks.pos + 32 * u, my_pos);
-                if (WH > 1) __syncthreads();
-                else wave_lds_sync();
-            }
-            f32x16 x = mma_rows<T, D>(s_k[team][b], 32 * u, qf, f32x16{});
-            x = tb.logits(x, c2, -m, wb, s_pairs[wq][u], s_bias[wh], ks.pos + 32 * u, my_pos);
-            hide(x, ks.hidden[u], ks.mask + 32 * u);
-            if (a.causal && k1 + 31 > w0) {
-                const int lim = my_q - k1 - 4 * half;
+            for (int u = 0; u < NS; ++u) {
+                const int k1 = k0 + 32 * u;
+                if (k1 >= my_end) break;
+                TileBuckets<true> tb;
+                tb.set(wb, q_lo, q_hi, ks.range[u]);
+                if (tb.many) {
+                    // all waves of a column tile are here, and share the lookups
+                    if (SH::TEAM == 1 && WH > 1) __syncthreads();   // the last tile's are no longer read
+                    tb.find_pairs(s_pairs[wq][u], wh, WH, s_buckets, a.n_bounds, a.cells, ks.pos + 32 * u, my_pos);
+                    if (WH > 1) __syncthreads();
+                    else wave_lds_sync();
+                }
+                f32x16 x = mma_rows<T, D>(s_k[team][b], 32 * u, qf, f32x16{});
+                x = tb.logits(x, c2, -m, wb, s_pairs[wq][u], s_bias[wh], ks.pos + 32 * u, my_pos);
+                hide(x, ks.hidden[u], ks.mask + 32 * u);
+                if (a.causal && k1 + 31 > w0) {
+                    const int lim = my_q - k1 - 4 * half;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) x[r] = tile_row(r, 0) <= lim ? x[r] : -INFINITY;
-            }
-            float top = x[0];
+                    for (int r = 0; r < 16; ++r) x[r] = tile_row(r, 0) <= lim ? x[r] : -INFINITY;
+                }
+                float top = x[0];
 #pragma unroll
-            for (int r = 1; r < 16; ++r) top = fmaxf(top, x[r]);
-            top = fmaxf(top, other_half(top));
-            const bool move = top > 8.f || (!set && top > -INFINITY);
-            set |= top > -INFINITY;
-            if (__any(move)) {
-                const float by = move ? top : 0.f, r = __builtin_amdgcn_exp2f(-by);
-                m += by;
-                // nothing summed yet: 0, also where exp2 overflows
-                l = l > 0.f ? l * r : 0.f;
+                for (int r = 1; r < 16; ++r) top = fmaxf(top, x[r]);
+                top = fmaxf(top, other_half(top));
+                const bool move = top > 8.f || (!set && top > -INFINITY);
+                set |= top > -INFINITY;
+                if (__any(move)) {
+                    const float by = move ? top : 0.f, r = __builtin_amdgcn_exp2f(-by);
+                    m += by;
+                    // nothing summed yet: 0, also where exp2 overflows
+                    l = l > 0.f ? l * r : 0.f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] -= by;
-                const float ro = r < INFINITY ? r : 0.f;
+                    for (int i = 0; i < 16; ++i) x[i] -= by;
+                    const float ro = r < INFINITY ? r : 0.f;
 #pragma unroll
-                for (int dt = 0; dt < ND; ++dt) {
-                    o[dt] *= ro;
-                    if (REST) rest[dt] *= ro;
+                    for (int dt = 0; dt < ND; ++dt) {
+                        o[dt] *= ro;
+                        if (REST) rest[dt] *= ro;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    x[r] = __builtin_amdgcn_exp2f(x[r]);
+                    l += x[r];
+                }
+                RowOperand<T> p;
+                p.set(x);
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) o[dt] = mma_over_rows<D>(s_v[team][b], 32 * u, dt, p, o[dt]);
+                if (REST) {
+                    RowOperand<T> lo;
+                    lo.set_rest(x, p);
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt) rest[dt] = mma_over_rows<D>(s_v[team][b], 32 * u, dt, lo, rest[dt]);
                 }
             }
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                x[r] = __builtin_amdgcn_exp2f(x[r]);
-                l += x[r];
-            }
-            RowOperand<T> p;
-            p.set(x);
-#pragma unroll
-            for (int dt = 0; dt < ND; ++dt) o[dt] = mma_over_rows<D>(s_v[team][b], 32 * u, dt, p, o[dt]);
-            if (REST) {
-                RowOperand<T> lo;
-                lo.set_rest(x, p);
-#pragma unroll
-                for (int dt = 0; dt < ND; ++dt) rest[dt] = mma_over_rows<D>(s_v[team][b], 32 * u, dt, lo, rest[dt]);
-            }
+            if (BRIEF) wave_lds_sync();         // read before the next tile is stored
         }
-        if (k0 + KT < end) {
-            if (SH::TEAM == 1) wave_lds_sync();
-            st.store(s_k[team][b ^ (NB - 1)], s_v[team][b ^ (NB - 1)], t);
-            side.store(s_side[team][b ^ (NB - 1)], t);
-            team_sync<SH::TEAM>();
-        }
-    }
-    l += other_half(l);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    if (my_q < len && live) {
-        T* dst = out.at(s + my_q, head);
+        l += other_half(l);
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        if (my_q < len && live) {
+            T* dst = out.at(s + my_q, head);
 #pragma unroll
-        for (int dt = 0; dt < ND; ++dt) store_column(dst + 32 * dt, o[dt], inv);
-        if (SAVE) {
-            if (half == 0) lse2[(int64_t)head * a.n_events + s + my_q] = l > 0.f ? m + log2f(l) : -INFINITY;
+            for (int dt = 0; dt < ND; ++dt) store_column(dst + 32 * dt, o[dt], inv);
+            if (S != SAVE_NONE && half == 0)
+                lse2[(int64_t)head * a.n_events + s + my_q] = l > 0.f ? m + log2f(l) : -INFINITY;
+            if (S == SAVE_OUT)
 #pragma unroll
-            for (int dt = 0; dt < ND; ++dt) {
-                if (REST) o[dt] += rest[dt];
-                store_column(out32 + ((s + my_q) * a.n_heads + head) * D + 32 * dt, o[dt], inv);
-            }
+                for (int dt = 0; dt < ND; ++dt) {
+                    if (REST) o[dt] += rest[dt];
+                    store_column(out32 + ((s + my_q) * a.n_heads + head) * D + 32 * dt, o[dt], inv);
+                }
         }
+        if (!BRIEF || !at.valid) return;
     }
 }
 
 // ------------------------------------------------------------------ host --
+// Blocks that go through the short sequences: as many as fit the GPU at once.
+constexpr int64_t SHORT_BLOCKS = 512;
+
 template <typename T, int D, int TEAM, int WH, int WQ>
 int run_fwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v,
             const rse_seq_rows* out, const Saved& sv, hipStream_t s) {
     using SH = Shape<T, D, TEAM, WH, WQ>;
+    constexpr int KEEP = TEAM == 1 ? SAVE : SAVE_OUT;
     const TileGrid tg = tile_grid(a.n_events, a.batch, a.max_len, 32 * WQ);
-    const int64_t blocks = tg.items * ((a.n_heads + WH - 1) / WH);
+    const int64_t hblocks = (a.n_heads + WH - 1) / WH;
+    const int64_t some = (SHORT_BLOCKS * 4 / SH::WAVES + hblocks - 1) / hblocks;
+    const int64_t blocks = hblocks * (TEAM > 1 ? tg.items : (a.batch < some ? a.batch : some));
     if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)blocks), block(SH::WAVES * WAVE);
     if (sv.lse2)
-        hipLaunchKernelGGL((k_attn_fwd<T, D, SH, true>), grid, block, 0, s, a, tg, rows_view<const T>(q),
+        hipLaunchKernelGGL((k_attn_fwd<T, D, SH, KEEP>), grid, block, 0, s, a, tg, rows_view<const T>(q),
                            rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), sv.lse2, sv.out32);
     else
-        hipLaunchKernelGGL((k_attn_fwd<T, D, SH, false>), grid, block, 0, s, a, tg, rows_view<const T>(q),
+        hipLaunchKernelGGL((k_attn_fwd<T, D, SH, SAVE_NONE>), grid, block, 0, s, a, tg, rows_view<const T>(q),
                            rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), nullptr, nullptr);
     return launch_status();
 }
@@ -303,7 +332,7 @@ int rse_seqattn_clear_status(rse_seqattn* attn, void* stream) {
 
 int rse_seqattn_saved_size(const rse_seqattn* attn, int64_t n_events, int64_t max_len, size_t* bytes_out) {
     if (!attn || !bytes_out || n_events < 0 || max_len < 0) return RSE_ERR_INVALID_ARG;
-    *bytes_out = saved_view(attn, n_events, nullptr).bytes;
+    *bytes_out = saved_view(attn, n_events, max_len, nullptr).bytes;
     return RSE_OK;
 }
 
@@ -316,7 +345,7 @@ int seq_attention_fwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
     if (!rows_ok(q, attn->dtype) || !rows_ok(k, attn->dtype) || !rows_ok(v, attn->dtype) || !rows_ok(out, attn->dtype))
         return RSE_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(d_saved) % 256) return RSE_ERR_INVALID_ARG;
-    Saved sv = saved_view(attn, batch->n_events, d_saved);
+    Saved sv = saved_view(attn, batch->n_events, batch->max_len, d_saved);
     if (d_saved && saved_bytes < sv.bytes) return RSE_ERR_WORKSPACE;
     if (!d_saved) sv.lse2 = sv.out32 = nullptr;
     const SeqArgs a = seq_args(attn, batch);
@@ -324,8 +353,8 @@ int seq_attention_fwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
         using T = decltype(t);
         constexpr int D = decltype(d)::value;
         const hipStream_t st = as_stream(stream);
-        if constexpr (short_form<T, D>(0))
-            if (short_form<T, D>(a.max_len)) {
+        if constexpr (HAS_SHORT<T, D>)
+            if (short_form(attn, batch->max_len)) {
                 if (a.n_heads > 1) return run_fwd<T, D, 1, 4, 1>(a, q, k, v, out, sv, st);
                 return run_fwd<T, D, 1, 1, 1>(a, q, k, v, out, sv, st);
             }

@@ -36,6 +36,22 @@ __device__ __forceinline__ void add_bucket(float* hist, int cols, int bucket, fl
 // Up to so many buckets of a tile are summed in registers.
 constexpr int SUMS = 3;
 
+// A block's bucket sums of each head, over its WQ waves and their columns: 8
+// lanes each, in a fixed order.
+template <int WH, int WQ>
+__device__ __forceinline__ void reduce_sums(const SeqArgs& a, int h0, int nb, int cols, const float* s_hist, float* part) {
+    for (int x = threadIdx.x / 8; x < WH * nb; x += blockDim.x / 8) {
+        const int hh = x / nb, bk = x % nb, eighth = threadIdx.x % 8;
+        float sum = 0.f;
+        for (int y = 0; y < WQ; ++y)
+            for (int c = eighth; c < cols; c += 8) sum += s_hist[((y * WH + hh) * nb + bk) * cols + c];
+        sum += __shfl_xor(sum, 1, 8);
+        sum += __shfl_xor(sum, 2, 8);
+        sum += __shfl_xor(sum, 4, 8);
+        if (eighth == 0 && h0 + hh < a.n_heads) part[((int64_t)(h0 + hh) * nb + bk) * gridDim.x + blockIdx.x] = sum;
+    }
+}
+
 // dq and the bias gradient, queries as columns: per tile of keys
 // S^T = K Q^T and dP^T = V dO^T, ds = p (dp - delta), dQ^T += K^T dS^T.
 // delta = sum_j p dp = dO . out, from the unrounded outputs.  ds of a tile in
@@ -189,18 +205,138 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
         }
     }
     __syncthreads();
-    // a head's sums, over its WQ waves and their columns: 8 lanes each, in a
-    // fixed order
-    for (int x = threadIdx.x / 8; x < WH * nb; x += SH::WAVES * 8) {
-        const int hh = x / nb, bk = x % nb, part8 = threadIdx.x % 8;
-        float sum = 0.f;
-        for (int y = 0; y < WQ; ++y)
-            for (int c = part8; c < cols; c += 8) sum += s_hist[((y * WH + hh) * nb + bk) * cols + c];
-        sum += __shfl_xor(sum, 1, 8);
-        sum += __shfl_xor(sum, 2, 8);
-        sum += __shfl_xor(sum, 4, 8);
-        if (part8 == 0 && h0 + hh < a.n_heads) part[((int64_t)(h0 + hh) * nb + bk) * gridDim.x + blockIdx.x] = sum;
+    reduce_sums<WH, WQ>(a, h0, nb, cols, s_hist, part);
+}
+
+// The same for short sequences: a block goes through its sequences' tiles of
+// queries, the next tile's first loads in flight meanwhile, and delta comes
+// from the probabilities themselves: forward through the tiles of keys it is
+// summed, then, backward, used.  The last tile of the way there is the first
+// of the way back, so its probabilities are formed once.  Nothing but the
+// log-sums is needed of the forward (its outputs in fp32 would be written and
+// read: 0.8 of 2.6 GB a training step on 8192 sequences of 1..100 events).
+template <typename T, int D, typename SH>
+__global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_attn_dq_short(
+    SeqArgs a, Rows<const T> q, Rows<const T> k, Rows<const T> v, const float* lse2, Rows<const T> dout, Rows<T> dq,
+    float* delta, float* part, int cols) {
+    constexpr int CH = SH::CH, KT = SH::KT, NT = SH::NT, WH = SH::WH, ND = D / 32;
+    static_assert(SH::TEAM == 1 && SH::WQ == 1 && KT == 32, "waves apart");
+    __shared__ u32x4 s_k[WH][KT * CH], s_v[WH][KT * CH];
+    __shared__ u32x4 s_pairs[WAVE];
+    __shared__ KeySide<KT> s_side[WH];
+    __shared__ LdsBuckets s_buckets;
+    __shared__ float s_bias[WH][RSE_SEQ_MAX_BOUNDARIES + 1];
+    extern __shared__ float s_hist[];           // [waves][n_bounds + 1][cols]
+    const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), half = lane >> 5;
+    const int h0 = blockIdx.y * WH, nb = a.n_bounds + 1;
+    const bool live = h0 + w < a.n_heads;
+    const int head = live ? h0 + w : a.n_heads - 1, g = head / a.group;
+    float* hist = s_hist + w * nb * cols;
+    SeqTiles at;
+    at.begin(a, blockIdx.x, gridDim.x, h0 == 0);
+
+    RowStage<T, D, NT, KT> st;
+    KeySideStage side;
+    ColFrag<T, D> qn, dn;
+    int32_t pn = 0;
+    float ln = 0.f;
+    auto end_of = [&](const SeqTiles& x) { return a.causal && (x.tile + 1) * 32 < x.len ? (x.tile + 1) * 32 : x.len; };
+    auto load_first = [&](const SeqTiles& x) {
+        st.load(k, g, v, g, x.s, 0, end_of(x), a.key_off, lane);
+        side.load(a, x.s, 0, end_of(x), KT, lane);
+        const int i = x.tile * 32 + (lane & 31);
+        const int64_t row = x.s + (i < x.len ? i : x.len - 1);
+        qn.load(q.at(row, head), half);
+        dn.load(dout.at(row, head), half);
+        pn = a.pos[row];
+        ln = lse2[(int64_t)head * a.n_events + row];
+    };
+    if (at.valid) load_first(at);
+    WaveBuckets wb;
+    wb.load(a.hdr, a.bias + head * nb, a.n_bounds, LOG2E);
+    s_buckets.load(a.hdr);
+    s_bias[w][lane] = wb.bias[0];
+    s_bias[w][64 + lane] = wb.bias[1];
+    for (int x = threadIdx.x; x < WH * nb * cols; x += WH * WAVE) s_hist[x] = 0.f;
+    const float c2 = fabsf(a.scale) * LOG2E;
+    __syncthreads();
+
+    while (at.valid) {
+        const int64_t s = at.s;
+        const int len = at.len, w0 = at.tile * 32, my_q = w0 + (lane & 31), end = end_of(at), nk = (end + 31) / 32;
+        ColFrag<T, D> qf = qn, df = dn;
+        if (a.scale < 0.f) qf.negate();
+        const float L = my_q >= len || ln == -INFINITY ? INFINITY : ln;         // infinity: p = 0
+        const int32_t my_pos = pn, q_lo = half_min(my_pos), q_hi = half_max(my_pos);
+        f32x16 acc[ND] = {};
+        float del = 0.f;
+        for (int step = 0; step < 2 * nk - 1; ++step) {
+            const int kt = step < nk ? step : 2 * nk - 2 - step, k1 = 32 * kt;
+            st.store(s_k[w], s_v[w], lane);
+            side.store(s_side[w], lane);
+            wave_lds_sync();
+            if (step + 1 < 2 * nk - 1) {
+                const int to = 32 * (step + 1 < nk ? step + 1 : 2 * nk - 3 - step);
+                st.load(k, g, v, g, s, to, end, a.key_off, lane);
+                side.load(a, s, to, end, KT, lane);
+            } else {
+                at.advance(a);
+                if (at.valid) load_first(at);
+            }
+            const KeySide<KT>& ks = s_side[w];
+            TileBuckets<true> tb;
+            tb.set(wb, q_lo, q_hi, ks.range[0]);
+            if (tb.many) {
+                if (WH > 1) __syncthreads();
+                tb.find_pairs(s_pairs, w, WH, s_buckets, a.n_bounds, a.cells, ks.pos, my_pos);
+                if (WH > 1) __syncthreads();
+                else wave_lds_sync();
+            }
+            f32x16 x = mma_rows<T, D>(s_k[w], 0, qf, f32x16{});
+            f32x16 dp = mma_rows<T, D>(s_v[w], 0, df, f32x16{});
+            x = tb.logits(x, c2, -L, wb, s_pairs, s_bias[w], ks.pos, my_pos);
+            hide(x, ks.hidden[0], ks.mask);
+            if (a.causal && k1 + 31 > w0) {
+                const int lim = my_q - k1 - 4 * half;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[r] = tile_row(r, 0) <= lim ? x[r] : -INFINITY;
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(x[r]);
+            if (step < nk) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) del = __builtin_fmaf(x[r], dp[r], del);
+            }
+            if (step == nk - 1) del += other_half(del);
+            if (step >= nk - 1) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[r] *= dp[r] - del;
+                if (tb.lo == tb.hi) {
+                    float sum = x[0];
+#pragma unroll
+                    for (int r = 1; r < 16; ++r) sum += x[r];
+                    add_bucket(hist, cols, tb.lo, sum);
+                } else {
+                    int idx[16];
+                    tb.index(idx, wb, s_pairs, ks.pos, my_pos);
+                    add_pairs(hist, cols, idx, x);
+                }
+                RowOperand<T> ds;
+                ds.set(x);
+#pragma unroll
+                for (int dt = 0; dt < ND; ++dt) acc[dt] = mma_over_rows<D>(s_k[w], 0, dt, ds, acc[dt]);
+            }
+            wave_lds_sync();
+        }
+        if (my_q < len && live) {
+            if (half == 0) delta[(int64_t)head * a.n_events + s + my_q] = del;
+            T* dst = dq.at(s + my_q, head);
+#pragma unroll
+            for (int dt = 0; dt < ND; ++dt) store_column(dst + 32 * dt, acc[dt], a.scale);
+        }
     }
+    __syncthreads();
+    reduce_sums<WH, 1>(a, h0, nb, cols, s_hist, part);
 }
 
 // The blocks' bucket sums, added in 64 bits in a fixed order: one block per
@@ -227,7 +363,7 @@ __global__ __launch_bounds__(256) void k_attn_dbias(const float* part, int block
 template <typename T, int D, typename SH, bool IN_GROUP>
 __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(DKV_WAVES<T, D>))) void k_attn_dkv(
     SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k, Rows<const T> v, const float* lse2, const float* delta,
-    Rows<const T> dout, Rows<T> dk, Rows<T> dv) {
+    Rows<const T> dout, Rows<T> dk, Rows<T> dv, int by_seq) {
     constexpr int CH = SH::CH, KT = SH::KT, NS = SH::NS, NB = SH::NB, NT = SH::NT, WH = SH::WH, WQ = SH::WQ, ND = D / 32,
                   NBP = RSE_SEQ_MAX_BOUNDARIES + 1;
     __shared__ u32x4 s_rows[2][SH::TEAMS][NB][KT * CH];
@@ -246,27 +382,31 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     const bool live = IN_GROUP || g0 + wh < n_kv;
     const int g = IN_GROUP ? g0 : (live ? g0 + wh : n_kv - 1);
     const int turns = IN_GROUP ? a.group / WH : a.group;            // heads one after the other
-    int64_t s;
-    int len, tile;
-    if (!find_tile(a, grid, blockIdx.x / gblocks, 32 * WQ, false, s, len, tile, false)) return;
-    const int j0 = tile * 32 * WQ, w0 = j0 + 32 * wq, my_k = w0 + (lane & 31), row = my_k < len ? my_k : len - 1;
-    const int first = a.causal ? j0 / KT * KT : 0;                  // queries of the block: first .. len
-    const int total = (len - first + KT - 1) / KT * turns;         // tiles of them, each in all turns
+    constexpr bool BRIEF = SH::TEAM == 1;
+    SeqTiles at;
+    // by_seq: the block goes on through its sequences' tiles
+    if (BRIEF && by_seq) {
+        at.begin(a, blockIdx.x / gblocks, gridDim.x / gblocks, false);
+        if (!at.valid) return;
+    } else if (!find_tile(a, grid, blockIdx.x / gblocks, 32 * WQ, false, at.s, at.len, at.tile, false)) {
+        return;
+    }
 
     RowStage<T, D, NT, KT> st;
     int32_t rp = 0;
     float rl = 0.f, rd = 0.f, rb[(NBP + NT - 1) / NT];
     bool rin = false;
-    auto load = [&](int it) {
-        const int h = g * a.group + (IN_GROUP ? it % turns * WH + wh : it % turns), i0 = first + it / turns * KT;
-        st.load(q, h, dout, h, s, i0, len, nullptr, t);
+    auto first_of = [&](const SeqTiles& x) { return a.causal ? x.tile * 32 * WQ / KT * KT : 0; };   // queries of a block's tile
+    auto load = [&](const SeqTiles& x, int it) {
+        const int h = g * a.group + (IN_GROUP ? it % turns * WH + wh : it % turns), i0 = first_of(x) + it / turns * KT;
+        st.load(q, h, dout, h, x.s, i0, x.len, nullptr, t);
         if (t < KT) {
             const int kk = i0 + t;
-            const int64_t j = s + (kk < len ? kk : len - 1);
+            const int64_t j = x.s + (kk < x.len ? kk : x.len - 1);
             rp = a.pos[j];
             rl = lse2[(int64_t)h * a.n_events + j];
             rd = delta[(int64_t)h * a.n_events + j];
-            rin = kk < len;
+            rin = kk < x.len;
         }
         if (it == 0 || turns > 1)
 #pragma unroll
@@ -291,24 +431,35 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
             if (i * NT + t < NBP) s_bias[team][b][i * NT + t] = rb[i] * LOG2E;
     };
 
-    load(0);
-    ColFrag<T, D> kf, vf;
-    kf.load(k.at(s + row, g), half);
-    vf.load(v.at(s + row, g), half);
-    const bool seen = !(a.key_off && a.key_off[s + row] < 0);
-    const int32_t my_pos = a.pos[s + row];
+    load(at, 0);
     s_buckets.load(a.hdr);
     WaveBuckets wb;
     wb.load(a.hdr, a.bias, a.n_bounds, LOG2E);
-    if (a.scale < 0.f) kf.negate();
     const float c2 = fabsf(a.scale) * LOG2E;
-    const int32_t k_lo = half_min(my_pos), k_hi = half_max(my_pos);
-    f32x16 ak[ND] = {}, av[ND] = {};
-    store(0);
     __syncthreads();
+    for (;;) {
+    const int64_t s = at.s;
+    const int len = at.len, w0 = at.tile * 32 * WQ + 32 * wq, my_k = w0 + (lane & 31), row = my_k < len ? my_k : len - 1;
+    const int first = first_of(at), total = (len - first + KT - 1) / KT * turns;    // tiles of queries, each in all turns
+    ColFrag<T, D> kf, vf;
+    kf.load(k.at(s + row, g), half);
+    vf.load(v.at(s + row, g), half);
+    const int32_t off = a.key_off ? reinterpret_cast<const int32_t*>(a.key_off + s + row)[1] : 0;
+    const int32_t my_pos = a.pos[s + row];
+    const int32_t k_lo = half_min(my_pos), k_hi = half_max(my_pos);
+    const bool seen = off >= 0;
+    if (a.scale < 0.f) kf.negate();
+    f32x16 ak[ND] = {}, av[ND] = {};
     for (int it = 0, b = 0; it < total; ++it, b ^= NB - 1) {
         const int i0 = first + it / turns * KT;
-        if (it + 1 < total) load(it + 1);
+        store(b);
+        team_sync<SH::TEAM>();
+        if (it + 1 < total) {
+            load(at, it + 1);
+        } else if (BRIEF && by_seq) {
+            at.advance(a);
+            if (at.valid) load(at, 0);
+        }
         if (w0 < len) {
             wb.bias[0] = s_bias[team][b][lane];
             wb.bias[1] = s_bias[team][b][64 + lane];
@@ -353,12 +504,10 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                 }
             }
         }
-        if (it + 1 < total) {
-            if (SH::TEAM == 1) wave_lds_sync();
-            store(b ^ (NB - 1));
-            team_sync<SH::TEAM>();
-        }
+        if (BRIEF) wave_lds_sync();             // read before the next tile is stored
     }
+    bool more = false;
+    if (BRIEF) more = by_seq && at.valid;
     if (!IN_GROUP) {
         if (my_k < len && live) {
             T* pk = dk.at(s + my_k, g);
@@ -370,7 +519,8 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                 store_column(pv + 32 * dt, av[dt], 1.f);
             }
         }
-        return;
+        if (!more) return;
+        continue;
     }
     // wave w adds and stores the w-th quarter of each 32 elements
     f32x4* s_sum = reinterpret_cast<f32x4*>(s_rows);
@@ -393,12 +543,17 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
             store_four(p, sum);
         }
     }
+    if (!more) return;
+    __syncthreads();                            // the sums are read before the next tile is stored
+    }
 }
 
 // ------------------------------------------------------------------ host --
 // Blocks of k_attn_dq over all heads: enough to fill the GPU several times
 // over; more would only add partial bucket sums.
 constexpr int64_t DQ_BLOCKS = 2048;
+// Blocks that go through the short sequences: as many as fit the GPU at once.
+constexpr int64_t SHORT_BLOCKS = 512;
 
 struct BwdWs {
     float* delta;
@@ -412,15 +567,14 @@ struct DqForm {
     int wh, wq;
 };
 DqForm dq_form(const rse_seqattn* a, int64_t max_len) {
-    const bool brief = by_type(a, [&](auto t, auto d) { return (int)short_form<decltype(t), decltype(d)::value>(max_len); });
-    if (brief) return {a->n_heads > 1 ? 4 : 1, 1};
+    if (short_form(a, max_len)) return {a->n_heads > 1 ? 4 : 1, 1};
     return a->n_heads / a->n_kv_heads % 4 == 0 ? DqForm{4, 1} : DqForm{1, 4};
 }
 
 BwdWs bwd_ws(const rse_seqattn* a, int64_t n, int64_t batch, int64_t max_len, void* base) {
     BwdWs w;
     const DqForm f = dq_form(a, max_len);
-    w.blocks = tile_grid(n, batch, max_len, 32 * f.wq).items;
+    w.blocks = short_form(a, max_len) ? batch : tile_grid(n, batch, max_len, 32 * f.wq).items;
     const int64_t most = DQ_BLOCKS * f.wh / a->n_heads;
     if (w.blocks > most) w.blocks = most > 16 ? most : 16;
     Carver c(base);
@@ -440,17 +594,26 @@ int run_bwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, cons
     const int cols = nb <= 32 ? 64 : 32;        // at most 32 KiB a block of 4 waves up to 64 buckets, 64 KiB past that
     const TileGrid tq = tile_grid(a.n_events, a.batch, a.max_len, 32 * WQ);
     const TileGrid tk = tile_grid(a.n_events, a.batch, a.max_len, 32 * KQ);
-    const int64_t blocks = tk.items * (IN_GROUP ? n_kv : (n_kv + KH - 1) / KH);
+    const bool brief = TEAM == 1;
+    const int64_t gblocks = IN_GROUP ? n_kv : (n_kv + KH - 1) / KH;
+    const int64_t some = (SHORT_BLOCKS * 4 / KS::WAVES + gblocks - 1) / gblocks;
+    const int64_t blocks = gblocks * (!brief ? tk.items : (a.batch < some ? a.batch : some));
     if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((k_attn_dq<T, D, QS>), dim3((unsigned)w.blocks, (a.n_heads + WH - 1) / WH), dim3(QS::WAVES * WAVE),
-                       QS::WAVES * nb * cols * sizeof(float), s, a, tq, rows_view<const T>(q), rows_view<const T>(k),
-                       rows_view<const T>(v), sv.lse2, sv.out32, rows_view<const T>(dout), rows_view<T>(dq), w.delta, w.part, cols);
+    const dim3 grid((unsigned)w.blocks, (a.n_heads + WH - 1) / WH), block(QS::WAVES * WAVE);
+    const size_t lds = QS::WAVES * nb * cols * sizeof(float);
+    if constexpr (TEAM == 1)
+        hipLaunchKernelGGL((k_attn_dq_short<T, D, QS>), grid, block, lds, s, a, rows_view<const T>(q), rows_view<const T>(k),
+                           rows_view<const T>(v), sv.lse2, rows_view<const T>(dout), rows_view<T>(dq), w.delta, w.part, cols);
+    else
+        hipLaunchKernelGGL((k_attn_dq<T, D, QS>), grid, block, lds, s, a, tq, rows_view<const T>(q), rows_view<const T>(k),
+                           rows_view<const T>(v), sv.lse2, sv.out32, rows_view<const T>(dout), rows_view<T>(dq), w.delta,
+                           w.part, cols);
     int rc = launch_status();
     if (rc) return rc;
     hipLaunchKernelGGL(k_attn_dbias, dim3(a.n_heads * nb), dim3(256), 0, s, w.part, (int)w.blocks, dbias);
     hipLaunchKernelGGL((k_attn_dkv<T, D, KS, IN_GROUP>), dim3((unsigned)blocks), dim3(KS::WAVES * WAVE), 0, s, a, tk,
                        rows_view<const T>(q), rows_view<const T>(k), rows_view<const T>(v), sv.lse2, w.delta,
-                       rows_view<const T>(dout), rows_view<T>(dk), rows_view<T>(dv));
+                       rows_view<const T>(dout), rows_view<T>(dk), rows_view<T>(dv), (int)brief);
     return launch_status();
 }
 
@@ -482,7 +645,7 @@ int seq_attention_bwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
     for (const rse_seq_rows* r : {q, k, v, dout, dq, dk, dv})
         if (!rows_ok(r, attn->dtype)) return RSE_ERR_INVALID_ARG;
     if (!d_saved || reinterpret_cast<uintptr_t>(d_saved) % 256) return RSE_ERR_INVALID_ARG;
-    const Saved sv = saved_view(attn, batch->n_events, const_cast<void*>(d_saved));
+    const Saved sv = saved_view(attn, batch->n_events, batch->max_len, const_cast<void*>(d_saved));
     if (saved_bytes < sv.bytes) return RSE_ERR_WORKSPACE;
     const SeqArgs a = seq_args(attn, batch);
     return by_type(attn, [&](auto t, auto d) {
@@ -498,8 +661,8 @@ int seq_attention_bwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
         std::false_type apart;
         const bool fours = a.group % 4 == 0;
         // (dq's team, heads, tiles; dkv's)
-        if constexpr (short_form<T, D>(0))
-            if (short_form<T, D>(a.max_len)) {
+        if constexpr (HAS_SHORT<T, D>)
+            if (short_form(attn, batch->max_len)) {
                 if (a.n_heads == 1) return run(I1(), I1(), I1(), I1(), I1(), I1(), apart);
                 if (fours) return run(I1(), I4(), I1(), I1(), I4(), I1(), in_group);
                 return run(I1(), I4(), I1(), I1(), I4(), I1(), apart);

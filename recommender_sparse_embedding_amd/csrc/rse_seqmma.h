@@ -432,6 +432,56 @@ __device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, i
     return true;
 }
 
+// The tiles a block works through, one after the other.  By sequence: block x
+// takes sequences x, + blocks, ..., all their tiles in order; the next
+// sequence's offsets are loaded one ahead, so that its first tile can be on
+// its way while the last one of the current sequence is computed.
+struct SeqTiles {
+    int64_t s;
+    int len, tile;
+    bool valid;
+    int64_t b, step;
+    int64_t next0, next1;                       // offsets of sequence b + step, as loaded
+    __device__ __forceinline__ void begin(const SeqArgs& a, int64_t first, int64_t blocks, bool check) {
+        if (check)
+            for (int64_t i = first * blockDim.x + threadIdx.x; i < a.batch; i += blocks * blockDim.x) {
+                const int64_t x = a.offsets[i], y = a.offsets[i + 1];
+                if (x > y || (i == 0 && x != 0) || (i == a.batch - 1 && y != a.n_events))
+                    set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
+            }
+        b = first - blocks;
+        step = blocks;
+        fetch(a);
+        next_sequence(a);
+    }
+    __device__ __forceinline__ void fetch(const SeqArgs& a) {
+        const int64_t n = b + step < a.batch ? b + step : a.batch - 1;
+        next0 = a.offsets[n];
+        next1 = a.offsets[n + 1];
+    }
+    __device__ __forceinline__ void next_sequence(const SeqArgs& a) {
+        for (;;) {
+            b += step;
+            valid = b < a.batch;
+            if (!valid) return;
+            s = uniform(next0);
+            const int64_t e = uniform(next1);
+            fetch(a);
+            if (s < 0 || e < s || e > a.n_events || e - s > a.max_len) {
+                if (lane_id() == 0) set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
+                continue;
+            }
+            len = (int)(e - s);
+            tile = 0;
+            if (len > 0) return;
+        }
+    }
+    __device__ __forceinline__ void advance(const SeqArgs& a) {
+        if ((tile + 1) * 32 < len) ++tile;
+        else next_sequence(a);
+    }
+};
+
 // ------------------------------------------------------------------ shapes --
 // A block's waves and what they share.  A team of waves stages tiles of rows
 // together; WH waves take heads side by side, WQ waves tiles of 32 columns.
@@ -442,7 +492,6 @@ __device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, i
 //  - up to SHORT events, where such a block would mostly idle: every wave a
 //    team of its own with one buffer, 4 heads of one column tile side by side.
 //    Rows past 128 bytes do not pass through one wave's registers: long form.
-constexpr int64_t SHORT = 128;
 template <typename T, int D, int TEAM_, int WH_, int WQ_>
 struct Shape {
     static constexpr int TEAM = TEAM_, WH = WH_, WQ = WQ_, WAVES = WH * WQ, TEAMS = WAVES / TEAM;
@@ -451,7 +500,7 @@ struct Shape {
     static constexpr int CH = Tile<T, D>::CH, NT = TEAM * WAVE;
 };
 template <typename T, int D>
-constexpr bool short_form(int64_t max_len) { return max_len <= SHORT && D * sizeof(T) <= 128; }
+constexpr bool HAS_SHORT = D * sizeof(T) <= 128;
 
 // Orders a team's LDS writes before its reads.
 template <int TEAM>
