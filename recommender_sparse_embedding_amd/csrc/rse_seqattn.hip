@@ -92,7 +92,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     constexpr int CH = SH::CH, KT = SH::KT, NS = SH::NS, NB = SH::NB, NT = SH::NT, WH = SH::WH, WQ = SH::WQ, ND = D / 32;
     constexpr bool REST = S == SAVE_OUT && sizeof(T) == 2, BRIEF = SH::TEAM == 1;
     __shared__ u32x4 s_k[SH::TEAMS][NB][KT * CH], s_v[SH::TEAMS][NB][KT * CH];
-    __shared__ u32x4 s_pairs[WQ][NS][WAVE];
+    __shared__ u32x4 s_pairs[BRIEF ? 2 : WQ][NS][WAVE];      // (BRIEF: this tile's and the last one's)
     __shared__ KeySide<KT> s_side[SH::TEAMS][NB];
     __shared__ LdsBuckets s_buckets;
     __shared__ float s_bias[WH][RSE_SEQ_MAX_BOUNDARIES + 1];
@@ -135,6 +135,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
         s_bias[wh][64 + lane] = wb.bias[1];
     }
     const float c2 = fabsf(a.scale) * LOG2E;
+    int wp = wq;
     __syncthreads();
     for (;;) {
         const int64_t s = at.s;
@@ -166,13 +167,13 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                 tb.set(wb, q_lo, q_hi, ks.range[u]);
                 if (tb.many) {
                     // all waves of a column tile are here, and share the lookups
-                    if (SH::TEAM == 1 && WH > 1) __syncthreads();   // the last tile's are no longer read
-                    tb.find_pairs(s_pairs[wq][u], wh, WH, s_buckets, a.n_bounds, a.cells, ks.pos + 32 * u, my_pos);
+                    if (BRIEF) wp ^= 1;
+                    tb.find_pairs(s_pairs[wp][u], wh, WH, s_buckets, a.n_bounds, a.cells, ks.pos + 32 * u, my_pos);
                     if (WH > 1) __syncthreads();
                     else wave_lds_sync();
                 }
                 f32x16 x = mma_rows<T, D>(s_k[team][b], 32 * u, qf, f32x16{});
-                x = tb.logits(x, c2, -m, wb, s_pairs[wq][u], s_bias[wh], ks.pos + 32 * u, my_pos);
+                x = tb.logits(x, c2, -m, wb, s_pairs[wp][u], s_bias[wh], ks.pos + 32 * u, my_pos);
                 hide(x, ks.hidden[u], ks.mask + 32 * u);
                 if (a.causal && k1 + 31 > w0) {
                     const int lim = my_q - k1 - 4 * half;

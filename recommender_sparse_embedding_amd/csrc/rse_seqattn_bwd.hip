@@ -13,18 +13,40 @@ namespace {
 // A wave's bucket sums in LDS, [bucket][cols]: lane l adds in column l % cols
 // by a plain read, addition and write, so every entry has a fixed order of
 // additions.  (An LDS atomic addition of floats took 93 LDS cycles here, a
-// read and a write together some ten.)  With 32 columns the two halves of the
-// wave take turns.
+// read and a write together some ten.)  Four at a time: read together, added
+// in order, a later one taking the earlier one's sum where both are in one
+// bucket, and written in order.  With 32 columns the two halves of the wave
+// take turns.
+__device__ __forceinline__ void add_sixteen(float* mine, int cols, const int (&idx)[16], const f32x16& x) {
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+        float* p[4];
+        float h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p[i] = mine + idx[r + i] * cols;
+            h[i] = *p[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int e = 0; e < i; ++e) h[i] = idx[r + e] == idx[r + i] ? h[e] : h[i];
+            h[i] += x[r + i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *p[i] = h[i];
+    }
+}
 __device__ __forceinline__ void add_pairs(float* hist, int cols, const int (&idx)[16], const f32x16& x) {
     const int lane = lane_id();
     float* mine = hist + (lane & (cols - 1));
-    if (cols == WAVE || lane < 32)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) mine[idx[r] * cols] += x[r];
-    wave_lds_sync();
-    if (cols < WAVE && lane >= 32)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) mine[idx[r] * cols] += x[r];
+    if (cols == WAVE) {
+        add_sixteen(mine, WAVE, idx, x);
+    } else {
+        if (lane < 32) add_sixteen(mine, 32, idx, x);
+        wave_lds_sync();
+        if (lane >= 32) add_sixteen(mine, 32, idx, x);
+    }
     wave_lds_sync();
 }
 // One lane's sum per column pair into one bucket.
@@ -222,7 +244,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     constexpr int CH = SH::CH, KT = SH::KT, NT = SH::NT, WH = SH::WH, ND = D / 32;
     static_assert(SH::TEAM == 1 && SH::WQ == 1 && KT == 32, "waves apart");
     __shared__ u32x4 s_k[WH][KT * CH], s_v[WH][KT * CH];
-    __shared__ u32x4 s_pairs[WAVE];
+    __shared__ u32x4 s_pairs[2][WAVE];          // this tile's and the last one's
     __shared__ KeySide<KT> s_side[WH];
     __shared__ LdsBuckets s_buckets;
     __shared__ float s_bias[WH][RSE_SEQ_MAX_BOUNDARIES + 1];
@@ -259,6 +281,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     s_bias[w][64 + lane] = wb.bias[1];
     for (int x = threadIdx.x; x < WH * nb * cols; x += WH * WAVE) s_hist[x] = 0.f;
     const float c2 = fabsf(a.scale) * LOG2E;
+    int wp = 0;
     __syncthreads();
 
     while (at.valid) {
@@ -287,14 +310,14 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
             TileBuckets<true> tb;
             tb.set(wb, q_lo, q_hi, ks.range[0]);
             if (tb.many) {
-                if (WH > 1) __syncthreads();
-                tb.find_pairs(s_pairs, w, WH, s_buckets, a.n_bounds, a.cells, ks.pos, my_pos);
+                wp ^= 1;
+                tb.find_pairs(s_pairs[wp], w, WH, s_buckets, a.n_bounds, a.cells, ks.pos, my_pos);
                 if (WH > 1) __syncthreads();
                 else wave_lds_sync();
             }
             f32x16 x = mma_rows<T, D>(s_k[w], 0, qf, f32x16{});
             f32x16 dp = mma_rows<T, D>(s_v[w], 0, df, f32x16{});
-            x = tb.logits(x, c2, -L, wb, s_pairs, s_bias[w], ks.pos, my_pos);
+            x = tb.logits(x, c2, -L, wb, s_pairs[wp], s_bias[w], ks.pos, my_pos);
             hide(x, ks.hidden[0], ks.mask);
             if (a.causal && k1 + 31 > w0) {
                 const int lim = my_q - k1 - 4 * half;
@@ -318,7 +341,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                     add_bucket(hist, cols, tb.lo, sum);
                 } else {
                     int idx[16];
-                    tb.index(idx, wb, s_pairs, ks.pos, my_pos);
+                    tb.index(idx, wb, s_pairs[wp], ks.pos, my_pos);
                     add_pairs(hist, cols, idx, x);
                 }
                 RowOperand<T> ds;
@@ -369,7 +392,8 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     __shared__ u32x4 s_rows[2][SH::TEAMS][NB][KT * CH];
     auto& s_q = s_rows[0];
     auto& s_d = s_rows[1];
-    __shared__ u32x4 s_pairs[WQ][NS][WAVE];
+    constexpr bool BRIEF = SH::TEAM == 1;
+    __shared__ u32x4 s_pairs[BRIEF ? 2 : WQ][NS][WAVE];      // (BRIEF: this tile's and the last one's)
     __shared__ float s_lse[SH::TEAMS][NB][KT], s_del[SH::TEAMS][NB][KT];
     __shared__ int32_t s_pos[SH::TEAMS][NB][KT];
     __shared__ int32_t s_range[SH::TEAMS][NB][NS][2];
@@ -382,7 +406,6 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     const bool live = IN_GROUP || g0 + wh < n_kv;
     const int g = IN_GROUP ? g0 : (live ? g0 + wh : n_kv - 1);
     const int turns = IN_GROUP ? a.group / WH : a.group;            // heads one after the other
-    constexpr bool BRIEF = SH::TEAM == 1;
     SeqTiles at;
     // by_seq: the block goes on through its sequences' tiles
     if (BRIEF && by_seq) {
@@ -436,6 +459,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     WaveBuckets wb;
     wb.load(a.hdr, a.bias, a.n_bounds, LOG2E);
     const float c2 = fabsf(a.scale) * LOG2E;
+    int wp = wq;
     __syncthreads();
     for (;;) {
     const int64_t s = at.s;
@@ -471,14 +495,14 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                 TileBuckets<false> tb;
                 tb.set(wb, k_lo, k_hi, s_range[team][b][u]);
                 if (tb.many && it % turns == 0) {
-                    if (WH > 1) __syncthreads();
-                    tb.find_pairs(s_pairs[wq][u], wh, WH, s_buckets, a.n_bounds, a.cells, s_pos[team][b] + 32 * u, my_pos);
+                    if (BRIEF) wp ^= 1;
+                    tb.find_pairs(s_pairs[wp][u], wh, WH, s_buckets, a.n_bounds, a.cells, s_pos[team][b] + 32 * u, my_pos);
                     if (WH > 1) __syncthreads();
                     else wave_lds_sync();
                 }
                 f32x16 x = mma_rows<T, D>(s_q[team][b], 32 * u, kf, f32x16{});
                 f32x16 dp = mma_rows<T, D>(s_d[team][b], 32 * u, vf, f32x16{});
-                x = tb.logits(x, c2, 0.f, wb, s_pairs[wq][u], s_bias[team][b], s_pos[team][b] + 32 * u, my_pos);
+                x = tb.logits(x, c2, 0.f, wb, s_pairs[wp][u], s_bias[team][b], s_pos[team][b] + 32 * u, my_pos);
                 if (a.causal && i1 < w0 + 31) {
                     const int lim = my_k - i1 - 4 * half;
 #pragma unroll

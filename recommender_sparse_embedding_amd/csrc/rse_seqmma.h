@@ -229,23 +229,24 @@ struct WaveBuckets {
     }
 };
 
-// Lowest and highest of each half of the wave.
-__device__ __forceinline__ int32_t half_min(int32_t x) {
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
-        const int32_t y = __shfl_xor(x, m, WAVE);
-        x = y < x ? y : x;
-    }
-    return x;
+// Lowest and highest of each half of the wave, by rotations within rows of 16
+// lanes and one exchange of rows (no trip through LDS: five dependent
+// shuffles took some 600 cycles of a tile).
+template <int N>
+__device__ __forceinline__ int32_t row_ror(int32_t x) { return __builtin_amdgcn_update_dpp(x, x, 0x120 + N, 0xF, 0xF, false); }
+template <bool MAX>
+__device__ __forceinline__ int32_t half_extreme(int32_t x) {
+    auto pick = [](int32_t a, int32_t b) { return MAX ? (a > b ? a : b) : (a < b ? a : b); };
+    x = pick(x, row_ror<8>(x));
+    x = pick(x, row_ror<4>(x));
+    x = pick(x, row_ror<2>(x));
+    x = pick(x, row_ror<1>(x));
+    const u32x2 s = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
+    return pick((int32_t)s.x, (int32_t)s.y);
 }
-__device__ __forceinline__ int32_t half_max(int32_t x) {
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) {
-        const int32_t y = __shfl_xor(x, m, WAVE);
-        x = y > x ? y : x;
-    }
-    return x;
-}
+__device__ __forceinline__ int32_t half_min(int32_t x) { return half_extreme<false>(x); }
+__device__ __forceinline__ int32_t half_max(int32_t x) { return half_extreme<true>(x); }
+
 constexpr float LOG2E = 1.4426950408889634f;
 // More boundaries than this inside a tile: looked up event by event.
 constexpr int CHAIN = 6;
