@@ -88,7 +88,7 @@ constexpr int FWD_WAVES = D * sizeof(T) <= 64 ? 3 : (D * sizeof(T) == 128 || (D 
 
 template <typename T, int D, typename SH, int S>
 __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(FWD_WAVES<T, D, S>))) void k_attn_fwd(
-    SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k, Rows<const T> v, Rows<T> out, float* lse2, float* out32) {
+    SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k, Rows<const T> v, Rows<T> out, float* lse2, float* out32, int split) {
     constexpr int CH = SH::CH, KT = SH::KT, NS = SH::NS, NB = SH::NB, NT = SH::NT, WH = SH::WH, WQ = SH::WQ, ND = D / 32;
     constexpr bool REST = S == SAVE_OUT && sizeof(T) == 2, BRIEF = SH::TEAM == 1;
     __shared__ u32x4 s_k[SH::TEAMS][NB][KT * CH], s_v[SH::TEAMS][NB][KT * CH];
@@ -103,7 +103,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     const int head = live ? h0 + wh : a.n_heads - 1, g = head / a.group;
     SeqTiles at;
     if (BRIEF) {
-        at.begin(a, blockIdx.x / hblocks, gridDim.x / hblocks, h0 == 0);
+        at.begin(a, blockIdx.x / hblocks, gridDim.x / hblocks, split, h0 == 0);
         if (!at.valid) return;
     } else if (!find_tile(a, grid, blockIdx.x / hblocks, 32 * WQ, a.causal, at.s, at.len, at.tile, h0 == 0)) {
         return;
@@ -238,9 +238,6 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
 }
 
 // ------------------------------------------------------------------ host --
-// Blocks that go through the short sequences: as many as fit the GPU at once.
-constexpr int64_t SHORT_BLOCKS = 512;
-
 template <typename T, int D, int TEAM, int WH, int WQ>
 int run_fwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v,
             const rse_seq_rows* out, const Saved& sv, hipStream_t s) {
@@ -248,16 +245,16 @@ int run_fwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, cons
     constexpr int KEEP = TEAM == 1 ? SAVE : SAVE_OUT;
     const TileGrid tg = tile_grid(a.n_events, a.batch, a.max_len, 32 * WQ);
     const int64_t hblocks = (a.n_heads + WH - 1) / WH;
-    const int64_t some = (SHORT_BLOCKS * 4 / SH::WAVES + hblocks - 1) / hblocks;
-    const int64_t blocks = hblocks * (TEAM > 1 ? tg.items : (a.batch < some ? a.batch : some));
+    const ShortGrid sg = short_grid(a.batch, hblocks, a.max_len, SH::WAVES);
+    const int64_t blocks = hblocks * (TEAM > 1 ? tg.items : sg.blocks);
     if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)blocks), block(SH::WAVES * WAVE);
     if (sv.lse2)
         hipLaunchKernelGGL((k_attn_fwd<T, D, SH, KEEP>), grid, block, 0, s, a, tg, rows_view<const T>(q),
-                           rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), sv.lse2, sv.out32);
+                           rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), sv.lse2, sv.out32, sg.split);
     else
         hipLaunchKernelGGL((k_attn_fwd<T, D, SH, SAVE_NONE>), grid, block, 0, s, a, tg, rows_view<const T>(q),
-                           rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), nullptr, nullptr);
+                           rows_view<const T>(k), rows_view<const T>(v), rows_view<T>(out), nullptr, nullptr, sg.split);
     return launch_status();
 }
 
@@ -360,7 +357,7 @@ int seq_attention_fwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
                 return run_fwd<T, D, 1, 1, 1>(a, q, k, v, out, sv, st);
             }
         if (a.group % 4 == 0) return run_fwd<T, D, 4, 4, 1>(a, q, k, v, out, sv, st);
-        return run_fwd<T, D, 4, 1, 4>(a, q, k, v, out, sv, st);
+        return run_fwd<T, D, LONG_WAVES<T, D>, 1, LONG_WAVES<T, D>>(a, q, k, v, out, sv, st);
     });
 }
 

@@ -240,7 +240,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
 template <typename T, int D, typename SH>
 __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(2))) void k_attn_dq_short(
     SeqArgs a, Rows<const T> q, Rows<const T> k, Rows<const T> v, const float* lse2, Rows<const T> dout, Rows<T> dq,
-    float* delta, float* part, int cols) {
+    float* delta, float* part, int cols, int split) {
     constexpr int CH = SH::CH, KT = SH::KT, NT = SH::NT, WH = SH::WH, ND = D / 32;
     static_assert(SH::TEAM == 1 && SH::WQ == 1 && KT == 32, "waves apart");
     __shared__ u32x4 s_k[WH][KT * CH], s_v[WH][KT * CH];
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     const int head = live ? h0 + w : a.n_heads - 1, g = head / a.group;
     float* hist = s_hist + w * nb * cols;
     SeqTiles at;
-    at.begin(a, blockIdx.x, gridDim.x, h0 == 0);
+    at.begin(a, blockIdx.x, gridDim.x, split, h0 == 0);
 
     RowStage<T, D, NT, KT> st;
     KeySideStage side;
@@ -386,7 +386,7 @@ __global__ __launch_bounds__(256) void k_attn_dbias(const float* part, int block
 template <typename T, int D, typename SH, bool IN_GROUP>
 __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(DKV_WAVES<T, D>))) void k_attn_dkv(
     SeqArgs a, TileGrid grid, Rows<const T> q, Rows<const T> k, Rows<const T> v, const float* lse2, const float* delta,
-    Rows<const T> dout, Rows<T> dk, Rows<T> dv, int by_seq) {
+    Rows<const T> dout, Rows<T> dk, Rows<T> dv, int split) {
     constexpr int CH = SH::CH, KT = SH::KT, NS = SH::NS, NB = SH::NB, NT = SH::NT, WH = SH::WH, WQ = SH::WQ, ND = D / 32,
                   NBP = RSE_SEQ_MAX_BOUNDARIES + 1;
     __shared__ u32x4 s_rows[2][SH::TEAMS][NB][KT * CH];
@@ -407,9 +407,9 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     const int g = IN_GROUP ? g0 : (live ? g0 + wh : n_kv - 1);
     const int turns = IN_GROUP ? a.group / WH : a.group;            // heads one after the other
     SeqTiles at;
-    // by_seq: the block goes on through its sequences' tiles
-    if (BRIEF && by_seq) {
-        at.begin(a, blockIdx.x / gblocks, gridDim.x / gblocks, false);
+    // split > 0: the block goes on through its sequences' tiles
+    if (BRIEF && split) {
+        at.begin(a, blockIdx.x / gblocks, gridDim.x / gblocks, split, false);
         if (!at.valid) return;
     } else if (!find_tile(a, grid, blockIdx.x / gblocks, 32 * WQ, false, at.s, at.len, at.tile, false)) {
         return;
@@ -480,7 +480,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
         team_sync<SH::TEAM>();
         if (it + 1 < total) {
             load(at, it + 1);
-        } else if (BRIEF && by_seq) {
+        } else if (BRIEF && split) {
             at.advance(a);
             if (at.valid) load(at, 0);
         }
@@ -531,7 +531,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
         if (BRIEF) wave_lds_sync();             // read before the next tile is stored
     }
     bool more = false;
-    if (BRIEF) more = by_seq && at.valid;
+    if (BRIEF) more = split && at.valid;
     if (!IN_GROUP) {
         if (my_k < len && live) {
             T* pk = dk.at(s + my_k, g);
@@ -576,14 +576,13 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
 // Blocks of k_attn_dq over all heads: enough to fill the GPU several times
 // over; more would only add partial bucket sums.
 constexpr int64_t DQ_BLOCKS = 2048;
-// Blocks that go through the short sequences: as many as fit the GPU at once.
-constexpr int64_t SHORT_BLOCKS = 512;
 
 struct BwdWs {
     float* delta;
     float* part;
     size_t bytes;
-    int64_t blocks;              // of k_attn_dq, per head
+    int64_t blocks;              // of k_attn_dq, per heads side by side
+    int split;
 };
 
 // The blocks of k_attn_dq, by the rules of the forward.
@@ -592,15 +591,22 @@ struct DqForm {
 };
 DqForm dq_form(const rse_seqattn* a, int64_t max_len) {
     if (short_form(a, max_len)) return {a->n_heads > 1 ? 4 : 1, 1};
-    return a->n_heads / a->n_kv_heads % 4 == 0 ? DqForm{4, 1} : DqForm{1, 4};
+    return a->n_heads / a->n_kv_heads % 4 == 0 ? DqForm{4, 1} : DqForm{1, by_type(a, [](auto t, auto d) { return LONG_WAVES<decltype(t), decltype(d)::value>; })};
 }
 
 BwdWs bwd_ws(const rse_seqattn* a, int64_t n, int64_t batch, int64_t max_len, void* base) {
     BwdWs w;
     const DqForm f = dq_form(a, max_len);
-    w.blocks = short_form(a, max_len) ? batch : tile_grid(n, batch, max_len, 32 * f.wq).items;
-    const int64_t most = DQ_BLOCKS * f.wh / a->n_heads;
-    if (w.blocks > most) w.blocks = most > 16 ? most : 16;
+    if (short_form(a, max_len)) {
+        const ShortGrid g = short_grid(batch, (a->n_heads + f.wh - 1) / f.wh, max_len, f.wh);
+        w.blocks = g.blocks;
+        w.split = g.split;
+    } else {
+        w.blocks = tile_grid(n, batch, max_len, 32 * f.wq).items;
+        const int64_t most = DQ_BLOCKS * f.wh / a->n_heads;
+        if (w.blocks > most) w.blocks = most > 16 ? most : 16;
+        w.split = 1;
+    }
     Carver c(base);
     w.delta = c.take<float>((size_t)a->n_heads * n);
     w.part = c.take<float>((size_t)a->n_heads * w.blocks * (a->n_bounds + 1));
@@ -620,14 +626,15 @@ int run_bwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, cons
     const TileGrid tk = tile_grid(a.n_events, a.batch, a.max_len, 32 * KQ);
     const bool brief = TEAM == 1;
     const int64_t gblocks = IN_GROUP ? n_kv : (n_kv + KH - 1) / KH;
-    const int64_t some = (SHORT_BLOCKS * 4 / KS::WAVES + gblocks - 1) / gblocks;
-    const int64_t blocks = gblocks * (!brief ? tk.items : (a.batch < some ? a.batch : some));
+    const ShortGrid sg = short_grid(a.batch, gblocks, a.max_len, KS::WAVES);
+    const int64_t blocks = gblocks * (brief ? sg.blocks : tk.items);
     if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)w.blocks, (a.n_heads + WH - 1) / WH), block(QS::WAVES * WAVE);
     const size_t lds = QS::WAVES * nb * cols * sizeof(float);
     if constexpr (TEAM == 1)
         hipLaunchKernelGGL((k_attn_dq_short<T, D, QS>), grid, block, lds, s, a, rows_view<const T>(q), rows_view<const T>(k),
-                           rows_view<const T>(v), sv.lse2, rows_view<const T>(dout), rows_view<T>(dq), w.delta, w.part, cols);
+                           rows_view<const T>(v), sv.lse2, rows_view<const T>(dout), rows_view<T>(dq), w.delta, w.part, cols,
+                           w.split);
     else
         hipLaunchKernelGGL((k_attn_dq<T, D, QS>), grid, block, lds, s, a, tq, rows_view<const T>(q), rows_view<const T>(k),
                            rows_view<const T>(v), sv.lse2, sv.out32, rows_view<const T>(dout), rows_view<T>(dq), w.delta,
@@ -637,7 +644,7 @@ int run_bwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, cons
     hipLaunchKernelGGL(k_attn_dbias, dim3(a.n_heads * nb), dim3(256), 0, s, w.part, (int)w.blocks, dbias);
     hipLaunchKernelGGL((k_attn_dkv<T, D, KS, IN_GROUP>), dim3((unsigned)blocks), dim3(KS::WAVES * WAVE), 0, s, a, tk,
                        rows_view<const T>(q), rows_view<const T>(k), rows_view<const T>(v), sv.lse2, w.delta,
-                       rows_view<const T>(dout), rows_view<T>(dk), rows_view<T>(dv), (int)brief);
+                       rows_view<const T>(dout), rows_view<T>(dk), rows_view<T>(dv), brief ? sg.split : 0);
     return launch_status();
 }
 
@@ -680,6 +687,7 @@ int seq_attention_bwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
                 a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
         };
         using I1 = std::integral_constant<int, 1>;
+        using IL = std::integral_constant<int, LONG_WAVES<T, D>>;
         using I4 = std::integral_constant<int, 4>;
         std::true_type in_group;
         std::false_type apart;
@@ -693,8 +701,8 @@ int seq_attention_bwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
             }
         if constexpr (sizeof(T) * D <= 256)
             if (fours) return run(I4(), I4(), I1(), I1(), I4(), I1(), in_group);
-        if (fours) return run(I4(), I4(), I1(), I4(), I1(), I4(), apart);
-        return run(I4(), I1(), I4(), I4(), I1(), I4(), apart);
+        if (fours) return run(I4(), I4(), I1(), IL(), I1(), IL(), apart);
+        return run(IL(), I1(), IL(), IL(), I1(), IL(), apart);
     });
 }
 

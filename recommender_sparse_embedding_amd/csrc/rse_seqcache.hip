@@ -11,7 +11,6 @@ using namespace rse_host;
 namespace {
 
 constexpr int CB = 256;                 // threads per block
-constexpr int CW = CB / WAVE;
 
 __global__ void k_cache_clear(SeqCacheHeader* h) { h->status = 0; }
 

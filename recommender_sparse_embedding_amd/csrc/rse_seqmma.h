@@ -442,10 +442,15 @@ struct SeqTiles {
     int len, tile;
     bool valid;
     int64_t b, step;
+    int phase, stride;                          // the block's tiles: phase, + stride, ...
     int64_t next0, next1;                       // offsets of sequence b + step, as loaded
-    __device__ __forceinline__ void begin(const SeqArgs& a, int64_t first, int64_t blocks, bool check) {
+    // `split` blocks share a sequence's tiles
+    __device__ __forceinline__ void begin(const SeqArgs& a, int64_t block, int64_t n_blocks, int split, bool check) {
+        const int64_t first = block / split, blocks = n_blocks / split;
+        phase = (int)(block % split);
+        stride = split;
         if (check)
-            for (int64_t i = first * blockDim.x + threadIdx.x; i < a.batch; i += blocks * blockDim.x) {
+            for (int64_t i = block * blockDim.x + threadIdx.x; i < a.batch; i += n_blocks * blockDim.x) {
                 const int64_t x = a.offsets[i], y = a.offsets[i + 1];
                 if (x > y || (i == 0 && x != 0) || (i == a.batch - 1 && y != a.n_events))
                     set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
@@ -473,15 +478,32 @@ struct SeqTiles {
                 continue;
             }
             len = (int)(e - s);
-            tile = 0;
-            if (len > 0) return;
+            tile = phase;
+            if (tile * 32 < len) return;
         }
     }
     __device__ __forceinline__ void advance(const SeqArgs& a) {
-        if ((tile + 1) * 32 < len) ++tile;
+        if ((tile + stride) * 32 < len) tile += stride;
         else next_sequence(a);
     }
 };
+
+// Blocks of W waves that go through the short sequences, for `heads` of them
+// side by side: four times as many as fit the GPU at once (what is left over
+// evens out; with as many as fit, dq took 620 us where it takes 553), a
+// sequence's tiles shared by several where there are few sequences.
+struct ShortGrid {
+    int64_t blocks;
+    int split;
+};
+inline ShortGrid short_grid(int64_t batch, int64_t heads, int64_t max_len, int waves) {
+    const int64_t fit = (8192 / waves + heads - 1) / heads;
+    const int64_t seqs = batch < fit ? batch : fit, tiles = (max_len + 31) / 32;
+    int64_t split = seqs > 0 ? fit / seqs : 1;
+    split = split > tiles ? tiles : split;
+    if (split < 1) split = 1;
+    return {seqs * split, (int)split};
+}
 
 // ------------------------------------------------------------------ shapes --
 // A block's waves and what they share.  A team of waves stages tiles of rows
@@ -497,9 +519,15 @@ template <typename T, int D, int TEAM_, int WH_, int WQ_>
 struct Shape {
     static constexpr int TEAM = TEAM_, WH = WH_, WQ = WQ_, WAVES = WH * WQ, TEAMS = WAVES / TEAM;
     static constexpr int RB = D * (int)sizeof(T);       // bytes of a row
-    static constexpr int KT = TEAM > 1 && RB <= 256 ? 64 : 32, NS = KT / 32, NB = TEAM > 1 ? 2 : 1;
+    static constexpr int KT = TEAM > 2 && RB <= 256 ? 64 : 32, NS = KT / 32, NB = TEAM > 1 ? 2 : 1;
     static constexpr int CH = Tile<T, D>::CH, NT = TEAM * WAVE;
 };
+// Waves that share a long sequence's keys, each with a column tile of one
+// head: 2 where that leaves room for several blocks (fp32 dim 32, sequences of
+// 1..203: 525 us a training step with 4, 493 with 2), 4 for wide rows (bf16
+// dim 128, 1..333: forward 46 us with 2, 38 with 4).
+template <typename T, int D>
+constexpr int LONG_WAVES = D * sizeof(T) <= 128 ? 2 : 4;
 template <typename T, int D>
 constexpr bool HAS_SHORT = D * sizeof(T) <= 128;
 

@@ -535,3 +535,56 @@ def test_prompt_then_steps_equal_one_pass():
         held += 1
         free = free[int(taken):].contiguous()
     assert cache.status() == 0 and attn.status() == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_boundaries_on_both_sides(causal, dtype):
+    """Every power of two and its negative, distances over all of int32: tiles
+    that span dozens of buckets, with at most one boundary to a cell."""
+    bounds = sorted([2**m for m in range(31)] + [-(2**m) for m in range(31)])
+    for seed in (0, 1):
+        c = Case([70, 190], 4, 4 if seed else 1, 32, dtype, bounds=bounds, causal=causal, seed=seed)
+        g = torch.Generator().manual_seed(seed)
+        span = torch.randint(-2**31, 2**31, c.pos.shape, generator=g)
+        c.pos = (span >> torch.randint(0, 31, c.pos.shape, generator=g)).to(torch.int32).cuda()
+        c.pos[::11] = 2**31 - 1
+        c.pos[5::11] = -2**31
+        c.check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (4, 4), (5, 5), (8, 2)])
+def test_many_short_sequences(H, Hk, dtype):
+    """More sequences than blocks: each block goes through several, of lengths
+    from none to the limit, some of them hidden."""
+    lens = [(37 * i) % 129 for i in range(700)]
+    c = Case(lens, H, Hk, 32, dtype, missing=0.1)
+    got = c.run()
+    sample = [0, 1, 3, 7, 100, 350, 501, 698, 699]
+    off = np.concatenate([[0], np.cumsum(lens)])
+    keep = np.concatenate([np.arange(off[b], off[b + 1]) for b in sample])
+    part = [lens[b] for b in sample]
+    q, k, v, do = (_np(t)[keep] for t in (c.q, c.k, c.v, c.dout))
+    ref = oseq.attention(q, k, v, c.pos.cpu().numpy()[keep], _np(c.bias), np.concatenate([[0], np.cumsum(part)]),
+                         c.bounds, True, c.attn.scale, c.key_off.cpu().numpy()[keep], do, KIND[dtype])
+    at = torch.from_numpy(keep).cuda()
+    for name in ("out", "dq", "dk", "dv"):
+        _check(got[name][at], ref[name], name)
+    # the bias gradient against the sum over sequence pieces, each run alone
+    total, slack = np.zeros_like(ref["dbias"][0]), np.zeros_like(ref["dbias"][0])
+    for a in range(0, 700, 100):
+        ids = np.arange(off[a], off[a + 100])
+        r = oseq.attention(*(_np(t)[ids] for t in (c.q, c.k, c.v)), c.pos.cpu().numpy()[ids], _np(c.bias),
+                           off[a:a + 101] - off[a], c.bounds, True, c.attn.scale, c.key_off.cpu().numpy()[ids],
+                           _np(c.dout)[ids], KIND[dtype])["dbias"]
+        total, slack = total + r[0], slack + r[1]
+    _check(got["dbias"], (total, slack), "dbias")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_negative_and_zero_scale(dtype):
+    for scale in (-0.3, 0.0):
+        c = Case([50, 200], 4, 1, 64, dtype)
+        c.attn = c.rse.SeqAttention(4, 1, 64, dtype, c.bounds, scale=scale)
+        c.check()
