@@ -74,7 +74,9 @@ __global__ void k_attn_clear(SeqHeader* h) { h->status = 0; }
 // SAVE: also leaves the log-sums for the backward, and SAVE_OUT the outputs:
 // its dO . out has to equal sum_j p dp to fp32 accuracy (the bias gradient
 // sums differences from it), so what bf16 rounds off the probabilities goes
-// through a second product into those outputs.
+// through two more products into those outputs (three bf16 terms hold a
+// float: the bias gradient is then as near to 64 bits as plain fp32 is, 3e-7
+// on 12 sequences of up to 2048 events, 8 heads; 92 -> 98 us).
 enum { SAVE_NONE = 0, SAVE = 1, SAVE_OUT = 2 };
 //
 // Short sequences: a block goes on through its sequences' tiles of queries,
@@ -210,10 +212,13 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
 #pragma unroll
                 for (int dt = 0; dt < ND; ++dt) o[dt] = mma_over_rows<D>(s_v[team][b], 32 * u, dt, p, o[dt]);
                 if (REST) {
-                    RowOperand<T> lo;
-                    lo.set_rest(x, p);
 #pragma unroll
-                    for (int dt = 0; dt < ND; ++dt) rest[dt] = mma_over_rows<D>(s_v[team][b], 32 * u, dt, lo, rest[dt]);
+                    for (int part = 0; part < 2; ++part) {
+                        p.take_from(x);
+                        p.set(x);
+#pragma unroll
+                        for (int dt = 0; dt < ND; ++dt) rest[dt] = mma_over_rows<D>(s_v[team][b], 32 * u, dt, p, rest[dt]);
+                    }
                 }
             }
             if (BRIEF) wave_lds_sync();         // read before the next tile is stored

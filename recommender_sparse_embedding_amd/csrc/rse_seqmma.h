@@ -109,7 +109,7 @@ template <>
 struct RowOperand<float> {
     f32x16 v;
     __device__ __forceinline__ void set(const f32x16& x) { v = x; }
-    __device__ __forceinline__ void set_rest(const f32x16&, const RowOperand&) { v = f32x16{}; }
+    __device__ __forceinline__ void take_from(f32x16& x) const { x = f32x16{}; }
 };
 template <>
 struct RowOperand<uint16_t> {
@@ -120,14 +120,15 @@ struct RowOperand<uint16_t> {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[s][i] = pack_bf16(x[8 * s + 2 * i], x[8 * s + 2 * i + 1]);
     }
-    // what hi's rounding left of x (exact), rounded in turn
-    __device__ __forceinline__ void set_rest(const f32x16& x, const RowOperand& hi) {
+    // x less what is held of it (exact: the rounding's remainder)
+    __device__ __forceinline__ void take_from(f32x16& x) const {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[s][i] = pack_bf16(x[8 * s + 2 * i] - __uint_as_float(hi.v[s][i] << 16),
-                                    x[8 * s + 2 * i + 1] - __uint_as_float(hi.v[s][i] & 0xFFFF0000u));
+            for (int i = 0; i < 4; ++i) {
+                x[8 * s + 2 * i] -= __uint_as_float(v[s][i] << 16);
+                x[8 * s + 2 * i + 1] -= __uint_as_float(v[s][i] & 0xFFFF0000u);
+            }
     }
 };
 
