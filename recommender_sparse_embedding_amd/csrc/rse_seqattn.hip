@@ -104,7 +104,8 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     const bool live = h0 + wh < a.n_heads;
     const int head = live ? h0 + wh : a.n_heads - 1, g = head / a.group;
     SeqTiles at;
-    if (BRIEF) {
+    const bool on = BRIEF && split > 0;         // the block goes on through its sequences' tiles
+    if (on) {
         at.begin(a, blockIdx.x / hblocks, gridDim.x / hblocks, split, h0 == 0);
         if (!at.valid) return;
     } else if (!find_tile(a, grid, blockIdx.x / hblocks, 32 * WQ, a.causal, at.s, at.len, at.tile, h0 == 0)) {
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
             if (k0 + KT < end) {
                 st.load(k, g, v, g, s, k0 + KT, end, a.key_off, t);
                 side.load(a, s, k0 + KT, end, KT, t);
-            } else if (BRIEF) {
+            } else if (on) {
                 at.advance(a);
                 if (at.valid) load_first(at);
             }
@@ -238,20 +239,21 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                     store_column(out32 + ((s + my_q) * a.n_heads + head) * D + 32 * dt, o[dt], inv);
                 }
         }
-        if (!BRIEF || !at.valid) return;
+        if (!on || !at.valid) return;
     }
 }
 
 // ------------------------------------------------------------------ host --
-template <typename T, int D, int TEAM, int WH, int WQ>
+// KEEP: what a forward before a backward leaves; SAVE is the short form.
+template <typename T, int D, int TEAM, int WH, int WQ, int KEEP>
 int run_fwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v,
             const rse_seq_rows* out, const Saved& sv, hipStream_t s) {
     using SH = Shape<T, D, TEAM, WH, WQ>;
-    constexpr int KEEP = TEAM == 1 ? SAVE : SAVE_OUT;
     const TileGrid tg = tile_grid(a.n_events, a.batch, a.max_len, 32 * WQ);
     const int64_t hblocks = (a.n_heads + WH - 1) / WH;
-    const ShortGrid sg = short_grid(a.batch, hblocks, a.max_len, SH::WAVES);
-    const int64_t blocks = hblocks * (TEAM > 1 ? tg.items : sg.blocks);
+    ShortGrid sg = {0, 0};
+    if (KEEP == SAVE) sg = short_grid(a.batch, hblocks, a.max_len, SH::WAVES);
+    const int64_t blocks = hblocks * (KEEP == SAVE ? sg.blocks : tg.items);
     if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)blocks), block(SH::WAVES * WAVE);
     if (sv.lse2)
@@ -358,11 +360,13 @@ int seq_attention_fwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
         const hipStream_t st = as_stream(stream);
         if constexpr (HAS_SHORT<T, D>)
             if (short_form(attn, batch->max_len)) {
-                if (a.n_heads > 1) return run_fwd<T, D, 1, 4, 1>(a, q, k, v, out, sv, st);
-                return run_fwd<T, D, 1, 1, 1>(a, q, k, v, out, sv, st);
+                if (a.n_heads > 1) return run_fwd<T, D, 1, 4, 1, SAVE>(a, q, k, v, out, sv, st);
+                return run_fwd<T, D, 1, 1, 1, SAVE>(a, q, k, v, out, sv, st);
             }
-        if (a.group % 4 == 0) return run_fwd<T, D, 4, 4, 1>(a, q, k, v, out, sv, st);
-        return run_fwd<T, D, LONG_WAVES<T, D>, 1, LONG_WAVES<T, D>>(a, q, k, v, out, sv, st);
+        if (a.group % 4 == 0) return run_fwd<T, D, 4, 4, 1, SAVE_OUT>(a, q, k, v, out, sv, st);
+        if constexpr (LONG_APART<T, D>)
+            if (a.n_heads > 2) return run_fwd<T, D, 1, 4, 1, SAVE_OUT>(a, q, k, v, out, sv, st);
+        return run_fwd<T, D, LONG_WAVES<T, D>, 1, LONG_WAVES<T, D>, SAVE_OUT>(a, q, k, v, out, sv, st);
     });
 }
 

@@ -591,7 +591,10 @@ struct DqForm {
 };
 DqForm dq_form(const rse_seqattn* a, int64_t max_len) {
     if (short_form(a, max_len)) return {a->n_heads > 1 ? 4 : 1, 1};
-    return a->n_heads / a->n_kv_heads % 4 == 0 ? DqForm{4, 1} : DqForm{1, by_type(a, [](auto t, auto d) { return LONG_WAVES<decltype(t), decltype(d)::value>; })};
+    if (a->n_heads / a->n_kv_heads % 4 == 0) return {4, 1};
+    const bool apart = by_type(a, [](auto t, auto d) { return LONG_APART<decltype(t), decltype(d)::value>; });
+    if (apart && a->n_heads > 2) return {4, 1};
+    return {1, by_type(a, [](auto t, auto d) { return LONG_WAVES<decltype(t), decltype(d)::value>; })};
 }
 
 BwdWs bwd_ws(const rse_seqattn* a, int64_t n, int64_t batch, int64_t max_len, void* base) {
@@ -614,7 +617,7 @@ BwdWs bwd_ws(const rse_seqattn* a, int64_t n, int64_t batch, int64_t max_len, vo
     return w;
 }
 
-template <typename T, int D, int TEAM, int WH, int WQ, int KTEAM, int KH, int KQ, bool IN_GROUP>
+template <typename T, int D, int TEAM, int WH, int WQ, int KTEAM, int KH, int KQ, bool IN_GROUP, bool brief>
 int run_bwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v, const Saved& sv,
             const rse_seq_rows* dout, const rse_seq_rows* dq, const rse_seq_rows* dk, const rse_seq_rows* dv,
             float* dbias, const BwdWs& w, hipStream_t s) {
@@ -624,14 +627,13 @@ int run_bwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, cons
     const int cols = nb <= 32 ? 64 : 32;        // at most 32 KiB a block of 4 waves up to 64 buckets, 64 KiB past that
     const TileGrid tq = tile_grid(a.n_events, a.batch, a.max_len, 32 * WQ);
     const TileGrid tk = tile_grid(a.n_events, a.batch, a.max_len, 32 * KQ);
-    const bool brief = TEAM == 1;
     const int64_t gblocks = IN_GROUP ? n_kv : (n_kv + KH - 1) / KH;
     const ShortGrid sg = short_grid(a.batch, gblocks, a.max_len, KS::WAVES);
     const int64_t blocks = gblocks * (brief ? sg.blocks : tk.items);
     if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)w.blocks, (a.n_heads + WH - 1) / WH), block(QS::WAVES * WAVE);
     const size_t lds = QS::WAVES * nb * cols * sizeof(float);
-    if constexpr (TEAM == 1)
+    if constexpr (brief)
         hipLaunchKernelGGL((k_attn_dq_short<T, D, QS>), grid, block, lds, s, a, rows_view<const T>(q), rows_view<const T>(k),
                            rows_view<const T>(v), sv.lse2, rows_view<const T>(dout), rows_view<T>(dq), w.delta, w.part, cols,
                            w.split);
@@ -682,27 +684,33 @@ int seq_attention_bwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
     return by_type(attn, [&](auto t, auto d) {
         using T = decltype(t);
         constexpr int D = decltype(d)::value;
-        auto run = [&](auto team, auto wh, auto wq, auto kteam, auto kh, auto kq, auto in_group) {
-            return run_bwd<T, D, team.value, wh.value, wq.value, kteam.value, kh.value, kq.value, in_group.value>(
+        auto run = [&](auto team, auto wh, auto wq, auto kteam, auto kh, auto kq, auto in_group, auto brief) {
+            return run_bwd<T, D, team.value, wh.value, wq.value, kteam.value, kh.value, kq.value, in_group.value, brief.value>(
                 a, q, k, v, sv, dout, dq, dk, dv, d_dbias, w, s);
         };
         using I1 = std::integral_constant<int, 1>;
         using IL = std::integral_constant<int, LONG_WAVES<T, D>>;
         using I4 = std::integral_constant<int, 4>;
-        std::true_type in_group;
-        std::false_type apart;
+        std::true_type in_group, brief;
+        std::false_type apart, full;
         const bool fours = a.group % 4 == 0;
         // (dq's team, heads, tiles; dkv's)
-        if constexpr (HAS_SHORT<T, D>)
+        if constexpr (HAS_SHORT<T, D>) {
             if (short_form(attn, batch->max_len)) {
-                if (a.n_heads == 1) return run(I1(), I1(), I1(), I1(), I1(), I1(), apart);
-                if (fours) return run(I1(), I4(), I1(), I1(), I4(), I1(), in_group);
-                return run(I1(), I4(), I1(), I1(), I4(), I1(), apart);
+                if (a.n_heads == 1) return run(I1(), I1(), I1(), I1(), I1(), I1(), apart, brief);
+                if (fours) return run(I1(), I4(), I1(), I1(), I4(), I1(), in_group, brief);
+                return run(I1(), I4(), I1(), I1(), I4(), I1(), apart, brief);
             }
+        }
         if constexpr (sizeof(T) * D <= 256)
-            if (fours) return run(I4(), I4(), I1(), I1(), I4(), I1(), in_group);
-        if (fours) return run(I4(), I4(), I1(), IL(), I1(), IL(), apart);
-        return run(IL(), I1(), IL(), IL(), I1(), IL(), apart);
+            if (fours) return run(I4(), I4(), I1(), I1(), I4(), I1(), in_group, full);
+        if (fours) return run(I4(), I4(), I1(), IL(), I1(), IL(), apart, full);
+        if constexpr (LONG_APART<T, D>)
+            if (a.n_heads > 2) {
+                if (attn->n_kv_heads > 2) return run(I1(), I4(), I1(), I1(), I4(), I1(), apart, full);
+                return run(I1(), I4(), I1(), IL(), I1(), IL(), apart, full);
+            }
+        return run(IL(), I1(), IL(), IL(), I1(), IL(), apart, full);
     });
 }
 

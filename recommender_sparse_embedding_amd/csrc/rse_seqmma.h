@@ -523,10 +523,17 @@ struct Shape {
     static constexpr int KT = TEAM > 2 && RB <= 256 ? 64 : 32, NS = KT / 32, NB = TEAM > 1 ? 2 : 1;
     static constexpr int CH = Tile<T, D>::CH, NT = TEAM * WAVE;
 };
-// Waves that share a long sequence's keys, each with a column tile of one
-// head: 2 where that leaves room for several blocks (fp32 dim 32, sequences of
-// 1..203: 525 us a training step with 4, 493 with 2), 4 for wide rows (bf16
-// dim 128, 1..333: forward 46 us with 2, 38 with 4).
+// Long sequences whose heads do not share keys by fours:
+//  - fp32 rows of 128 bytes: the matrix products are 8 times as long as in
+//    bf16 and the staging beside them free, so waves apart (even work) win:
+//    512 sequences of 1..203, both ways, dq 217 -> 160 us;
+//  - else teams, each wave with a column tile of one head: of 2 where that
+//    leaves room for several blocks (the same sequences 525 -> 493 us a
+//    training step; bf16 dim 64, 16 of up to 4096: forward 318 us, 396 with
+//    waves apart), of 4 for wide rows (bf16 dim 128, 1..333: forward 38 us, 46
+//    with 2).
+template <typename T, int D>
+constexpr bool LONG_APART = sizeof(T) == 4 && D == 32;
 template <typename T, int D>
 constexpr int LONG_WAVES = D * sizeof(T) <= 128 ? 2 : 4;
 template <typename T, int D>
