@@ -55,8 +55,33 @@ __device__ __forceinline__ void add_bucket(float* hist, int cols, int bucket, fl
     if (lane_id() < 32) hist[bucket * cols + lane_id()] += sum;
     wave_lds_sync();
 }
-// Up to so many buckets of a tile are summed in registers.
-constexpr int SUMS = 3;
+__device__ __forceinline__ void add_one(float* hist, int cols, int bucket, const f32x16& x) {
+    float sum = x[0];
+#pragma unroll
+    for (int r = 1; r < 16; ++r) sum += x[r];
+    add_bucket(hist, cols, bucket, sum);
+}
+
+// A tile's ds into the bucket sums: up to SUMS buckets one by one in
+// registers, else pair by pair.  (dq of 12 sequences of up to 2048 events: 195
+// us with only single buckets in registers, 172 with 2, 156 with 3, 154 with 7.)
+constexpr int SUMS = 7;
+
+__device__ __forceinline__ void add_tile(float* hist, int cols, const TileBuckets<true>& tb, const int (&idx)[16], const f32x16& x) {
+    if (tb.lo == tb.hi) {
+        add_one(hist, cols, tb.lo, x);
+    } else if (tb.hi - tb.lo < SUMS) {
+#pragma unroll 1
+        for (int bk = tb.lo; bk <= tb.hi; ++bk) {
+            float sum = 0.f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sum += idx[r] == bk ? x[r] : 0.f;
+            add_bucket(hist, cols, bk, sum);
+        }
+    } else {
+        add_pairs(hist, cols, idx, x);
+    }
+}
 
 // A block's bucket sums of each head, over its WQ waves and their columns: 8
 // lanes each, in a fixed order.
@@ -192,22 +217,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                 }
 #pragma unroll
                 for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(x[r]) * (dp[r] - del);
-                if (tb.lo == tb.hi) {
-                    float sum = x[0];
-#pragma unroll
-                    for (int r = 1; r < 16; ++r) sum += x[r];
-                    add_bucket(hist, cols, tb.lo, sum);
-                } else if (tb.hi - tb.lo < SUMS) {
-#pragma unroll 1
-                    for (int bk = tb.lo; bk <= tb.hi; ++bk) {
-                        float sum = 0.f;
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) sum += idx[r] == bk ? x[r] : 0.f;
-                        add_bucket(hist, cols, bk, sum);
-                    }
-                } else {
-                    add_pairs(hist, cols, idx, x);
-                }
+                add_tile(hist, cols, tb, idx, x);
                 RowOperand<T> ds;
                 ds.set(x);
 #pragma unroll
@@ -335,11 +345,8 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
 #pragma unroll
                 for (int r = 0; r < 16; ++r) x[r] *= dp[r] - del;
                 if (tb.lo == tb.hi) {
-                    float sum = x[0];
-#pragma unroll
-                    for (int r = 1; r < 16; ++r) sum += x[r];
-                    add_bucket(hist, cols, tb.lo, sum);
-                } else {
+                    add_one(hist, cols, tb.lo, x);
+                } else {                        // (sums in registers, as add_tile's, took 771 us here for 566)
                     int idx[16];
                     tb.index(idx, wb, s_pairs[wp], ks.pos, my_pos);
                     add_pairs(hist, cols, idx, x);
