@@ -271,7 +271,8 @@ struct LdsBuckets {
 //  - one bucket (most tiles of a long history): the bias is a constant;
 //  - up to CHAIN boundaries: each is passed by the rows on one side of a
 //    position that is the lane's own (col_pos -/+ the boundary, saturated),
-//    one comparison per pair and boundary.  A saturated threshold is met
+//    one comparison per pair and boundary (all sixteen before their uses: a
+//    selection right behind its comparison waits for it).  A saturated threshold is met
 //    wrongly only by a row at the very end of int32: such tiles go with
 //  - many: every pair is looked up (find_pairs), into LDS as bytes in the
 //    order of the registers, so that the heads share the work.
@@ -339,15 +340,23 @@ struct TileBuckets {
             {
                 const int32_t th = threshold(wb, lo, col_pos);
                 const float bm = wb.value(lo + 1) + shift;
+                bool c[16];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) b[r] = passed(p[r], th) ? bm : b0;
+                for (int r = 0; r < 16; ++r) c[r] = passed(p[r], th);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) b[r] = c[r] ? bm : b0;
             }
 #pragma unroll 1
             for (int m = lo + 1; m < hi; ++m) {
                 const int32_t th = threshold(wb, m, col_pos);
                 const float bm = wb.value(m + 1) + shift;
+                bool c[16];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) b[r] = passed(p[r], th) ? bm : b[r];
+                for (int r = 0; r < 16; ++r) c[r] = passed(p[r], th);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) b[r] = c[r] ? bm : b[r];
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], c, b[r]);
