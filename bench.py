@@ -141,15 +141,20 @@ def ceilings():
 
 
 def kernel_sources_sha() -> str:
-    """Hash of the HIP sources and headers the library is built from: stored
-    counter summaries apply only to the kernels they were taken on."""
+    """Hash of the HIP sources and headers that the step's kernels are built
+    from: stored counter summaries apply only to the kernels they were taken
+    on.  The sequence attention (rse_seq* and its part of rse.h) is not in
+    the step."""
     h = hashlib.sha256()
     files = sorted(glob.glob(os.path.join(ROOT, "recommender_sparse_embedding_amd", "csrc", "*")))
+    files = [f for f in files if not os.path.basename(f).startswith("rse_seq")]
     files.append(os.path.join(ROOT, "include", "rse.h"))
     for f in files:
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:
-            h.update(fh.read())
+            text = fh.read()
+        a, b = text.find(b"/* " + b"-" * 31 + b" attention over"), text.find(b"/* " + b"-" * 55 + b" kernel trace")
+        h.update(text[:a] + text[b:] if 0 < a < b else text)
     return h.hexdigest()[:16]
 
 
