@@ -547,8 +547,9 @@ int dlrm_interaction_bwd(const float* d_dense, const float* d_pooled, const floa
  *             that i may see: those whose key_off is not negative and, when
  *             causal, that do not come after i
  *   out_ih  = sum_j p_ij v_jg
- * An event that may see none gets out = 0 and lse = -infinity, and no
- * gradient.  Keys and values that no event may see (a negative key_off: a
+ * A bias of -1e30 or below hides its pairs like -infinity (the type's lowest
+ * value as a mask).  An event that may see none gets out = 0 and
+ * lse = -infinity, and no gradient.  Keys and values that no event may see (a negative key_off: a
  * lookup that found no row) are never used, whatever they hold; a value that
  * is not finite in a visible place may reach every event of its sequence.
  *
@@ -690,8 +691,8 @@ int rse_seqattn_step_workspace_size(const rse_seqattn* attn, int64_t batch, int6
  * formulas above (key_off aside; the event is the last, so causal or not is
  * the same).  d_lens[b] < 0: the user is idle, out[b] = 0 and nothing is
  * stored.  d_lens[b] + 1 > max_len or past the table, or a page out of the
- * pool: RSE_ERR_BAD_INPUT in the cache's status and out[b] = 0 (a bad page's
- * events left out).  Slots behind a history are not used, whatever they
+ * pool: RSE_ERR_BAD_INPUT in the cache's status and out[b] = 0 (of a bad
+ * page, only its cached events are left out).  Slots behind a history are not used, whatever they
  * hold.  The lengths are not changed: the caller adds 1.
  */
 int seq_attention_step(const rse_seqattn* attn, rse_seqcache* cache, const rse_seq_rows* q, const rse_seq_rows* k,

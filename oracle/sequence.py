@@ -38,6 +38,8 @@ def _one(q, k, v, pos, bias, key_off, boundaries, causal, scale, do=None):
         see &= (key_off >= 0)[None, :]
     k = np.where(see.any(0)[:, None], k, 0.0)    # what nobody sees is not used
     v = np.where(see.any(0)[:, None], v, 0.0)
+    see &= bias[cell] > -1e30                    # a bias that hides its pairs; their k and v are still read
+    bias = np.where(bias > -1e30, bias, 0.0)
     s = scale * (q @ k.T) + bias[cell]
     # an exponent's error: D products, the scale, the bias, the difference
     # from the row's statistic, the conversion to base 2

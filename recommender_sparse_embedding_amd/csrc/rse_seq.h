@@ -77,6 +77,11 @@ __device__ __forceinline__ int seq_bucket_cell(const uint8_t* cell, const int32_
     return e < n_bounds ? e : n_bounds;
 }
 
+// A bias in base 2.  One that far down, the type's lowest value as a mask for
+// example, hides its pairs like -infinity: such a sum holds nothing of the
+// score, and in base 2 the lowest value would overflow.
+__device__ __forceinline__ float bias2(float b) { return b <= -1e30f ? -INFINITY : b * 1.4426950408889634f; }
+
 // Wave-level ordering of a wave's own LDS writes before its other lanes read them.
 __device__ __forceinline__ void wave_lds_sync() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");

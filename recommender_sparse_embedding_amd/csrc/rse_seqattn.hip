@@ -131,7 +131,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     };
     load_first(at);
     WaveBuckets wb;
-    wb.load(a.hdr, a.bias + head * nb, a.n_bounds, LOG2E);
+    wb.load(a.hdr, a.bias + head * nb, a.n_bounds);
     s_buckets.load(a.hdr);
     if (wq == 0) {
         s_bias[wh][lane] = wb.bias[0];

@@ -131,7 +131,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     float* hist = s_hist + w * nb * cols;
 
     WaveBuckets wb;
-    wb.load(a.hdr, a.bias + head * nb, a.n_bounds, LOG2E);
+    wb.load(a.hdr, a.bias + head * nb, a.n_bounds);
     s_buckets.load(a.hdr);
     if (wq == 0) {
         s_bias[wh][lane] = wb.bias[0];
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     };
     if (at.valid) load_first(at);
     WaveBuckets wb;
-    wb.load(a.hdr, a.bias + head * nb, a.n_bounds, LOG2E);
+    wb.load(a.hdr, a.bias + head * nb, a.n_bounds);
     s_buckets.load(a.hdr);
     s_bias[w][lane] = wb.bias[0];
     s_bias[w][64 + lane] = wb.bias[1];
@@ -458,13 +458,13 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
         }
 #pragma unroll
         for (int i = 0; i * NT < NBP; ++i)
-            if (i * NT + t < NBP) s_bias[team][b][i * NT + t] = rb[i] * LOG2E;
+            if (i * NT + t < NBP) s_bias[team][b][i * NT + t] = bias2(rb[i]);
     };
 
     load(at, 0);
     s_buckets.load(a.hdr);
     WaveBuckets wb;
-    wb.load(a.hdr, a.bias, a.n_bounds, LOG2E);
+    wb.load(a.hdr, a.bias, a.n_bounds);
     const float c2 = fabsf(a.scale) * LOG2E;
     int wp = wq;
     __syncthreads();

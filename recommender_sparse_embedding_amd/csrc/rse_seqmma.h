@@ -209,13 +209,13 @@ struct WaveBuckets {
     int32_t bnd[2];
     float bias[2];
     int n;
-    __device__ __forceinline__ void load(const SeqHeader* hdr, const float* head_bias, int n_bounds, float factor) {
+    __device__ __forceinline__ void load(const SeqHeader* hdr, const float* head_bias, int n_bounds) {
         n = n_bounds;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int at = 64 * u + lane_id();
             bnd[u] = hdr->bounds[at];
-            bias[u] = at <= n_bounds ? head_bias[at] * factor : 0.f;
+            bias[u] = at <= n_bounds ? bias2(head_bias[at]) : 0.f;
         }
     }
     __device__ __forceinline__ int bucket(int32_t d) const {

@@ -588,3 +588,45 @@ def test_negative_and_zero_scale(dtype):
         c = Case([50, 200], 4, 1, 64, dtype)
         c.attn = c.rse.SeqAttention(4, 1, 64, dtype, c.bounds, scale=scale)
         c.check()
+
+
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(torch.float32).min, -1e30])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_bias_that_hides(low, dtype):
+    """Buckets whose bias is -infinity, the lowest value or -1e30 hide their
+    pairs: each event sees the two before it, the first ones nothing."""
+    c = Case([1, 40, 150], 2, 1, 32, dtype, bounds=(0, 1, 3), times=False)
+    c.bias[:, 1] = low                           # the event itself
+    c.bias[:, 3] = low                           # three events back and further
+    c.check()
+    got = c.run()
+    first = torch.tensor([0, 1, 41]).cuda()
+    assert all(torch.all(torch.isfinite(got[n])) for n in ("out", "dq", "dk", "dv", "dbias"))
+    assert torch.all(got["out"][first] == 0) and torch.all(got["dq"][first] == 0)
+    assert torch.all(got["dbias"][:, [1, 3]] == 0)
+
+
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(torch.float32).min])
+@pytest.mark.parametrize("lens", [[0, 40, 5], [0, 2000]])
+def test_step_bias_that_hides(lens, low):
+    """The event itself and what is long past hidden: nothing is left of a user
+    without history, and whole parts of a long one."""
+    c = Serving(lens, 4, 1, 64, BF16, bounds=(0, 1, 300))
+    c.bias[:, 1] = low
+    c.bias[:, 3] = low
+    out = c.check()
+    assert torch.all(out[0] == 0) and torch.all(torch.isfinite(out))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,Hk", [(4, 1), (3, 3)])
+def test_most_buckets_and_wide_rows(H, Hk, D, dtype):
+    """127 boundaries with the widest rows: the largest use of LDS."""
+    Case([20, 170], H, Hk, D, dtype, bounds=tuple(range(1, 128)), times=False).check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H,Hk", [(64, 1), (33, 1), (8, 8)])
+def test_step_most_buckets_and_heads(H, Hk, dtype):
+    Serving([150, 700, 0], H, Hk, 128, dtype, bounds=tuple(range(1, 128))).check()

@@ -49,6 +49,24 @@ def test_oracle_matches_autograd(causal):
         np.testing.assert_allclose(got[name][0], x.grad.numpy(), rtol=1e-10, atol=1e-12)
 
 
+@pytest.mark.parametrize("low", [-np.inf, float(np.finfo(np.float32).min), -1e30])
+def test_oracle_bias_that_hides(low):
+    """Distances of 0 and of 3 or more hidden by their bias: each event sees the
+    two before it, the first one nothing."""
+    rng = np.random.default_rng(8)
+    q, k, v, do = (rng.standard_normal((6, 1, 4)) for _ in range(4))
+    bias = np.array([[0.5, low, 0.25, low]])
+    got = oseq.attention(q, k, v, np.arange(6), bias, [0, 6], [0, 1, 3], True, 0.5, None, do)
+    assert np.all(got["out"][0][0] == 0) and got["lse"][0, 0] == -np.inf and np.all(got["dq"][0][0] == 0)
+    for i in range(1, 6):
+        js = list(range(max(i - 2, 0), i))
+        e = np.exp(0.5 * k[js, 0] @ q[i, 0] + 0.25)
+        np.testing.assert_allclose(got["out"][0][i, 0], e @ v[js, 0] / e.sum(), rtol=1e-12)
+        np.testing.assert_allclose(got["lse"][0, i], np.log(e.sum()), rtol=1e-12)
+    assert got["dbias"][0][0, 1] == 0 and got["dbias"][0][0, 3] == 0
+    assert all(np.all(np.isfinite(x)) for n in ("out", "dq", "dk", "dv", "dbias") for x in got[n])
+
+
 def test_oracle_gradients_match_differences():
     rng = np.random.default_rng(6)
     q, k, v, pos, bias, off, bounds = _case(rng, [6, 2], 2, 1, 3, 5)
