@@ -389,6 +389,234 @@ __global__ __launch_bounds__(SW * 64) __attribute__((amdgpu_waves_per_eu(STEP_WA
     }
 }
 
+// Sum over the LR lanes that share a row, in every one of them.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x) {
+    return x + __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(x), CTRL, 0xF, 0xF, false));
+}
+template <int LR>
+__device__ __forceinline__ float row_sum(float x) {
+    x = dpp_add<0xB1>(x);                       // the other of a pair, the other pair of four,
+    x = dpp_add<0x4E>(x);
+    x = dpp_add<0x141>(x);                      // 8 mirrored, 16 mirrored
+    if (LR >= 16) x = dpp_add<0x140>(x);
+    if (LR >= 32) x += __shfl_xor(x, 16, WAVE);
+    return x;
+}
+
+// The same in fp32 for few heads a key/value head.  Products of tiles would
+// fill as few of the matrix cores' 32 columns, at 64 cycles for two of the
+// summed elements; here LR = D / 4 lanes hold a row in 16-byte pieces, a wave
+// FEW_LOADS loads of 64 / LR rows, and each lane multiplies its piece for all
+// NH heads.  Each group of LR lanes keeps the softmax of the rows that it
+// took; they are joined at the end.
+constexpr int FEW_LOADS = 8;
+
+template <int D, int NH>
+__global__ __launch_bounds__(SW * 64) void k_step_few(StepArgs a, Rows<const float> q, Rows<const float> k,
+                                                      Rows<const float> v, float* kp, float* vp, Rows<float> out,
+                                                      int splits, float* part_o, float* part_ml) {
+    constexpr int LR = D / 4, RG = WAVE / LR, NI = FEW_LOADS, TE = NI * RG;
+    extern __shared__ float s_few[];            // bias in base 2 [nb][NH]
+    __shared__ int32_t s_bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
+    __shared__ float s_ml[SW][2][NH];
+    __shared__ float s_sum[SW][NH][D];
+    const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), piece = lane % LR, row = lane / LR;
+    const int n_kv = a.n_heads / a.group, nb = a.n_bounds + 1, nc = a.group;
+    int64_t x = blockIdx.x;
+    const int split = (int)(x % splits);
+    x /= splits;
+    const int g = (int)(x % n_kv);
+    const int64_t b = x / n_kv;
+    const int h0 = g * nc;
+
+    for (int t = threadIdx.x; t <= RSE_SEQ_MAX_BOUNDARIES; t += SW * 64) s_bounds[t] = a.hdr->bounds[t];
+    for (int t = threadIdx.x; t < nb * NH; t += SW * 64) {
+        const int c = t % NH;
+        s_few[t] = bias2(a.bias[(h0 + (c < nc ? c : nc - 1)) * nb + t / NH]);
+    }
+    int64_t n = uniform(a.lens[b]);
+    if (!step_ok(a, n)) n = -1;
+    const int64_t nt = (n + TE) / TE, t0 = nt * split / splits, t1 = nt * (split + 1) / splits;
+    const int32_t my_pos = a.pos[b];
+    const int64_t row_elems = (int64_t)n_kv * D;
+    const float *k_new = k.at(b, g) + piece * 4, *v_new = v.at(b, g) + piece * 4;
+    if (n >= 0 && split == 0 && w == 0) {                           // the new event into its page
+        const int64_t s = slot_of(a, b, n);
+        if (s >= 0 && lane < LR) {
+            gstore_u4(kp + s * row_elems + g * D + piece * 4, gload_u4(k_new));
+            gstore_u4(vp + s * row_elems + g * D + piece * 4, gload_u4(v_new));
+            if (g == 0 && lane == 0) a.tp[s] = my_pos;
+        }
+    }
+    f32x4 qf[NH];
+#pragma unroll
+    for (int c = 0; c < NH; ++c)
+        qf[c] = __builtin_bit_cast(f32x4, gload_u4(q.at(b, h0 + (c < nc ? c : nc - 1)) + piece * 4));
+    const float c2 = a.scale * LOG2E;
+    __syncthreads();
+
+    // lane j < TE looks event j of a tile up: its page two tiles ahead, its
+    // slot (-1: the new event's rows, also for lanes that may not look) and
+    // time one ahead
+    auto page_of = [&](int64_t t) -> int64_t {
+        const int64_t e = t * TE + lane;
+        return t < t1 && lane < TE && e < n ? (int64_t)a.table[b * a.max_pages + (e >> a.shift)] : 0;
+    };
+    int64_t slot = -1;
+    int32_t rp = my_pos;
+    bool see = false;
+    auto look = [&](int64_t t, int64_t page) {
+        const int64_t e = t * TE + lane;
+        slot = -1;
+        rp = my_pos;
+        see = lane < TE && e <= n;
+        if (t < t1 && lane < TE && e < n) {
+            if (page < 0 || page >= a.n_pages) {
+                set_status(&a.status->status, RSE_ERR_BAD_INPUT);
+                see = false;
+            } else {
+                slot = (page << a.shift) + (e & ((1ll << a.shift) - 1));
+                rp = a.tp[slot];
+            }
+        }
+    };
+    // a tile's rows, from each lane's piece of the pool
+    const int64_t mine = (int64_t)g * D + piece * 4;
+    auto load = [&](u32x4 (&r)[NI], const float* pool, const float* fresh, int64_t sl) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int64_t at = __shfl(sl, i * RG + row, WAVE);
+            r[i] = gload_u4(at < 0 ? fresh : pool + at * row_elems + mine);
+        }
+    };
+
+    f32x4 o[NH] = {};
+    float m[NH], l[NH];
+#pragma unroll
+    for (int c = 0; c < NH; ++c) {
+        m[c] = -INFINITY;
+        l[c] = 0.f;
+    }
+    u32x4 rk[NI], rv[NI];
+    int64_t t = t0 + w;
+    if (t < t1) {
+        look(t, page_of(t));
+        load(rk, kp, k_new, slot);
+    }
+    int64_t page = page_of(t + SW);
+    for (; t < t1; t += SW) {
+        load(rv, vp, v_new, slot);
+        const uint64_t seen = __ballot(see);
+        const int idx = seq_bucket(s_bounds, a.n_bounds, seq_dist(my_pos, rp));
+        const int lo = __builtin_amdgcn_readfirstlane(idx);
+        const bool one = __all(idx == lo || lane >= TE);
+        float s[NI][NH];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const f32x4 kk = __builtin_bit_cast(f32x4, rk[i]);
+#pragma unroll
+            for (int c = 0; c < NH; ++c) {
+                float d = kk[0] * qf[c][0];
+#pragma unroll
+                for (int u = 1; u < 4; ++u) d = __builtin_fmaf(kk[u], qf[c][u], d);
+                s[i][c] = row_sum<LR>(d);
+            }
+        }
+        look(t + SW, page);
+        page = page_of(t + 2 * SW);
+        if (t + SW < t1) load(rk, kp, k_new, slot);
+        if (one) {
+#pragma unroll
+            for (int c = 0; c < NH; ++c) {
+                const float b0 = s_few[lo * NH + c];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) s[i][c] = __builtin_fmaf(s[i][c], c2, b0);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const float* bias = s_few + __shfl(idx, i * RG + row, WAVE) * NH;
+#pragma unroll
+                for (int c = 0; c < NH; ++c) s[i][c] = __builtin_fmaf(s[i][c], c2, bias[c]);
+            }
+        }
+        if (seen != (TE == WAVE ? ~0ull : (1ull << (TE % WAVE)) - 1)) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const bool here = (seen >> (i * RG + row)) & 1;
+                if (!here) rv[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int c = 0; c < NH; ++c) s[i][c] = here ? s[i][c] : -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < NH; ++c) {
+            float top = s[0][c];
+#pragma unroll
+            for (int i = 1; i < NI; ++i) top = fmaxf(top, s[i][c]);
+            const float ref = fmaxf(m[c], top);
+            if (__any(ref > m[c])) {
+                const float r = ref == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[c] - ref);
+                m[c] = ref;
+                l[c] *= r;
+                o[c] *= r;
+            }
+            const float shift = m[c] == -INFINITY ? 0.f : m[c];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const float p = __builtin_amdgcn_exp2f(s[i][c] - shift);
+                const f32x4 vv = __builtin_bit_cast(f32x4, rv[i]);
+                l[c] += p;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) o[c][u] = __builtin_fmaf(p, vv[u], o[c][u]);
+            }
+        }
+    }
+    // the wave's groups of lanes, then its waves, then (k_step_join) the parts
+#pragma unroll
+    for (int c = 0; c < NH; ++c) {
+        float M = m[c];
+#pragma unroll
+        for (int u = LR; u < WAVE; u *= 2) M = fmaxf(M, __shfl_xor(M, u, WAVE));
+        const float r = M == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[c] - M);
+        l[c] *= r;
+        o[c] *= r;
+#pragma unroll
+        for (int u = LR; u < WAVE; u *= 2) {
+            l[c] += __shfl_xor(l[c], u, WAVE);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[c][e] += __shfl_xor(o[c][e], u, WAVE);
+        }
+        if (lane < LR) *reinterpret_cast<f32x4*>(&s_sum[w][c][piece * 4]) = o[c];
+        if (lane == 0) {
+            s_ml[w][0][c] = M;
+            s_ml[w][1][c] = l[c];
+        }
+    }
+    __syncthreads();
+    for (int y = threadIdx.x; y < nc * D; y += SW * 64) {
+        const int c = y / D, d = y % D;
+        float M = -INFINITY, L = 0.f, O = 0.f;
+        for (int u = 0; u < SW; ++u) M = fmaxf(M, s_ml[u][0][c]);
+        for (int u = 0; u < SW; ++u) {
+            const float r = M == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(s_ml[u][0][c] - M);
+            L = __builtin_fmaf(s_ml[u][1][c], r, L);
+            O = __builtin_fmaf(s_sum[u][c][d], r, O);
+        }
+        if (splits == 1) {
+            out.at(b, h0 + c)[d] = L > 0.f ? O / L : 0.f;
+        } else {
+            const int64_t at = (b * a.n_heads + h0 + c) * splits + split;
+            part_o[at * D + d] = O;
+            if (d == 0) {
+                part_ml[2 * at] = M;
+                part_ml[2 * at + 1] = L;
+            }
+        }
+    }
+}
+
 // Joins a head's parts: one block per user and head, CB / D groups of threads
 // taking parts in turn, their sums added in order.
 template <typename T, int D>
@@ -435,6 +663,13 @@ __global__ __launch_bounds__(CB) void k_step_join(const float* part_o, const flo
 // wave with two tiles at least; k_step_join reads at most 64.
 constexpr int64_t STEP_BLOCKS = 1024;
 
+// fp32 heads a key/value head that k_step_few takes.  128 users of up to 2048
+// events, one head to a key/value head, 4 of them, 64 (128) elements: 95 ->
+// 50 us (232 -> 107), 4.9 TB/s; 4 heads to the only one: 37 -> 28 (80 -> 43);
+// 8 heads: 38 -> 58 (82 -> 93), its registers leaving one wave a SIMD.  In
+// bf16 a product of tiles takes an eighth of the time and is no bound.
+constexpr int FEW_HEADS = 4;
+
 struct StepPlan {
     int cols, blocks, splits;
 };
@@ -473,9 +708,22 @@ int run_step(const rse_seqattn* at, const rse_seqcache* c, const StepArgs& a, co
     const size_t lds = (tiles > sums ? tiles : sums) + (size_t)(a.n_bounds + 1) * p.cols * sizeof(float);
     const int64_t grid = a.batch * at->n_kv_heads * p.blocks * p.splits;
     if (grid > INT32_MAX) return RSE_ERR_UNSUPPORTED;
-    hipLaunchKernelGGL((k_step<T, D>), dim3((unsigned)grid), dim3(SW * WAVE), lds, s, a, rows_view<const T>(q),
-                       rows_view<const T>(k), rows_view<const T>(v), static_cast<T*>(c->k), static_cast<T*>(c->v),
-                       rows_view<T>(out), p.splits, p.cols, ws.o, ws.ml);
+    const int few = std::is_same_v<T, float> && p.cols <= FEW_HEADS ? p.cols : 0;
+    if constexpr (std::is_same_v<T, float>) {
+        const auto run = [&](auto kernel, int heads) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(SW * WAVE), (a.n_bounds + 1) * heads * sizeof(float),
+                               s, a, rows_view<const T>(q), rows_view<const T>(k), rows_view<const T>(v),
+                               static_cast<T*>(c->k), static_cast<T*>(c->v), rows_view<T>(out), p.splits, ws.o, ws.ml);
+        };
+        if (few == 1) run(k_step_few<D, 1>, 1);
+        if (few == 2) run(k_step_few<D, 2>, 2);
+        if (few > 2) run(k_step_few<D, 4>, 4);
+    }
+    if (!few) {
+        hipLaunchKernelGGL((k_step<T, D>), dim3((unsigned)grid), dim3(SW * WAVE), lds, s, a, rows_view<const T>(q),
+                           rows_view<const T>(k), rows_view<const T>(v), static_cast<T*>(c->k), static_cast<T*>(c->v),
+                           rows_view<T>(out), p.splits, p.cols, ws.o, ws.ml);
+    }
     if (p.splits > 1) {
         hipLaunchKernelGGL((k_step_join<T, D>), dim3((unsigned)(a.batch * a.n_heads)), dim3(CB), 0, s, ws.o, ws.ml,
                            a.n_heads, p.splits, rows_view<T>(out));

@@ -630,3 +630,27 @@ def test_most_buckets_and_wide_rows(H, Hk, D, dtype):
 @pytest.mark.parametrize("H,Hk", [(64, 1), (33, 1), (8, 8)])
 def test_step_most_buckets_and_heads(H, Hk, dtype):
     Serving([150, 700, 0], H, Hk, 128, dtype, bounds=tuple(range(1, 128))).check()
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (4, 2), (3, 1), (4, 1), (5, 1)])
+@pytest.mark.parametrize("lens", [[0, 1, -1, 7, 8, 15, 16, 17], [31, 32, 33, 63, 64, 65, 127], [1500, 3, 300]])
+def test_step_fp32_few_heads(lens, H, Hk, D):
+    """Up to 4 heads a key/value head have a kernel of their own, 5 the other."""
+    Serving(lens, H, Hk, D, F32, page=8).check()
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_step_fp32_scale(scale):
+    s = Serving([90, 0, 700], 4, 2, 64, F32)
+    s.attn = s.rse.SeqAttention(4, 2, 64, F32, s.bounds, scale=scale)
+    s.check()
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_step_fp32_many_parts_and_hidden(D):
+    s = Serving([9000, 40, 0], 2, 1, D, F32, page=64, bounds=(0, 1, 3000))
+    s.bias[:, 1] = float("-inf")
+    s.bias[:, 3] = torch.finfo(torch.float32).min
+    out = s.check()
+    assert torch.all(out[2] == 0)
