@@ -38,7 +38,7 @@ __device__ __forceinline__ void add_sixteen(float* mine, int cols, const int (&i
     }
 }
 __device__ __forceinline__ void add_pairs(float* hist, int cols, const int (&idx)[16], const f32x16& x) {
-    const int lane = lane_id();
+    const int lane = lane_anew();
     float* mine = hist + (lane & (cols - 1));
     if (cols == WAVE) {
         add_sixteen(mine, WAVE, idx, x);
@@ -52,7 +52,8 @@ __device__ __forceinline__ void add_pairs(float* hist, int cols, const int (&idx
 // One lane's sum per column pair into one bucket.
 __device__ __forceinline__ void add_bucket(float* hist, int cols, int bucket, float sum) {
     sum += other_half(sum);
-    if (lane_id() < 32) hist[bucket * cols + lane_id()] += sum;
+    const int lane = lane_anew();
+    if (lane < 32) hist[bucket * cols + lane] += sum;
     wave_lds_sync();
 }
 __device__ __forceinline__ void add_one(float* hist, int cols, int bucket, const f32x16& x) {

@@ -30,6 +30,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// The lane, formed anew where it stands (the compiler may not keep what it
+// derives from it over a loop): addresses of lookups kept so were spilled, and
+// a spill's reload waits for every load in flight, the next tile's among them.
+__device__ __forceinline__ int lane_anew() {
+    uint32_t none = 0;
+    asm volatile("" : "+s"(none));
+    return (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, none));
+}
+
 // One value from the other half of the wave (lane l ^ 32).
 __device__ __forceinline__ float other_half(float x) {
     const u32x2 s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -172,7 +181,7 @@ __device__ __forceinline__ f32x16 mma_over_rows(const u32x4* tile, int r0, int d
 // Elements 32 dt .. 32 dt + 31 of the lane's column from acc, times f, to
 // p[0 .. 31] of the column's row; 16 bytes a store.
 __device__ __forceinline__ void store_column(float* p, const f32x16& acc, float f) {
-    const int h = lane_id() >> 5;
+    const int h = lane_anew() >> 5;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         gstore_f4(p + 8 * j + 4 * h, f32x4{acc[4 * j] * f, acc[4 * j + 1] * f, acc[4 * j + 2] * f, acc[4 * j + 3] * f});
@@ -296,7 +305,7 @@ struct TileBuckets {
     // Of `many` tiles: registers 4 j .. 4 j + 3 for j = first, + step, ... < 4.
     static __device__ __forceinline__ void find_pairs(u32x4* bytes, int first, int step, const LdsBuckets& lb, int n, bool cells,
                                                       const int32_t* row_pos, int32_t col_pos) {
-        const int lane = lane_id(), h = lane >> 5;
+        const int lane = lane_anew(), h = lane >> 5;
         uint32_t* mine = reinterpret_cast<uint32_t*>(bytes + lane);
 #pragma unroll 1
         for (int j = first; j < 4; j += step) {
@@ -317,7 +326,7 @@ struct TileBuckets {
     }
     static __device__ __forceinline__ int pair(const u32x4& bytes, int r) { return (bytes[r >> 2] >> (8 * (r & 3))) & 255; }
     static __device__ __forceinline__ void positions(int32_t (&p)[16], const int32_t* row_pos) {
-        const int h = lane_id() >> 5;
+        const int h = lane_anew() >> 5;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const i32x4 v = *reinterpret_cast<const i32x4*>(row_pos + 8 * j + 4 * h);
@@ -361,7 +370,7 @@ struct TileBuckets {
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], c, b[r]);
         } else {
-            const u32x4 at = bytes[lane_id()];
+            const u32x4 at = bytes[lane_anew()];
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r] = __builtin_fmaf(s[r], c, s_bias[pair(at, r)] + shift);
         }
@@ -382,7 +391,7 @@ struct TileBuckets {
                 for (int r = 0; r < 16; ++r) idx[r] += passed(p[r], th);
             }
         } else {
-            const u32x4 at = bytes[lane_id()];
+            const u32x4 at = bytes[lane_anew()];
 #pragma unroll
             for (int r = 0; r < 16; ++r) idx[r] = pair(at, r);
         }
