@@ -168,6 +168,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                 if (k1 >= my_end) break;
                 TileBuckets<true> tb;
                 tb.set(wb, q_lo, q_hi, ks.range[u]);
+                f32x16 x = mma_rows<T, D>(s_k[team][b], 32 * u, qf, f32x16{});
                 if (tb.many) {
                     // all waves of a column tile are here, and share the lookups
                     if (BRIEF) wp ^= 1;
@@ -175,7 +176,6 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                     if (WH > 1) __syncthreads();
                     else wave_lds_sync();
                 }
-                f32x16 x = mma_rows<T, D>(s_k[team][b], 32 * u, qf, f32x16{});
                 x = tb.logits(x, c2, -m, wb, s_pairs[wp][u], s_bias[wh], ks.pos + 32 * u, my_pos);
                 hide(x, ks.hidden[u], ks.mask + 32 * u);
                 if (a.causal && k1 + 31 > w0) {

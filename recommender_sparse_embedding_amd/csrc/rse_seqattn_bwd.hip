@@ -320,14 +320,14 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
             const KeySide<KT>& ks = s_side[w];
             TileBuckets<true> tb;
             tb.set(wb, q_lo, q_hi, ks.range[0]);
+            f32x16 x = mma_rows<T, D>(s_k[w], 0, qf, f32x16{});
+            f32x16 dp = mma_rows<T, D>(s_v[w], 0, df, f32x16{});
             if (tb.many) {
                 wp ^= 1;
                 tb.find_pairs(s_pairs[wp], w, WH, s_buckets, a.n_bounds, a.cells, ks.pos, my_pos);
                 if (WH > 1) __syncthreads();
                 else wave_lds_sync();
             }
-            f32x16 x = mma_rows<T, D>(s_k[w], 0, qf, f32x16{});
-            f32x16 dp = mma_rows<T, D>(s_v[w], 0, df, f32x16{});
             x = tb.logits(x, c2, -L, wb, s_pairs[wp], s_bias[w], ks.pos, my_pos);
             hide(x, ks.hidden[0], ks.mask);
             if (a.causal && k1 + 31 > w0) {
@@ -502,14 +502,14 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                 if (a.causal && i1 + 31 < w0) continue;
                 TileBuckets<false> tb;
                 tb.set(wb, k_lo, k_hi, s_range[team][b][u]);
+                f32x16 x = mma_rows<T, D>(s_q[team][b], 32 * u, kf, f32x16{});
+                f32x16 dp = mma_rows<T, D>(s_d[team][b], 32 * u, vf, f32x16{});
                 if (tb.many && it % turns == 0) {
                     if (BRIEF) wp ^= 1;
                     tb.find_pairs(s_pairs[wp][u], wh, WH, s_buckets, a.n_bounds, a.cells, s_pos[team][b] + 32 * u, my_pos);
                     if (WH > 1) __syncthreads();
                     else wave_lds_sync();
                 }
-                f32x16 x = mma_rows<T, D>(s_q[team][b], 32 * u, kf, f32x16{});
-                f32x16 dp = mma_rows<T, D>(s_d[team][b], 32 * u, vf, f32x16{});
                 x = tb.logits(x, c2, 0.f, wb, s_pairs[wp][u], s_bias[team][b], s_pos[team][b] + 32 * u, my_pos);
                 if (a.causal && i1 < w0 + 31) {
                     const int lim = my_k - i1 - 4 * half;
