@@ -14,8 +14,11 @@ import numpy as np
 
 U = 2.0 ** -24          # unit roundoff of fp32
 UB = 2.0 ** -8          # unit roundoff of bf16: 8 significant bits, to nearest
-R = {"f32": 0.0, "bf16": UB}             # rounding of a factor before a product
-OUT = {"f32": U, "bf16": UB}
+# rounding of a factor before a product; "bf16 pairs": the factor as the sum of
+# two bf16 values, the second one the rounded remainder of the first
+R = {"f32": 0.0, "bf16": UB, "bf16 pairs": UB * UB}
+TERMS = {"f32": 1, "bf16": 1, "bf16 pairs": 2}
+OUT = {"f32": U, "bf16": UB, "bf16 pairs": UB}
 
 
 def bucket(pos_i, pos_j, boundaries):
@@ -70,7 +73,7 @@ def attention(q, k, v, pos, bias, offsets, boundaries, causal, scale, key_off=No
     q, k, v, bias = (np.asarray(x, np.float64) for x in (q, k, v, bias))
     N, H, D = q.shape
     Hk = k.shape[1]
-    r, ro = R[kind], OUT[kind]
+    r, ro, terms = R[kind], OUT[kind], TERMS[kind]
     zeros = lambda *s: [np.zeros(s), np.zeros(s)]  # noqa: E731
     out = zeros(N, H, D)
     lse = np.full((H, N), -np.inf)
@@ -88,14 +91,14 @@ def attention(q, k, v, pos, bias, offsets, boundaries, causal, scale, key_off=No
                      None if dout is None else dout[a:e, h])
             p, ep = m["p"], m["ep"][:, None]
             out[0][a:e, h] = p @ m["v"]
-            out[1][a:e, h] = (ep + n * U + r) * (p @ np.abs(m["v"]))
+            out[1][a:e, h] = (ep + terms * n * U + r) * (p @ np.abs(m["v"]))
             lse[h, a:e] = m["lse"]
             if dout is None:
                 continue
             do, ds, eds = dout[a:e, h], m["ds"], m["eds"]
-            sums = (len(q) * (H // Hk) + 4) * U       # at most that many terms in a key's sums
+            sums = (terms * len(q) * (H // Hk) + 4) * U       # at most that many terms in a key's sums
             dq[0][a:e, h] = scale * (ds @ m["k"])
-            dq[1][a:e, h] = abs(scale) * ((eds + (r + (n + 2) * U) * np.abs(ds)) @ np.abs(m["k"]))
+            dq[1][a:e, h] = abs(scale) * ((eds + (r + (terms * n + 2) * U) * np.abs(ds)) @ np.abs(m["k"]))
             dk[0][a:e, g] += scale * (ds.T @ q[a:e, h])
             dk[1][a:e, g] += abs(scale) * ((eds + (r + sums) * np.abs(ds)).T @ np.abs(q[a:e, h]))
             dv[0][a:e, g] += p.T @ do
@@ -128,7 +131,7 @@ def step(histories, q, bias, boundaries, scale, kind="f32"):
                      False, scale)
             p = m["p"][-1]
             out[b, h] = p @ m["v"]
-            err[b, h] = (m["ep"][-1] + n * U + R[kind]) * (p @ np.abs(m["v"])) + OUT[kind] * np.abs(out[b, h]) + 1e-30
+            err[b, h] = (m["ep"][-1] + TERMS[kind] * n * U + R[kind]) * (p @ np.abs(m["v"])) + OUT[kind] * np.abs(out[b, h]) + 1e-30
     return out, err
 
 

@@ -111,39 +111,48 @@ __device__ __forceinline__ f32x16 mma_rows(const u32x4* tile, int r0, const ColF
     return c;
 }
 
-// A 32 x 32 tile's values as the operand of a product over its rows.
-template <typename T>
+// A 32 x 32 tile's values as the operand of a product over its rows.  bf16: as
+// the sum of TERMS bf16 values, each the rounded remainder of those before it.
+template <typename T, int TERMS = 1>
 struct RowOperand;
-template <>
-struct RowOperand<float> {
+template <int TERMS>
+struct RowOperand<float, TERMS> {
     f32x16 v;
     __device__ __forceinline__ void set(const f32x16& x) { v = x; }
     __device__ __forceinline__ void take_from(f32x16& x) const { x = f32x16{}; }
 };
-template <>
-struct RowOperand<uint16_t> {
-    u32x4 v[2];
-    __device__ __forceinline__ void set(const f32x16& x) {
+template <int TERMS>
+struct RowOperand<uint16_t, TERMS> {
+    u32x4 v[TERMS][2];
+    __device__ __forceinline__ void set(f32x16 x) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int t = 0; t < TERMS; ++t) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[s][i] = pack_bf16(x[8 * s + 2 * i], x[8 * s + 2 * i + 1]);
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[t][s][i] = pack_bf16(x[8 * s + 2 * i], x[8 * s + 2 * i + 1]);
+            if (t + 1 < TERMS) take(t, x);
+        }
     }
-    // x less what is held of it (exact: the rounding's remainder)
+    // x less what is held of it (exact: the roundings' remainder)
     __device__ __forceinline__ void take_from(f32x16& x) const {
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) take(t, x);
+    }
+    __device__ __forceinline__ void take(int t, f32x16& x) const {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[8 * s + 2 * i] -= __uint_as_float(v[s][i] << 16);
-                x[8 * s + 2 * i + 1] -= __uint_as_float(v[s][i] & 0xFFFF0000u);
+                x[8 * s + 2 * i] -= __uint_as_float(v[t][s][i] << 16);
+                x[8 * s + 2 * i + 1] -= __uint_as_float(v[t][s][i] & 0xFFFF0000u);
             }
     }
 };
 
 // acc[d, column] += sum over rows r0 .. r0 + 31 of tile[row, 32 dt + d] x[row, column].
-template <int D>
-__device__ __forceinline__ f32x16 mma_over_rows(const u32x4* tile, int r0, int dt, const RowOperand<float>& x, f32x16 acc) {
+template <int D, int TERMS>
+__device__ __forceinline__ f32x16 mma_over_rows(const u32x4* tile, int r0, int dt, const RowOperand<float, TERMS>& x, f32x16 acc) {
     const int lane = lane_id(), d = 32 * dt + (lane & 31), h = lane >> 5;
     const float* f = reinterpret_cast<const float*>(tile);
 #pragma unroll
@@ -156,8 +165,8 @@ __device__ __forceinline__ f32x16 mma_over_rows(const u32x4* tile, int r0, int d
 // bf16: four rows of a column at a time by the transposing LDS read: in each
 // group of 16 lanes, lane i supplies the address of row i / 4, elements
 // 4 (i % 4) .., and receives column i of the four rows.
-template <int D>
-__device__ __forceinline__ f32x16 mma_over_rows(const u32x4* tile, int r0, int dt, const RowOperand<uint16_t>& x, f32x16 acc) {
+template <int D, int TERMS>
+__device__ __forceinline__ f32x16 mma_over_rows(const u32x4* tile, int r0, int dt, const RowOperand<uint16_t, TERMS>& x, f32x16 acc) {
     const int lane = lane_id(), h = lane >> 5, i = lane & 15;
     const int c = 4 * dt + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);       // chunk of elements 32 dt + 16 half + 4 (i % 4)
     const char* base = reinterpret_cast<const char*>(tile);
@@ -173,7 +182,9 @@ __device__ __forceinline__ f32x16 mma_over_rows(const u32x4* tile, int r0, int d
         u32x4 a;
         a.xy = __builtin_bit_cast(u32x2, p[0]);
         a.zw = __builtin_bit_cast(u32x2, p[1]);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, x.v[s]), acc, 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t)
+            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, x.v[t][s]), acc, 0, 0, 0);
     }
     return acc;
 }

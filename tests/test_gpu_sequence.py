@@ -654,3 +654,21 @@ def test_step_fp32_many_parts_and_hidden(D):
     s.bias[:, 3] = torch.finfo(torch.float32).min
     out = s.check()
     assert torch.all(out[2] == 0)
+
+
+# ------------------------------------------------------------ bf16 accuracy --
+KIND["pairs"] = "bf16 pairs"
+
+
+@pytest.mark.parametrize("lens", [[1, 2, 40, 128], [300, 5, 33]])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (4, 2), (4, 1)])
+def test_bf16_forward_rounds_once(H, Hk, D, lens):
+    """bf16 outputs are fp32 arithmetic rounded once: the probabilities enter
+    their product as pairs of bf16 values."""
+    for causal in (True, False):
+        c = Case(lens, H, Hk, D, BF16, causal=causal, missing=0.2)
+        c.dtype = "pairs"
+        ref = c.oracle(False)["out"]
+        _check(c.forward(), ref, "out")
+        _check(c.run()["out"], ref, "out before a backward")
