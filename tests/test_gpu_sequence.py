@@ -672,3 +672,15 @@ def test_bf16_forward_rounds_once(H, Hk, D, lens):
         ref = c.oracle(False)["out"]
         _check(c.forward(), ref, "out")
         _check(c.run()["out"], ref, "out before a backward")
+
+
+@pytest.mark.parametrize("lens", [[1, 2, 40, 128], [300, 5, 33]])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (4, 2), (4, 1)])
+def test_bf16_gradients_round_once(H, Hk, D, lens):
+    for causal in (True, False):
+        c = Case(lens, H, Hk, D, BF16, causal=causal, missing=0.2)
+        c.dtype = "pairs"
+        got, ref = c.run(), c.oracle()
+        for name in got:
+            _check(got[name], ref[name], name)
