@@ -559,10 +559,9 @@ int dlrm_interaction_bwd(const float* d_dense, const float* d_pooled, const floa
  * free (views of one joint projection, for example).  Addresses and both
  * strides are multiples of 16 bytes, else RSE_ERR_INVALID_ARG.  Products are
  * accumulated and the softmax is held in fp32.  With RSE_BF16 outputs are
- * rounded once at the end: in the forward and backward the probabilities and
- * their gradients enter their products as pairs of bf16 values (2^-16 of each
- * is lost).  In the step the probabilities are rounded to bf16 there.  The
- * bias gradient is summed from the unrounded fp32 values.  No floating-point atomics are shared
+ * rounded once at the end: the probabilities and their gradients enter their
+ * products as pairs of bf16 values (2^-16 of each is lost); the bias gradient
+ * is summed from the fp32 values.  No floating-point atomics are shared
  * between lanes: results are run-to-run identical.
  */
 #define RSE_SEQ_MAX_BOUNDARIES 127

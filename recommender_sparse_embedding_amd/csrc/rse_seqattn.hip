@@ -74,8 +74,8 @@ __global__ void k_attn_clear(SeqHeader* h) { h->status = 0; }
 // bf16: the probabilities enter V^T P^T as pairs of bf16 values (2^-16 of each
 // is lost), so that out is fp32 arithmetic rounded once.  With one value each
 // their rounding put as much into out again as its own: 0.0022 of its size
-// against 0.0017, for 204 instead of 229 us on 16 histories of up to 4096
-// events and 37 instead of 40 on 96 sessions of up to 333 (dim 128).
+// against 0.0017, for 205 instead of 227 us on 16 histories of up to 4096
+// events and 38 instead of 40 on 96 sessions of up to 333 (dim 128).
 //
 // SAVE: also leaves the log-sums for the backward, and SAVE_OUT the outputs:
 // its dO . out has to equal sum_j p dp to fp32 accuracy (the bias gradient
@@ -214,17 +214,8 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                     x[r] = __builtin_amdgcn_exp2f(x[r]);
                     l += x[r];
                 }
-                RowOperand<T, 2> p;
-                p.set(x);
-#pragma unroll
-                for (int dt = 0; dt < ND; ++dt) o[dt] = mma_over_rows<D>(s_v[team][b], 32 * u, dt, p, o[dt]);
-                if (REST) {
-                    p.take_from(x);
-                    RowOperand<T> third;
-                    third.set(x);
-#pragma unroll
-                    for (int dt = 0; dt < ND; ++dt) rest[dt] = mma_over_rows<D>(s_v[team][b], 32 * u, dt, third, rest[dt]);
-                }
+                OverRows<T, D>::add(o, s_v[team][b], 32 * u, x);
+                if constexpr (REST) OverRows<T, D, 1>::add(rest, s_v[team][b], 32 * u, x);
             }
             if (BRIEF) wave_lds_sync();         // read before the next tile is stored
         }

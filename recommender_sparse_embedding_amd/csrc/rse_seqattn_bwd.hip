@@ -6,9 +6,9 @@
 //
 // bf16: p and ds enter their products as pairs of bf16 values (2^-16 of each is
 // lost), so that the gradients are fp32 arithmetic rounded once.  With one
-// value each dq and dk were half again as far off as that; 8192 sequences of
-// 1..100 events, 4 heads of 64, both ways 1305 -> 1375 us a training step, 12
-// of up to 2048, 8 heads on 2: 384 -> 422.
+// value each dq and dk were half again as far off as that, for 1285 instead of
+// 1333 us a training step on 8192 sequences of 1..100 events, 4 heads of 64,
+// and 377 instead of 411 on 12 of up to 2048, 8 heads on 2.
 #include "rse_seqmma.h"
 
 using namespace rse;
@@ -225,10 +225,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
 #pragma unroll
                 for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(x[r]) * (dp[r] - del);
                 add_tile(hist, cols, tb, idx, x);
-                RowOperand<T, 2> ds;
-                ds.set(x);
-#pragma unroll
-                for (int dt = 0; dt < ND; ++dt) acc[dt] = mma_over_rows<D>(s_k[team][b], 32 * u, dt, ds, acc[dt]);
+                OverRows<T, D>::add(acc, s_k[team][b], 32 * u, x);
             }
             if (k0 + KT < end) {
                 if (SH::TEAM == 1) wave_lds_sync();
@@ -358,10 +355,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                     tb.index(idx, wb, s_pairs[wp], ks.pos, my_pos);
                     add_pairs(hist, cols, idx, x);
                 }
-                RowOperand<T, 2> ds;
-                ds.set(x);
-#pragma unroll
-                for (int dt = 0; dt < ND; ++dt) acc[dt] = mma_over_rows<D>(s_k[w], 0, dt, ds, acc[dt]);
+                OverRows<T, D>::add(acc, s_k[w], 0, x);
             }
             wave_lds_sync();
         }
@@ -532,13 +526,8 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                         dp[4 * j + i] = x[4 * j + i] * (dp[4 * j + i] - de[i]);
                     }
                 }
-                RowOperand<T, 2> in;
-                in.set(x);
-#pragma unroll
-                for (int dt = 0; dt < ND; ++dt) av[dt] = mma_over_rows<D>(s_d[team][b], 32 * u, dt, in, av[dt]);
-                in.set(dp);
-#pragma unroll
-                for (int dt = 0; dt < ND; ++dt) ak[dt] = mma_over_rows<D>(s_q[team][b], 32 * u, dt, in, ak[dt]);
+                OverRows<T, D>::add(av, s_d[team][b], 32 * u, x);
+                OverRows<T, D>::add(ak, s_q[team][b], 32 * u, dp);
             }
         }
         if (BRIEF) wave_lds_sync();             // read before the next tile is stored

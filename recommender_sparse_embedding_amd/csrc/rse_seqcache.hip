@@ -196,7 +196,9 @@ __device__ __forceinline__ bool step_ok(const StepArgs& a, int64_t n) {
 // rows pass through the wave's LDS tile.  The waves' softmax sums are joined
 // in LDS at the end; with more than one part, k_step_join joins the parts.
 // The new event's own key and value are read from the call's arguments (no
-// other block waits for the store that the first part makes).
+// other block waits for the store that the first part makes).  bf16: the
+// probabilities enter their product as pairs of bf16 values (2^-16 of each is
+// lost), so that out is fp32 arithmetic rounded once.
 constexpr int SW = 4;
 
 // Registers are held to what lets STEP_WAVES waves share a SIMD.
@@ -346,10 +348,7 @@ __global__ __launch_bounds__(SW * 64) __attribute__((amdgpu_waves_per_eu(STEP_WA
             s[r] = __builtin_amdgcn_exp2f(s[r] - shift);
             l += s[r];
         }
-        RowOperand<T> p;
-        p.set(s);
-#pragma unroll
-        for (int dt = 0; dt < ND; ++dt) o[dt] = mma_over_rows<D>(tile, 0, dt, p, o[dt]);
+        OverRows<T, D>::add(o, tile, 0, s);
         wave_lds_sync();
     }
     l += other_half(l);

@@ -111,83 +111,68 @@ __device__ __forceinline__ f32x16 mma_rows(const u32x4* tile, int r0, const ColF
     return c;
 }
 
-// A 32 x 32 tile's values as the operand of a product over its rows.  bf16: as
-// the sum of TERMS bf16 values, each the rounded remainder of those before it.
-template <typename T, int TERMS = 1>
-struct RowOperand;
-template <int TERMS>
-struct RowOperand<float, TERMS> {
-    f32x16 v;
-    __device__ __forceinline__ void set(const f32x16& x) { v = x; }
-    __device__ __forceinline__ void take_from(f32x16& x) const { x = f32x16{}; }
-};
-template <int TERMS>
-struct RowOperand<uint16_t, TERMS> {
-    u32x4 v[TERMS][2];
-    __device__ __forceinline__ void set(f32x16 x) {
+// acc[dt][d, column] += sum over rows r0 .. r0 + 31 of tile[row, 32 dt + d] x[row, column].
+template <typename T, int D, int TERMS = 2>
+struct OverRows;
+template <int D, int TERMS>
+struct OverRows<float, D, TERMS> {
+    static __device__ __forceinline__ void add(f32x16 (&acc)[D / 32], const u32x4* tile, int r0, f32x16& x) {
+        const int lane = lane_id(), h = lane >> 5;
+        const float* f = reinterpret_cast<const float*>(tile);
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t) {
+        for (int dt = 0; dt < D / 32; ++dt) {
+            const int d = 32 * dt + (lane & 31);
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[t][s][i] = pack_bf16(x[8 * s + 2 * i], x[8 * s + 2 * i + 1]);
-            if (t + 1 < TERMS) take(t, x);
-        }
-    }
-    // x less what is held of it (exact: the roundings' remainder)
-    __device__ __forceinline__ void take_from(f32x16& x) const {
-#pragma unroll
-        for (int t = 0; t < TERMS; ++t) take(t, x);
-    }
-    __device__ __forceinline__ void take(int t, f32x16& x) const {
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[8 * s + 2 * i] -= __uint_as_float(v[t][s][i] << 16);
-                x[8 * s + 2 * i + 1] -= __uint_as_float(v[t][s][i] & 0xFFFF0000u);
+            for (int r = 0; r < 16; ++r) {
+                const int row = r0 + tile_row(r, h);
+                acc[dt] = __builtin_amdgcn_mfma_f32_32x32x2f32(f[Tile<float, D>::chunk_at(row, d >> 2) * 4 + (d & 3)], x[r], acc[dt], 0, 0, 0);
             }
+        }
     }
 };
-
-// acc[d, column] += sum over rows r0 .. r0 + 31 of tile[row, 32 dt + d] x[row, column].
+// bf16: x enters as the sum of TERMS bf16 values, each the rounded remainder of
+// those before it, and is left less what entered (exact).  Half of the rows
+// after the other, so that few operands are held at once (both halves formed
+// first: spills in the step, 256 users of 1..1000 events 34 us for 26).  Four
+// rows of a column at a time by the transposing LDS read: in each group of 16 lanes,
+// lane i supplies the address of row i / 4, elements 4 (i % 4) .., and receives
+// column i of the four rows.
 template <int D, int TERMS>
-__device__ __forceinline__ f32x16 mma_over_rows(const u32x4* tile, int r0, int dt, const RowOperand<float, TERMS>& x, f32x16 acc) {
-    const int lane = lane_id(), d = 32 * dt + (lane & 31), h = lane >> 5;
-    const float* f = reinterpret_cast<const float*>(tile);
+struct OverRows<uint16_t, D, TERMS> {
+    static __device__ __forceinline__ void add(f32x16 (&acc)[D / 32], const u32x4* tile, int r0, f32x16& x) {
+        const int lane = lane_id(), h = lane >> 5, i = lane & 15;
+        const char* base = reinterpret_cast<const char*>(tile);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int row = r0 + tile_row(r, h);
-        acc = __builtin_amdgcn_mfma_f32_32x32x2f32(f[Tile<float, D>::chunk_at(row, d >> 2) * 4 + (d & 3)], x.v[r], acc, 0, 0, 0);
-    }
-    return acc;
-}
-// bf16: four rows of a column at a time by the transposing LDS read: in each
-// group of 16 lanes, lane i supplies the address of row i / 4, elements
-// 4 (i % 4) .., and receives column i of the four rows.
-template <int D, int TERMS>
-__device__ __forceinline__ f32x16 mma_over_rows(const u32x4* tile, int r0, int dt, const RowOperand<uint16_t, TERMS>& x, f32x16 acc) {
-    const int lane = lane_id(), h = lane >> 5, i = lane & 15;
-    const int c = 4 * dt + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);       // chunk of elements 32 dt + 16 half + 4 (i % 4)
-    const char* base = reinterpret_cast<const char*>(tile);
+        for (int s = 0; s < 2; ++s) {
+            u32x4 v[TERMS];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        s16x4 p[2];
+            for (int t = 0; t < TERMS; ++t)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int row = r0 + 16 * s + 8 * u + 4 * h + (i >> 2);
-            const char* at = base + Tile<uint16_t, D>::chunk_at(row, c) * 16 + (i & 1) * 8;
-            p[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RSE_LDS s16x4*)at);
+                for (int j = 0; j < 4; ++j) {
+                    v[t][j] = pack_bf16(x[8 * s + 2 * j], x[8 * s + 2 * j + 1]);
+                    x[8 * s + 2 * j] -= __uint_as_float(v[t][j] << 16);
+                    x[8 * s + 2 * j + 1] -= __uint_as_float(v[t][j] & 0xFFFF0000u);
+                }
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt) {
+                const int c = 4 * dt + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);       // chunk of elements 32 dt + 16 half + 4 (i % 4)
+                s16x4 p[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int row = r0 + 16 * s + 8 * u + 4 * h + (i >> 2);
+                    const char* at = base + Tile<uint16_t, D>::chunk_at(row, c) * 16 + (i & 1) * 8;
+                    p[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((RSE_LDS s16x4*)at);
+                }
+                u32x4 a;
+                a.xy = __builtin_bit_cast(u32x2, p[0]);
+                a.zw = __builtin_bit_cast(u32x2, p[1]);
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t)
+                    acc[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, v[t]), acc[dt], 0, 0, 0);
+            }
         }
-        u32x4 a;
-        a.xy = __builtin_bit_cast(u32x2, p[0]);
-        a.zw = __builtin_bit_cast(u32x2, p[1]);
-#pragma unroll
-        for (int t = 0; t < TERMS; ++t)
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, x.v[t][s]), acc, 0, 0, 0);
     }
-    return acc;
-}
+};
 
 // Elements 32 dt .. 32 dt + 31 of the lane's column from acc, times f, to
 // p[0 .. 31] of the column's row; 16 bytes a store.

@@ -684,3 +684,12 @@ def test_bf16_gradients_round_once(H, Hk, D, lens):
         got, ref = c.run(), c.oracle()
         for name in got:
             _check(got[name], ref[name], name)
+
+
+@pytest.mark.parametrize("lens", [[0, 1, 31, 65], [1500, -1, 300]])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (4, 2), (16, 1)])
+def test_bf16_step_rounds_once(H, Hk, D, lens):
+    s = Serving(lens, H, Hk, D, BF16)
+    s.dtype = "pairs"
+    s.check()
