@@ -188,6 +188,10 @@ __device__ __forceinline__ bool step_ok(const StepArgs& a, int64_t n) {
     return true;
 }
 
+// A row's result from its sums.  Nothing seen: 0.  A score of NaN or +infinity
+// has left l NaN, and stays.
+__device__ __forceinline__ float over(float o, float l) { return l == 0.f ? 0.f : o / l; }
+
 // One new event per user.  A block of SW waves takes the heads that share one
 // key/value head (at most 32, as columns; column c is head h0 + c) and one of
 // `splits` equal parts of a user's tiles of 32 events; its waves take tiles in
@@ -376,7 +380,7 @@ __global__ __launch_bounds__(SW * 64) __attribute__((amdgpu_waves_per_eu(STEP_WA
             O = __builtin_fmaf(s_sum[(u * cols + c) * D + d], r, O);
         }
         if (splits == 1) {
-            from_f32(out.at(b, h0 + c)[d], L > 0.f ? O / L : 0.f);
+            from_f32(out.at(b, h0 + c)[d], over(O, L));
         } else {
             const int64_t at = (b * a.n_heads + h0 + c) * splits + split;
             part_o[at * D + d] = O;
@@ -604,7 +608,7 @@ __global__ __launch_bounds__(SW * 64) void k_step_few(StepArgs a, Rows<const flo
             O = __builtin_fmaf(s_sum[u][c][d], r, O);
         }
         if (splits == 1) {
-            out.at(b, h0 + c)[d] = L > 0.f ? O / L : 0.f;
+            out.at(b, h0 + c)[d] = over(O, L);
         } else {
             const int64_t at = (b * a.n_heads + h0 + c) * splits + split;
             part_o[at * D + d] = O;
@@ -654,7 +658,7 @@ __global__ __launch_bounds__(CB) void k_step_join(const float* part_o, const flo
     if (grp == 0) {
 #pragma unroll
         for (int x = 1; x < G; ++x) o += s_o[x][d];
-        from_f32(out.at(at / n_heads, at % n_heads)[d], s_l > 0.f ? o / s_l : 0.f);
+        from_f32(out.at(at / n_heads, at % n_heads)[d], over(o, s_l));
     }
 }
 

@@ -693,3 +693,63 @@ def test_bf16_step_rounds_once(H, Hk, D, lens):
     s = Serving(lens, H, Hk, D, BF16)
     s.dtype = "pairs"
     s.check()
+
+
+# --------------------------------------------------- values that are not finite --
+@pytest.mark.parametrize("dtype,H,Hk", [(F32, 4, 2), (F32, 5, 1), (BF16, 4, 2), (BF16, 5, 1)])
+@pytest.mark.parametrize("lens", [[40, 0, 33], [1500, 3, 700]])
+def test_step_keeps_what_is_not_finite(lens, dtype, H, Hk):
+    """NaN in a query, a cached key or value or a bias, and scores that
+    overflow, give NaN where the formula does, and nowhere else."""
+    def fresh():
+        return Serving(lens, H, Hk, 64, dtype, bounds=(1, 2, 4, 8, 16, 32, 64, 128))
+
+    def check(s, want_nan, what):
+        out = _np(s.run())
+        ref, bound = s.oracle()
+        assert np.array_equal(np.isnan(out), want_nan), what
+        assert np.all(np.abs(out - ref)[~want_nan] <= bound[~want_nan]), what
+        assert s.cache.status() == 0
+
+    none = np.zeros((3, H, 64), bool)
+    nan = float("nan")
+    group = H // Hk
+    s = fresh()                                  # one head's query
+    want = none.copy()
+    ref = s.oracle()
+    s.q[0, 1, 5] = nan
+    want[0, 1] = True
+    s.oracle = lambda: ref
+    check(s, want, "q")
+    for at in (2, lens[0] - 1, lens[0]):         # a key: cached early, cached last, new
+        s = fresh()
+        ref = s.oracle()
+        s.oracle = lambda: ref  # noqa: B023
+        if at < lens[0]:
+            s.cache.k[s.table[0, at // s.page], at % s.page, Hk - 1, 7] = nan
+        else:
+            s.nk[0, Hk - 1, 7] = nan
+        want = none.copy()
+        want[0, (Hk - 1) * group:] = True
+        check(s, want, f"k {at}")
+    s = fresh()                                  # one element of a value
+    ref = s.oracle()
+    s.oracle = lambda: ref
+    s.cache.v[s.table[2, 0], 3, 0, 11] = nan
+    want = none.copy()
+    want[2, :group, 11] = True
+    check(s, want, "v")
+    s = fresh()                                  # the bias of the event itself
+    ref = s.oracle()
+    s.oracle = lambda: ref
+    s.bias[H - 1, 0] = nan
+    want = none.copy()
+    want[:, H - 1] = True
+    check(s, want, "bias")
+    s = fresh()                                  # a score that overflows: infinity less infinity
+    ref = s.oracle()
+    s.oracle = lambda: ref
+    s.q[2, 0, 0] = 3e38
+    s.cache.k[s.table[2, 0], 1, 0, 0] = 3e38
+    out = _np(s.run())
+    assert np.all(np.isnan(out[2, 0])) and np.all(np.isfinite(out[:2]))
