@@ -552,7 +552,8 @@ int dlrm_interaction_bwd(const float* d_dense, const float* d_pooled, const floa
  * lse = -infinity, and no gradient.  Keys and values that no event may see (a negative key_off: a
  * lookup that found no row) are never used, whatever they hold; a value that
  * is not finite in a visible place may reach every event of its sequence.  A
- * score that is NaN or +infinity makes its row's out NaN.
+ * score that is NaN or +infinity makes its row's out and lse NaN, and with them
+ * the row's gradients and those of the keys and values that it sees.
  *
  * q, k, v, out and their gradients are [n_events, heads, dim] in the
  * handle's type (RSE_F32 or RSE_BF16), given as rse_seq_rows: the elements

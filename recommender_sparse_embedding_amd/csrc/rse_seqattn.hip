@@ -199,7 +199,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                     const float by = move ? top : 0.f, r = __builtin_amdgcn_exp2f(-by);
                     m += by;
                     // nothing summed yet: 0, also where exp2 overflows
-                    l = l > 0.f ? l * r : 0.f;
+                    l = l == 0.f ? 0.f : l * r;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] -= by;
                     const float ro = r < INFINITY ? r : 0.f;
@@ -220,13 +220,14 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
             if (BRIEF) wave_lds_sync();         // read before the next tile is stored
         }
         l += other_half(l);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        // a score of NaN or +infinity has left l NaN, and o: both stay
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         if (my_q < len && live) {
             T* dst = out.at(s + my_q, head);
 #pragma unroll
             for (int dt = 0; dt < ND; ++dt) store_column(dst + 32 * dt, o[dt], inv);
             if (S != SAVE_NONE && half == 0)
-                lse2[(int64_t)head * a.n_events + s + my_q] = l > 0.f ? m + log2f(l) : -INFINITY;
+                lse2[(int64_t)head * a.n_events + s + my_q] = l == 0.f ? -INFINITY : m + log2f(l);
             if (S == SAVE_OUT)
 #pragma unroll
                 for (int dt = 0; dt < ND; ++dt) {

@@ -449,7 +449,7 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
             const int32_t lo = half_min(rp), hi = half_max(rp);
             if (t < KT) {
                 s_pos[team][b][t] = rp;
-                s_lse[team][b][t] = rin && rl > -INFINITY ? rl : INFINITY;      // else p = 0
+                s_lse[team][b][t] = !rin || rl == -INFINITY ? INFINITY : rl;    // infinity: p = 0
                 s_del[team][b][t] = rin ? rd : 0.f;
                 if ((t & 31) == 0) {
                     s_range[team][b][t / 32][0] = lo;
@@ -511,18 +511,23 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                     else wave_lds_sync();
                 }
                 x = tb.logits(x, c2, 0.f, wb, s_pairs[wp][u], s_bias[team][b], s_pos[team][b] + 32 * u, my_pos);
-                if (a.causal && i1 < w0 + 31) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f32x4 L = *reinterpret_cast<const f32x4*>(&s_lse[team][b][32 * u + 8 * j + 4 * half]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[4 * j + i] -= L[i];
+                }
+                if (a.causal && i1 < w0 + 31) {         // (after the log-sums: one of NaN goes no further than it is seen)
                     const int lim = my_k - i1 - 4 * half;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) x[r] = tile_row(r, 0) >= lim ? x[r] : -INFINITY;
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const f32x4 L = *reinterpret_cast<const f32x4*>(&s_lse[team][b][32 * u + 8 * j + 4 * half]);
                     const f32x4 de = *reinterpret_cast<const f32x4*>(&s_del[team][b][32 * u + 8 * j + 4 * half]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        x[4 * j + i] = __builtin_amdgcn_exp2f(x[4 * j + i] - L[i]);
+                        x[4 * j + i] = __builtin_amdgcn_exp2f(x[4 * j + i]);
                         dp[4 * j + i] = x[4 * j + i] * (dp[4 * j + i] - de[i]);
                     }
                 }

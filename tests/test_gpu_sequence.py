@@ -753,3 +753,37 @@ def test_step_keeps_what_is_not_finite(lens, dtype, H, Hk):
     s.cache.k[s.table[2, 0], 1, 0, 0] = 3e38
     out = _np(s.run())
     assert np.all(np.isnan(out[2, 0])) and np.all(np.isfinite(out[:2]))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lens,most", [([20, 90, 7], 90), ([150, 290, 33], 290)])
+@pytest.mark.parametrize("H,Hk", [(2, 1), (4, 1)])
+def test_training_keeps_what_is_not_finite(H, Hk, lens, most, dtype):
+    """A row with a score that is NaN or +infinity has no log-sum: its output,
+    its gradient and what it sends to the keys that it sees are NaN; the other
+    sequences keep their values."""
+    a, b = lens[0], lens[0] + lens[1]
+    for what in ("q", "k", "overflow"):
+        c = Case(lens, H, Hk, 64, dtype)
+        ref = c.oracle()
+        i = a + 60                               # of the second sequence
+        if what == "q":
+            c.q[i, 0, 3] = float("nan")
+        elif what == "k":
+            c.k[i, 0, 3] = float("nan")
+        else:
+            c.q[i, 0], c.k[i, 0] = 3e38, 3e38
+        got = c.run(max_len=most)
+        rows = [i] if what != "k" else list(range(i, b))
+        heads = [0] if what != "k" else list(range(H // Hk))
+        for name in ("out", "dq"):
+            assert torch.all(torch.isnan(got[name][rows][:, heads])), (what, name)
+        last = rows[-1] + 1                      # the keys that the last such row sees
+        for name in ("dk", "dv"):
+            assert torch.all(torch.isnan(got[name][a:last, 0])), (what, name)
+        keep = torch.ones(sum(lens), dtype=torch.bool)
+        keep[a:b] = False
+        for name in ("out", "dq", "dk", "dv"):
+            _check(got[name][keep.cuda()], tuple(x[keep.numpy()] for x in ref[name]), name)
+        if what == "q":                          # later keys are not seen by it
+            assert torch.all(torch.isfinite(got["dv"][last:b]))
