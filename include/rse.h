@@ -670,7 +670,9 @@ int rse_seqcache_clear_status(rse_seqcache* cache, void* stream);
  * list on by that).  If the free list is too short (RSE_ERR_NEED_GROW) or a
  * length is negative, a history exceeds max_pages or the counts do not sum to
  * n_events (RSE_ERR_BAD_INPUT), the page table is unchanged, *d_taken is 0
- * and every slot is -1.  d_ws: rse_seqcache_assign_workspace_size bytes.
+ * and every slot is -1.  A page outside the pool, held or from d_free, gives
+ * RSE_ERR_BAD_INPUT: its events get slot -1 and it is not entered in the table;
+ * the rest is assigned.  d_ws: rse_seqcache_assign_workspace_size bytes.
  */
 int rse_seqcache_assign_workspace_size(int64_t batch, size_t* bytes_out);
 int seq_cache_assign(rse_seqcache* cache, const int64_t* d_counts, const int64_t* d_lens, int64_t batch,

@@ -104,7 +104,8 @@ __global__ __launch_bounds__(1024) void k_assign_scan(SeqCacheHeader* h, const i
 // Slots, one event a thread, and the page table: the event that begins a page
 // enters it.  The events of a wave mostly belong to one or two users: one
 // search by the whole wave, then a step or two, or a search of the lane's own.
-__global__ __launch_bounds__(CB) void k_assign_slots(const int64_t* lens, const int64_t* offsets, int64_t batch,
+// An event on a page outside the pool gets no slot, and the page no entry.
+__global__ __launch_bounds__(CB) void k_assign_slots(SeqCacheHeader* h, int64_t n_pages, const int64_t* lens, const int64_t* offsets, int64_t batch,
                                                      int shift, int32_t* table, int64_t max_pages,
                                                      const int32_t* free_pages, int64_t n_events, int64_t* slots,
                                                      const AssignWs* ws) {
@@ -129,6 +130,11 @@ __global__ __launch_bounds__(CB) void k_assign_slots(const int64_t* lens, const 
         const int64_t len = lens[b], e = len + i - offsets[b], p = e >> shift, held = pages_of(len, shift);
         const int64_t in = e & ((1ll << shift) - 1);
         const int32_t page = p < held ? table[b * max_pages + p] : free_pages[ws->page_at[b] + p - held];
+        if (page < 0 || page >= n_pages) {
+            set_status(&h->status, RSE_ERR_BAD_INPUT);
+            slots[i] = -1;
+            continue;
+        }
         if (in == 0) table[b * max_pages + p] = page;
         slots[i] = ((int64_t)page << shift) + in;
     }
@@ -824,8 +830,8 @@ int seq_cache_assign(rse_seqcache* cache, const int64_t* d_counts, const int64_t
     hipLaunchKernelGGL(k_assign_scan, dim3(1), dim3(1024), 0, s, cache->hdr, d_counts, d_lens, batch, shift,
                        (int64_t)max_pages, n_free, n_events, d_offsets, d_taken, ws);
     if (n_events > 0)
-        hipLaunchKernelGGL(k_assign_slots, dim3(fill_blocks(n_events, CB, 4096)), dim3(CB), 0, s, d_lens, d_offsets,
-                           batch, shift, d_page_table, (int64_t)max_pages, d_free, n_events, d_slots, ws);
+        hipLaunchKernelGGL(k_assign_slots, dim3(fill_blocks(n_events, CB, 4096)), dim3(CB), 0, s, cache->hdr,
+                           cache->n_pages, d_lens, d_offsets, batch, shift, d_page_table, (int64_t)max_pages, d_free, n_events, d_slots, ws);
     return launch_status();
 }
 

@@ -257,7 +257,8 @@ def seq_cache_assign(cache: SeqCache, counts: torch.Tensor, lens: torch.Tensor, 
     b (int64 [batch]).  page_table int32 [batch, max_pages] gets the pages,
     taken in order from free_pages (int32).  Returns (slots int64 [n_events],
     seq_offsets int64 [batch + 1], taken int64 [1]); n_events is the counts'
-    sum.  cache.status() tells of a free list that was too short."""
+    sum.  cache.status() tells of a free list that was too short, and of pages
+    outside the pool, whose events get slot -1."""
     batch = counts.numel()
     _need(counts, torch.int64, "counts")
     lens_p = _vector(lens, torch.int64, batch, "lens")

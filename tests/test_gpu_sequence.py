@@ -787,3 +787,40 @@ def test_training_keeps_what_is_not_finite(H, Hk, lens, most, dtype):
             _check(got[name][keep.cuda()], tuple(x[keep.numpy()] for x in ref[name]), name)
         if what == "q":                          # later keys are not seen by it
             assert torch.all(torch.isfinite(got["dv"][last:b]))
+
+
+def test_assign_reports_bad_pages():
+    """Held pages and free pages outside the pool: their events get slot -1,
+    the table keeps its entry and the status says so; the others are assigned."""
+    import recommender_sparse_embedding_amd as rse
+
+    P, n_pages = 8, 10
+    cuda = lambda x, dt: torch.tensor(x, dtype=dt).cuda()  # noqa: E731
+    cache = rse.SeqCache.empty(n_pages, P, 1, 32)
+    for bad in (-1, -7, n_pages, 2**31 - 1):
+        for where in ("held", "free"):
+            # users: 3 cached in page 4, 2 new; 5 cached in `held`, 6 new; none cached, 9 new
+            held, free = [4, 2], [5, 6, 7]
+            if where == "held":
+                held[1] = bad
+            else:
+                free[1] = bad
+            table = cuda([[held[0], -3, -3], [held[1], -3, -3], [-3, -3, -3]], torch.int32)
+            slots, off, taken = rse.seq_cache_assign(cache, cuda([2, 6, 9], torch.int64), cuda([3, 5, 0], torch.int64),
+                                                     table, cuda(free, torch.int32), 17)
+            assert cache.status() == -9, (bad, where)
+            cache.clear_status()
+            second = held[1] * P + np.arange(5, 8) if where == "held" else 2 * P + np.arange(5, 8)
+            third = 6 * P + np.arange(8) if where == "held" else np.full(8, -1)
+            if where == "held":
+                second = np.full(3, -1)
+            want = [4 * P + 3, 4 * P + 4, *second, *(5 * P + np.arange(3)), *third, 7 * P]
+            assert slots.tolist() == want, (bad, where)
+            assert off.tolist() == [0, 2, 8, 17] and taken.item() == 3
+            first = -3 if where == "free" else 6
+            assert table.tolist() == [[4, -3, -3], [held[1], 5, -3], [first, 7, -3]], (bad, where)
+            # what is written is what has a slot
+            cache.k.zero_()
+            x = torch.ones((17, 1, 32), dtype=torch.bfloat16, device="cuda")
+            rse.seq_cache_write(cache, slots, x, x, torch.zeros(17, dtype=torch.int32, device="cuda"))
+            assert int((cache.k.view(-1, 32)[:, 0] != 0).sum()) == sum(w >= 0 for w in want) and cache.status() == 0
