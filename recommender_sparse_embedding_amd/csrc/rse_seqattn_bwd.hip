@@ -402,8 +402,9 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
     auto& s_d = s_rows[1];
     constexpr bool BRIEF = SH::TEAM == 1;
     __shared__ u32x4 s_pairs[BRIEF ? 2 : WQ][NS][WAVE];      // (BRIEF: this tile's and the last one's)
-    __shared__ float s_lse[SH::TEAMS][NB][KT], s_del[SH::TEAMS][NB][KT];
-    __shared__ int32_t s_pos[SH::TEAMS][NB][KT];
+    // (read by 16 bytes)
+    alignas(16) __shared__ float s_lse[SH::TEAMS][NB][KT], s_del[SH::TEAMS][NB][KT];
+    alignas(16) __shared__ int32_t s_pos[SH::TEAMS][NB][KT];
     __shared__ int32_t s_range[SH::TEAMS][NB][NS][2];
     __shared__ LdsBuckets s_buckets;
     __shared__ float s_bias[SH::TEAMS][NB][NBP];

@@ -222,7 +222,7 @@ __global__ __launch_bounds__(SW * 64) __attribute__((amdgpu_waves_per_eu(STEP_WA
     constexpr int CH = TL::CH, ND = D / 32, NC = CH / 2;
     extern __shared__ u32x4 s_mem[];            // SW tiles of V, then the waves' sums; s_bias [nb][cols]
     __shared__ int32_t s_bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
-    __shared__ int32_t s_idx[SW][32];
+    alignas(16) __shared__ int32_t s_idx[SW][32];       // (read by 16 bytes)
     __shared__ float s_ml[SW][2][32];
     const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), half = lane >> 5, col = lane & 31;
     const int n_kv = a.n_heads / a.group, nb = a.n_bounds + 1, blocks = (a.group + cols - 1) / cols;
@@ -429,7 +429,7 @@ __global__ __launch_bounds__(SW * 64) void k_step_few(StepArgs a, Rows<const flo
     extern __shared__ float s_few[];            // bias in base 2 [nb][NH]
     __shared__ int32_t s_bounds[RSE_SEQ_MAX_BOUNDARIES + 1];
     __shared__ float s_ml[SW][2][NH];
-    __shared__ float s_sum[SW][NH][D];
+    alignas(16) __shared__ float s_sum[SW][NH][D];      // (written by 16 bytes)
     const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), piece = lane % LR, row = lane / LR;
     const int n_kv = a.n_heads / a.group, nb = a.n_bounds + 1, nc = a.group;
     int64_t x = blockIdx.x;

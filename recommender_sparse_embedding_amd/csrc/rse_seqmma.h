@@ -10,6 +10,8 @@
 // because the order of a contraction is free as long as both operands agree.
 #pragma once
 
+#include <cstddef>
+
 #include "rse_seq.h"
 
 namespace rse {
@@ -601,14 +603,17 @@ struct RowStage {
 
 // The events of a tile of keys beside its rows (the team's first KT threads):
 // positions, which may be seen, and of each 32 of them the lowest and highest
-// position and whether any may not be seen.
+// position and whether any may not be seen.  mask and pos are read by 16 bytes,
+// in every element of an array of these.
 template <int KT>
-struct KeySide {
+struct alignas(16) KeySide {
     float mask[KT];
     int32_t pos[KT];
     int32_t range[KT / 32][2];
     uint32_t hidden[KT / 32];                   // bit per event
 };
+static_assert(sizeof(KeySide<32>) % 16 == 0 && offsetof(KeySide<32>, pos) % 16 == 0, "16-byte reads");
+static_assert(sizeof(KeySide<64>) % 16 == 0 && offsetof(KeySide<64>, pos) % 16 == 0, "16-byte reads");
 struct KeySideStage {
     int32_t p, off;
     bool in;
