@@ -559,7 +559,9 @@ int dlrm_interaction_bwd(const float* d_dense, const float* d_pooled, const floa
  * handle's type (RSE_F32 or RSE_BF16), given as rse_seq_rows: the elements
  * of a head are adjacent, the distances between events and between heads are
  * free (views of one joint projection, for example).  Addresses and both
- * strides are multiples of 16 bytes, else RSE_ERR_INVALID_ARG.  Products are
+ * strides are multiples of 16 bytes, and no two heads of an output overlap (of
+ * an input they may: one head given for several, say), else
+ * RSE_ERR_INVALID_ARG.  Products are
  * accumulated and the softmax is held in fp32.  With RSE_BF16 outputs are
  * rounded once at the end: the probabilities and their gradients enter their
  * products as pairs of bf16 values (2^-16 of each is lost); the bias gradient

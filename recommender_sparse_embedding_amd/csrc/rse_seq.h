@@ -154,6 +154,26 @@ inline bool rows_ok(const rse_seq_rows* r, int32_t dtype) {
            r->head_stride % (16 / e) == 0;
 }
 
+// Rows to be written: no element belongs to two events or heads.  Two of them,
+// di events and dh heads apart, overlap where their distance is less than a
+// head; of the di only those next to cancelling dh heads can be.
+inline bool out_rows_ok(const rse_seq_rows* r, int32_t dtype, int64_t n, int64_t heads, int32_t dim) {
+    if (!rows_ok(r, dtype)) return false;
+    using Wide = __int128;
+    const auto apart = [&](Wide di, int64_t dh) {
+        if (di <= -(Wide)n || di >= n || (di == 0 && dh == 0)) return true;
+        const Wide x = di * r->row_stride + (Wide)dh * r->head_stride;
+        return x >= dim || x <= -dim;
+    };
+    for (int64_t dh = 0; dh < heads; ++dh) {
+        Wide near = r->row_stride ? -((Wide)dh * r->head_stride) / r->row_stride : 0;
+        near = near < 1 - (Wide)n ? 1 - (Wide)n : (near > (Wide)n - 1 ? (Wide)n - 1 : near);
+        for (int u = -1; u <= 1; ++u)
+            if (!apart(near + u, dh)) return false;
+    }
+    return true;
+}
+
 template <typename T>
 inline rse::Rows<T> rows_view(const rse_seq_rows* r) {
     return {static_cast<T*>(r->data), r->row_stride, r->head_stride};

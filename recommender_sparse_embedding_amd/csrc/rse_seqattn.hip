@@ -343,7 +343,8 @@ int seq_attention_fwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
     int rc = batch_ok(attn, batch);
     if (rc) return rc;
     if (batch->n_events == 0) return RSE_OK;
-    if (!rows_ok(q, attn->dtype) || !rows_ok(k, attn->dtype) || !rows_ok(v, attn->dtype) || !rows_ok(out, attn->dtype))
+    if (!rows_ok(q, attn->dtype) || !rows_ok(k, attn->dtype) || !rows_ok(v, attn->dtype) ||
+        !out_rows_ok(out, attn->dtype, batch->n_events, attn->n_heads, attn->dim))
         return RSE_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(d_saved) % 256) return RSE_ERR_INVALID_ARG;
     Saved sv = saved_view(attn, batch->n_events, batch->max_len, d_saved);

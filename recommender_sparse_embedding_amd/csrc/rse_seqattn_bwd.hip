@@ -683,8 +683,11 @@ int seq_attention_bwd(const rse_seqattn* attn, const rse_seq_batch* batch, const
         hipLaunchKernelGGL(k_attn_dbias, dim3(attn->n_heads * (attn->n_bounds + 1)), dim3(256), 0, s, w.part, 0, d_dbias);
         return launch_status();
     }
-    for (const rse_seq_rows* r : {q, k, v, dout, dq, dk, dv})
+    for (const rse_seq_rows* r : {q, k, v, dout})
         if (!rows_ok(r, attn->dtype)) return RSE_ERR_INVALID_ARG;
+    for (const rse_seq_rows* r : {dq, dk, dv})
+        if (!out_rows_ok(r, attn->dtype, batch->n_events, r == dq ? attn->n_heads : attn->n_kv_heads, attn->dim))
+            return RSE_ERR_INVALID_ARG;
     if (!d_saved || reinterpret_cast<uintptr_t>(d_saved) % 256) return RSE_ERR_INVALID_ARG;
     const Saved sv = saved_view(attn, batch->n_events, batch->max_len, const_cast<void*>(d_saved));
     if (saved_bytes < sv.bytes) return RSE_ERR_WORKSPACE;

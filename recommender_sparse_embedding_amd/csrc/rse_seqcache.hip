@@ -866,8 +866,9 @@ int seq_attention_step(const rse_seqattn* attn, rse_seqcache* cache, const rse_s
         return RSE_ERR_INVALID_ARG;
     if (batch == 0) return RSE_OK;
     if (!d_pos || !d_bias || !d_page_table || !d_lens) return RSE_ERR_INVALID_ARG;
-    for (const rse_seq_rows* r : {q, k, v, out})
+    for (const rse_seq_rows* r : {q, k, v})
         if (!rows_ok(r, attn->dtype)) return RSE_ERR_INVALID_ARG;
+    if (!out_rows_ok(out, attn->dtype, batch, attn->n_heads, attn->dim)) return RSE_ERR_INVALID_ARG;
     const StepPlan plan = step_plan(attn, batch, max_len);
     const StepWs ws = step_ws(attn, batch, plan, d_ws);
     if (ws_bytes < ws.bytes) return RSE_ERR_WORKSPACE;

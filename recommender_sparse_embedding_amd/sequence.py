@@ -4,7 +4,8 @@
 distance boundaries); ``SeqCache`` the paged keys, values and times of every
 user's history for serving.  Rows are [n_events, heads, dim] tensors whose
 last dimension is contiguous; the other strides are free in steps of 16 bytes
-(views of a joint projection, for example).  Every call is ordered on the
+(views of a joint projection, for example); only inputs may overlap
+themselves (an expanded tensor).  Every call is ordered on the
 given stream (default: the current one), and tensors it returns are allocated
 for that stream.
 """

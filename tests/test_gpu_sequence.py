@@ -824,3 +824,49 @@ def test_assign_reports_bad_pages():
             x = torch.ones((17, 1, 32), dtype=torch.bfloat16, device="cuda")
             rse.seq_cache_write(cache, slots, x, x, torch.zeros(17, dtype=torch.int32, device="cuda"))
             assert int((cache.k.view(-1, 32)[:, 0] != 0).sum()) == sum(w >= 0 for w in want) and cache.status() == 0
+
+
+def test_outputs_that_overlap_are_refused():
+    """Outputs whose heads or events share memory are refused before anything
+    is written; other layouts, and inputs that overlap themselves, are not."""
+    c = Case([2, 1], 3, 1, 32, BF16)
+    rse, where = c.rse, (c.attn, c.q, c.k, c.v, c.pos, c.bias, c.off)
+    want, saved = rse.seq_attention_fwd(*where, for_backward=True)
+    grads = rse.seq_attention_bwd(*where, saved, c.dout)
+    new = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    flat = new(4096)
+    bad = [new(1, 3, 32).expand(3, 3, 32), new(3, 1, 32).expand(3, 3, 32), flat.as_strided((3, 3, 32), (96, 16, 1)),
+           flat.as_strided((3, 3, 32), (24, 1024, 1)), flat.as_strided((3, 3, 32), (32, 64, 1)),
+           flat.as_strided((3, 3, 32), (64, 40, 1))]
+    for t in bad:
+        with pytest.raises(rse.RseError) as e:
+            rse.seq_attention_fwd(*where, out=t)
+        assert e.value.code == -1
+        with pytest.raises(rse.RseError):
+            rse.seq_attention_bwd(*where, saved, c.dout, grads=(t, new(3, 1, 32), new(3, 1, 32)))
+    with pytest.raises(rse.RseError):
+        rse.seq_attention_bwd(*where, saved, c.dout, grads=(new(3, 3, 32), new(1, 1, 32).expand(3, 1, 32), new(3, 1, 32)))
+    assert torch.all(flat == 0)
+    one = Case([1], 3, 1, 32, BF16)
+    for shape in ((8, 16, 1), (4096, 24, 1), (0, 0, 1)):
+        with pytest.raises(rse.RseError):
+            one.forward(out=flat.as_strided((1, 3, 32), shape))
+    assert torch.equal(one.forward(out=flat.as_strided((1, 3, 32), (8, 40, 1))), one.forward())
+    flat.zero_()
+    good = [new(3, 3, 32).transpose(0, 1), flat.as_strided((3, 3, 32), (32, 96, 1)),
+            flat.as_strided((3, 3, 32), (256, 64, 1)), flat.as_strided((3, 3, 32), (160, 64, 1))]
+    for t in good:
+        assert torch.equal(rse.seq_attention_fwd(*where, out=t), want)
+        got = rse.seq_attention_bwd(*where, saved, c.dout, grads=(t, new(3, 1, 32), new(3, 1, 32)))
+        assert torch.equal(got[0], grads[0])
+    # one key and one gradient given for all events or heads
+    k, do = c.k[:1].expand(3, 1, 32), c.dout[:, :1].expand(3, 3, 32)
+    out, saved = rse.seq_attention_fwd(c.attn, c.q, k, *where[3:], for_backward=True)
+    got = rse.seq_attention_bwd(c.attn, c.q, k, *where[3:], saved, do)
+    full = rse.seq_attention_bwd(c.attn, c.q, k.contiguous(), *where[3:], saved, do.contiguous())
+    assert all(torch.equal(x, y) for x, y in zip(got, full))
+
+    s = Serving([5, 9], 4, 2, 64, BF16)
+    with pytest.raises(rse.RseError):
+        s.run(out=new(1, 4, 64).expand(2, 4, 64))
+    assert torch.equal(s.run(out=new(4, 2, 64).transpose(0, 1)), s.run())
