@@ -99,7 +99,7 @@ class SeqAttention:
                                      self.dim, dtype, int(self.causal), self.scale, arr, n, _stream(stream)),
               "rse_seqattn_create")
         self.handle = h
-        self.step_bytes: dict[tuple[int, int], int] = {}     # workspace sizes of steps, by (batch, max_len)
+        self.step_bytes = (-1, -1, 0)            # the last step's batch, max_len and workspace size
         self._finalizer = weakref.finalize(self, lib.rse_seqattn_destroy, h)
 
     @property
@@ -303,10 +303,12 @@ def seq_attention_step(attn: SeqAttention, cache: SeqCache, q: torch.Tensor, k: 
     pos_p = _vector(pos, torch.int32, batch, "pos")
     bias_p = _vector(bias, torch.float32, H * attn.n_buckets, "bias")
     lens_p = _vector(lens, torch.int64, batch, "lens")
-    size = attn.step_bytes.get((batch, most))
-    if size is None:
+    known = attn.step_bytes
+    if known[:2] == (batch, most):
+        size = known[2]
+    else:
         size = _size(lib.rse_seqattn_step_workspace_size, "rse_seqattn_step_workspace_size", attn.handle, batch, most)
-        attn.step_bytes[(batch, most)] = size
+        attn.step_bytes = (batch, most, size)
     if out is None:
         out = _on_empty(stream, (batch, H, D), dt, q.device)
     ws = _on_empty(stream, size, torch.uint8, q.device) if size else None

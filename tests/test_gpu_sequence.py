@@ -870,3 +870,16 @@ def test_outputs_that_overlap_are_refused():
     with pytest.raises(rse.RseError):
         s.run(out=new(1, 4, 64).expand(2, 4, 64))
     assert torch.equal(s.run(out=new(4, 2, 64).transpose(0, 1)), s.run())
+
+
+def test_steps_keep_nothing_per_length():
+    """A server whose longest history grows by one a step: the layer holds no
+    more afterwards than before."""
+    s = Serving([20, 40], 4, 2, 64, BF16)
+    s.run()
+    held = lambda: sum(len(x) for x in vars(s.attn).values() if isinstance(x, (dict, list, set, tuple)))  # noqa: E731
+    before = held()
+    want = s.run()
+    for most in range(41, 141):
+        assert torch.equal(s.run(max_len=most), want)
+    assert held() <= before
