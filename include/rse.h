@@ -650,8 +650,9 @@ typedef struct rse_seqcache rse_seqcache;
 /* Device bytes of a cache's metadata (its status). */
 int rse_seqcache_meta_size(size_t* bytes_out);
 
-/* Create over caller memory.  page_size is a power of two in [8, 1024];
- * n_pages * page_size may not exceed 2^40.  k, v and pos are 16-byte aligned. */
+/* Create over caller memory.  page_size is a power of two in [8, 1024], else
+ * RSE_ERR_UNSUPPORTED; n_pages is below 2^31 and n_pages * page_size at most
+ * 2^40, else RSE_ERR_INVALID_ARG.  k, v and pos are 16-byte aligned. */
 int rse_seqcache_create(rse_seqcache** out, void* d_meta, size_t meta_bytes, void* d_k, void* d_v, int32_t* d_pos,
                         int64_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t dim, int32_t dtype,
                         void* stream);

@@ -762,7 +762,7 @@ int rse_seqcache_create(rse_seqcache** out, void* d_meta, size_t meta_bytes, voi
     if (dim != 32 && dim != 64 && dim != 128) return RSE_ERR_UNSUPPORTED;
     if (n_kv_heads < 1 || n_kv_heads > RSE_SEQ_MAX_HEADS) return RSE_ERR_INVALID_ARG;
     if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1))) return RSE_ERR_UNSUPPORTED;
-    if (n_pages < 1 || n_pages > INT32_MAX) return RSE_ERR_INVALID_ARG;
+    if (n_pages < 1 || n_pages > INT32_MAX || n_pages * page_size > 1ll << 40) return RSE_ERR_INVALID_ARG;
     rse_seqcache* c = new (std::nothrow) rse_seqcache();
     if (!c) return RSE_ERR_INVALID_ARG;
     c->hdr = static_cast<SeqCacheHeader*>(d_meta);

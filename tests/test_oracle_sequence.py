@@ -165,3 +165,10 @@ def test_binding_refuses_before_any_call():
         sequence._rows(x, torch.bfloat16, 3, 2, 64, "q")
     with pytest.raises(TypeError):
         rse.SeqCache(torch.zeros((3, 8, 64)), None, None)
+
+
+def test_cache_handle_refuses_too_many_slots(lib):
+    """The stated limit of 2^40 events; refused before the memory is touched."""
+    h = ctypes.c_void_p()
+    for pages, size in ((2**30 + 1, 1024), (2**31 - 1, 1024), (2**31, 8)):
+        assert lib.rse_seqcache_create(ctypes.byref(h), MEM, 1 << 20, MEM, MEM, MEM, pages, size, 1, 32, 1, None) == INV
