@@ -35,6 +35,7 @@ import hashlib
 import json
 import os
 import platform
+import re
 import sys
 import time
 
@@ -140,6 +141,24 @@ def ceilings():
     print(json.dumps({"ceilings": res, "peak_gbs": PEAK_HBM_GBS}))
 
 
+# sections of rse.h that declare nothing of the step
+NOT_IN_STEP = (b"attention over behaviour sequences", b"history cache and single events")
+
+
+def step_header(text: bytes) -> bytes:
+    """rse.h without the sections of NOT_IN_STEP.  A section goes from its
+    title line to the next one's; one that is not there exactly once, or that
+    declares anything but sequence operators, stays."""
+    at = [m.start() for m in re.finditer(rb"^/\* -{2,} .* -{2,} \*/$", text, re.M)] + [len(text)]
+    sections = [text[:at[0]]] + [text[a:b] for a, b in zip(at, at[1:])]
+    for title in NOT_IN_STEP:
+        mine = [s for s in sections if s.split(b"\n", 1)[0].strip(b"/* -") == title]
+        code = re.sub(rb"/\*.*?\*/", b"", mine[0], flags=re.S) if len(mine) == 1 else b"int other("
+        if all(b"seq" in name for name in re.findall(rb"(\w+)\s*\(", code)):
+            sections.remove(mine[0])
+    return b"".join(sections)
+
+
 def kernel_sources_sha() -> str:
     """Hash of the HIP sources and headers that the step's kernels are built
     from: stored counter summaries apply only to the kernels they were taken
@@ -153,8 +172,7 @@ def kernel_sources_sha() -> str:
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:
             text = fh.read()
-        a, b = text.find(b"/* " + b"-" * 31 + b" attention over"), text.find(b"/* " + b"-" * 55 + b" kernel trace")
-        h.update(text[:a] + text[b:] if 0 < a < b else text)
+        h.update(step_header(text) if f.endswith("rse.h") else text)
     return h.hexdigest()[:16]
 
 
