@@ -74,24 +74,33 @@ class Recommender:
         return diff.square().mean()
 
     def cache(self, ids, times, counts, n_pages: int, max_pages: int):
-        """Users' histories in a new cache: (cache, page table, lengths, free pages)."""
-        _, _, x = self.lookup(ids, train=False)
-        _, k, v = self.project(x)
+        """Users' histories in a new cache: (cache, page table, lengths, free
+        pages).  Training hides events whose id has no row; here they are not
+        cached, which is the same to every later event (distances are by time)."""
+        rows, _, x = self.lookup(ids, train=False)
+        seen = rows >= 0
+        user = torch.repeat_interleave(torch.arange(counts.numel(), device=ids.device), counts)
+        lens = torch.bincount(user[seen], minlength=counts.numel())
+        _, k, v = self.project(x[seen])
         cache = rse.SeqCache.empty(n_pages, PAGE, KV_HEADS, HEAD_DIM)
         table = torch.full((counts.numel(), max_pages), -1, dtype=torch.int32, device=ids.device)
         free = torch.arange(n_pages, dtype=torch.int32, device=ids.device)
-        slots, _, taken = rse.seq_cache_assign(cache, counts, torch.zeros_like(counts), table, free, len(ids))
-        rse.seq_cache_write(cache, slots, k, v, times)
-        return cache, table, counts.clone(), free[int(taken):].contiguous()
+        slots, _, taken = rse.seq_cache_assign(cache, lens, torch.zeros_like(lens), table, free, len(k))
+        rse.seq_cache_write(cache, slots, k, v, times[seen].contiguous())
+        return cache, table, lens, free[int(taken):].contiguous()
 
     def answer(self, cache, table, lens, free, ids, times):
-        """One new event per user: its attention over the user's history."""
-        one = torch.ones_like(lens)
-        _, _, taken = rse.seq_cache_assign(cache, one, lens, table, free, len(lens))
-        _, _, x = self.lookup(ids, train=False)
+        """One new event per user: its attention over the user's history.  An
+        id without a row is neither answered (0) nor cached: a step's event
+        always sees itself."""
+        rows, _, x = self.lookup(ids, train=False)
+        seen = rows >= 0
+        one = seen.long()
+        _, _, taken = rse.seq_cache_assign(cache, one, lens, table, free, int(one.sum()))
         q, k, v = self.project(x)
-        out = rse.seq_attention_step(self.attn, cache, q, k, v, times, self.bias, table, lens)
-        lens += 1
+        at = torch.where(seen, lens, -1)
+        out = rse.seq_attention_step(self.attn, cache, q, k, v, times, self.bias, table, at)
+        lens += one
         return out, free[int(taken):].contiguous()
 
 
@@ -109,16 +118,20 @@ def main(users: int = 200, longest: int = 100, steps: int = 30, device="cuda"):
     losses = [round(float(x), 5) for x in losses]
     print("loss", losses[0], "->", losses[-1])
 
-    # the histories without their last event, then that event as the next one:
-    # the answer is the forward's row of it
+    # some events of ids that training never met, which have no row; then the
+    # histories without their last event, and that event as the next one: the
+    # answer is the forward's row of it
     last = offsets[1:] - 1
-    _, _, x = model.lookup(ids, train=False)
-    want = rse.seq_attention_fwd(model.attn, *model.project(x), times, model.bias, offsets, max_len=longest)[last]
+    ids = torch.where(torch.rand(n, generator=g, device=device) < 0.05, ids + 10**6, ids)
+    rows, _, x = model.lookup(ids, train=False)
+    want = rse.seq_attention_fwd(model.attn, *model.project(x), times, model.bias, offsets, key_off=rows,
+                                 max_len=longest)[last]
     keep = torch.ones(n, dtype=torch.bool, device=device)
     keep[last] = False
     cache, table, lens, free = model.cache(ids[keep], times[keep].contiguous(), counts - 1, users * 8, 8)
     got, free = model.answer(cache, table, lens, free, ids[last], times[last].contiguous())
-    off = float((got.float() - want.float()).abs().max())
+    found = rows[last] >= 0
+    off = float((got[found].float() - want[found].float()).abs().max())
     print("one step against the whole forward: largest difference", off)
     assert model.attn.status() == 0 and cache.status() == 0
     return losses, off

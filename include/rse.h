@@ -695,8 +695,9 @@ int rse_seqattn_step_workspace_size(const rse_seqattn* attn, int64_t batch, int6
  * One new event for each user: its k, v, pos are stored at event number
  * d_lens[b] of user b (whose page must be in the table), and out[b] =
  * attention of q[b] over the d_lens[b] + 1 events, itself included, by the
- * formulas above (key_off aside; the event is the last, so causal or not is
- * the same).  d_lens[b] < 0: the user is idle, out[b] = 0 and nothing is
+ * formulas above (the event is the last, so causal or not is the same).  There
+ * is no key_off: an event without a row is kept out of the cache, and the new
+ * event always sees itself.  d_lens[b] < 0: the user is idle, out[b] = 0 and nothing is
  * stored.  d_lens[b] + 1 > max_len or past the table, or a page out of the
  * pool: RSE_ERR_BAD_INPUT in the cache's status and out[b] = 0 (of a bad
  * page, only its cached events are left out).  Slots behind a history are not used, whatever they

@@ -294,7 +294,8 @@ def seq_attention_step(attn: SeqAttention, cache: SeqCache, q: torch.Tensor, k: 
     int32 [batch] as event lens[b] (int64; negative: idle) and returns its
     attention [batch, n_heads, dim] over the whole history, itself included.
     max_len: no history with its new event is longer (default: the table's
-    width).  lens is not changed."""
+    width).  lens is not changed.  There is no key_off here: events that
+    seq_attention_fwd would hide are kept out of the cache."""
     batch = q.shape[0]
     dt, H, Hk, D = attn.torch_dtype, attn.n_heads, attn.n_kv_heads, attn.dim
     args = [_rows(q, dt, batch, H, D, "q"), _rows(k, dt, batch, Hk, D, "k"), _rows(v, dt, batch, Hk, D, "v")]
