@@ -883,3 +883,110 @@ def test_steps_keep_nothing_per_length():
     for most in range(41, 141):
         assert torch.equal(s.run(max_len=most), want)
     assert held() <= before
+
+
+# ------------------------------------------------- batches past one grid's size --
+def _grid_fit(head_blocks, waves):
+    """Sequences that a grid of the short form takes side by side (short_grid);
+    with more, each block goes on to further ones."""
+    return -(-(8192 // waves) // head_blocks)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("H,Hk,batch", [(1, 1, 8207), (8, 8, 1301), (32, 32, 555), (64, 16, 301)])
+def test_blocks_that_go_on_to_further_sequences(H, Hk, batch, dtype):
+    """More sequences than the short form's blocks, by an uneven amount, of
+    lengths from none to the limit: the grouped (64 on 16 heads) and the plain
+    kernels of dk and dv, and those of the forward and dq."""
+    wh = 4 if H > 1 else 1
+    grouped = H // Hk % 4 == 0 and H > 1
+    dkv_blocks = Hk if grouped else -(-Hk // wh)
+    for fit in (_grid_fit(-(-H // wh), wh), _grid_fit(dkv_blocks, wh)):
+        assert fit < batch and batch % fit       # each block takes one or more, not all as many
+    lens = [(37 * i) % 129 if i % 9 == 4 else (5 * i) % 8 for i in range(batch)]
+    Case(lens, H, Hk, 32, dtype, causal=H != 8, missing=0.1).check()
+
+
+def _searched(lens, tile, most):
+    """Whether tiles of that many events are numbered by the offsets and found
+    by a search (tile_grid)."""
+    n, batch = sum(lens), len(lens)
+    return -(-min(most, n) // tile) > 4 * (n // tile + batch) // batch
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (3, 3), (4, 1), (8, 2)])
+def test_tiles_found_by_a_search(H, Hk, D, dtype):
+    """One long sequence among many short ones and empty ones, first, between
+    and last; and a usual batch without max_len."""
+    short = [(7 * i) % 10 for i in range(40)]
+    for at, causal in ((0, True), (17, False), (40, True)):
+        lens = short[:at] + [600] + short[at:]
+        assert all(_searched(lens, tile, 600) for tile in (32, 64, 128))
+        Case(lens, H, Hk, D, dtype, causal=causal, missing=0.1).check()
+    lens = [0, 0] + [11 + (13 * i) % 20 for i in range(58)]
+    c = Case(lens, H, Hk, D, dtype, causal=H != 3)
+    assert all(_searched(lens, tile, sum(lens)) for tile in (32, 64, 128))
+    ref, got = c.oracle(), c.run(max_len=None)
+    for name in got:
+        _check(got[name], ref[name], name)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D,H,Hk", [(32, 4, 4), (64, 2, 1), (128, 4, 1)])
+def test_malformed_offsets_of_searched_tiles(D, H, Hk, dtype):
+    """Reported, forward and backward, and the call after them is right."""
+    lens = [(7 * i) % 10 for i in range(40)] + [600]
+    c = Case(lens, H, Hk, D, dtype)
+    good, n = c.off.clone(), sum(lens)
+    dout = c.dout
+    for at, x in ((1, n + 5), (20, -3), (40, 0), (0, 2), (41, n - 1), (30, 2**62), (7, -2**62)):
+        c.off = good.clone()
+        c.off[at] = x
+        where = (c.attn, c.q, c.k, c.v, c.pos, c.bias, c.off)
+        out, saved = c.rse.seq_attention_fwd(*where, max_len=600, for_backward=True)
+        assert c.attn.status() == -9, (at, x)
+        c.attn.clear_status()
+        c.rse.seq_attention_bwd(*where, saved, dout, max_len=600)
+        assert c.attn.status() == -9, (at, x)
+        c.attn.clear_status()
+    c.off = good
+    c.forward(max_len=599)                       # the long one is longer
+    assert c.attn.status() == -9
+    c.attn.clear_status()
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_malformed_offsets_of_many_short_sequences(dtype):
+    lens = [(5 * i) % 8 for i in range(1301)]
+    c = Case(lens, 8, 8, 32, dtype)
+    good, n = c.off.clone(), sum(lens)
+    for at, x in ((1, n + 5), (1200, -3), (1300, 0), (0, 2), (1301, n - 1), (700, 2**62)):
+        c.off = good.clone()
+        c.off[at] = x
+        where = (c.attn, c.q, c.k, c.v, c.pos, c.bias, c.off)
+        out, saved = c.rse.seq_attention_fwd(*where, max_len=100, for_backward=True)
+        assert c.attn.status() == -9, (at, x)
+        c.attn.clear_status()
+        c.rse.seq_attention_bwd(*where, saved, c.dout, max_len=100)
+        assert c.attn.status() == -9, (at, x)
+        c.attn.clear_status()
+    c.off = good
+    c.check()
+
+
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(torch.float32).min, -1e30])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_bias_that_hides_from_both_key_heads(low, dtype):
+    """A hidden bucket in the middle, and for one head also that of the event
+    itself: rows with nothing left are 0 in out and dq and send nothing."""
+    c = Case([1, 40, 90], 2, 2, 32, dtype, bounds=(1, 2, 4), times=False)
+    c.bias[:, 2] = low
+    c.bias[0, 0] = low
+    got = c.check()
+    first = torch.tensor([0, 1, 41]).cuda()      # of head 0: the event itself hidden
+    assert torch.all(got["out"][first, 0] == 0) and torch.all(got["dq"][first, 0] == 0)
+    assert torch.equal(got["out"][first, 1], c.v[first, 1])      # of head 1: only itself
+    assert torch.all(got["dbias"][:, 2] == 0) and got["dbias"][0, 0] == 0
