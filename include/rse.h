@@ -608,8 +608,9 @@ typedef struct rse_seq_batch {
     const float* d_bias;      /* [n_heads, n_boundaries + 1] */
 } rse_seq_batch;
 
-/* Bytes of what a forward leaves for its backward (fp32 statistics of every
- * event and head), for the same n_events and max_len. */
+/* Bytes of what a forward leaves for its backward, for the same n_events and
+ * max_len: in fp32 the lse of every event and head and, unless max_len is at
+ * most 128 and a head at most 128 bytes, the outputs (4 bytes an element). */
 int rse_seqattn_saved_size(const rse_seqattn* attn, int64_t n_events, int64_t max_len, size_t* bytes_out);
 
 /* Forward.  d_saved: rse_seqattn_saved_size bytes (256-byte aligned) written

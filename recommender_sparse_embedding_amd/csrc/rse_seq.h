@@ -206,7 +206,13 @@ inline rse::SeqArgs seq_args(const rse_seqattn* a, const rse_seq_batch* b) {
 }
 
 // Sequences short enough (and rows narrow enough) for the kernels whose waves
-// work apart: see SHORT.
+// work apart.  us, short / long form, forward and training step, 8192
+// sequences of 1..100 events: 4 heads on 4 of 64 in bf16 329 / 450 and 1283 /
+// 1746, of 32 217 / 236 and 895 / 1137, of 32 in fp32 416 / 473 and 1669 / 1660.
+// 8 heads on 2 share keys by fours, which suits the long form's forward: bf16
+// of 64 594 / 447 and 2370 / 2510, fp32 of 32 750 / 597 and 3084 / 2862.  Past
+// 128 events a block's sequences become too unequal (512 of 1..203, fp32 of 32,
+// both ways: 525 us in the long form, 1190 with this one up to 256).
 constexpr int64_t SHORT = 128;
 inline bool short_form(const rse_seqattn* a, int64_t max_len) {
     return max_len <= SHORT && a->dim * (a->dtype == RSE_F32 ? 4 : 2) <= 128;

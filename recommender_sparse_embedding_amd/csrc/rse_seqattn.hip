@@ -1,6 +1,6 @@
 // rse_seqattn.hip -- attention over the events of each behaviour sequence of
 // a jagged batch, with a learned bias by buckets of the events' distance:
-// forward, and the backward that recomputes the probabilities.
+// handles and the forward.
 #include <cmath>
 #include <new>
 
@@ -74,8 +74,8 @@ __global__ void k_attn_clear(SeqHeader* h) { h->status = 0; }
 // bf16: the probabilities enter V^T P^T as pairs of bf16 values (2^-16 of each
 // is lost), so that out is fp32 arithmetic rounded once.  With one value each
 // their rounding put as much into out again as its own: 0.0022 of its size
-// against 0.0017, for 205 instead of 227 us on 16 histories of up to 4096
-// events and 38 instead of 40 on 96 sessions of up to 333 (dim 128).
+// against 0.0016, for 188 instead of 218 us on 16 histories of up to 4096
+// events and 37 instead of 38 on 96 sessions of up to 333 (dim 128).
 //
 // SAVE: also leaves the log-sums for the backward, and SAVE_OUT the outputs:
 // its dO . out has to equal sum_j p dp to fp32 accuracy (the bias gradient

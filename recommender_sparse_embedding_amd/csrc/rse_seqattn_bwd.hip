@@ -6,9 +6,9 @@
 //
 // bf16: p and ds enter their products as pairs of bf16 values (2^-16 of each is
 // lost), so that the gradients are fp32 arithmetic rounded once.  With one
-// value each dq and dk were half again as far off as that, for 1285 instead of
-// 1333 us a training step on 8192 sequences of 1..100 events, 4 heads of 64,
-// and 377 instead of 411 on 12 of up to 2048, 8 heads on 2.
+// value each dq and dk were half again as far off as that, for 1240 instead of
+// 1280 us a training step on 8192 sequences of 1..100 events, 4 heads of 64,
+// and 365 instead of 397 on 12 of up to 2048, 8 heads on 2.
 #include "rse_seqmma.h"
 
 using namespace rse;

@@ -668,8 +668,11 @@ __global__ __launch_bounds__(CB) void k_step_join(const float* part_o, const flo
     }
 }
 
-// Parts of a history: enough blocks to fill the GPU four times over, each
-// wave with two tiles at least; k_step_join reads at most 64.
+// Parts of a history: 1024 blocks in all where histories are long enough (4 a
+// CU, of which registers let 1 to 3 be there at once; 2048 and 4096 were no
+// faster), a part of 256 events at least (two tiles a wave of k_step; of
+// k_step_few one at 32 elements a head, else two or four), and at most the 64
+// parts that k_step_join reads: one user on one key head keeps 64 CUs busy.
 constexpr int64_t STEP_BLOCKS = 1024;
 
 // fp32 heads a key/value head that k_step_few takes.  128 users of up to 2048

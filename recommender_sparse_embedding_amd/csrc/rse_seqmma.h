@@ -507,7 +507,7 @@ struct SeqTiles {
 
 // Blocks of W waves that go through the short sequences, for `heads` of them
 // side by side: four times as many as fit the GPU at once (what is left over
-// evens out; with as many as fit, dq took 620 us where it takes 553), a
+// evens out; with as many as fit, dq took 620 us for 553), a
 // sequence's tiles shared by several where there are few sequences.
 struct ShortGrid {
     int64_t blocks;
@@ -541,13 +541,21 @@ struct Shape {
 };
 // Long sequences whose heads do not share keys by fours:
 //  - fp32 rows of 128 bytes: the matrix products are 8 times as long as in
-//    bf16 and the staging beside them free, so waves apart (even work) win:
-//    512 sequences of 1..203, both ways, dq 217 -> 160 us;
+//    bf16 and the staging beside them free, so waves apart (even work) win;
 //  - else teams, each wave with a column tile of one head: of 2 where that
-//    leaves room for several blocks (the same sequences 525 -> 493 us a
-//    training step; bf16 dim 64, 16 of up to 4096: forward 318 us, 396 with
-//    waves apart), of 4 for wide rows (bf16 dim 128, 1..333: forward 38 us, 46
-//    with 2).
+//    leaves room for several blocks, of 4 for wide rows.
+// us, causal, 4 heads on 4, forward / training step:
+//                   512 sequences of 1..203           24 of up to 1500
+//               teams of 2  teams of 4  apart     of 2        of 4        apart
+//   bf16   32     35 /  188   39 /  224   37 /  172   67 /  252   53 /  238   79 /  250
+//   bf16   64     60 /  267   54 /  324   57 /  233   84 /  307   59 /  288   90 /  311
+//   bf16  128     95 /  600   95 /  781  222 /  680  114 /  560   76 /  553  283 /  741
+//   fp32   32     78 /  356   83 /  417   73 /  293  134 /  566  123 /  547  126 /  484
+//   fp32   64    181 /  751  153 /  964  215 /  743  266 /  966  185 / 1000  302 /  948
+//   fp32  128    289 / 1999  418 / 1999    -         301 / 2311  355 / 1899    -
+// No one choice is the best for both batches of a row: teams of 4 suit the
+// forward of long sequences, teams of 2 or waves apart the backward of
+// shorter ones.
 template <typename T, int D>
 constexpr bool LONG_APART = sizeof(T) == 4 && D == 32;
 template <typename T, int D>
