@@ -210,10 +210,8 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                     }
                 }
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    x[r] = __builtin_amdgcn_exp2f(x[r]);
-                    l += x[r];
-                }
+                for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(x[r]);
+                l += sum_registers(x);
                 OverRows<T, D>::add(o, s_v[team][b], 32 * u, x);
                 if constexpr (REST) OverRows<T, D, 1>::add(rest, s_v[team][b], 32 * u, x);
             }

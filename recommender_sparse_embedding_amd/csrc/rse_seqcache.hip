@@ -354,10 +354,8 @@ __global__ __launch_bounds__(SW * 64) __attribute__((amdgpu_waves_per_eu(STEP_WA
         }
         const float shift = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            s[r] = __builtin_amdgcn_exp2f(s[r] - shift);
-            l += s[r];
-        }
+        for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(s[r] - shift);
+        l += sum_registers(s);
         OverRows<T, D>::add(o, tile, 0, s);
         wave_lds_sync();
     }

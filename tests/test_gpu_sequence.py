@@ -3,6 +3,8 @@ forward, every gradient, the single-event step over the paged history, page
 tables and slots.  An element may be off by the oracle's bound for it (sums in
 fp32, bf16 products where the type is bf16), no more."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -990,3 +992,33 @@ def test_bias_that_hides_from_both_key_heads(low, dtype):
     assert torch.all(got["out"][first, 0] == 0) and torch.all(got["dq"][first, 0] == 0)
     assert torch.equal(got["out"][first, 1], c.v[first, 1])      # of head 1: only itself
     assert torch.all(got["dbias"][:, 2] == 0) and got["dbias"][0, 0] == 0
+
+
+@pytest.mark.parametrize("H,Hk", [(1, 1), (4, 1), (4, 4)])
+def test_many_small_probabilities_count(H, Hk):
+    """One key of probability almost 1, then 4095 of 2^-25 of it: added one by
+    one to a running sum of 1 in fp32 each would be lost.  Summed by tiles of
+    32 the sum errs by at most 2^-24 for each of 128 tiles and of some 20 steps
+    within and after them; a row's out is what the small ones bring (exact in
+    fp32, the bias being -25 in base 2), over it."""
+    n, D = 4096, 32
+    c = Case([n], H, Hk, D, F32, causal=False, bounds=(10**5,))
+    c.pos = torch.arange(n, dtype=torch.int32).cuda()
+    c.pos[0] = -10**6                            # far from every other event: bucket 1
+    low, log2e = np.float32(-25 * math.log(2.0)), np.float32(1.4426950408889634)
+    while low * log2e < -25:
+        low = np.nextafter(low, np.float32(0))
+    while low * log2e > -25:
+        low = np.nextafter(low, np.float32(-30))
+    assert low * log2e == -25
+    c.bias[:, 0], c.bias[:, 1] = float(low), 0.0
+    c.q.zero_()
+    c.v.fill_(1.0)
+    c.v[0] = 0.0
+    small = (n - 1) * math.exp(float(low))
+    want = small / (1 + small)
+    got = _np(c.run()["out"])[1:]
+    u = 2.0**-24
+    # the bias in base 2 is off by 4 u of 25 or less, its power by as much
+    bound = want * (128 + 20 + 100) * u
+    assert np.all(np.abs(got - want) <= bound), np.abs(got / want - 1).max()
