@@ -532,8 +532,16 @@ __global__ __launch_bounds__(SH::WAVES * 64) __attribute__((amdgpu_waves_per_eu(
                         dp[4 * j + i] = x[4 * j + i] * (dp[4 * j + i] - de[i]);
                     }
                 }
-                OverRows<T, D>::add(av, s_d[team][b], 32 * u, x);
-                OverRows<T, D>::add(ak, s_q[team][b], 32 * u, dp);
+                if constexpr (sizeof(T) == 4) {     // (one after the other: more spills at 128 elements, 64 of up to 333 671 us for 630)
+#pragma unroll
+                    for (int dt = 0; dt < ND; ++dt) {
+                        OverRows<T, D>::add(av[dt], s_d[team][b], 32 * u, dt, x);
+                        OverRows<T, D>::add(ak[dt], s_q[team][b], 32 * u, dt, dp);
+                    }
+                } else {
+                    OverRows<T, D>::add(av, s_d[team][b], 32 * u, x);
+                    OverRows<T, D>::add(ak, s_q[team][b], 32 * u, dp);
+                }
             }
         }
         if (BRIEF) wave_lds_sync();             // read before the next tile is stored

@@ -133,18 +133,18 @@ template <typename T, int D, int TERMS = 2>
 struct OverRows;
 template <int D, int TERMS>
 struct OverRows<float, D, TERMS> {
-    static __device__ __forceinline__ void add(f32x16 (&acc)[D / 32], const u32x4* tile, int r0, f32x16& x) {
-        const int lane = lane_id(), h = lane >> 5;
+    static __device__ __forceinline__ void add(f32x16& acc, const u32x4* tile, int r0, int dt, const f32x16& x) {
+        const int lane = lane_id(), h = lane >> 5, d = 32 * dt + (lane & 31);
         const float* f = reinterpret_cast<const float*>(tile);
 #pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) {
-            const int d = 32 * dt + (lane & 31);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = r0 + tile_row(r, h);
-                acc[dt] = __builtin_amdgcn_mfma_f32_32x32x2f32(f[Tile<float, D>::chunk_at(row, d >> 2) * 4 + (d & 3)], x[r], acc[dt], 0, 0, 0);
-            }
+        for (int r = 0; r < 16; ++r) {
+            const int row = r0 + tile_row(r, h);
+            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(f[Tile<float, D>::chunk_at(row, d >> 2) * 4 + (d & 3)], x[r], acc, 0, 0, 0);
         }
+    }
+    static __device__ __forceinline__ void add(f32x16 (&acc)[D / 32], const u32x4* tile, int r0, const f32x16& x) {
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt) add(acc[dt], tile, r0, dt, x);
     }
 };
 // bf16: x enters as the sum of TERMS bf16 values, each the rounded remainder of
