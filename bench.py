@@ -142,7 +142,8 @@ def ceilings():
 
 
 # sections of rse.h that declare nothing of the step
-NOT_IN_STEP = (b"attention over behaviour sequences", b"history cache and single events")
+NOT_IN_STEP = (b"attention over behaviour sequences", b"history cache and single events",
+               b"the layer around the sequence attention")
 
 
 def step_header(text: bytes) -> bytes:

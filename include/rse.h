@@ -709,6 +709,90 @@ int seq_attention_step(const rse_seqattn* attn, rse_seqcache* cache, const rse_s
                        const int32_t* d_page_table, int32_t max_pages, const int64_t* d_lens, int64_t batch,
                        int64_t max_len, const rse_seq_rows* out, void* d_ws, size_t ws_bytes, void* stream);
 
+/* --------------------------- the layer around the sequence attention --- */
+/*
+ * What a layer over event rows needs beside the attention: the norm of the
+ * residual stream and the gated feed-forward.  Rows are [n, width] in the
+ * given type (RSE_F32 or RSE_BF16): the elements of a row are adjacent, the
+ * distance between rows is free (a slice of a wider tensor; 0 or negative for
+ * inputs too).  No two rows of an output overlap, else RSE_ERR_INVALID_ARG.
+ * These calls have no handle and no device-side errors; results are run-to-run
+ * identical (no floating-point atomics).
+ */
+#define RSE_SEQ_MAX_NORM_DIM 8192
+#define RSE_SEQ_MAX_GATED 65536
+
+typedef struct rse_seq_mat {
+    void* data;      /* element (0, 0); only written through for outputs */
+    int64_t stride;  /* elements from one row to the next */
+} rse_seq_mat;
+
+/*
+ * Layer norm of each row of dim elements (1 .. RSE_SEQ_MAX_NORM_DIM, else
+ * RSE_ERR_UNSUPPORTED; any dim, addresses and strides aligned to an element):
+ *   s = x + residual, rounded to the type (without a residual: x)
+ *   mean = sum s / dim,  r = 1 / sqrt(sum (s - mean)^2 / dim + eps)
+ *   y = (s - mean) r weight + bias
+ * residual and sum are given both or neither; sum gets s, which later layers
+ * and the backward read.  weight, bias: fp32 [dim], or NULL for 1 and 0.
+ * eps >= 0.  d_stats: fp32 [n, 2] (mean, r) for the backward, or NULL.  Sums in
+ * fp32, the squares about the mean.  sum and y may each be one of the inputs (the
+ * same address and stride), not overlap them otherwise.
+ */
+int seq_layer_norm_fwd(const rse_seq_mat* x, const rse_seq_mat* residual, const rse_seq_mat* sum, const float* d_weight,
+                       const float* d_bias, float eps, int64_t n, int32_t dim, int32_t dtype, const rse_seq_mat* y,
+                       float* d_stats, void* stream);
+
+/* Workspace bytes of one seq_layer_norm_bwd that sums over the rows. */
+int rse_seq_layer_norm_bwd_workspace_size(int64_t n, int32_t dim, int32_t dtype, size_t* bytes_out);
+
+/*
+ * Backward, for the rows s that were normalised (x, or the forward's sum):
+ *   xh = (s - mean) r,  dn = dy weight
+ *   dx = r (dn - sum dn / dim - xh sum(dn xh) / dim)  [+ dsum]
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ * dsum: the gradient that reaches s by the stream (with a residual dx is then
+ * the gradient of x and of the residual), or NULL.  dweight, dbias: fp32
+ * [dim], overwritten (with 0 for n = 0), either may be NULL; without both no
+ * workspace is needed.  dx may be dy or dsum.
+ */
+int seq_layer_norm_bwd(const rse_seq_mat* x, const rse_seq_mat* dy, const float* d_weight, const float* d_stats,
+                       const rse_seq_mat* dsum, int64_t n, int32_t dim, int32_t dtype, const rse_seq_mat* dx,
+                       float* d_dweight, float* d_dbias, void* d_ws, size_t ws_bytes, void* stream);
+
+/* act of the gated feed-forward: 1 / (1 + e^-g), g / (1 + e^-g), g Phi(g) with
+ * the normal distribution's Phi. */
+enum { RSE_SIGMOID = 0, RSE_SILU = 1, RSE_GELU = 2 };
+
+/*
+ * The gated feed-forward's projections, activation and product:
+ *   out = act(x w_gate^T) (x w_up^T)        elementwise product
+ * x [n, dim], w_gate, w_up [hidden, dim], out [n, hidden], all of one type.
+ * (The product with the third matrix is a plain one, like the projections
+ * around the attention.)  dim and hidden are multiples of 16 bytes, at most
+ * RSE_SEQ_MAX_GATED, else RSE_ERR_UNSUPPORTED; addresses and strides are
+ * multiples of 16 bytes, else RSE_ERR_INVALID_ARG.  Sums and activation in
+ * fp32, out rounded once.
+ */
+int seq_gated_linear_fwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const rse_seq_mat* w_up, int64_t n, int32_t dim,
+                         int32_t hidden, int32_t dtype, int32_t act, const rse_seq_mat* out, void* stream);
+
+/* Workspace bytes of one seq_gated_linear_bwd. */
+int rse_seq_gated_linear_bwd_workspace_size(int64_t n, int32_t dim, int32_t hidden, int32_t dtype, size_t* bytes_out);
+
+/*
+ * Backward; the forward leaves nothing for it, g = x w_gate^T and u = x w_up^T
+ * are formed again:
+ *   dg = dout u act'(g),  du = dout act(g)
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
+ * All gradients are of the rows' type and overwritten (the weights' with 0 for
+ * n = 0).  With RSE_BF16, dg and du are rounded to bf16 before their products,
+ * which are summed in fp32 and rounded once.
+ */
+int seq_gated_linear_bwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const rse_seq_mat* w_up, const rse_seq_mat* dout,
+                         int64_t n, int32_t dim, int32_t hidden, int32_t dtype, int32_t act, const rse_seq_mat* dx,
+                         const rse_seq_mat* dw_gate, const rse_seq_mat* dw_up, void* d_ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------- kernel trace -- */
 /*
  * Per-kernel timing with HIP events, for measurement: while a trace is

@@ -11,7 +11,8 @@ and embedding_bag_bwd_update's two halves, embedding_bag_bwd_prepare (sort;
 may overlap the forward on another stream) and embedding_bag_bwd_apply.
 
 Attention over behaviour sequences (``SeqAttention``, ``SeqCache`` and the
-``seq_*`` calls) is in ``sequence.py``.
+``seq_*`` calls) is in ``sequence.py``, the layer around it (layer norm, gated
+feed-forward) in ``seqlayer.py``.
 
 ``IdMap`` and ``EmbeddingBlocks`` own the caller-side device memory of the two
 library objects.  Importing this package loads librse.so and fails if it is
@@ -33,6 +34,7 @@ from ._lib import RseBwdPlan, RseError, RseOptim, check
 F32, BF16 = 0, 1
 SGD, ADAGRAD, ADAM = 0, 1, 2
 SUM, MEAN = 0, 1
+SIGMOID, SILU, GELU = 0, 1, 2
 MAX_TABLES = 1024
 MAX_MERGED_TABLES = 128
 
@@ -699,10 +701,14 @@ __all__ = [
     "bwd_workspace", "row_bytes", "status_str", "lib", "trace_start", "trace_stop", "K_PROBE", "K_FWD",
     "K_SORT_SCATTER", "K_SEG_UPDATE", "K_COMBINE", "K_INTERACT", "save", "load", "dlrm_interaction_fwd",
     "dlrm_interaction_bwd", "SeqAttention", "SeqCache", "seq_attention_fwd", "seq_attention_bwd",
-    "seq_attention_step", "seq_cache_assign", "seq_cache_write",
+    "seq_attention_step", "seq_cache_assign", "seq_cache_write", "SIGMOID", "SILU", "GELU", "LayerNormOut",
+    "seq_layer_norm_fwd", "seq_layer_norm_bwd", "seq_gated_linear_fwd", "seq_gated_linear_bwd",
 ]
 
 from .saver import load, save  # noqa: E402  (the Saver uses the classes above)
 from .sequence import (  # noqa: E402
     SeqAttention, SeqCache, seq_attention_bwd, seq_attention_fwd, seq_attention_step, seq_cache_assign, seq_cache_write,
+)
+from .seqlayer import (  # noqa: E402
+    LayerNormOut, seq_gated_linear_bwd, seq_gated_linear_fwd, seq_layer_norm_bwd, seq_layer_norm_fwd,
 )

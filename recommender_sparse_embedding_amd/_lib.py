@@ -52,6 +52,10 @@ class RseSeqBatch(ctypes.Structure):
                 ("d_bias", ctypes.c_void_p)]
 
 
+class RseSeqMat(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I32, _I64, _U64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
 _SZ = ctypes.c_size_t
@@ -127,6 +131,12 @@ SIGNATURES = {
     "seq_cache_write": ([_P, _P, _I64, _P, _P, _P, _P], ctypes.c_int),
     "rse_seqattn_step_workspace_size": ([_P, _I64, _I64, _PSZ], ctypes.c_int),
     "seq_attention_step": ([_P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _I64, _P, _P, _SZ, _P], ctypes.c_int),
+    "seq_layer_norm_fwd": ([_P, _P, _P, _P, _P, ctypes.c_float, _I64, _I32, _I32, _P, _P, _P], ctypes.c_int),
+    "rse_seq_layer_norm_bwd_workspace_size": ([_I64, _I32, _I32, _PSZ], ctypes.c_int),
+    "seq_layer_norm_bwd": ([_P, _P, _P, _P, _P, _I64, _I32, _I32, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
+    "seq_gated_linear_fwd": ([_P, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P], ctypes.c_int),
+    "rse_seq_gated_linear_bwd_workspace_size": ([_I64, _I32, _I32, _I32, _PSZ], ctypes.c_int),
+    "seq_gated_linear_bwd": ([_P, _P, _P, _P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
     "rse_trace_start": ([_I32], ctypes.c_int),
     "rse_trace_stop": ([_PI64, ctypes.POINTER(ctypes.c_double)], ctypes.c_int),
 }

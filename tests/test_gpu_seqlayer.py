@@ -1,0 +1,365 @@
+"""The layer around the sequence attention on the GPU against the float64
+oracle: layer norm with the residual stream and the gated feed-forward's
+projections, each with every gradient.  An element may be off by the oracle's
+bound for it, no more."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import seqlayer as olayer
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+ACTS = ["sigmoid", "silu", "gelu"]
+
+
+@pytest.fixture(scope="module")
+def rse():
+    import recommender_sparse_embedding_amd as m
+
+    return m
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _check(got, ref, what):
+    value, bound = ref
+    got = _np(got)
+    assert got.shape == value.shape, what
+    assert np.all(np.isfinite(got)), f"{what}: not finite"
+    off = np.abs(got - value)
+    bad = off > bound
+    if np.any(bad):
+        at = np.unravel_index(np.argmax(np.where(bad, off, 0)), off.shape)
+        raise AssertionError(f"{what} at {at}: {got[at]} for {value[at]}, bound {bound[at]:.3g}")
+
+
+def _randn(g, *s, dt=torch.float32):
+    return torch.randn(s, generator=g).to(dt).cuda()
+
+
+def _gen(*key):
+    return torch.Generator().manual_seed(sum(int(k) * m for k, m in zip(key, (1, 1009, 100003, 7))))
+
+
+# -------------------------------------------------------------------- norm --
+def _norm_case(rse, kind, n, dim, residual, seed=0, size=1.0, shift=1.0):
+    dt, g = DT[kind], _gen(n, dim, seed)
+    x = (torch.randn((n, dim), generator=g) * size + torch.randn((n, 1), generator=g) * shift).to(dt).cuda()
+    res = _randn(g, n, dim, dt=dt) if residual else None
+    w, b = 1 + 0.3 * _randn(g, dim), _randn(g, dim)
+    return x, res, w, b, _randn(g, n, dim, dt=dt), _randn(g, n, dim, dt=dt) if residual else None
+
+
+def _check_norm(rse, kind, x, res, w, b, dy, dsum, eps=1e-5):
+    got = rse.seq_layer_norm_fwd(x, w, b, eps, residual=res, for_backward=True)
+    s = x
+    if res is not None:
+        _check(got.sum, olayer.norm_sum(_np(x), _np(res), kind), "sum")
+        s = got.sum
+    one = np.ones(x.shape[1])
+    ref = olayer.norm(_np(s), one if w is None else _np(w), 0 * one if b is None else _np(b), eps, kind)
+    _check(got.y, ref["y"], "y")
+    _check(got.stats[:, :1], ref["mean"], "mean")
+    _check(got.stats[:, 1:], ref["r"], "r")
+    exact = torch.from_numpy(np.concatenate(olayer.norm_stats(_np(s), eps), 1)).float().cuda()
+    dx, dw, db = rse.seq_layer_norm_bwd(s, dy, w, exact, dsum=dsum)
+    ref = olayer.norm_backward(_np(s), _np(dy), one if w is None else _np(w), eps, None if dsum is None else _np(dsum), kind)
+    _check(dx, ref["dx"], "dx")
+    _check(dw, ref["dweight"], "dweight")
+    _check(db, ref["dbias"], "dbias")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [1, 2, 3, 7, 8, 9, 32, 63, 65, 128, 200, 256, 321, 512, 516, 1000, 1024, 1031, 2048, 3000,
+                                 4096, 4099, 8191, 8192])
+def test_norm_dims(rse, kind, dim):
+    for n, residual in ((1, False), (19, True)):
+        _check_norm(rse, kind, *_norm_case(rse, kind, n, dim, residual))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [2, 31, 64, 257, 5000, 20011])
+def test_norm_rows(rse, kind, n):
+    for dim in (24, 72):
+        _check_norm(rse, kind, *_norm_case(rse, kind, n, dim, n % 2 == 0))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_norm_without_weights_and_eps(rse, kind):
+    x, res, w, b, dy, dsum = _norm_case(rse, kind, 37, 96, True)
+    _check_norm(rse, kind, x, res, None, None, dy, dsum)
+    _check_norm(rse, kind, x, None, w, None, dy, None, eps=0.5)
+    _check_norm(rse, kind, x, res, None, b, dy, None)
+
+
+def test_norm_rows_far_from_zero(rse):
+    """The squares are taken about the mean: a mean 1000 times the spread."""
+    _check_norm(rse, "f32", *_norm_case(rse, "f32", 50, 300, False, shift=1000.0))
+
+
+def test_norm_constant_and_zero_rows(rse):
+    x, _, w, b, dy, _ = _norm_case(rse, "f32", 4, 64, False)
+    x[0], x[1], x[2] = 0.0, 3.0, 1e-20
+    _check_norm(rse, "f32", x, None, w, b, dy, None)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_norm_strides_and_odd_addresses(rse, kind):
+    """Slices of wider tensors at any element, a row given for all, rows that
+    run backwards in memory; what lies between the rows stays."""
+    dt, g = DT[kind], _gen(3, 4, 5)
+    n, dim = 21, 45
+    wide = _randn(g, n, 3 * dim + 1, dt=dt)
+    x, res = wide[:, 1:1 + dim], wide[:, 1 + dim:1 + 2 * dim]
+    dy, dsum = _randn(g, 1, dim, dt=dt).expand(n, dim), wide[:, 1 + 2 * dim:]
+    _check_norm(rse, kind, x, res, _randn(g, dim), _randn(g, dim), dy, dsum)
+    out = torch.full((n, dim + 5), 7.0, dtype=dt, device="cuda")
+    both = torch.full((n, dim + 5), 7.0, dtype=dt, device="cuda")
+    a = rse.seq_layer_norm_fwd(x, None, None, residual=res, out=out[:, 3:3 + dim], sum_out=both[:, 2:2 + dim], for_backward=True)
+    b = rse.seq_layer_norm_fwd(x.contiguous(), None, None, residual=res.contiguous(), for_backward=True)
+    assert torch.equal(a.y, b.y) and torch.equal(a.sum, b.sum) and torch.equal(a.stats, b.stats)
+    for t, lo in ((out, 3), (both, 2)):
+        assert torch.all(t[:, :lo] == 7) and torch.all(t[:, lo + dim:] == 7)
+    dx = torch.full((n, dim + 5), 7.0, dtype=dt, device="cuda")
+    rse.seq_layer_norm_bwd(b.sum, dy, None, b.stats, dsum, out=dx[:, 1:1 + dim])
+    ref, _, _ = rse.seq_layer_norm_bwd(b.sum, dy.contiguous(), None, b.stats, dsum.contiguous())
+    assert torch.equal(dx[:, 1:1 + dim], ref) and torch.all(dx[:, 0] == 7) and torch.all(dx[:, 1 + dim:] == 7)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 321, 4096])
+def test_norm_in_place(rse, kind, dim):
+    x, res, w, b, dy, dsum = _norm_case(rse, kind, 33, dim, True)
+    ref = rse.seq_layer_norm_fwd(x, w, b, residual=res, for_backward=True)
+    x2, r2 = x.clone(), res.clone()
+    got = rse.seq_layer_norm_fwd(x2, w, b, residual=r2, out=x2, sum_out=r2)
+    assert torch.equal(got.y, ref.y) and torch.equal(r2, ref.sum) and got.y is x2
+    g1 = rse.seq_layer_norm_bwd(ref.sum, dy, w, ref.stats, dsum)
+    dy2 = dy.clone()
+    g2 = rse.seq_layer_norm_bwd(ref.sum, dy2, w, ref.stats, dsum, out=dy2)
+    s2 = dsum.clone()
+    g3 = rse.seq_layer_norm_bwd(ref.sum, dy, w, ref.stats, s2, out=s2)
+    for a, b_, c in zip(g1, g2, g3):
+        assert torch.equal(a, b_) and torch.equal(a, c)
+
+
+def test_norm_not_finite_stays_in_its_row(rse):
+    x, _, w, b, dy, _ = _norm_case(rse, "f32", 9, 100, False)
+    clean = rse.seq_layer_norm_fwd(x, w, b, for_backward=True)
+    bad = x.clone()
+    bad[3, 7], bad[5, 99] = float("nan"), float("inf")
+    got = rse.seq_layer_norm_fwd(bad, w, b, for_backward=True)
+    keep = [i for i in range(9) if i not in (3, 5)]
+    assert torch.equal(got.y[keep], clean.y[keep]) and torch.all(torch.isnan(got.y[[3, 5]]))
+    dx, dw, _ = rse.seq_layer_norm_bwd(bad, dy, w, got.stats)
+    ref, _, _ = rse.seq_layer_norm_bwd(x, dy, w, clean.stats)
+    assert torch.equal(dx[keep], ref[keep]) and torch.all(torch.isnan(dx[[3, 5]])) and torch.all(torch.isnan(dw))
+
+
+def test_norm_no_rows(rse):
+    x = torch.empty((0, 40), device="cuda")
+    got = rse.seq_layer_norm_fwd(x, None, None, residual=x, for_backward=True)
+    assert got.y.shape == (0, 40) and got.sum.shape == (0, 40) and got.stats.shape == (0, 2)
+    dx, dw, db = rse.seq_layer_norm_bwd(x, x, None, got.stats)
+    assert dx.shape == (0, 40) and torch.all(dw == 0) and torch.all(db == 0)
+
+
+def test_norm_refusals(rse):
+    x = torch.zeros((4, 64), device="cuda")
+    w = torch.zeros(64, device="cuda")
+    for bad in (lambda: rse.seq_layer_norm_fwd(x, w[:63], None), lambda: rse.seq_layer_norm_fwd(x, w, w, residual=x[:3]),
+                lambda: rse.seq_layer_norm_fwd(x.t(), None, None), lambda: rse.seq_layer_norm_fwd(x, w, w, sum_out=x),
+                lambda: rse.seq_layer_norm_bwd(x, x, w, w)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: rse.seq_layer_norm_fwd(x.half(), None, None), lambda: rse.seq_layer_norm_fwd(x, w.double(), None),
+                lambda: rse.seq_layer_norm_fwd(x, w, w, residual=x.bfloat16()), lambda: rse.seq_layer_norm_fwd(x[0], w, w),
+                lambda: rse.seq_layer_norm_fwd(x, w, w, residual=x.cpu())):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(rse.RseError):
+        rse.seq_layer_norm_fwd(torch.zeros((1, 8193), device="cuda"), None, None)
+    with pytest.raises(rse.RseError):
+        rse.seq_layer_norm_fwd(x, w, w, out=x[:1].expand(4, 64))
+
+
+# ------------------------------------------------------------------- gated --
+def _gated_case(kind, n, dim, hidden, seed=0, size=1.0):
+    dt, g = DT[kind], _gen(n, dim, hidden, seed)
+    x = (torch.randn((n, dim), generator=g) * size).to(dt).cuda()
+    wg, wu = ((torch.randn((hidden, dim), generator=g) * dim**-0.5).to(dt).cuda() for _ in range(2))
+    return x, wg, wu, _randn(g, n, hidden, dt=dt)
+
+
+def _check_gated(rse, kind, x, wg, wu, dout, act):
+    code = {"sigmoid": rse.SIGMOID, "silu": rse.SILU, "gelu": rse.GELU}[act]
+    wide = [_np(t) for t in (x, wg, wu, dout)]
+    _check(rse.seq_gated_linear_fwd(x, wg, wu, code), olayer.gated(*wide[:3], act, kind), "out")
+    got = rse.seq_gated_linear_bwd(x, wg, wu, dout, code)
+    ref = olayer.gated_backward(*wide, act, kind)
+    for t, name in zip(got, ("dx", "dw_gate", "dw_up")):
+        _check(t, ref[name], name)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("n,dim,hidden", [(1, 8, 8), (1, 256, 1024), (2, 64, 64), (5, 24, 40), (16, 512, 136), (31, 136, 72),
+                                          (32, 32, 256), (33, 64, 128), (63, 200, 264), (64, 96, 96), (65, 128, 64),
+                                          (127, 72, 136), (128, 128, 128), (129, 256, 200), (255, 16, 520), (256, 320, 64),
+                                          (300, 40, 328), (513, 64, 72), (1025, 48, 56), (2500, 136, 88)])
+def test_gated_sizes(rse, kind, n, dim, hidden):
+    _check_gated(rse, kind, *_gated_case(kind, n, dim, hidden), ACTS[(n + dim) % 3])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("act", ACTS)
+def test_gated_activations(rse, kind, act):
+    _check_gated(rse, kind, *_gated_case(kind, 70, 64, 80), act)
+    _check_gated(rse, kind, *_gated_case(kind, 70, 64, 80, size=20.0), act)      # far into both ends
+
+
+def test_gated_fp32_elements_of_four(rse):
+    _check_gated(rse, "f32", *_gated_case("f32", 50, 36, 52), "silu")
+    _check_gated(rse, "f32", *_gated_case("f32", 1, 4, 4), "gelu")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [3, 150])
+def test_gated_strides(rse, kind, n):
+    """Views of joint tensors, an expanded gradient, outputs beside each other;
+    what lies between the rows stays."""
+    dt, g = DT[kind], _gen(8, n, 1)
+    dim, hidden = 72, 104
+    x = _randn(g, n, 3 * dim, dt=dt)[:, dim:2 * dim]
+    w = _randn(g, hidden, 2 * dim, dt=dt) * 0.1
+    wg, wu = w[:, :dim], w[:, dim:]
+    dout = _randn(g, 1, hidden, dt=dt).expand(n, hidden)
+    out = torch.full((n, hidden + 16), 7.0, dtype=dt, device="cuda")
+    rse.seq_gated_linear_fwd(x, wg, wu, out=out[:, 8:8 + hidden])
+    assert torch.equal(out[:, 8:8 + hidden], rse.seq_gated_linear_fwd(x.contiguous(), wg.contiguous(), wu.contiguous()))
+    assert torch.all(out[:, :8] == 7) and torch.all(out[:, 8 + hidden:] == 7)
+    ref = rse.seq_gated_linear_bwd(x.contiguous(), wg.contiguous(), wu.contiguous(), dout.contiguous())
+    dx = torch.full((n, dim + 16), 7.0, dtype=dt, device="cuda")
+    dw = torch.full((hidden, 2 * dim + 8), 7.0, dtype=dt, device="cuda")
+    rse.seq_gated_linear_bwd(x, wg, wu, dout, grads=(dx[:, 8:8 + dim], dw[:, :dim], dw[:, dim:2 * dim]))
+    assert torch.equal(dx[:, 8:8 + dim], ref[0]) and torch.all(dx[:, :8] == 7) and torch.all(dx[:, 8 + dim:] == 7)
+    assert torch.equal(dw[:, :dim], ref[1]) and torch.equal(dw[:, dim:2 * dim], ref[2]) and torch.all(dw[:, 2 * dim:] == 7)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_gated_not_finite_stays_in_its_row(rse, kind):
+    x, wg, wu, dout = _gated_case(kind, 140, 72, 104)
+    bad = x.clone()
+    bad[3, 70], bad[135, 0] = float("nan"), float("inf")
+    keep = torch.tensor([i for i in range(140) if i not in (3, 135)])
+    out, ref = rse.seq_gated_linear_fwd(bad, wg, wu), rse.seq_gated_linear_fwd(x, wg, wu)
+    assert torch.equal(out[keep], ref[keep]) and torch.all(torch.isnan(out[3]))
+    dx, ref = rse.seq_gated_linear_bwd(bad, wg, wu, dout)[0], rse.seq_gated_linear_bwd(x, wg, wu, dout)[0]
+    assert torch.equal(dx[keep], ref[keep]) and torch.all(torch.isnan(dx[3]))
+
+
+def test_gated_no_rows(rse):
+    x, w = torch.empty((0, 64), device="cuda"), torch.ones((40, 64), device="cuda")
+    assert rse.seq_gated_linear_fwd(x, w, w).shape == (0, 40)
+    dx, dg, du = rse.seq_gated_linear_bwd(x, w, w, torch.empty((0, 40), device="cuda"))
+    assert dx.shape == (0, 64) and torch.all(dg == 0) and torch.all(du == 0)
+
+
+def test_gated_refusals(rse):
+    x, w = torch.zeros((4, 64), device="cuda"), torch.zeros((40, 64), device="cuda")
+    for bad in (lambda: rse.seq_gated_linear_fwd(x, w, w[:39]), lambda: rse.seq_gated_linear_fwd(x, w[:, :60], w),
+                lambda: rse.seq_gated_linear_fwd(x, w, w, out=torch.zeros((4, 41), device="cuda")),
+                lambda: rse.seq_gated_linear_fwd(torch.zeros((4, 65), device="cuda")[:, 1:], w, w),
+                lambda: rse.seq_gated_linear_bwd(x, w, w, torch.zeros((4, 64), device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: rse.seq_gated_linear_fwd(x, w.bfloat16(), w), lambda: rse.seq_gated_linear_fwd(x.half(), w, w)):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: rse.seq_gated_linear_fwd(x, w, w, act=3),
+                lambda: rse.seq_gated_linear_fwd(*(torch.zeros((4, 6), device="cuda")[:, :6],) * 3),
+                lambda: rse.seq_gated_linear_fwd(x, w, w, out=torch.zeros((1, 40), device="cuda").expand(4, 40))):
+        with pytest.raises((rse.RseError, ValueError)):
+            bad()
+
+
+# ------------------------------------------------------ both, as they are used --
+def test_gradients_are_slopes(rse):
+    """fp32 gradients against central differences of the oracle's forward."""
+    x, wg, wu, dout = _gated_case("f32", 40, 32, 24)
+    wide = [_np(t) for t in (x, wg, wu, dout)]
+    got, ref = rse.seq_gated_linear_bwd(x, wg, wu, dout), olayer.gated_backward(*wide, "silu", "f32")
+    r = np.random.default_rng(0)
+    for i, name in enumerate(("dx", "dw_gate", "dw_up")):
+        v = r.standard_normal(wide[i].shape)
+        f = lambda t: (olayer.gated(*wide[:i], t, *wide[i + 1:3], "silu", "f32")[0] * wide[3]).sum()  # noqa: E731
+        slope = (f(wide[i] + 1e-5 * v) - f(wide[i] - 1e-5 * v)) / 2e-5
+        assert abs((_np(got[i]) * v).sum() - slope) <= (ref[name][1] * np.abs(v)).sum() + 1e-6, name
+
+
+def test_repeated_calls_are_identical(rse):
+    x, wg, wu, dout = _gated_case("bf16", 3000, 136, 264)
+    a, b = (rse.seq_gated_linear_bwd(x, wg, wu, dout) for _ in range(2))
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    y = rse.seq_layer_norm_fwd(x, None, None, for_backward=True)
+    a, b = (rse.seq_layer_norm_bwd(x, x, None, y.stats) for _ in range(2))
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def _layer(rse, x, res, w, b, wg, wu, dout, dsum, stream=None):
+    """Norm with the stream and gated projections, forward and backward."""
+    got = rse.seq_layer_norm_fwd(x, w, b, residual=res, for_backward=True, stream=stream)
+    out = rse.seq_gated_linear_fwd(got.y, wg, wu, stream=stream)
+    dy, dg, du = rse.seq_gated_linear_bwd(got.y, wg, wu, dout, stream=stream)
+    return (got.y, got.sum, out, dy, dg, du, *rse.seq_layer_norm_bwd(got.sum, dy, w, got.stats, dsum, stream=stream))
+
+
+def _layer_inputs(rse, kind, n, dim, hidden, seed):
+    x, res, w, b, _, dsum = _norm_case(rse, kind, n, dim, True, seed=seed)
+    _, wg, wu, dout = _gated_case(kind, n, dim, hidden, seed=seed)
+    return x, res, w, b, wg, wu, dout, dsum
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_layer_on_another_stream_and_captured(rse, kind):
+    """The same results on a stream of its own and from a captured graph, whose
+    replays follow new inputs, with eager work between them."""
+    ins = [_layer_inputs(rse, kind, 150, 72, 104, s) for s in range(3)]
+    refs = [_layer(rse, *i) for i in ins]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = _layer(rse, *ins[1], stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, refs[1]))
+    static = [t.clone() for t in ins[0]]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = _layer(rse, *static)
+    for i in (0, 1, 2, 1, 0):
+        for a, b in zip(static, ins[i]):
+            a.copy_(b)
+        graph.replay()
+        eager = _layer(rse, *ins[(i + 1) % 3])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, refs[i])), i
+        assert all(torch.equal(a, b) for a, b in zip(eager, refs[(i + 1) % 3])), i
+
+
+def test_two_streams_at_once(rse):
+    ins = [_layer_inputs(rse, "bf16", 700, 136, 264, s) for s in range(2)]
+    refs = [_layer(rse, *i) for i in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for k in range(2):
+            got[k].append(_layer(rse, *ins[k], stream=streams[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for g in got[k]:
+            assert all(torch.equal(a, b) for a, b in zip(g, refs[k]))
