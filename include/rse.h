@@ -709,6 +709,33 @@ int seq_attention_step(const rse_seqattn* attn, rse_seqcache* cache, const rse_s
                        const int32_t* d_page_table, int32_t max_pages, const int64_t* d_lens, int64_t batch,
                        int64_t max_len, const rse_seq_rows* out, void* d_ws, size_t ws_bytes, void* stream);
 
+/* Workspace bytes of one seq_attention_chunk; may be 0 (d_ws may be NULL then). */
+int rse_seqattn_chunk_workspace_size(const rse_seqattn* attn, int64_t n_events, int64_t batch, int64_t max_new, int64_t max_len,
+                                     size_t* bytes_out);
+
+/*
+ * Several new events for each user: `batch` holds them as a jagged batch
+ * (d_offsets, max_len the most that a user has, d_pos, d_bias; d_key_off must
+ * be NULL: events without a row are kept out of the cache).  The k, v, pos of
+ * new event i of user b are stored at event number d_lens[b] + i (pages as
+ * seq_cache_assign enters them), and its out is the attention of its q over the
+ * d_lens[b] cached events and the new ones up to itself (all of the new ones if
+ * the handle is not causal), by the formulas above.  One event for every user is
+ * seq_attention_step's work; a whole history in several calls gives what
+ * seq_attention_fwd gives for it at once.
+ * d_lens[b] < 0: the user is idle, the out of its events is 0 and nothing is
+ * stored.  d_lens[b] plus the new events past `max_len` or past the table, or a
+ * page out of the pool: as in seq_attention_step, for the user's new events.
+ * Malformed offsets, or more new events than batch->max_len: RSE_ERR_BAD_INPUT
+ * in the attention handle's status, the sequences concerned are skipped and
+ * their out is left as it was.  The lengths are not changed: the caller adds
+ * the counts.
+ */
+int seq_attention_chunk(const rse_seqattn* attn, rse_seqcache* cache, const rse_seq_batch* batch, const rse_seq_rows* q,
+                        const rse_seq_rows* k, const rse_seq_rows* v, const int32_t* d_page_table, int32_t max_pages,
+                        const int64_t* d_lens, int64_t max_len, const rse_seq_rows* out, void* d_ws, size_t ws_bytes,
+                        void* stream);
+
 /* --------------------------- the layer around the sequence attention --- */
 /*
  * What a layer over event rows needs beside the attention: the norm of the

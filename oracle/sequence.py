@@ -135,6 +135,30 @@ def step(histories, q, bias, boundaries, scale, kind="f32"):
     return out, err
 
 
+def chunk(histories, q, bias, boundaries, causal, scale, kind="f32"):
+    """histories: per user (k [n, Hk, D], v, pos [n], new) with its `new` new
+    events last, or (None, None, None, new) for an idle one; q [sum of new, H, D].
+    Returns (out, bound)."""
+    N, H, D = q.shape
+    out, err = np.zeros((N, H, D)), np.zeros((N, H, D))
+    a = 0
+    for k, v, pos, new in histories:
+        a += new
+        if k is None or new == 0:
+            continue
+        k, v, n = np.asarray(k, np.float64), np.asarray(v, np.float64), len(k)
+        group, at = H // k.shape[1], slice(a - new, a)
+        for h in range(H):
+            rows = np.zeros((n, D))
+            rows[n - new:] = q[at, h]
+            m = _one(rows, k[:, h // group], v[:, h // group], np.asarray(pos), np.asarray(bias[h], np.float64), None,
+                     boundaries, causal, scale)
+            p, ep = m["p"][n - new:], m["ep"][n - new:, None]
+            out[at, h] = p @ m["v"]
+            err[at, h] = (ep + TERMS[kind] * n * U + R[kind]) * (p @ np.abs(m["v"])) + OUT[kind] * np.abs(out[at, h]) + 1e-30
+    return out, err
+
+
 def assign(counts, lens, table, free, page_size):
     """(slots, offsets, pages taken, table) in Python integers."""
     table = [list(map(int, row)) for row in table]

@@ -701,13 +701,14 @@ __all__ = [
     "bwd_workspace", "row_bytes", "status_str", "lib", "trace_start", "trace_stop", "K_PROBE", "K_FWD",
     "K_SORT_SCATTER", "K_SEG_UPDATE", "K_COMBINE", "K_INTERACT", "save", "load", "dlrm_interaction_fwd",
     "dlrm_interaction_bwd", "SeqAttention", "SeqCache", "seq_attention_fwd", "seq_attention_bwd",
-    "seq_attention_step", "seq_cache_assign", "seq_cache_write", "SIGMOID", "SILU", "GELU", "LayerNormOut",
+    "seq_attention_step", "seq_attention_chunk", "seq_cache_assign", "seq_cache_write", "SIGMOID", "SILU", "GELU", "LayerNormOut",
     "seq_layer_norm_fwd", "seq_layer_norm_bwd", "seq_gated_linear_fwd", "seq_gated_linear_bwd",
 ]
 
 from .saver import load, save  # noqa: E402  (the Saver uses the classes above)
 from .sequence import (  # noqa: E402
-    SeqAttention, SeqCache, seq_attention_bwd, seq_attention_fwd, seq_attention_step, seq_cache_assign, seq_cache_write,
+    SeqAttention, SeqCache, seq_attention_bwd, seq_attention_chunk, seq_attention_fwd, seq_attention_step, seq_cache_assign,
+    seq_cache_write,
 )
 from .seqlayer import (  # noqa: E402
     LayerNormOut, seq_gated_linear_bwd, seq_gated_linear_fwd, seq_layer_norm_bwd, seq_layer_norm_fwd,

@@ -131,6 +131,8 @@ SIGNATURES = {
     "seq_cache_write": ([_P, _P, _I64, _P, _P, _P, _P], ctypes.c_int),
     "rse_seqattn_step_workspace_size": ([_P, _I64, _I64, _PSZ], ctypes.c_int),
     "seq_attention_step": ([_P, _P, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _I64, _P, _P, _SZ, _P], ctypes.c_int),
+    "rse_seqattn_chunk_workspace_size": ([_P, _I64, _I64, _I64, _I64, _PSZ], ctypes.c_int),
+    "seq_attention_chunk": ([_P, _P, _P, _P, _P, _P, _P, _I32, _P, _I64, _P, _P, _SZ, _P], ctypes.c_int),
     "seq_layer_norm_fwd": ([_P, _P, _P, _P, _P, ctypes.c_float, _I64, _I32, _I32, _P, _P, _P], ctypes.c_int),
     "rse_seq_layer_norm_bwd_workspace_size": ([_I64, _I32, _I32, _PSZ], ctypes.c_int),
     "seq_layer_norm_bwd": ([_P, _P, _P, _P, _P, _I64, _I32, _I32, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),

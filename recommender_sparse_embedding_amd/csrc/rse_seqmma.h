@@ -252,6 +252,28 @@ struct WaveBuckets {
     }
 };
 
+// The same where the lanes' heads differ: `bias` is the lane's row of a table
+// in LDS, in base 2.
+struct LaneBuckets {
+    int32_t bnd[2];
+    const float* bias;
+    int n;
+    __device__ __forceinline__ void load(const SeqHeader* hdr, const float* lane_bias, int n_bounds) {
+        n = n_bounds;
+        bias = lane_bias;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) bnd[u] = hdr->bounds[64 * u + lane_id()];
+    }
+    __device__ __forceinline__ int bucket(int32_t d) const {
+        const int b = __popcll(__ballot(bnd[0] <= d)) + __popcll(__ballot(bnd[1] <= d));
+        return b < n ? b : n;
+    }
+    __device__ __forceinline__ int32_t boundary(int m) const {
+        return __builtin_amdgcn_readlane(m < 64 ? bnd[0] : bnd[1], m & 63);
+    }
+    __device__ __forceinline__ float value(int b) const { return bias[b]; }
+};
+
 // Lowest and highest of each half of the wave, by rotations within rows of 16
 // lanes and one exchange of rows (no trip through LDS: five dependent
 // shuffles took some 600 cycles of a tile).
@@ -302,13 +324,15 @@ template <bool column_first>
 struct TileBuckets {
     int lo, hi;
     bool many;
-    __device__ __forceinline__ void set(const WaveBuckets& wb, int32_t col_lo, int32_t col_hi, const int32_t* range) {
+    template <typename WB>
+    __device__ __forceinline__ void set(const WB& wb, int32_t col_lo, int32_t col_hi, const int32_t* range) {
         const int32_t r_lo = __builtin_amdgcn_readfirstlane(range[0]), r_hi = __builtin_amdgcn_readfirstlane(range[1]);
         lo = wb.bucket(column_first ? seq_dist(col_lo, r_hi) : seq_dist(r_lo, col_hi));
         hi = wb.bucket(column_first ? seq_dist(col_hi, r_lo) : seq_dist(r_hi, col_lo));
         many = lo != hi && (hi - lo > CHAIN || (column_first ? r_lo == INT32_MIN : r_hi == INT32_MAX));
     }
-    __device__ __forceinline__ int32_t threshold(const WaveBuckets& wb, int m, int32_t col_pos) const {
+    template <typename WB>
+    __device__ __forceinline__ int32_t threshold(const WB& wb, int m, int32_t col_pos) const {
         const int32_t edge = wb.boundary(m);
         return column_first ? seq_dist(col_pos, edge) : sat_add(col_pos, edge);
     }
@@ -347,8 +371,10 @@ struct TileBuckets {
             for (int i = 0; i < 4; ++i) p[4 * j + i] = v[i];
         }
     }
-    // s c + bias + shift of every pair
-    __device__ __forceinline__ f32x16 logits(f32x16 s, float c, float shift, const WaveBuckets& wb, const u32x4* bytes,
+    // s c + bias + shift of every pair (WB: WaveBuckets, or LaneBuckets where the
+    // lanes' heads differ)
+    template <typename WB>
+    __device__ __forceinline__ f32x16 logits(f32x16 s, float c, float shift, const WB& wb, const u32x4* bytes,
                                              const float* s_bias, const int32_t* row_pos, int32_t col_pos) const {
         if (lo == hi) {
             const float b = wb.value(lo) + shift;
@@ -431,10 +457,10 @@ inline TileGrid tile_grid(int64_t n_events, int64_t batch, int64_t max_len, int 
     return {slots, 0};
 }
 
-// The item's sequence (first event, length) and tile; false if it is idle.
-// backwards: items of a grid by tile index start from the last tile.
+// The item's sequence (number, first event, length) and tile; false if it is
+// idle.  backwards: items of a grid by tile index start from the last tile.
 __device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, int64_t item, int tq, bool backwards,
-                                          int64_t& s, int& len, int& tile, bool check) {
+                                          int64_t& b, int64_t& s, int& len, int& tile, bool check) {
     if (check) {
         for (int64_t i = item * blockDim.x + threadIdx.x; i < a.batch; i += g.items * blockDim.x) {
             const int64_t x = a.offsets[i], y = a.offsets[i + 1];
@@ -442,7 +468,7 @@ __device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, i
                 set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
         }
     }
-    int64_t b, t;
+    int64_t t;
     if (g.per_seq) {
         t = item / a.batch;
         b = item - t * a.batch + t % a.batch;           // a sequence's tiles on different XCDs
@@ -463,6 +489,11 @@ __device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, i
     len = (int)(e - s);
     tile = (int)t;
     return true;
+}
+__device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, int64_t item, int tq, bool backwards,
+                                          int64_t& s, int& len, int& tile, bool check) {
+    int64_t b;
+    return find_tile(a, g, item, tq, backwards, b, s, len, tile, check);
 }
 
 // The tiles a block works through, one after the other.  By sequence: block x

@@ -319,3 +319,35 @@ def seq_attention_step(attn: SeqAttention, cache: SeqCache, q: torch.Tensor, k: 
                                  bias_p, page_table.data_ptr(), max_pages, lens_p, batch, most, byref(o), _ptr(ws),
                                  size, _stream(stream)), "seq_attention_step")
     return out
+
+
+def seq_attention_chunk(attn: SeqAttention, cache: SeqCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        pos: torch.Tensor, bias: torch.Tensor, seq_offsets: torch.Tensor, page_table: torch.Tensor,
+                        lens: torch.Tensor, max_new: int | None = None, max_len: int | None = None,
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Several new events per user: events seq_offsets[b] .. seq_offsets[b+1]
+    (int64, batch + 1) of q [n, n_heads, dim], k, v [n, n_kv_heads, dim] and pos
+    int32 [n] are user b's, stored as events lens[b] and on (int64 [batch];
+    negative: idle).  Returns their attention [n, n_heads, dim] over the history
+    and each other (a causal handle: up to themselves).  max_new: no user has
+    more new events (default: n); max_len: no history with them is longer
+    (default: the table's width).  lens is not changed, and there is no key_off,
+    as in seq_attention_step."""
+    n = q.shape[0]
+    dt, H, Hk, D = attn.torch_dtype, attn.n_heads, attn.n_kv_heads, attn.dim
+    args = [_rows(q, dt, n, H, D, "q"), _rows(k, dt, n, Hk, D, "k"), _rows(v, dt, n, Hk, D, "v")]
+    b = _batch(attn, n, pos, bias, seq_offsets, None, max_new)
+    max_pages = _table(page_table, b.batch)
+    lens_p = _vector(lens, torch.int64, b.batch, "lens")
+    most = max_pages * cache.page_size if max_len is None else int(max_len)
+    size = _size(lib.rse_seqattn_chunk_workspace_size, "rse_seqattn_chunk_workspace_size", attn.handle, n, b.batch,
+                 b.max_len, most)
+    if out is None:
+        out = _on_empty(stream, (n, H, D), dt, q.device)
+    ws = _on_empty(stream, size, torch.uint8, q.device) if size else None
+    o = _rows(out, dt, n, H, D, "out")
+    byref = ctypes.byref
+    check(lib.seq_attention_chunk(attn.handle, cache.handle, byref(b), byref(args[0]), byref(args[1]), byref(args[2]),
+                                  page_table.data_ptr(), max_pages, lens_p, most, byref(o), _ptr(ws), size,
+                                  _stream(stream)), "seq_attention_chunk")
+    return out
