@@ -16,10 +16,10 @@ using namespace rse_host;
 
 namespace {
 
-constexpr int GT = 256;                 // threads of a block: 4 waves, 2 by 2
-constexpr int TILE = 128;               // rows and columns of a block's tile
-constexpr int KB = 128;                 // bytes of the contraction a step: 64 bf16, 32 fp32
+constexpr int JT = 256;                 // threads of a block that adds parts up
+constexpr int KB = 64;                  // bytes of the contraction a step: 32 bf16, 16 fp32
 constexpr int KCH = KB / 16;
+constexpr int NBUF = 3;                 // steps in LDS: one multiplied, two on their way
 
 template <typename T>
 struct Mat {
@@ -33,39 +33,64 @@ constexpr int EPC = 16 / (int)sizeof(T);
 template <typename T>
 constexpr int KT = KB / (int)sizeof(T);
 
+// A block's tile of the result: WQ by WP waves with MQ by MP tiles of 32 by 32
+// each; Q rows are the lanes' side, P rows the registers'.
+template <int MQ_, int MP_, int WQ_, int WP_>
+struct Block {
+    static constexpr int MQ = MQ_, MP = MP_, WQ = WQ_, WP = WP_, TQ = 32 * MQ * WQ, TP = 32 * MP * WP;
+    static constexpr int GT = WQ * WP * WAVE;           // threads
+};
+
 // ------------------------------------------------------------- operands --
-// A block's operand of TILE rows (of the result) by KT<T> of the contraction,
-// on its way from memory through registers to LDS, and read from there as
-// matrix operands: 16 bytes a lane, of row `lane % 32` the elements
-// 8 s' + 4 (lane / 32) .. of step s in fp32, 16 s + 8 (lane / 32) .. in bf16.
-// Pieces past an end are zeros.
-constexpr int PER = TILE * KCH / GT;
+// 16 bytes from memory straight to LDS: lane l's piece lands at lds + l.  In
+// assembly, so that the compiler does not make every read of LDS wait for the
+// loads in flight to other buffers; the waits are multiply's.  Nothing is
+// returned to registers, and the compiler keeps nothing in m0.
+__device__ __forceinline__ void to_lds(const void* p, u32x4* lds) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(RSE_LDS void*)lds);
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(at) : "memory");
+}
+// At most N of the wave's loads are still in flight.
+template <int N>
+__device__ __forceinline__ void loads_left() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// A block's operand of R rows (of the result) by KT<T> of the contraction, on
+// its way from memory to LDS, and read from there as matrix operands: 16 bytes a
+// lane, of row `lane % 32` the elements 8 s' + 4 (lane / 32) .. of step s in
+// fp32, 16 s + 8 (lane / 32) .. in bf16.  Thread t moves the pieces that stand at
+// t, t + GT, ... in LDS.  Rows of the result past the end are doubles of an existing one
+// (their results are not stored); of a last, partial step the pieces past the
+// end are zeros, written through registers.
 
 // Rows of the result are rows in memory: the contraction is contiguous.
-template <typename T, typename F>
+template <typename T, int R, int GT>
 struct AlongRows {
     using TL = Tile<T, KT<T>>;
-    F row_at;                           // pointer of tile row r, or null past the end
+    static constexpr int PER = R * KCH / GT;
+    const T* p[PER];
     int64_t k_end;
-    u32x4 x[PER];
-    uint32_t in;
-    __device__ __forceinline__ void load(int64_t k0) {
-        in = 0;
+    template <typename F>
+    __device__ __forceinline__ void begin(F row_at, int64_t end) {
+        k_end = end;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = i * GT + threadIdx.x, r = t / KCH, c = t % KCH;
-            const T* p = row_at(r);
-            const int64_t k = k0 + c * EPC<T>;
-            const bool ok = p && k < k_end;
-            x[i] = u32x4{0, 0, 0, 0};
-            if (ok) x[i] = gload_u4(p + k);
+            const int t = i * GT + threadIdx.x, r = t / KCH;
+            p[i] = row_at(r) + ((t % KCH) ^ TL::swz(r)) * EPC<T>;
         }
     }
-    __device__ __forceinline__ void store(u32x4* lds) const {
+    __device__ __forceinline__ void issue(int64_t k0, u32x4* lds, int w) const {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) to_lds(p[i] + k0, lds + i * GT + w * WAVE);
+    }
+    __device__ __forceinline__ void partial(int64_t k0, u32x4* lds) const {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int t = i * GT + threadIdx.x;
-            lds[TL::chunk_at(t / KCH, t % KCH)] = x[i];
+            const int64_t k = k0 + ((t % KCH) ^ TL::swz(t / KCH)) * EPC<T>;
+            u32x4 x = {0, 0, 0, 0};
+            if (k < k_end) x = gload_u4(p[i] + k0);
+            lds[t] = x;
         }
     }
     static __device__ __forceinline__ u32x4 frag(const u32x4* lds, int r0, int s) {
@@ -75,28 +100,29 @@ struct AlongRows {
 };
 
 // Rows of the result are columns in memory: one row in memory a step of the
-// contraction.
-template <typename T, typename F>
+// contraction.  F: pointer of the row of contraction index k.
+template <typename T, int R, int GT, typename F>
 struct AcrossRows {
-    using TL = Tile<T, TILE>;
-    F k_row;                            // pointer of the row of contraction index k
+    using TL = Tile<T, R>;
+    static constexpr int PER = R * KCH / GT;
+    F k_row;
     int64_t k_end;
     int cols;                           // of the tile, that exist
-    u32x4 x[PER];
-    __device__ __forceinline__ void load(int64_t k0) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int t = i * GT + threadIdx.x, c = t % TL::CH;
-            const int64_t k = k0 + t / TL::CH;
-            x[i] = u32x4{0, 0, 0, 0};
-            if (k < k_end && c * EPC<T> < cols) x[i] = gload_u4(k_row(k) + c * EPC<T>);
-        }
+    __device__ __forceinline__ const T* at(int64_t k0, int i) const {
+        const int t = i * GT + threadIdx.x, r = t / TL::CH, c = ((t % TL::CH) ^ TL::swz(r)) * EPC<T>;
+        return k_row(k0 + r) + (c < cols ? c : 0);
     }
-    __device__ __forceinline__ void store(u32x4* lds) const {
+    __device__ __forceinline__ void issue(int64_t k0, u32x4* lds, int w) const {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) to_lds(at(k0, i), lds + i * GT + w * WAVE);
+    }
+    __device__ __forceinline__ void partial(int64_t k0, u32x4* lds) const {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int t = i * GT + threadIdx.x;
-            lds[TL::chunk_at(t / TL::CH, t % TL::CH)] = x[i];
+            u32x4 x = {0, 0, 0, 0};
+            if (k0 + t / TL::CH < k_end) x = gload_u4(at(k0, i));
+            lds[t] = x;
         }
     }
     static __device__ __forceinline__ u32x4 frag(const u32x4* lds, int r0, int s) {
@@ -124,186 +150,286 @@ struct AcrossRows {
     }
 };
 
-// acc[j][i] += P rows p0 + p_step j .. times Q rows q0 + 32 i .., over the
-// contraction from k0 to k1.  Two buffers in LDS: the next step's pieces fly
-// while the current one is multiplied.
-template <typename T, typename P, typename Q>
-__device__ __forceinline__ void multiply(P& p, Q& q, int64_t k0, int64_t k1, int p0, int p_step, int q0, f32x16 (&acc)[2][2],
-                                         u32x4 (*lds)[2][TILE * KCH]) {
-    if (k0 >= k1) return;
-    p.load(k0);
-    q.load(k0);
-    for (int b = 0; k0 < k1; k0 += KT<T>, b ^= 1) {
-        p.store(lds[b][0]);
-        q.store(lds[b][1]);
-        __syncthreads();
-        if (k0 + KT<T> < k1) {
-            p.load(k0 + KT<T>);
-            q.load(k0 + KT<T>);
+// acc[j][i] += P rows p0(j) .. times Q rows q0 + 32 i .., over the contraction
+// from k0 to k1 (not empty).  One barrier a step: past it, the step's pieces have landed and
+// all waves are done with the buffer that the step after next is sent to.
+template <typename T, typename B, typename P, typename Q, typename P0>
+__device__ __forceinline__ void multiply(const P& p, const Q& q, int64_t k0, int64_t k1, P0 p0, int q0, f32x16 (&acc)[B::MP][B::MQ],
+                                         u32x4* lds, int w) {
+    constexpr int SIZE = (B::TP + B::TQ) * KCH;
+    const int steps = (int)((k1 - k0 + KT<T> - 1) / KT<T>), full = (int)((k1 - k0) / KT<T>);
+    auto send = [&](int i, int b) {
+        u32x4* to = lds + b * SIZE;
+        if (i < full) {
+            p.issue(k0 + (int64_t)i * KT<T>, to, w);
+            q.issue(k0 + (int64_t)i * KT<T>, to + B::TP * KCH, w);
+        } else if (i < steps) {
+            p.partial(k0 + (int64_t)i * KT<T>, to);
+            q.partial(k0 + (int64_t)i * KT<T>, to + B::TP * KCH);
         }
+    };
+    send(0, 0);
+    send(1, 1);
+    int b = 0, i = 0;
+    do {
+        if (i + 1 < full) loads_left<P::PER + Q::PER>();
+        else loads_left<0>();
+        lds_barrier();
+        send(i + 2, b == 0 ? 2 : b - 1);
+        const u32x4 *lp = lds + b * SIZE, *lq = lp + B::TP * KCH;
 #pragma unroll
         for (int s = 0; s < KCH / 2; ++s) {
-            u32x4 a[2], c[2];
+            u32x4 a[B::MP], c[B::MQ];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) a[j] = P::frag(lds[b][0], p0 + j * p_step, s);
+            for (int j = 0; j < B::MP; ++j) a[j] = P::frag(lp, p0(j), s);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) c[i] = Q::frag(lds[b][1], q0 + 32 * i, s);
+            for (int u = 0; u < B::MQ; ++u) c[u] = Q::frag(lq, q0 + 32 * u, s);
+#pragma unroll
+            for (int j = 0; j < B::MP; ++j)
+#pragma unroll
+                for (int u = 0; u < B::MQ; ++u) acc[j][u] = mma_chunk<T>(a[j], c[u], acc[j][u]);
+        }
+        b = b == 2 ? 0 : b + 1;
+    } while (++i < steps);
+}
+
+// A 32 by 32 tile of a lane's row as 16-byte pieces: piece(j) gives elements
+// EPC (2 j + half) .. of the 32 along the registers.
+template <typename T>
+struct Pieces {
+    static constexpr int N = sizeof(T);         // pieces a lane: 4 of fp32, 2 of bf16
+    u32x4 v[N];
+    __device__ __forceinline__ explicit Pieces(const f32x16& acc) {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e / 4][e % 4] = __float_as_uint(acc[e]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)         // (the exchange of store_column)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const u32x2 s = __builtin_amdgcn_permlane32_swap(pack_bf16(acc[8 * j + 2 * i], acc[8 * j + 2 * i + 1]),
+                                                                     pack_bf16(acc[8 * j + 4 + 2 * i], acc[8 * j + 5 + 2 * i]), false, false);
+                    v[j][i] = s.x;
+                    v[j][2 + i] = s.y;
+                }
+        }
+    }
+};
+// Straight to a row of memory; elements at `left` and on do not exist.
+template <typename T>
+__device__ __forceinline__ void put_column(T* p, const f32x16& acc, int64_t left) {
+    const Pieces<T> x(acc);
+    const int h = lane_id() >> 5;
+#pragma unroll
+    for (int j = 0; j < Pieces<T>::N; ++j)
+        if (EPC<T> * (2 * j + h) < left) gstore_u4(p + EPC<T> * (2 * j + h), x.v[j]);
+}
+// To row `row`, columns c0 .. of a tile of W columns in LDS.
+template <typename T, int W>
+__device__ __forceinline__ void put_lds(u32x4* lds, int row, int c0, const f32x16& acc) {
+    const Pieces<T> x(acc);
+    const int h = lane_id() >> 5;
+#pragma unroll
+    for (int j = 0; j < Pieces<T>::N; ++j) lds[Tile<T, W>::chunk_at(row, c0 / EPC<T> + 2 * j + h)] = x.v[j];
+}
+// A tile of R rows by W columns from LDS to memory, whole lines of a row by
+// neighbouring lanes; `rows` and `cols` exist.
+template <typename T, int R, int W, int GT>
+__device__ __forceinline__ void rows_to_memory(const u32x4* lds, const Mat<T>& out, int64_t r0, int64_t c0, int64_t rows, int64_t cols) {
+    constexpr int CH = Tile<T, W>::CH;
+#pragma unroll
+    for (int i = 0; i < R * CH / GT; ++i) {
+        const int t = i * GT + threadIdx.x, r = t / CH, c = t % CH;
+        if (r < rows && c * EPC<T> < cols) gstore_u4(out.row(r0 + r) + c0 + c * EPC<T>, lds[Tile<T, W>::chunk_at(r, c)]);
+    }
+}
+
+// The same elements read, as they stand in memory (0 past the end), and widened.
+template <typename T>
+struct RawColumn {
+    u32x4 v[2 * (int)sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p, int64_t left) {
+        const int h = lane_id() >> 5;
+        constexpr int N = 2 * (int)sizeof(T) / 2, E = EPC<T>;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            v[j] = u32x4{0, 0, 0, 0};
+            if (E * (2 * j + h) < left) v[j] = gload_u4(p + E * (2 * j + h));
+        }
+    }
+    __device__ __forceinline__ f32x16 widen() const {
+        f32x16 x;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e / 4][e % 4]);
+        } else {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) acc[j][i] = mma_chunk<T>(a[j], c[i], acc[j][i]);
+                for (int i = 0; i < 2; ++i) {
+                    const u32x2 s = __builtin_amdgcn_permlane32_swap(v[j][i], v[j][2 + i], false, false);
+                    x[8 * j + 2 * i] = __uint_as_float(s.x << 16);
+                    x[8 * j + 2 * i + 1] = __uint_as_float(s.x & 0xFFFF0000u);
+                    x[8 * j + 4 + 2 * i] = __uint_as_float(s.y << 16);
+                    x[8 * j + 5 + 2 * i] = __uint_as_float(s.y & 0xFFFF0000u);
+                }
         }
+        return x;
     }
-}
+};
 
-// Elements of the lane's row from registers, 16 bytes a store: acc's register
-// r is element tile_row(r, half) of p[0 .. 31]; pieces at `left` and on do not exist.
-__device__ __forceinline__ void put_column(float* p, const f32x16& acc, int64_t left) {
-    const int h = lane_id() >> 5;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (8 * j + 4 * h < left) gstore_f4(p + 8 * j + 4 * h, f32x4{acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]});
-}
-__device__ __forceinline__ void put_column(uint16_t* p, const f32x16& acc, int64_t left) {
-    const int h = lane_id() >> 5;
-#pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-        u32x4 o;                                // (the exchange of store_column)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const u32x2 s = __builtin_amdgcn_permlane32_swap(pack_bf16(acc[4 * j + 2 * i], acc[4 * j + 2 * i + 1]),
-                                                             pack_bf16(acc[4 * j + 4 + 2 * i], acc[4 * j + 5 + 2 * i]), false, false);
-            o[i] = s.x;
-            o[2 + i] = s.y;
-        }
-        if (8 * (j + h) < left) gstore_u4(p + 8 * (j + h), o);
-    }
-}
-// The same elements read; 0 past the end (and where the row does not exist).
-__device__ __forceinline__ void get_column(const float* p, f32x16& x, int64_t left) {
-    const int h = lane_id() >> 5;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        if (8 * j + 4 * h < left) v = gload_f4(p + 8 * j + 4 * h);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[4 * j + i] = v[i];
-    }
-}
-__device__ __forceinline__ void get_column(const uint16_t* p, f32x16& x, int64_t left) {
-    const int h = lane_id() >> 5;
-#pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-        u32x4 o = {0, 0, 0, 0};
-        if (8 * (j + h) < left) o = gload_u4(p + 8 * (j + h));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const u32x2 s = __builtin_amdgcn_permlane32_swap(o[i], o[2 + i], false, false);
-            x[4 * j + 2 * i] = __uint_as_float(s.x << 16);
-            x[4 * j + 2 * i + 1] = __uint_as_float(s.x & 0xFFFF0000u);
-            x[4 * j + 4 + 2 * i] = __uint_as_float(s.y << 16);
-            x[4 * j + 5 + 2 * i] = __uint_as_float(s.y & 0xFFFF0000u);
-        }
-    }
-}
-
-// act(g) and act'(g).
-__device__ __forceinline__ void activate(int act, float g, float& a, float& da) {
-    if (act == RSE_GELU) {
-        const float cdf = 0.5f * erfcf(g * -0.70710678118654752f);
+// act(g) and act'(g), by the hardware's exponential and reciprocal (one unit in
+// the last place each).  GELU: Phi(-x) = e^(-x^2 / 2) R(x) for x >= 0, R / t a
+// polynomial in t = 1 / (1 + 0.32 x) fitted to erfcx (3e-8 relative), and the
+// exponential serves the derivative too.
+template <int ACT>
+__device__ __forceinline__ void activate(float g, float& a, float& da) {
+    if (ACT == RSE_GELU) {
+        const float x = fabsf(g), e = __builtin_amdgcn_exp2f(g * g * (-0.5f * LOG2E));
+        const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(x, 0.32f, 1.f));
+        float r = -0.021151972926650987f;
+        r = __builtin_fmaf(r, t, 0.09575628588024625f);
+        r = __builtin_fmaf(r, t, -0.1474010975314183f);
+        r = __builtin_fmaf(r, t, 0.06607995419458114f);
+        r = __builtin_fmaf(r, t, -0.009860294843239454f);
+        r = __builtin_fmaf(r, t, 0.058840354541432945f);
+        r = __builtin_fmaf(r, t, 0.0877871262999502f);
+        r = __builtin_fmaf(r, t, 0.11462742044437546f);
+        r = __builtin_fmaf(r, t, 0.1276606749658141f);
+        r = __builtin_fmaf(r, t, 0.12766153278717118f);
+        r *= t * e;                             // Phi(-x)
+        const float cdf = g < 0.f ? r : 1.f - r;
         a = g * cdf;
-        da = __builtin_fmaf(g * 0.39894228040143268f, __builtin_amdgcn_exp2f(g * g * (-0.5f * LOG2E)), cdf);
+        da = __builtin_fmaf(g * 0.39894228040143268f, e, cdf);
     } else {
-        const float s = 1.f / (1.f + __builtin_amdgcn_exp2f(-LOG2E * g)), t = s - s * s;
-        a = act == RSE_SILU ? g * s : s;
-        da = act == RSE_SILU ? __builtin_fmaf(g, t, s) : t;
+        const float s = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-LOG2E * g)), t = __builtin_fmaf(-s, s, s);
+        a = ACT == RSE_SILU ? g * s : s;
+        da = ACT == RSE_SILU ? __builtin_fmaf(g, t, s) : t;
     }
 }
 
 // Block x's tile of a grid of `total`: blocks of one XCD (x % 8) take
 // consecutive ones, so that what they share stays in its L2.
-__device__ __forceinline__ int64_t xcd_tile(int64_t x, int64_t total) {
-    const int64_t per = total / 8, rest = total % 8, xcd = x % 8;
+__device__ __forceinline__ uint32_t xcd_tile(uint32_t x, uint32_t total) {
+    const uint32_t per = total / 8, rest = total % 8, xcd = x % 8;
     return xcd * per + (xcd < rest ? xcd : rest) + x / 8;
 }
 
 struct GatedArgs {
     int64_t n;
-    int32_t dim, hidden, act;
+    int32_t dim, hidden;
 };
 
-// out (BWD: dg beside du) of TILE rows by TILE / 2 hidden elements: the tile's
-// P rows are TILE / 2 rows of Wg, then the same ones of Wu, and a wave's
+#ifndef INB
+#define INB Block<2, 4, 2, 2>
+#endif
+// Shapes, by the type's rate on the matrix cores.  bf16: a step of a block's
+// tile is 1024 cycles of products, 1152 of LDS reads and writes, 768 of the
+// vector memory path; two blocks a CU.  fp32 is 16 times as long in its
+// products, and small tiles fill the GPU more evenly.
+template <typename T>
+using InBlock = std::conditional_t<sizeof(T) == 2, INB, Block<1, 2, 2, 2>>;
+template <typename T>
+using OutBlock = std::conditional_t<sizeof(T) == 2, Block<2, 4, 2, 2>, Block<1, 1, 2, 2>>;
+template <typename B>
+constexpr int SHARE = B::MQ * B::MP >= 8 ? 2 : 4;       // waves that share a SIMD
+template <typename B>
+constexpr int AT_ONCE = 256 * SHARE<B> * 4 * WAVE / B::GT;      // blocks on the GPU at once
+
+// out (BWD: dg beside du) of TQ rows by TP / 2 hidden elements: the tile's P
+// rows are TP / 2 rows of Wg, then the same ones of Wu, and a wave's
 // accumulators hold g and u of the same elements.
-template <typename T, bool BWD>
-__global__ __launch_bounds__(GT) void k_gated(GatedArgs a, Mat<const T> x, Mat<const T> wg, Mat<const T> wu,
-                                              Mat<const T> dout, Mat<T> out) {
-    constexpr int HT = TILE / 2;
-    __shared__ u32x4 lds[2][2][TILE * KCH];
+template <typename T, typename B, int ACT, bool BWD>
+__global__ __launch_bounds__(B::GT) __attribute__((amdgpu_waves_per_eu(SHARE<B>))) void k_gated(
+    GatedArgs a, Mat<const T> x, Mat<const T> wg, Mat<const T> wu, Mat<const T> dout, Mat<T> out) {
+    constexpr int HT = B::TP / 2, MH = B::MP / 2;
+    __shared__ u32x4 lds[NBUF * (B::TP + B::TQ) * KCH];
     const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE);
-    const int64_t ht = (a.hidden + HT - 1) / HT, tile = xcd_tile(blockIdx.x, gridDim.x);
-    const int64_t r0 = tile / ht * TILE;
+    const uint32_t ht = (a.hidden + HT - 1) / HT, tile = xcd_tile(blockIdx.x, gridDim.x);
+    const int64_t r0 = (int64_t)(tile / ht) * B::TQ;
     const int h0 = (int)(tile % ht) * HT;
-    auto w_row = [&](int r) -> const T* {
+    AlongRows<T, B::TP, B::GT> p;
+    p.begin([&](int r) {
         const int h = h0 + r % HT;
-        return h < a.hidden ? (r < HT ? wg.row(h) : wu.row(h)) : nullptr;
-    };
-    auto x_row = [&](int r) -> const T* { return r0 + r < a.n ? x.row(r0 + r) : nullptr; };
-    AlongRows<T, decltype(w_row)> p = {w_row, a.dim};
-    AlongRows<T, decltype(x_row)> q = {x_row, a.dim};
-    f32x16 acc[2][2] = {};
-    const int hw = 32 * (w & 1), qw = 64 * (w >> 1);
-    multiply<T>(p, q, 0, a.dim, hw, HT, qw, acc, lds);
-    const int64_t left = a.hidden - h0 - hw;
+        return (r < HT ? wg : wu).row(h < a.hidden ? h : a.hidden - 1);
+    }, a.dim);
+    AlongRows<T, B::TQ, B::GT> q;
+    q.begin([&](int r) { return x.row(r0 + r < a.n ? r0 + r : a.n - 1); }, a.dim);
+    f32x16 acc[B::MP][B::MQ] = {};
+    const int hw = 32 * MH * (w % B::WP), qw = 32 * B::MQ * (w / B::WP);
+    RawColumn<T> d[BWD ? MH : 1][B::MQ];
+    if constexpr (BWD)                          // on its way while the projections are formed
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int64_t r = r0 + qw + 32 * i + (lane & 31);
-        f32x16 &g = acc[0][i], &u = acc[1][i];
-        if constexpr (BWD) {
-            f32x16 d;
-            get_column(dout.row(r < a.n ? r : a.n - 1) + h0 + hw, d, left);
+        for (int i = 0; i < B::MQ; ++i) {
+            const int64_t r = r0 + qw + 32 * i + (lane & 31);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float f, df;
-                activate(a.act, g[e], f, df);
-                g[e] = d[e] * u[e] * df;
-                u[e] = d[e] * f;
+            for (int j = 0; j < MH; ++j) {
+                const int h = h0 + hw + 32 * j;
+                d[j][i].load(dout.row(r < a.n ? r : 0) + h, r < a.n ? a.hidden - h : 0);
             }
-            const int64_t there = r < a.n ? left : 0;
-            put_column(out.row(r < a.n ? r : 0) + h0 + hw, g, there);
-            put_column(out.row(r < a.n ? r : 0) + a.hidden + h0 + hw, u, there);
-        } else {
+        }
+    multiply<T, B>(p, q, 0, a.dim, [&](int j) { return hw + (j < MH ? 32 * j : HT + 32 * (j - MH)); }, qw, acc, lds, w);
+    // by way of LDS, so that a store instruction writes whole lines (32 bytes of
+    // 32 rows each ran at 2.8 TB/s)
+    constexpr int SIZE = B::TQ * HT / EPC<T>;
+    static_assert((BWD ? 2 : 1) * SIZE <= NBUF * (B::TP + B::TQ) * KCH, "tiles of results in LDS");
+    lds_barrier();                              // all waves are done with the operands
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float f, df;
-                activate(a.act, g[e], f, df);
-                g[e] = f * u[e];
+    for (int i = 0; i < B::MQ; ++i) {
+        const int r = qw + 32 * i + (lane & 31);
+#pragma unroll
+        for (int j = 0; j < MH; ++j) {
+            f32x16 &g = acc[j][i], &u = acc[j + MH][i];
+            if constexpr (BWD) {
+                const f32x16 up = d[j][i].widen();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float f, df;
+                    activate<ACT>(g[e], f, df);
+                    g[e] = up[e] * u[e] * df;
+                    u[e] = up[e] * f;
+                }
+                put_lds<T, HT>(lds, r, hw + 32 * j, g);
+                put_lds<T, HT>(lds + SIZE, r, hw + 32 * j, u);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float f, df;
+                    activate<ACT>(g[e], f, df);
+                    g[e] = f * u[e];
+                }
+                put_lds<T, HT>(lds, r, hw + 32 * j, g);
             }
-            put_column(out.row(r < a.n ? r : 0) + h0 + hw, g, r < a.n ? left : 0);
         }
     }
+    lds_barrier();
+    rows_to_memory<T, B::TQ, HT, B::GT>(lds, out, r0, h0, a.n - r0, a.hidden - h0);
+    if constexpr (BWD) rows_to_memory<T, B::TQ, HT, B::GT>(lds + SIZE, out, r0, a.hidden + h0, a.n - r0, a.hidden - h0);
 }
 
 // dx = [dg du] [Wg; Wu].
-template <typename T>
-__global__ __launch_bounds__(GT) void k_gated_dx(GatedArgs a, Mat<const T> d, Mat<const T> wg, Mat<const T> wu, Mat<T> dx) {
-    __shared__ u32x4 lds[2][2][TILE * KCH];
+template <typename T, typename B>
+__global__ __launch_bounds__(B::GT) __attribute__((amdgpu_waves_per_eu(SHARE<B>))) void k_gated_dx(GatedArgs a, Mat<const T> d,
+                                                                                                Mat<const T> wg, Mat<const T> wu,
+                                                                                                Mat<T> dx) {
+    __shared__ u32x4 lds[NBUF * (B::TP + B::TQ) * KCH];
     const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE);
-    const int64_t ct = (a.dim + TILE - 1) / TILE, tile = xcd_tile(blockIdx.x, gridDim.x);
-    const int64_t r0 = tile / ct * TILE;
-    const int c0 = (int)(tile % ct) * TILE;
+    const uint32_t ct = (a.dim + B::TP - 1) / B::TP, tile = xcd_tile(blockIdx.x, gridDim.x);
+    const int64_t r0 = (int64_t)(tile / ct) * B::TQ, k_end = 2ll * a.hidden;
+    const int c0 = (int)(tile % ct) * B::TP;
     auto w_row = [&](int64_t k) -> const T* { return (k < a.hidden ? wg.row(k) : wu.row(k - a.hidden)) + c0; };
-    auto d_row = [&](int r) -> const T* { return r0 + r < a.n ? d.row(r0 + r) : nullptr; };
-    AcrossRows<T, decltype(w_row)> p = {w_row, 2ll * a.hidden, a.dim - c0};
-    AlongRows<T, decltype(d_row)> q = {d_row, 2ll * a.hidden};
-    f32x16 acc[2][2] = {};
-    const int pw = 64 * (w & 1), qw = 64 * (w >> 1);
-    multiply<T>(p, q, 0, 2ll * a.hidden, pw, 32, qw, acc, lds);
+    AcrossRows<T, B::TP, B::GT, decltype(w_row)> p = {w_row, k_end, a.dim - c0};
+    AlongRows<T, B::TQ, B::GT> q;
+    q.begin([&](int r) { return d.row(r0 + r < a.n ? r0 + r : a.n - 1); }, k_end);
+    f32x16 acc[B::MP][B::MQ] = {};
+    const int pw = 32 * B::MP * (w % B::WP), qw = 32 * B::MQ * (w / B::WP);
+    multiply<T, B>(p, q, 0, k_end, [&](int j) { return pw + 32 * j; }, qw, acc, lds, w);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < B::MQ; ++i) {
         const int64_t r = r0 + qw + 32 * i + (lane & 31);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < B::MP; ++j) {
             const int c = c0 + pw + 32 * j;
             put_column(dx.row(r < a.n ? r : 0) + c, acc[j][i], r < a.n ? a.dim - c : 0);
         }
@@ -311,29 +437,31 @@ __global__ __launch_bounds__(GT) void k_gated_dx(GatedArgs a, Mat<const T> d, Ma
 }
 
 // Part s of [dWg; dWu] = [dg du]^T x: the rows from s `rows` on.
-template <typename T>
-__global__ __launch_bounds__(GT) void k_gated_dw(GatedArgs a, Mat<const T> d, Mat<const T> x, int64_t rows, float* part) {
-    __shared__ u32x4 lds[2][2][TILE * KCH];
+template <typename T, typename B>
+__global__ __launch_bounds__(B::GT) __attribute__((amdgpu_waves_per_eu(SHARE<B>))) void k_gated_dw(GatedArgs a, Mat<const T> d,
+                                                                                                Mat<const T> x, int64_t rows,
+                                                                                                float* part) {
+    __shared__ u32x4 lds[NBUF * (B::TP + B::TQ) * KCH];
     const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE);
-    const int64_t ct = (a.dim + TILE - 1) / TILE, ht = (2ll * a.hidden + TILE - 1) / TILE;
-    int64_t tile = xcd_tile(blockIdx.x, gridDim.x);
-    const int c0 = (int)(tile % ct) * TILE;
+    const uint32_t ct = (a.dim + B::TP - 1) / B::TP, ht = (2u * a.hidden + B::TQ - 1) / B::TQ;
+    uint32_t tile = xcd_tile(blockIdx.x, gridDim.x);
+    const int c0 = (int)(tile % ct) * B::TP;
     tile /= ct;
-    const int h0 = (int)(tile % ht) * TILE;
+    const int h0 = (int)(tile % ht) * B::TQ;
     const int64_t s = tile / ht, k0 = s * rows, k1 = k0 + rows < a.n ? k0 + rows : a.n;
     auto x_row = [&](int64_t k) -> const T* { return x.row(k) + c0; };
     auto d_row = [&](int64_t k) -> const T* { return d.row(k) + h0; };
-    AcrossRows<T, decltype(x_row)> p = {x_row, k1, a.dim - c0};
-    AcrossRows<T, decltype(d_row)> q = {d_row, k1, 2 * a.hidden - h0};
-    f32x16 acc[2][2] = {};
-    const int pw = 64 * (w & 1), qw = 64 * (w >> 1);
-    multiply<T>(p, q, k0, k1, pw, 32, qw, acc, lds);
+    AcrossRows<T, B::TP, B::GT, decltype(x_row)> p = {x_row, k1, a.dim - c0};
+    AcrossRows<T, B::TQ, B::GT, decltype(d_row)> q = {d_row, k1, 2 * a.hidden - h0};
+    f32x16 acc[B::MP][B::MQ] = {};
+    const int pw = 32 * B::MP * (w % B::WP), qw = 32 * B::MQ * (w / B::WP);
+    multiply<T, B>(p, q, k0, k1, [&](int j) { return pw + 32 * j; }, qw, acc, lds, w);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < B::MQ; ++i) {
         const int64_t h = h0 + qw + 32 * i + (lane & 31);
         const bool in = h < 2ll * a.hidden;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < B::MP; ++j) {
             const int c = c0 + pw + 32 * j;
             put_column(part + ((s * 2 * a.hidden + (in ? h : 0)) * a.dim + c), acc[j][i], in ? a.dim - c : 0);
         }
@@ -342,9 +470,9 @@ __global__ __launch_bounds__(GT) void k_gated_dw(GatedArgs a, Mat<const T> d, Ma
 
 // The parts added, rounded once: four elements a thread.
 template <typename T>
-__global__ __launch_bounds__(GT) void k_gated_dw_join(GatedArgs a, const float* part, int splits, Mat<T> dwg, Mat<T> dwu) {
+__global__ __launch_bounds__(JT) void k_gated_dw_join(GatedArgs a, const float* part, int splits, Mat<T> dwg, Mat<T> dwu) {
     const int64_t size = 2ll * a.hidden * a.dim;
-    for (int64_t t = 4 * ((int64_t)blockIdx.x * GT + threadIdx.x); t < size; t += 4ll * GT * gridDim.x) {
+    for (int64_t t = 4 * ((int64_t)blockIdx.x * JT + threadIdx.x); t < size; t += 4ll * JT * gridDim.x) {
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
         for (int s = 0; s < splits; ++s) o += gload_f4(part + s * size + t);
@@ -373,18 +501,29 @@ int gated_args(int64_t n, int32_t dim, int32_t hidden, int32_t dtype) {
     return RSE_OK;
 }
 
-// Parts of the events for dW: 512 blocks in all (two a CU), parts of whole
-// steps, 512 events at least.
+// Parts of the events for dW, of whole steps and 512 events at least: as many
+// as make the rounds of blocks (SHARE a CU at once) fullest, the cost of adding a
+// part up taken as that of 64 events.
 struct DwPlan {
     int splits;
     int64_t rows;
 };
-DwPlan dw_plan(int64_t n, int32_t dim, int32_t hidden) {
-    const int64_t tiles = (int64_t)((dim + TILE - 1) / TILE) * ((2ll * hidden + TILE - 1) / TILE);
-    int64_t s = (512 + tiles - 1) / tiles;
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+template <typename T>
+int64_t dw_tiles(int32_t dim, int32_t hidden) { return up(dim, OutBlock<T>::TP) * up(2ll * hidden, OutBlock<T>::TQ); }
+DwPlan dw_plan(int64_t n, int32_t dim, int32_t hidden, int32_t dtype) {
+    const int64_t tiles = dtype == RSE_F32 ? dw_tiles<float>(dim, hidden) : dw_tiles<uint16_t>(dim, hidden);
+    const int64_t at_once = dtype == RSE_F32 ? AT_ONCE<OutBlock<float>> : AT_ONCE<OutBlock<uint16_t>>;
     const int64_t most = (n + 511) / 512;
-    if (s > most) s = most;
-    if (s < 1) s = 1;
+    int64_t s = 1;
+    double best = 0;
+    for (int64_t c = 1; c <= 64 && c <= most; ++c) {
+        const double cost = (double)(up(tiles * c, at_once)) * ((double)n / c + 64.0 * c);
+        if (c == 1 || cost < best) {
+            best = cost;
+            s = c;
+        }
+    }
     DwPlan p;
     p.rows = ((n + s - 1) / s + 63) / 64 * 64;
     p.splits = (int)(p.rows > 0 ? (n + p.rows - 1) / p.rows : 0);
@@ -401,14 +540,18 @@ GatedWs gated_ws(int64_t n, int32_t dim, int32_t hidden, int32_t dtype, void* ba
     const size_t e = dtype == RSE_F32 ? 4 : 2;
     GatedWs w;
     w.d = c.take<char>((size_t)n * 2 * hidden * e);
-    w.part = c.take<float>((size_t)dw_plan(n, dim, hidden).splits * 2 * hidden * dim);
+    w.part = c.take<float>((size_t)dw_plan(n, dim, hidden, dtype).splits * 2 * hidden * dim);
     w.bytes = c.size();
     return w;
 }
 
+// f(T(), integral_constant<act>)
 template <typename F>
-int by_dtype(int32_t dtype, F f) {
-    return dtype == RSE_F32 ? f(float()) : f(uint16_t());
+int by_kind(int32_t dtype, int32_t act, F f) {
+    const auto go = [&](auto a) { return dtype == RSE_F32 ? f(float(), a) : f(uint16_t(), a); };
+    if (act == RSE_SIGMOID) return go(std::integral_constant<int, RSE_SIGMOID>());
+    if (act == RSE_SILU) return go(std::integral_constant<int, RSE_SILU>());
+    return go(std::integral_constant<int, RSE_GELU>());
 }
 
 }  // namespace
@@ -422,12 +565,14 @@ int seq_gated_linear_fwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const 
     if (act < RSE_SIGMOID || act > RSE_GELU || !mat_ok(w_gate, dtype) || !mat_ok(w_up, dtype)) return RSE_ERR_INVALID_ARG;
     if (n == 0) return RSE_OK;
     if (!mat_ok(x, dtype) || !out_mat_ok(out, dtype, n, hidden)) return RSE_ERR_INVALID_ARG;
-    const int64_t blocks = (n + TILE - 1) / TILE * ((hidden + TILE / 2 - 1) / (TILE / 2));
-    if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
-    const GatedArgs a = {n, dim, hidden, act};
-    return by_dtype(dtype, [&](auto t) {
+    const GatedArgs a = {n, dim, hidden};
+    return by_kind(dtype, act, [&](auto t, auto ac) -> int {
         using T = decltype(t);
-        hipLaunchKernelGGL((k_gated<T, false>), dim3((unsigned)blocks), dim3(GT), 0, as_stream(stream), a, view<const T>(x),
+        constexpr int ACT = decltype(ac)::value;
+        using B = InBlock<T>;
+        const int64_t blocks = up(n, B::TQ) * up(hidden, B::TP / 2);
+        if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+        hipLaunchKernelGGL((k_gated<T, B, ACT, false>), dim3((unsigned)blocks), dim3(B::GT), 0, as_stream(stream), a, view<const T>(x),
                            view<const T>(w_gate), view<const T>(w_up), Mat<const T>{nullptr, 0}, view<T>(out));
         return launch_status();
     });
@@ -453,26 +598,28 @@ int seq_gated_linear_bwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const 
     const GatedWs ws = gated_ws(n, dim, hidden, dtype, d_ws);
     if (ws_bytes < ws.bytes) return RSE_ERR_WORKSPACE;
     if (ws.bytes && (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256)) return RSE_ERR_INVALID_ARG;
-    const DwPlan dp = dw_plan(n, dim, hidden);
-    const int64_t rt = (n + TILE - 1) / TILE, ct = (dim + TILE - 1) / TILE;
-    const int64_t in_blocks = rt * ((hidden + TILE / 2 - 1) / (TILE / 2)), dx_blocks = rt * ct;
-    const int64_t dw_blocks = dp.splits * ct * ((2ll * hidden + TILE - 1) / TILE);
-    if (in_blocks > INT32_MAX || dw_blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
-    const GatedArgs a = {n, dim, hidden, act};
+    const DwPlan dp = dw_plan(n, dim, hidden, dtype);
+    const GatedArgs a = {n, dim, hidden};
     hipStream_t s = as_stream(stream);
-    return by_dtype(dtype, [&](auto t) {
+    return by_kind(dtype, act, [&](auto t, auto ac) -> int {
         using T = decltype(t);
+        constexpr int ACT = decltype(ac)::value;
+        using BI = InBlock<T>;
+        using BO = OutBlock<T>;
+        const int64_t in_blocks = up(n, BI::TQ) * up(hidden, BI::TP / 2), dx_blocks = up(n, BO::TQ) * up(dim, BO::TP);
+        const int64_t dw_blocks = dp.splits * dw_tiles<T>(dim, hidden);
+        if (in_blocks > INT32_MAX || dx_blocks > INT32_MAX || dw_blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
         const Mat<T> d = {static_cast<T*>(ws.d), 2ll * hidden};
         const Mat<const T> dc = {d.p, d.stride};
         if (n > 0) {
-            hipLaunchKernelGGL((k_gated<T, true>), dim3((unsigned)in_blocks), dim3(GT), 0, s, a, view<const T>(x),
+            hipLaunchKernelGGL((k_gated<T, BI, ACT, true>), dim3((unsigned)in_blocks), dim3(BI::GT), 0, s, a, view<const T>(x),
                                view<const T>(w_gate), view<const T>(w_up), view<const T>(dout), d);
-            hipLaunchKernelGGL((k_gated_dx<T>), dim3((unsigned)dx_blocks), dim3(GT), 0, s, a, dc, view<const T>(w_gate),
+            hipLaunchKernelGGL((k_gated_dx<T, BO>), dim3((unsigned)dx_blocks), dim3(BO::GT), 0, s, a, dc, view<const T>(w_gate),
                                view<const T>(w_up), view<T>(dx));
-            hipLaunchKernelGGL((k_gated_dw<T>), dim3((unsigned)dw_blocks), dim3(GT), 0, s, a, dc, view<const T>(x), dp.rows,
+            hipLaunchKernelGGL((k_gated_dw<T, BO>), dim3((unsigned)dw_blocks), dim3(BO::GT), 0, s, a, dc, view<const T>(x), dp.rows,
                                ws.part);
         }
-        hipLaunchKernelGGL((k_gated_dw_join<T>), dim3(fill_blocks(2ll * hidden * dim, 4 * GT, 4096)), dim3(GT), 0, s, a, ws.part,
+        hipLaunchKernelGGL((k_gated_dw_join<T>), dim3(fill_blocks(2ll * hidden * dim, 4 * JT, 4096)), dim3(JT), 0, s, a, ws.part,
                            dp.splits, view<T>(dw_gate), view<T>(dw_up));
         return launch_status();
     });
