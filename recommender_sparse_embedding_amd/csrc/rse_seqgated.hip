@@ -79,7 +79,7 @@ struct AlongRows {
             p[i] = row_at(r) + ((t % KCH) ^ TL::swz(r)) * EPC<T>;
         }
     }
-    __device__ __forceinline__ void issue(int64_t k0, u32x4* lds, int w) const {
+    __device__ __forceinline__ void issue(int64_t k0, bool, u32x4* lds, int w) const {
 #pragma unroll
         for (int i = 0; i < PER; ++i) to_lds(p[i] + k0, lds + i * GT + w * WAVE);
     }
@@ -112,7 +112,7 @@ struct AcrossRows {
         const int t = i * GT + threadIdx.x, r = t / TL::CH, c = ((t % TL::CH) ^ TL::swz(r)) * EPC<T>;
         return k_row(k0 + r) + (c < cols ? c : 0);
     }
-    __device__ __forceinline__ void issue(int64_t k0, u32x4* lds, int w) const {
+    __device__ __forceinline__ void issue(int64_t k0, bool, u32x4* lds, int w) const {
 #pragma unroll
         for (int i = 0; i < PER; ++i) to_lds(at(k0, i), lds + i * GT + w * WAVE);
     }
@@ -150,19 +150,76 @@ struct AcrossRows {
     }
 };
 
+// The same of a first matrix and, from contraction index `turn` on, of a second
+// one.  Steps are sent in order: a step's rows are the last one's, KT further,
+// but for the first step and the two around the turn (addresses formed anew every
+// step: 575 us for 540 in k_gated_dx of 413696 rows of 256 by 1024; without a
+// second matrix k_gated_dw is the faster the other way, 477 for 517).
+template <typename T, int R, int GT>
+struct StackedRows {
+    using TL = Tile<T, R>;
+    static constexpr int PER = R * KCH / GT;
+    Mat<const T> m, m2;
+    int64_t turn, k_end;
+    const T* p[PER];                    // of the step sent last
+    int c[PER];
+    __device__ __forceinline__ const T* row(int64_t k) const {
+        const bool first = k < turn;
+        const int64_t i = first ? k : k - turn;
+        const uint64_t base = first ? reinterpret_cast<uint64_t>(m.p) : reinterpret_cast<uint64_t>(m2.p);
+        return reinterpret_cast<const T*>(base) + i * (first ? m.stride : m2.stride);
+    }
+    // cols: of the tile, that exist
+    __device__ __forceinline__ void begin(Mat<const T> a, Mat<const T> b, int64_t at, int64_t end, int cols) {
+        m = a;
+        m2 = b;
+        turn = at;
+        k_end = end;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int t = i * GT + threadIdx.x, x = ((t % TL::CH) ^ TL::swz(t / TL::CH)) * EPC<T>;
+            c[i] = x < cols ? x : 0;
+            p[i] = nullptr;
+        }
+    }
+    __device__ __forceinline__ void issue(int64_t k0, bool first, u32x4* lds, int w) {
+        const bool anew = first || (k0 + KT<T> > turn && k0 < turn + KT<T>);
+        const int64_t ahead = KT<T> * (k0 < turn ? m.stride : m2.stride);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (anew) p[i] = row(k0 + (i * GT + (int)threadIdx.x) / TL::CH) + c[i];
+            else p[i] += ahead;
+            to_lds(p[i], lds + i * GT + w * WAVE);
+        }
+    }
+    __device__ __forceinline__ void partial(int64_t k0, u32x4* lds) const {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int t = i * GT + threadIdx.x;
+            const int64_t k = k0 + t / TL::CH;
+            u32x4 x = {0, 0, 0, 0};
+            if (k < k_end) x = gload_u4(row(k) + c[i]);
+            lds[t] = x;
+        }
+    }
+    static __device__ __forceinline__ u32x4 frag(const u32x4* lds, int r0, int s) {
+        return AcrossRows<T, R, GT, int>::frag(lds, r0, s);
+    }
+};
+
 // acc[j][i] += P rows p0(j) .. times Q rows q0 + 32 i .., over the contraction
 // from k0 to k1 (not empty).  One barrier a step: past it, the step's pieces have landed and
 // all waves are done with the buffer that the step after next is sent to.
 template <typename T, typename B, typename P, typename Q, typename P0>
-__device__ __forceinline__ void multiply(const P& p, const Q& q, int64_t k0, int64_t k1, P0 p0, int q0, f32x16 (&acc)[B::MP][B::MQ],
+__device__ __forceinline__ void multiply(P& p, Q& q, int64_t k0, int64_t k1, P0 p0, int q0, f32x16 (&acc)[B::MP][B::MQ],
                                          u32x4* lds, int w) {
     constexpr int SIZE = (B::TP + B::TQ) * KCH;
     const int steps = (int)((k1 - k0 + KT<T> - 1) / KT<T>), full = (int)((k1 - k0) / KT<T>);
     auto send = [&](int i, int b) {
         u32x4* to = lds + b * SIZE;
         if (i < full) {
-            p.issue(k0 + (int64_t)i * KT<T>, to, w);
-            q.issue(k0 + (int64_t)i * KT<T>, to + B::TP * KCH, w);
+            p.issue(k0 + (int64_t)i * KT<T>, i == 0, to, w);
+            q.issue(k0 + (int64_t)i * KT<T>, i == 0, to + B::TP * KCH, w);
         } else if (i < steps) {
             p.partial(k0 + (int64_t)i * KT<T>, to);
             q.partial(k0 + (int64_t)i * KT<T>, to + B::TP * KCH);
@@ -418,8 +475,8 @@ __global__ __launch_bounds__(B::GT) __attribute__((amdgpu_waves_per_eu(SHARE<B>)
     const uint32_t ct = (a.dim + B::TP - 1) / B::TP, tile = xcd_tile(blockIdx.x, gridDim.x);
     const int64_t r0 = (int64_t)(tile / ct) * B::TQ, k_end = 2ll * a.hidden;
     const int c0 = (int)(tile % ct) * B::TP;
-    auto w_row = [&](int64_t k) -> const T* { return (k < a.hidden ? wg.row(k) : wu.row(k - a.hidden)) + c0; };
-    AcrossRows<T, B::TP, B::GT, decltype(w_row)> p = {w_row, k_end, a.dim - c0};
+    StackedRows<T, B::TP, B::GT> p;
+    p.begin({wg.p + c0, wg.stride}, {wu.p + c0, wu.stride}, a.hidden, k_end, a.dim - c0);
     AlongRows<T, B::TQ, B::GT> q;
     q.begin([&](int r) { return d.row(r0 + r < a.n ? r0 + r : a.n - 1); }, k_end);
     f32x16 acc[B::MP][B::MQ] = {};

@@ -69,12 +69,12 @@ template <typename T, int D>
 struct Tile {
     static constexpr int CH = D * (int)sizeof(T) / 16;      // chunks of a row
     static constexpr int EPC = 16 / (int)sizeof(T);         // elements of a chunk
-    static __device__ __forceinline__ int swz(int r) {
+    static __device__ __forceinline__ constexpr int swz(int r) {
         if (CH == 4) return (r >> 2) & 3;
         if (CH == 8) return ((r >> 1) & 1) << 2 | ((r >> 2) & 1) << 1 | ((r >> 3) & 1);
         return (r & 1) << 2 | ((r >> 1) & 1) << 3 | ((r >> 2) & 1) | ((r >> 3) & 1) << 1;
     }
-    static __device__ __forceinline__ int chunk_at(int r, int c) { return r * CH + (c ^ swz(r)); }
+    static __device__ __forceinline__ constexpr int chunk_at(int r, int c) { return r * CH + (c ^ swz(r)); }
 };
 
 // The column operand of a product over dim: chunks 2 s + h of the lane's row.
