@@ -2,9 +2,10 @@
 // way, and its backward with the sums over the rows.
 //
 // Bound by memory: forward x (and the residual) in, y (and the sum) out;
-// backward x, dy (and the stream's gradient) in, dx out.  A row stays in the
-// registers of the G lanes that share it (V pieces of 16 bytes a lane), so its
-// mean, the sum of squares about that mean and the result are one reading.
+// backward x, dy (and the stream's gradient) in, dx out: 5.5 and 5.1 TB/s on
+// 413696 rows of 256 in bf16.  A row stays in the registers of the G lanes that
+// share it (V pieces of 16 bytes a lane), so its mean, the sum of squares about
+// that mean and the result are one reading.
 #include "rse_seqmma.h"
 
 using namespace rse;
@@ -46,18 +47,32 @@ struct Piece {
         }
         return v;
     }
-    // Piece c of a row of dim elements; past the end 0.
+    // Piece c of a row of dim elements, on its way: of a row that ends inside the
+    // piece its last 16 bytes, which `settle` moves to their places (element by
+    // element such a row's loads waited for one another: 132 us for 66 on 100003
+    // rows of 321).
     static __device__ __forceinline__ u32x4 load(const T* row, int c, int dim) {
-        const T* p = row + c * EPC;
-        if ((c + 1) * EPC <= dim) return *(const RSE_GLOBAL u32x4_at2*)p;
+        if (dim >= EPC) return *(const RSE_GLOBAL u32x4_at2*)(row + (c * EPC < dim - EPC ? c * EPC : dim - EPC));
         u32x4 v = {0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < EPC; ++e)
-            if (c * EPC + e < dim) {
-                const T x = *(const RSE_GLOBAL T*)(p + e);
+            if (e < dim) {
+                const T x = *(const RSE_GLOBAL T*)(row + e);
                 if constexpr (sizeof(T) == 4) v[e] = __float_as_uint(x);
                 else v[e / 2] |= (uint32_t)x << (16 * (e & 1));
             }
+        return v;
+    }
+    static __device__ __forceinline__ u32x4 settle(u32x4 v, int c, int dim) {
+        if (dim % EPC == 0 || dim < EPC) return v;
+        int by = c * EPC - (dim - EPC);         // elements
+        by = by > 0 ? by : 0;
+        if (sizeof(T) == 2) {
+            if (by & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+            by >>= 1;
+        }
+        if (by & 1) v = u32x4{v[1], v[2], v[3], 0};
+        if (by & 2) v = u32x4{v[2], v[3], 0, 0};
         return v;
     }
     static __device__ __forceinline__ void store(T* row, int c, int dim, u32x4 v) {
@@ -115,6 +130,12 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(Mat<const T> x, Mat<const T> re
     __shared__ float s_sum[NB / WAVE][2];
     const int g = threadIdx.x % G;
     const float inv = 1.f / (float)dim;
+    float w[V][EPC], bb[V][EPC];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        P::weights(w[v], weight, v * G + g, dim, 1.f);
+        P::weights(bb[v], bias, v * G + g, dim, 0.f);
+    }
     // (of a block's rows, all take part in the barriers of row_sums)
     for (int64_t r0 = (int64_t)blockIdx.x * RB; r0 < n; r0 += (int64_t)gridDim.x * RB) {
         const int64_t r = r0 + threadIdx.x / G;
@@ -133,10 +154,10 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(Mat<const T> x, Mat<const T> re
         float a = 0.f, b = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            P::widen(f[v], raw[v]);
+            P::widen(f[v], P::settle(raw[v], v * G + g, dim));
             if (res.p) {
                 float o[EPC];
-                P::widen(o, more[v]);
+                P::widen(o, P::settle(more[v], v * G + g, dim));
 #pragma unroll
                 for (int e = 0; e < EPC; ++e) f[v][e] += o[e];
                 const u32x4 st = P::narrow(f[v]);           // the stream as it is stored is what is normalised
@@ -163,11 +184,8 @@ __global__ __launch_bounds__(NB) void k_norm_fwd(Mat<const T> x, Mat<const T> re
         for (int v = 0; v < V; ++v) {
             const int c = v * G + g;
             if (live && c * EPC < dim) {
-                float w[EPC], bb[EPC];
-                P::weights(w, weight, c, dim, 1.f);
-                P::weights(bb, bias, c, dim, 0.f);
 #pragma unroll
-                for (int e = 0; e < EPC; ++e) f[v][e] = __builtin_fmaf(f[v][e] * rs, w[e], bb[e]);
+                for (int e = 0; e < EPC; ++e) f[v][e] = __builtin_fmaf(f[v][e] * rs, w[v][e], bb[v][e]);
                 P::store(y.row(r), c, dim, P::narrow(f[v]));
             }
         }
@@ -213,8 +231,8 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(Mat<const T> x, Mat<const T> dy
         float a = 0.f, b = 0.f, xh[V][EPC], dn[V][EPC];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            P::widen(xh[v], xr[v]);
-            P::widen(dn[v], yr[v]);
+            P::widen(xh[v], P::settle(xr[v], v * G + g, dim));
+            P::widen(dn[v], P::settle(yr[v], v * G + g, dim));
 #pragma unroll
             for (int e = 0; e < EPC; ++e) {
                 xh[v][e] = live && (v * G + g) * EPC + e < dim ? (xh[v][e] - mean) * rs : 0.f;
@@ -233,7 +251,7 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(Mat<const T> x, Mat<const T> dy
             const int c = v * G + g;
             if (live && c * EPC < dim) {
                 float o[EPC];
-                P::widen(o, sr[v]);
+                P::widen(o, P::settle(sr[v], c, dim));
 #pragma unroll
                 for (int e = 0; e < EPC; ++e) {
                     const float d = (dn[v][e] - a - xh[v][e] * b) * rs;
@@ -244,38 +262,33 @@ __global__ __launch_bounds__(NB) void k_norm_bwd(Mat<const T> x, Mat<const T> dy
         }
     }
     if (!part) return;
-    // the block's groups of lanes, one after the other
-    extern __shared__ float s_part[];           // [RB][2][V * G * EPC], RB > 1
+    // the block's groups of lanes, one after the other (all of them side by side in
+    // LDS would leave room for two blocks a CU at rows of 4 KB)
+    extern __shared__ float s_part[];           // [2][V * G * EPC], RB > 1
     constexpr int W = V * G * EPC;
     float* mine = part + (int64_t)blockIdx.x * 2 * dim;
-    if constexpr (RB == 1) {
+    const int q = threadIdx.x / G;
+    for (int turn = 0; turn < RB; ++turn) {
+        if (q == turn)
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+            for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int e = 0; e < EPC; ++e) {
-                const int d = (v * G + g) * EPC + e;
-                if (d < dim) {
-                    mine[d] = dw[v][e];
-                    mine[dim + d] = db[v][e];
+                for (int e = 0; e < EPC; ++e) {
+                    const int d = (v * G + g) * EPC + e;
+                    if constexpr (RB > 1) {
+                        if (turn > 0) {
+                            dw[v][e] += s_part[d];
+                            db[v][e] += s_part[W + d];
+                        }
+                        s_part[d] = dw[v][e];
+                        s_part[W + d] = db[v][e];
+                    }
+                    if (turn == RB - 1 && d < dim) {
+                        mine[d] = dw[v][e];
+                        mine[dim + d] = db[v][e];
+                    }
                 }
-            }
-    } else {
-        const int q = threadIdx.x / G;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int e = 0; e < EPC; ++e) {
-                const int d = (v * G + g) * EPC + e;
-                s_part[(2 * q) * W + d] = dw[v][e];
-                s_part[(2 * q + 1) * W + d] = db[v][e];
-            }
-        __syncthreads();
-        for (int t = threadIdx.x; t < 2 * dim; t += NB) {
-            const int which = t >= dim, d = t - which * dim;
-            float s = 0.f;
-            for (int q2 = 0; q2 < RB; ++q2) s += s_part[(2 * q2 + which) * W + d];
-            mine[t] = s;
-        }
+        if constexpr (RB > 1) __syncthreads();
     }
 }
 
@@ -316,28 +329,33 @@ Mat<T> view(const rse_seq_mat* m) {
     return m ? Mat<T>{static_cast<T*>(m->data), m->stride} : Mat<T>{nullptr, 0};
 }
 
-// f(T(), integral_constant<G>, integral_constant<V>): the fewest lanes (8 to
-// a wave) that hold a row in one piece each, then more pieces, then a block.
-template <typename T, typename F>
+// f(T(), integral_constant<G>, integral_constant<V>): the fewest lanes (4 to
+// a wave) that hold a row in one piece each, then more pieces, then a block; the
+// backward, whose sums of four pieces a lane would leave two waves a SIMD, goes from
+// two pieces to a block.  us, four pieces a lane of one wave / a block: forward of 133333
+// rows of 1500 in bf16 200 / 258, of 97656 of 2048 171 / 189; backward 482 / 325 and
+// 332 / 240.
+template <bool BWD, typename T, typename F>
 int by_pieces(int32_t dim, F f) {
     constexpr int EPC = 16 / (int)sizeof(T);
     const int pieces = (dim + EPC - 1) / EPC;
     const auto go = [&](auto g, auto v) { return f(T(), g, v); };
 #define RSE_C(x) std::integral_constant<int, x>()
+    if (pieces <= 4) return go(RSE_C(4), RSE_C(1));
     if (pieces <= 8) return go(RSE_C(8), RSE_C(1));
     if (pieces <= 16) return go(RSE_C(16), RSE_C(1));
     if (pieces <= 32) return go(RSE_C(32), RSE_C(1));
     if (pieces <= 64) return go(RSE_C(64), RSE_C(1));
     if (pieces <= 128) return go(RSE_C(64), RSE_C(2));
-    if (pieces <= 256) return go(RSE_C(64), RSE_C(4));
+    if (pieces <= 256) return go(RSE_C(BWD ? 256 : 64), RSE_C(BWD ? 1 : 4));
     if (pieces <= 512) return go(RSE_C(256), RSE_C(2));
     if (pieces <= 1024) return go(RSE_C(256), RSE_C(4));
     return go(RSE_C(256), RSE_C(8));
 #undef RSE_C
 }
-template <typename F>
+template <bool BWD, typename F>
 int by_norm(int32_t dtype, int32_t dim, F f) {
-    return dtype == RSE_F32 ? by_pieces<float>(dim, f) : by_pieces<uint16_t>(dim, f);
+    return dtype == RSE_F32 ? by_pieces<BWD, float>(dim, f) : by_pieces<BWD, uint16_t>(dim, f);
 }
 
 int norm_args(int64_t n, int32_t dim, int32_t dtype) {
@@ -345,8 +363,14 @@ int norm_args(int64_t n, int32_t dim, int32_t dtype) {
     return dim > RSE_SEQ_MAX_NORM_DIM ? RSE_ERR_UNSUPPORTED : RSE_OK;
 }
 
-// Blocks of the backward: each leaves sums of two rows' length.
-constexpr int64_t BWD_BLOCKS = 1024;
+// Blocks that go through the rows, their weights in registers (a block for
+// every few rows, which loaded them each time, took 383 us for 153 on 413696 rows
+// of 256).  us, forward with 1024 / 1536 / 2048, backward with 512 / 768 / 1024
+// blocks: 413696 rows of 256 bf16 153 / 164 / 172 and 172 / 166 / 174, 24571 of
+// 2048 fp32 72 / 74 / 83 and 133 / 119 / 127, 100003 of 321 bf16 67 / 63 / 73 and
+// 139 / 73 / 65.  A block of the backward leaves sums of two rows' length.
+constexpr int FWD_BLOCKS = 1024;
+constexpr int64_t BWD_BLOCKS = 768;
 template <int G>
 int64_t bwd_blocks(int64_t n) {
     const int64_t b = (n + NB / G - 1) / (NB / G);
@@ -366,10 +390,10 @@ int seq_layer_norm_fwd(const rse_seq_mat* x, const rse_seq_mat* residual, const 
     if (n == 0) return RSE_OK;
     if (!mat_ok(x, dtype) || !out_mat_ok(y, dtype, n, dim)) return RSE_ERR_INVALID_ARG;
     if (residual && (!mat_ok(residual, dtype) || !out_mat_ok(sum, dtype, n, dim))) return RSE_ERR_INVALID_ARG;
-    return by_norm(dtype, dim, [&](auto t, auto g, auto v) {
+    return by_norm<false>(dtype, dim, [&](auto t, auto g, auto v) {
         using T = decltype(t);
         constexpr int G = decltype(g)::value, V = decltype(v)::value;
-        hipLaunchKernelGGL((k_norm_fwd<T, G, V>), dim3(fill_blocks(n, NB / G, 1 << 20)), dim3(NB), 0, as_stream(stream),
+        hipLaunchKernelGGL((k_norm_fwd<T, G, V>), dim3(fill_blocks(n, NB / G, FWD_BLOCKS)), dim3(NB), 0, as_stream(stream),
                            view<const T>(x), view<const T>(residual), view<T>(sum), d_weight, d_bias, eps, n, dim,
                            view<T>(y), d_stats);
         return launch_status();
@@ -380,7 +404,7 @@ int rse_seq_layer_norm_bwd_workspace_size(int64_t n, int32_t dim, int32_t dtype,
     int rc = norm_args(n, dim, dtype);
     if (rc) return rc;
     if (!bytes_out) return RSE_ERR_INVALID_ARG;
-    return by_norm(dtype, dim, [&](auto, auto g, auto) {
+    return by_norm<true>(dtype, dim, [&](auto, auto g, auto) {
         *bytes_out = align_up((size_t)bwd_blocks<decltype(g)::value>(n) * 2 * dim * sizeof(float), 256);
         return RSE_OK;
     });
@@ -399,11 +423,10 @@ int seq_layer_norm_bwd(const rse_seq_mat* x, const rse_seq_mat* dy, const float*
     const bool sums = d_dweight || d_dbias;
     if (sums && n > 0 && ws_bytes < need) return RSE_ERR_WORKSPACE;
     if (sums && n > 0 && (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256)) return RSE_ERR_INVALID_ARG;
-    return by_norm(dtype, dim, [&](auto t, auto g, auto v) {
+    return by_norm<true>(dtype, dim, [&](auto t, auto g, auto v) {
         using T = decltype(t);
         constexpr int G = decltype(g)::value, V = decltype(v)::value;
-        constexpr size_t lds = G < NB ? (size_t)(NB / G) * 2 * V * G * Piece<T>::EPC * sizeof(float) : 0;
-        static_assert(lds <= 64 * 1024, "LDS of the row sums");
+        constexpr size_t lds = G < NB ? (size_t)2 * V * G * Piece<T>::EPC * sizeof(float) : 0;
         const int64_t blocks = bwd_blocks<G>(n);
         float* part = sums ? static_cast<float*>(d_ws) : nullptr;
         if (n > 0)
