@@ -18,6 +18,12 @@ using namespace rse_host;
 
 namespace {
 
+#ifndef FW3
+#define FW3 2
+#endif
+#ifndef FEWT
+#define FEWT 2
+#endif
 constexpr int CW = 4;                   // waves of a block
 
 // What the kernels know of the cache.
@@ -46,35 +52,229 @@ __device__ __forceinline__ int64_t slot_of(const PageArgs& p, int64_t page, int6
     return (page << p.shift) + (e & ((1ll << p.shift) - 1));
 }
 
-// Events that user b has cached before its `count` new ones; -1: idle, or they
-// do not fit (status set).
-__device__ __forceinline__ int64_t cached_of(const PageArgs& p, int64_t b, int count) {
-    const int64_t n = uniform(p.lens[b]);
-    if (n < 0) return -1;
-    if (n > p.max_len - count || (n + count - 1) >> p.shift >= p.max_pages) {
-        set_status(&p.status->status, RSE_ERR_BAD_INPUT);
-        return -1;
-    }
-    return n;
-}
-
-// A block's part of the work.
+// What a block works on: the keys of a part, if the keys are split, with a tile
+// of columns.
 struct Work {
     int64_t b, s;                       // user, its first new event
+    int64_t had;                        // events cached; -1: they do not fit
     int count, tile;                    // new events, tile of them
-    int split, g, h0, nc;               // part of the keys; key/value head, first query head, query heads
+    int g, h0, nc;                      // key/value head, first query head, query heads
+    int split, parts, tiles;            // part of the keys, of how many; the user's tiles
+    int per;                            // tiles of keys of a part
+    int number;                         // of all parts' results; those of a tile stand `tiles` apart
+    __device__ __forceinline__ void heads(const SeqArgs& a, const Columns& cl, uint32_t u) {
+        g = (int)(u / (uint32_t)cl.blocks);
+        const int cb = (int)(u % (uint32_t)cl.blocks);
+        h0 = g * a.group + cb * cl.cols;
+        nc = a.group - cb * cl.cols < cl.cols ? a.group - cb * cl.cols : cl.cols;
+    }
 };
-__device__ __forceinline__ bool find_work(const SeqArgs& a, const TileGrid& grid, const Columns& cl, int splits, int tq, int64_t x,
-                                          Work& w) {
-    w.split = (int)(x % splits);
-    x /= splits;
-    const int n_kv = a.n_heads / a.group, units = n_kv * cl.blocks, u = (int)(x % units);
-    x /= units;
-    w.g = u / cl.blocks;
-    const int cb = u % cl.blocks;
-    w.h0 = w.g * a.group + cb * cl.cols;
-    w.nc = a.group - cb * cl.cols < cl.cols ? a.group - cb * cl.cols : cl.cols;
-    return find_tile(a, grid, x, tq, false, w.b, w.s, w.count, w.tile, u == 0 && w.split == 0);
+
+// The keys split: k_chunk_plan leaves an entry for every block.
+struct alignas(16) Item {
+    int64_t s, had;
+    int32_t b, count, tile, unit;       // b = -1: idle
+    int32_t split, parts, tiles, per;
+    int32_t number, pad[3];
+};
+
+// The blocks of a launch: groups of query heads of all key/value heads
+// (fastest) by tiles of new events (TileGrid's items), or the entries of `list`.
+struct Layout {
+    uint32_t units, items, per_seq;
+    const Item* list;
+};
+
+// What is wrong with a user's events and what they take: its new events'
+// count, or 0, and the number cached, or -1 where they do not fit.
+__device__ __forceinline__ int user_events(const SeqArgs& a, const PageArgs& p, int64_t s, int64_t e, int64_t& had, bool tell) {
+    if (s < 0 || e < s || e > a.n_events || e - s > a.max_len) {
+        if (tell) set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
+        return 0;
+    }
+    const int count = (int)(e - s);
+    if (had < 0) {
+        had = -1;
+    } else if (count > 0 && (had > p.max_len - count || (had + count - 1) >> p.shift >= p.max_pages)) {
+        if (tell) set_status(&p.status->status, RSE_ERR_BAD_INPUT);
+        had = -1;
+    }
+    return count;
+}
+
+// (The block numbers fit 32 bits, as 64-bit divisions took a third of a small
+// call, and the lengths are loaded beside the offsets.)  False if the block has no tile.
+__device__ __forceinline__ bool find_work(const SeqArgs& a, const PageArgs& p, const Columns& cl, const Layout& lo, int tq, Work& w) {
+    if (lo.list) {
+        const Item& i = lo.list[blockIdx.x];
+        if (i.b < 0) return false;
+        w.b = i.b;
+        w.s = i.s;
+        w.had = i.had;
+        w.count = i.count;
+        w.tile = i.tile;
+        w.split = i.split;
+        w.parts = i.parts;
+        w.tiles = i.tiles;
+        w.per = i.per;
+        w.number = i.number;
+        w.heads(a, cl, (uint32_t)i.unit);
+        return true;
+    }
+    const uint32_t item = blockIdx.x / lo.units, u = blockIdx.x - item * lo.units;
+    if (u == 0) {                               // every call checks the offsets once
+        for (int64_t i = (int64_t)item * blockDim.x + threadIdx.x; i < a.batch; i += (int64_t)lo.items * blockDim.x) {
+            const int64_t x = a.offsets[i], y = a.offsets[i + 1];
+            if (x > y || (i == 0 && x != 0) || (i == a.batch - 1 && y != a.n_events)) set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
+        }
+    }
+    int64_t t;
+    if (lo.per_seq) {
+        const uint32_t n = (uint32_t)a.batch, first = item / n;
+        w.b = item - first * n;
+        t = first;
+    } else {
+        w.b = wave_last_le(a.batch, [&](int64_t x) { return a.offsets[x] / tq + x; }, (int64_t)item);
+        t = (int64_t)item - (a.offsets[w.b] / tq + w.b);
+    }
+    const int64_t s = a.offsets[w.b], e = a.offsets[w.b + 1], n = p.lens[w.b];
+    w.s = uniform(s);
+    const int64_t end = uniform(e);
+    w.had = uniform(n);
+    t = uniform(t);
+    w.count = user_events(a, p, w.s, end, w.had, lane_id() == 0);
+    if (t < 0 || t * tq >= w.count) return false;
+    w.tile = (int)t;
+    w.split = 0;
+    w.parts = 1;
+    w.heads(a, cl, u);
+    return true;
+}
+
+// The parts of the keys, by what the lengths on the device are: parts of
+// nearly equal length, as few tiles each as make about `want` parts of them all
+// (what the card runs at a time), but at least `least`, and a user's equal.
+// (Parts of max_len / n keys, with lengths up to it: 304 us for <T>, 8 users of
+// up to 32768 events.)  One block; the lists of a user's units, parts and tiles, tiles
+// fastest, are dealt out so that an XCD gets neighbours, which read the same keys.
+constexpr int PLAN_THREADS = 1024, PLAN_USERS = 2048;
+__device__ __forceinline__ int32_t wave_total(int32_t x) {
+    x += row_ror<8>(x);
+    x += row_ror<4>(x);
+    x += row_ror<2>(x);
+    x += row_ror<1>(x);
+    const u32x2 r = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
+    const uint32_t y = r.x + r.y;
+    const u32x2 h = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+    return (int32_t)(h.x + h.y);
+}
+__device__ __forceinline__ int parts_of(int n, int per) { return n <= per ? 1 : (int)(((uint32_t)n + (uint32_t)per - 1) / (uint32_t)per); }
+__global__ __launch_bounds__(PLAN_THREADS) void k_chunk_plan(SeqArgs a, PageArgs p, int units, int tq, int kt, int least, int want,
+                                                             int bound, Item* list) {
+    constexpr int NW = PLAN_THREADS / WAVE, EACH = PLAN_USERS / PLAN_THREADS;
+    __shared__ float s_work[NW];
+    __shared__ int32_t s_sum[2][NW], s_first[PLAN_USERS];
+    const int t = threadIdx.x, lane = lane_id(), w = t / WAVE;
+    int turn = 0;
+    auto total = [&](int32_t x) {
+        x = wave_total(x);
+        if (lane == 0) s_sum[turn][w] = x;
+        __syncthreads();
+        x = 0;
+#pragma unroll
+        for (int i = 0; i < NW; ++i) x += s_sum[turn][i];
+        turn ^= 1;
+        return x;
+    };
+    int n[EACH], blocks[EACH];                  // tiles of keys; blocks of a part, above `bound` if not possible
+    float work = 0.f;
+    int whole = 0;
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) {
+        const int64_t b = (int64_t)t * EACH + u;
+        n[u] = blocks[u] = 0;
+        if (b < a.batch) {
+            const int64_t s = a.offsets[b], e = a.offsets[b + 1];
+            int64_t had = p.lens[b];
+            if (s > e || (b == 0 && s != 0) || (b == a.batch - 1 && e != a.n_events)) set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
+            const int count = user_events(a, p, s, e, had, true);
+            const int64_t x = (int64_t)units * ((count + (int64_t)tq - 1) / tq);
+            blocks[u] = x > bound ? bound + 1 : (int)x;
+            n[u] = (int)(had < 0 || !count ? 0 : (had + count + kt - 1) / kt);
+        }
+        work += (float)n[u] * (float)blocks[u];
+        whole += blocks[u];
+    }
+#pragma unroll
+    for (int m = 1; m < WAVE; m *= 2) work += __shfl_xor(work, m);
+    if (lane == 0) s_work[w] = work;
+    whole = total(whole);
+    work = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) work += s_work[i];
+    int items = 0, per = 1, mine = 0;
+    if (whole <= bound) {                       // only offsets that are wrong make more
+        // the least length that makes no more than `most` parts is from `per` to high
+        const int most = want > whole + want / 2 ? want : whole + want / 2;
+        int high = (int)(work * (1.f + 1e-5f) / (float)(most - whole)) + 1;
+        per = (int)(work / (float)most);
+        per = per < least ? least : per;
+        while (per < high) {
+            const int mid = (per + high) / 2;
+            mine = 0;
+#pragma unroll
+            for (int u = 0; u < EACH; ++u) mine += blocks[u] * parts_of(n[u], mid);
+            if (total(mine) <= most) high = mid;
+            else per = mid + 1;
+        }
+        mine = 0;
+#pragma unroll
+        for (int u = 0; u < EACH; ++u) mine += blocks[u] * parts_of(n[u], per);
+        items = total(mine);
+        if (items > bound) items = 0;
+    }
+    // where the users begin
+    int sum = mine;
+#pragma unroll
+    for (int m = 1; m < WAVE; m *= 2) {
+        const int x = __shfl_up(sum, m);
+        if (lane >= m) sum += x;
+    }
+    if (lane == WAVE - 1) s_sum[turn][w] = sum;
+    __syncthreads();
+    for (int i = 0; i < w; ++i) sum += s_sum[turn][i];
+    int first = sum - mine;
+#pragma unroll
+    for (int u = 0; u < EACH; ++u) {
+        s_first[t * EACH + u] = first;
+        first += blocks[u] * parts_of(n[u], per);
+    }
+    __syncthreads();
+    const int row = (items + 7) / 8;
+    for (int x = t; x < bound; x += PLAN_THREADS) {
+        const int at = (x & 7) * row + (x >> 3);
+        Item it = {};
+        it.b = -1;
+        if (x >> 3 < row && at < items) {
+            int b = 0;                          // the last user that begins at or before `at`
+            for (int step = PLAN_USERS / 2; step > 0; step /= 2)
+                if (b + step < a.batch && s_first[b + step] <= at) b += step;
+            it.s = a.offsets[b];
+            it.had = p.lens[b];
+            it.b = b;
+            it.count = user_events(a, p, it.s, a.offsets[b + 1], it.had, false);
+            it.tiles = (int)((it.count + (int64_t)tq - 1) / tq);
+            const int keys = it.had < 0 ? 0 : (int)((it.had + it.count + kt - 1) / kt);
+            it.parts = parts_of(keys, per);
+            it.per = (keys + it.parts - 1) / it.parts;
+            const int i = at - s_first[b];
+            it.tile = i % it.tiles;
+            it.split = i / it.tiles % it.parts;
+            it.unit = i / it.tiles / it.parts;
+            it.number = at;
+        }
+        list[x] = it;
+    }
 }
 
 // The tile's new events into their pages, by the threads of the blocks that
@@ -181,12 +381,12 @@ struct Column {
 // tiles of 32 keys in turn, each from memory to its own registers and LDS, so
 // that no wave waits for another; they are joined in LDS at the end.
 template <typename T, int D>
-constexpr int FEW_WAVES = D * sizeof(T) <= 128 ? 2 : 1;
+constexpr int FEW_WAVES = D * sizeof(T) <= 128 ? FW3 : 1;
 
 template <typename T, int D>
 __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(FEW_WAVES<T, D>))) void k_chunk_few(
-    SeqArgs a, PageArgs p, TileGrid grid, Columns cl, Rows<const T> q, Rows<const T> k, Rows<const T> v, T* kp, T* vp, Rows<T> out,
-    int splits, float* part_o, float* part_ml) {
+    SeqArgs a, PageArgs p, Layout lo, Columns cl, Rows<const T> q, Rows<const T> k, Rows<const T> v, T* kp, T* vp, Rows<T> out,
+    float* part_o, float* part_ml) {
     using TL = Tile<T, D>;
     constexpr int CH = TL::CH, ND = D / 32, NC = CH / 2;
     extern __shared__ float s_bias[];           // [cols][bias_stride]
@@ -197,10 +397,18 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(FEW_WAV
     __shared__ float s_ml[CW][2][32];
     const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), half = lane >> 5, col = lane & 31;
     Work wk;
-    if (!find_work(a, grid, cl, splits, cl.events, blockIdx.x, wk)) return;
+    if (!find_work(a, p, cl, lo, cl.events, wk)) return;
     u32x4* tile = s_mem + w * 32 * CH;
     const int first = wk.tile * cl.events, last = first + cl.events < wk.count ? first + cl.events : wk.count;
-    const int64_t had = cached_of(p, wk.b, wk.count);
+    const int64_t had = wk.had;
+    // keys that some column may see: 0 .. end - 1; the wave's tiles t0 + w, + CW, ...
+    const int64_t end = had < 0 ? 0 : had + (a.causal ? last : wk.count);
+    int64_t t0 = 0, t1 = (end + 31) / 32;
+    if (wk.parts > 1) {
+        t0 = (int64_t)wk.split * wk.per;
+        t1 = t0 + wk.per < t1 ? t0 + wk.per : t1;
+        if (t0 >= t1) return;                   // (the join knows)
+    }
     load_bias(s_bias, a, wk);
     s_buckets.load(a.hdr);
     if (had >= 0 && wk.split == 0 && wk.h0 == wk.g * a.group) store_events<T, D>(a, p, wk, had, first, last, k, v, kp, vp);
@@ -210,9 +418,6 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(FEW_WAV
     lb.load(a.hdr, s_bias + (c.head - wk.h0) * bias_stride(a.n_bounds), a.n_bounds);
     __syncthreads();
 
-    // keys that some column may see: 0 .. end - 1; the wave's tiles t0 + w, + CW, ...
-    const int64_t end = had < 0 ? 0 : had + (a.causal ? last : wk.count);
-    const int64_t nt = (end + 31) / 32, t0 = nt * wk.split / splits, t1 = nt * (wk.split + 1) / splits;
     const int64_t row_elems = (int64_t)(a.n_heads / a.group) * D;
     const float c2 = fabsf(a.scale) * LOG2E;
     auto page_of = [&](int64_t t) -> int64_t {
@@ -304,10 +509,10 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(FEW_WAV
         }
         const int64_t ev = wk.s + first + cc / wk.nc;
         const int head = wk.h0 + cc % wk.nc;
-        if (splits == 1) {
+        if (wk.parts == 1) {
             from_f32(out.at(ev, head)[d], L == 0.f ? 0.f : O / L);
         } else {
-            const int64_t at = (ev * a.n_heads + head) * splits + wk.split;
+            const int64_t at = (int64_t)wk.number * 32 + cc;
             part_o[at * D + d] = O;
             if (d == 0) {
                 part_ml[2 * at] = M;
@@ -318,33 +523,47 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(FEW_WAV
 }
 
 // Many columns: every wave has a tile of columns of its own, and the block
-// stages tiles of KT keys for them in LDS, the next one's loads in flight
-// meanwhile; slots are looked up two tiles ahead.
+// brings tiles of KT keys to LDS for them, NST - 1 tiles ahead and without
+// registers in between (with the next tile's rows in registers waves waited 57 % of
+// their time: 345 us for <T> on 8 users of up to 32768 events and 128 new ones).
 template <typename T, int D>
 struct Many {
-    static constexpr int RB = D * (int)sizeof(T), KT = RB <= 256 ? 64 : 32, NS = KT / 32;
-    static constexpr int CH = Tile<T, D>::CH, NT = CW * WAVE, PER = KT * CH / NT, STEP = NT / CH;
+    static constexpr int RB = D * (int)sizeof(T), KT = RB == 64 ? 64 : 32, NST = RB <= 256 ? 4 : 3;
+    static constexpr int CH = Tile<T, D>::CH, NT = CW * WAVE, PER = KT * CH / NT;
     static constexpr int WAVES = RB <= 256 ? 2 : 1;         // that share a SIMD
+    static constexpr int PAGES = 512;                       // of the table in LDS at a time
 };
+
+// What rows past the end and of pages out of the pool are read from.
+__device__ u32x4 g_no_row[32];
 
 template <typename T, int D>
 __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(Many<T, D>::WAVES))) void k_chunk_many(
-    SeqArgs a, PageArgs p, TileGrid grid, Columns cl, Rows<const T> q, Rows<const T> k, Rows<const T> v, T* kp, T* vp, Rows<T> out,
-    int splits, float* part_o, float* part_ml) {
+    SeqArgs a, PageArgs p, Layout lo, Columns cl, Rows<const T> q, Rows<const T> k, Rows<const T> v, T* kp, T* vp, Rows<T> out,
+    float* part_o, float* part_ml) {
     using TL = Tile<T, D>;
     using MY = Many<T, D>;
-    constexpr int CH = MY::CH, KT = MY::KT, NS = MY::NS, PER = MY::PER, STEP = MY::STEP, ND = D / 32;
+    constexpr int CH = MY::CH, KT = MY::KT, PER = MY::PER, NST = MY::NST, ND = D / 32, SENT = 2 * PER + 1;
     extern __shared__ float s_bias[];           // [cols][bias_stride]
-    __shared__ u32x4 s_k[2][KT * CH], s_v[2][KT * CH];
-    __shared__ KeySide<KT> s_side[2];
-    __shared__ int64_t s_slot[2][KT];           // of a tile's keys: slot, -1: hidden, -2 - i: new event i
+    __shared__ u32x4 s_k[NST][KT * CH], s_v[NST][KT * CH];
+    alignas(16) __shared__ int32_t s_pos[CW][NST][KT];      // (read by 16 bytes; each wave brings its own)
+    __shared__ int32_t s_page[MY::PAGES];       // -1: out of the pool
+    __shared__ uint64_t s_seen[CW][NST];        // bit per key that may be seen
     __shared__ LdsBuckets s_buckets;
     __shared__ u32x4 s_pairs[CW][WAVE];
     const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), half = lane >> 5, t = threadIdx.x;
     Work wk;
-    if (!find_work(a, grid, cl, splits, CW * cl.events, blockIdx.x, wk)) return;
+    if (!find_work(a, p, cl, lo, CW * cl.events, wk)) return;
     const int begin = wk.tile * CW * cl.events, past = begin + CW * cl.events < wk.count ? begin + CW * cl.events : wk.count;
-    const int64_t had = cached_of(p, wk.b, wk.count);
+    const int64_t had = wk.had;
+    // keys that some column of the block may see: 0 .. end - 1; its tiles of KT: t0 .. t1 - 1
+    const int64_t end = had < 0 ? 0 : had + (a.causal ? past : wk.count);
+    int64_t t0 = 0, t1 = (end + KT - 1) / KT;
+    if (wk.parts > 1) {
+        t0 = (int64_t)wk.split * wk.per;
+        t1 = t0 + wk.per < t1 ? t0 + wk.per : t1;
+        if (t0 >= t1) return;                   // (the join knows)
+    }
     load_bias(s_bias, a, wk);
     s_buckets.load(a.hdr);
     if (had >= 0 && wk.split == 0 && wk.h0 == wk.g * a.group) store_events<T, D>(a, p, wk, had, begin, past, k, v, kp, vp);
@@ -353,125 +572,147 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(Many<T,
     c.load(a, cl, wk, first, q);
     LaneBuckets lb;
     lb.load(a.hdr, s_bias + (c.head - wk.h0) * bias_stride(a.n_bounds), a.n_bounds);
-
-    // the block's tiles of keys, and the end of those that the wave's columns see
-    const int64_t end = had < 0 ? 0 : had + (a.causal ? past : wk.count);
-    const int64_t nt = (end + KT - 1) / KT, t0 = nt * wk.split / splits, t1 = nt * (wk.split + 1) / splits;
-    const int my_last = first + cl.events < wk.count ? first + cl.events : wk.count;
-    const int64_t my_end = had < 0 || first >= wk.count ? 0 : had + (a.causal ? my_last : wk.count);
     const int64_t row_elems = (int64_t)(a.n_heads / a.group) * D;
     const float c2 = fabsf(a.scale) * LOG2E;
 
-    // thread t < KT: key t of a tile, its page one step before its slot
-    int64_t page = 0, slot = -1;
-    int32_t key_pos = 0;
-    auto page_of = [&](int64_t tile) {
-        const int64_t e = tile * KT + t;
-        page = t < KT && tile < t1 && e < had ? (int64_t)p.table[wk.b * p.max_pages + (e >> p.shift)] : 0;
+    // the part of the page table for keys from `from` on; all threads come here
+    int64_t window = 0, window_end = 0;         // keys
+    auto load_pages = [&](int64_t from) {
+        __syncthreads();                        // the last part has been used
+        window = from >> p.shift << p.shift;
+        window_end = window + ((int64_t)MY::PAGES << p.shift);
+        for (int i = t; i < MY::PAGES; i += MY::NT) {
+            const int64_t e = window + ((int64_t)i << p.shift);
+            int32_t page = 0;
+            if (e < had && e < t1 * KT) {
+                page = p.table[wk.b * p.max_pages + (e >> p.shift)];
+                if (page < 0 || page >= p.n_pages) {
+                    set_status(&p.status->status, RSE_ERR_BAD_INPUT);
+                    page = -1;
+                }
+            }
+            s_page[i] = page;
+        }
+        __syncthreads();
     };
-    auto find_slot = [&](int64_t tile) {        // and the load of its time
-        if (t >= KT) return;
-        const int64_t e = tile * KT + t;
-        slot = -1;
-        const int32_t* at = a.pos + wk.s;
-        if (tile < t1 && e < end) {
+    int64_t off_at[PER];                        // elements from a tile's first row to the thread's pieces
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int at = i * MY::NT + t, row = at / CH;
+        off_at[i] = row * row_elems + ((at % CH) ^ TL::swz(row)) * TL::EPC;
+    }
+    const bool in_page = p.shift >= (KT == 64 ? 6 : 5);         // a tile lies in one page
+    auto send = [&](int64_t tile, int st) {
+        if (tile * KT >= window_end) load_pages(tile * KT);
+        const int64_t k0 = tile * KT;
+        if (in_page && k0 + KT <= had) {
+            const int64_t page = uniform((int64_t)s_page[(k0 - window) >> p.shift]);
+            if (page >= 0) {
+                const int64_t first_slot = (page << p.shift) + (k0 & ((1ll << p.shift) - 1));
+                const T *kt = kp + first_slot * row_elems + wk.g * D, *vt = vp + first_slot * row_elems + wk.g * D;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    to_lds(kt + off_at[i], &s_k[st][i * MY::NT + w * WAVE]);
+                    to_lds(vt + off_at[i], &s_v[st][i * MY::NT + w * WAVE]);
+                }
+                if (lane < KT) to_lds4(p.tp + first_slot + lane, s_pos[w][st]);
+                if (lane == 0) s_seen[w][st] = KT == 64 ? ~0ull : 0xFFFFFFFFull;
+                return;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int at = i * MY::NT + t, row = at / CH, off = ((at % CH) ^ TL::swz(row)) * TL::EPC;
+            const int64_t e = k0 + row;
+            const T *kr = reinterpret_cast<const T*>(g_no_row), *vr = kr;
             if (e < had) {
-                slot = slot_of(p, page, e);
-                if (slot >= 0) at = p.tp + slot;
-            } else {
-                slot = -2 - (e - had);
-                at += e - had;
+                const int64_t page = s_page[(e - window) >> p.shift];
+                if (page >= 0) {
+                    const int64_t s = ((page << p.shift) + (e & ((1ll << p.shift) - 1))) * row_elems + wk.g * D;
+                    kr = kp + s;
+                    vr = vp + s;
+                }
+            } else if (e < end) {
+                kr = k.at(wk.s + (e - had), wk.g);
+                vr = v.at(wk.s + (e - had), wk.g);
             }
+            to_lds(kr + off, &s_k[st][i * MY::NT + w * WAVE]);
+            to_lds(vr + off, &s_v[st][i * MY::NT + w * WAVE]);
         }
-        key_pos = *at;
-        s_slot[tile & 1][t] = slot;
-    };
-    u32x4 x[PER], y[PER];
-    uint32_t hid = 0;                           // bit i: the thread's row i is hidden
-    auto load_rows = [&](int64_t tile) {
-        const int row = t / CH, ch = t % CH;
-        hid = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int64_t s = s_slot[tile & 1][row + i * STEP];
-            if (s == -1) hid |= 1u << i;
-            const int64_t ev = wk.s + (s <= -2 ? -2 - s : 0);
-            const T* kr = s >= 0 ? kp + s * row_elems + wk.g * D : k.at(ev, wk.g);
-            const T* vr = s >= 0 ? vp + s * row_elems + wk.g * D : v.at(ev, wk.g);
-            x[i] = gload_u4(kr + ch * TL::EPC);
-            y[i] = gload_u4(vr + ch * TL::EPC);
+        const int64_t e = k0 + lane;
+        const int32_t* at = a.pos + wk.s;
+        bool see = lane < KT && e < end;
+        if (see && e < had) {
+            const int64_t page = s_page[(e - window) >> p.shift];
+            see = page >= 0;
+            if (see) at = p.tp + (page << p.shift) + (e & ((1ll << p.shift) - 1));
+        } else if (see) {
+            at += e - had;
         }
-    };
-    auto store_rows = [&](int b) {
-        const int row = t / CH, ch = t % CH;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int at = TL::chunk_at(row + i * STEP, ch);
-            const bool z = (hid >> i) & 1;
-            s_k[b][at] = z ? u32x4{0, 0, 0, 0} : x[i];
-            s_v[b][at] = z ? u32x4{0, 0, 0, 0} : y[i];
-        }
-    };
-    auto store_side = [&](KeySide<KT>& ks) {    // of the key whose slot was found last
-        if (t >= WAVE) return;
-        const bool see = slot != -1;
-        const int32_t lo = half_min(key_pos), hi = half_max(key_pos);
-        const uint64_t hm = __ballot(t < KT && !see);
-        if (t < KT) {
-            ks.mask[t] = see ? 0.f : -INFINITY;
-            ks.pos[t] = key_pos;
-            if ((t & 31) == 0) {
-                ks.range[t / 32][0] = lo;
-                ks.range[t / 32][1] = hi;
-                ks.hidden[t / 32] = (uint32_t)(hm >> t);
-            }
-        }
+        if (lane < KT) to_lds4(at, s_pos[w][st]);
+        const uint64_t seen = __ballot(see);
+        if (lane == 0) s_seen[w][st] = seen;
     };
     Online<T, D> sm;
     sm.clear();
-    if (t0 < t1) {
-        page_of(t0);
-        find_slot(t0);
-        page_of(t0 + 1);
-    }
-    __syncthreads();
-    if (t0 < t1) load_rows(t0);
-    for (int64_t tile = t0; tile < t1; ++tile) {
-        const int b = (int)(tile - t0) & 1;
-        store_rows(b);
-        store_side(s_side[b]);
-        find_slot(tile + 1);
-        __syncthreads();
-        page_of(tile + 2);
-        if (tile + 1 < t1) load_rows(tile + 1);
-        const KeySide<KT>& ks = s_side[b];
+    if (t0 < t1) load_pages(t0 * KT);
+    else __syncthreads();
 #pragma unroll 1
-        for (int u = 0; u < NS; ++u) {
+    for (int i = 0; i < NST - 1; ++i)
+        if (t0 + i < t1) send(t0 + i, i);
+    none_left();
+    int st = 0;
+    auto next = [&](int64_t tile) {
+        // the tiles behind this one stay in flight
+        if (tile + NST - 2 < t1) loads_left<(NST - 2) * SENT>();
+        else loads_left<0>();
+        lds_barrier();                          // the tile has landed; all are done with the last one's place
+        if (tile + NST - 1 < t1) send(tile + NST - 1, st == 0 ? NST - 1 : st - 1);
+    };
+    if (first >= wk.count) {                    // a wave without columns (a condition in the loop below had the sums
+        for (int64_t tile = t0; tile < t1; ++tile) {        // copied from registers to registers, and spilled)
+            next(tile);
+            st = st == NST - 1 ? 0 : st + 1;
+        }
+        return;
+    }
+    for (int64_t tile = t0; tile < t1; ++tile) {
+        next(tile);
+#pragma unroll
+        for (int u = 0; u < KT / 32; ++u) {
             const int64_t k1 = tile * KT + 32 * u;
-            if (k1 >= my_end) break;
+            const int32_t* pos = s_pos[w][st] + 32 * u;
+            const int32_t rp = pos[lane & 31];
+            const int32_t range[2] = {half_min(rp), half_max(rp)};
             TileBuckets<true> tb;
-            tb.set(lb, c.lo, c.hi, ks.range[u]);
-            f32x16 z = mma_rows<T, D>(s_k[b], 32 * u, c.q, f32x16{});
+            tb.set(lb, c.lo, c.hi, range);
+            f32x16 z = mma_rows<T, D>(s_k[st], 32 * u, c.q, f32x16{});
             if (tb.many) {
-                tb.find_pairs(s_pairs[w], 0, 1, s_buckets, a.n_bounds, a.cells, ks.pos + 32 * u, c.pos);
+                tb.find_pairs(s_pairs[w], 0, 1, s_buckets, a.n_bounds, a.cells, pos, c.pos);
                 wave_lds_sync();
             }
-            z = tb.logits(z, c2, -sm.m, lb, s_pairs[w], lb.bias, ks.pos + 32 * u, c.pos);
-            hide(z, ks.hidden[u], ks.mask + 32 * u);
+            z = tb.logits(z, c2, -sm.m, lb, s_pairs[w], lb.bias, pos, c.pos);
+            const uint32_t seen = __builtin_amdgcn_readfirstlane((uint32_t)(s_seen[w][st] >> (32 * u)));
+            if (seen != ~0u) {
+                const uint32_t bits = seen >> (4 * half);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) z[r] = (bits >> tile_row(r, 0)) & 1 ? z[r] : -INFINITY;
+            }
             if (a.causal && k1 + 31 > had + first) hide_after(z, (int)(had - k1) + c.event - 4 * half);
-            sm.add(z, s_v[b], 32 * u);
+            sm.add(z, s_v[st], 32 * u);
         }
+        st = st == NST - 1 ? 0 : st + 1;
     }
     sm.l += other_half(sm.l);
     if (!c.live) return;
     const int64_t ev = wk.s + c.event;
-    if (splits == 1) {
+    if (wk.parts == 1) {
         const float inv = sm.l == 0.f ? 0.f : 1.f / sm.l;
         T* dst = out.at(ev, c.head);
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) store_column(dst + 32 * dt, sm.o[dt], inv);
     } else {
-        const int64_t at = (ev * a.n_heads + c.head) * splits + wk.split;
+        const int64_t at = ((int64_t)wk.number * CW + w) * 32 + (lane & 31);
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) store_column(part_o + at * D + 32 * dt, sm.o[dt], 1.f);
         if (half == 0) {
@@ -481,77 +722,92 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(Many<T,
     }
 }
 
-// Joins the parts: a block for the columns of one tile, D / 4 threads a column.
+// Joins the parts: blocks (x, y) take the columns of a tile, D / 4 threads a
+// column.  kt, waves: of the kernel that left the parts.
 constexpr int JT = 256;
 template <typename T, int D>
-__global__ __launch_bounds__(JT) void k_chunk_join(SeqArgs a, TileGrid grid, Columns cl, int tq, int splits, const float* part_o,
+__global__ __launch_bounds__(JT) void k_chunk_join(SeqArgs a, PageArgs p, Layout lo, Columns cl, int kt, int waves, const float* part_o,
                                                    const float* part_ml, Rows<T> out) {
     constexpr int LR = D / 4;
     Work wk;
-    if (!find_work(a, grid, cl, 1, tq, blockIdx.x, wk)) return;
-    const int first = wk.tile * tq, last = first + tq < wk.count ? first + tq : wk.count;
-    for (int c = threadIdx.x / LR; c < (last - first) * wk.nc; c += JT / LR) {
-        const int64_t ev = wk.s + first + c / wk.nc;
-        const int head = wk.h0 + c % wk.nc, d = 4 * (threadIdx.x % LR);
-        const int64_t at = (ev * a.n_heads + head) * splits;
-        float M = -INFINITY, L = 0.f;
-        for (int s = 0; s < splits; ++s) M = fmaxf(M, part_ml[2 * (at + s)]);
-        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    if (!find_work(a, p, cl, lo, waves * cl.events, wk)) return;
+    if (wk.split != 0 || wk.parts == 1) return;
+    const int col = (int)blockIdx.y * (JT / LR) + threadIdx.x / LR, d = 4 * (threadIdx.x % LR), in = col & 31;
+    const int begin = wk.tile * waves * cl.events, past = begin + waves * cl.events < wk.count ? begin + waves * cl.events : wk.count;
+    const int event = begin + (col >> 5) * cl.events + in / wk.nc, head = wk.h0 + in % wk.nc;
+    if (in >= cl.events * wk.nc || event >= wk.count) return;
+    // parts with keys that some of the tile's columns see
+    const int64_t end = wk.had + (a.causal ? past : wk.count);
+    const int parts = (int)(((end + kt - 1) / kt + wk.per - 1) / wk.per);
+    const int64_t at = (int64_t)wk.number * 32 * waves + col, step = (int64_t)wk.tiles * 32 * waves;
+    float M = -INFINITY, L = 0.f;
 #pragma unroll 4
-        for (int s = 0; s < splits; ++s) {
-            const float r = part_weight(part_ml[2 * (at + s)], M);
-            L = __builtin_fmaf(part_ml[2 * (at + s) + 1], r, L);
-            const f32x4 x = gload_f4(part_o + (at + s) * D + d);
+    for (int s = 0; s < parts; ++s) M = fmaxf(M, part_ml[2 * (at + s * step)]);
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < parts; ++s) {
+        const float r = part_weight(part_ml[2 * (at + s * step)], M);
+        L = __builtin_fmaf(part_ml[2 * (at + s * step) + 1], r, L);
+        const f32x4 x = gload_f4(part_o + (at + s * step) * D + d);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], r, o[i]);
-        }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] *= inv;
-        store_four(out.at(ev, head) + d, o);
+        for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], r, o[i]);
     }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] *= inv;
+    store_four(out.at(wk.s + event, head) + d, o);
 }
 
 // ------------------------------------------------------------------ host --
-// Blocks in all where histories are long enough, and the parts of one: of 256
-// keys at least, at most 64.
-constexpr int64_t CHUNK_BLOCKS = 1024;
-
+#ifndef FWANT
+#define FWANT 512
+#endif
+#ifndef FROOM
+#define FROOM 512
+#endif
+#ifndef MWANT
+#define MWANT 1
+#endif
 struct ChunkPlan {
     Columns cl;
     bool few;
-    int tq, splits;
+    int tq, kt;
     TileGrid grid;
-    int64_t units;              // blocks of one part
+    int64_t units;
+    int want, least;                    // want > 0: the keys are split
+    int64_t whole() const { return grid.items * units; }
+    int64_t blocks() const { return whole() + want; }
 };
 ChunkPlan chunk_plan(const rse_seqattn* at, int64_t n_events, int64_t batch, int64_t max_new, int64_t max_len) {
     ChunkPlan p;
-    const int group = at->n_heads / at->n_kv_heads;
+    const int group = at->n_heads / at->n_kv_heads, row = at->dim * (at->dtype == RSE_BF16 ? 2 : 4);
     p.cl.cols = group < 32 ? group : 32;
     p.cl.blocks = (group + p.cl.cols - 1) / p.cl.cols;
     p.cl.events = 32 / p.cl.cols;
-    p.few = max_new <= p.cl.events;
+    p.few = max_new <= FEWT * p.cl.events;
     p.tq = p.few ? p.cl.events : CW * p.cl.events;
+    p.kt = p.few || row > 64 ? 32 : 64;
     p.grid = tile_grid(n_events, batch, max_new, p.tq);
-    p.units = p.grid.items * at->n_kv_heads * p.cl.blocks;
-    int64_t s = p.units > 0 ? (CHUNK_BLOCKS + p.units - 1) / p.units : 1;
-    const int64_t most = max_len / 256;
-    if (s > most) s = most;
-    p.splits = (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
+    p.units = (int64_t)at->n_kv_heads * p.cl.blocks;
+    const int want = p.few ? FWANT : (row > 256 ? 256 : 512) * MWANT;
+    p.least = 256 / p.kt;
+    p.want = max_len >= 512 && p.whole() < (p.few ? FROOM : PLAN_USERS) ? want : 0;
     return p;
 }
 
 struct ChunkWs {
     float* o;
     float* ml;
+    Item* list;
     size_t bytes;
 };
-ChunkWs chunk_ws(const rse_seqattn* at, int64_t n_events, const ChunkPlan& p, void* base) {
+ChunkWs chunk_ws(const rse_seqattn* at, const ChunkPlan& p, void* base) {
     Carver c(base);
-    const size_t n = p.splits > 1 ? (size_t)n_events * at->n_heads * p.splits : 0;
+    const size_t n = p.want ? (size_t)p.blocks() * 32 * (p.few ? 1 : CW) : 0;
     ChunkWs w;
     w.o = c.take<float>(n * at->dim);
     w.ml = c.take<float>(2 * n);
+    w.list = c.take<Item>(p.want ? (size_t)p.blocks() : 0);
     w.bytes = c.size();
     return w;
 }
@@ -559,19 +815,24 @@ ChunkWs chunk_ws(const rse_seqattn* at, int64_t n_events, const ChunkPlan& p, vo
 template <typename T, int D>
 int run_chunk(const rse_seqcache* c, const SeqArgs& a, const PageArgs& pg, const ChunkPlan& p, const ChunkWs& ws,
               const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v, const rse_seq_rows* out, hipStream_t s) {
-    if (p.units * p.splits > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+    if (p.blocks() > INT32_MAX) return RSE_ERR_UNSUPPORTED;
     const size_t lds = (size_t)p.cl.cols * ((a.n_bounds + 1) | 1) * sizeof(float);
-    const dim3 grid((unsigned)(p.units * p.splits)), block(CW * WAVE);
+    const Layout lo = {(uint32_t)p.units, (uint32_t)p.grid.items, (uint32_t)p.grid.per_seq, p.want ? ws.list : nullptr};
+    const dim3 grid((unsigned)p.blocks()), block(CW * WAVE);
+    if (p.want)
+        hipLaunchKernelGGL(k_chunk_plan, dim3(1), dim3(PLAN_THREADS), 0, s, a, pg, (int)p.units, p.tq, p.kt, p.least, p.want,
+                           (int)p.blocks(), ws.list);
     const auto run = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, block, lds, s, a, pg, p.grid, p.cl, rows_view<const T>(q), rows_view<const T>(k),
-                           rows_view<const T>(v), static_cast<T*>(c->k), static_cast<T*>(c->v), rows_view<T>(out), p.splits, ws.o,
-                           ws.ml);
+        hipLaunchKernelGGL(kernel, grid, block, lds, s, a, pg, lo, p.cl, rows_view<const T>(q), rows_view<const T>(k),
+                           rows_view<const T>(v), static_cast<T*>(c->k), static_cast<T*>(c->v), rows_view<T>(out), ws.o, ws.ml);
     };
     if (p.few) run(k_chunk_few<T, D>);
     else run(k_chunk_many<T, D>);
-    if (p.splits > 1)
-        hipLaunchKernelGGL((k_chunk_join<T, D>), dim3((unsigned)p.units), dim3(JT), 0, s, a, p.grid, p.cl, p.tq, p.splits, ws.o,
-                           ws.ml, rows_view<T>(out));
+    if (p.want) {
+        const int waves = p.few ? 1 : CW;
+        hipLaunchKernelGGL((k_chunk_join<T, D>), dim3(grid.x, (unsigned)(waves * 32 * (D / 4) / JT)), dim3(JT), 0, s, a, pg, lo, p.cl,
+                           p.kt, waves, ws.o, ws.ml, rows_view<T>(out));
+    }
     return launch_status();
 }
 
@@ -582,7 +843,7 @@ extern "C" {
 int rse_seqattn_chunk_workspace_size(const rse_seqattn* attn, int64_t n_events, int64_t batch, int64_t max_new, int64_t max_len,
                                      size_t* bytes_out) {
     if (!attn || !bytes_out || n_events < 0 || batch < 0 || max_new < 0 || max_len < 0) return RSE_ERR_INVALID_ARG;
-    *bytes_out = n_events ? chunk_ws(attn, n_events, chunk_plan(attn, n_events, batch, max_new, max_len), nullptr).bytes : 0;
+    *bytes_out = n_events ? chunk_ws(attn, chunk_plan(attn, n_events, batch, max_new, max_len), nullptr).bytes : 0;
     return RSE_OK;
 }
 
@@ -601,7 +862,7 @@ int seq_attention_chunk(const rse_seqattn* attn, rse_seqcache* cache, const rse_
         if (!rows_ok(r, attn->dtype)) return RSE_ERR_INVALID_ARG;
     if (!out_rows_ok(out, attn->dtype, batch->n_events, attn->n_heads, attn->dim)) return RSE_ERR_INVALID_ARG;
     const ChunkPlan plan = chunk_plan(attn, batch->n_events, batch->batch, batch->max_len, max_len);
-    const ChunkWs ws = chunk_ws(attn, batch->n_events, plan, d_ws);
+    const ChunkWs ws = chunk_ws(attn, plan, d_ws);
     if (ws_bytes < ws.bytes) return RSE_ERR_WORKSPACE;
     if (ws.bytes && (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256)) return RSE_ERR_INVALID_ARG;
     const SeqArgs a = seq_args(attn, batch);

@@ -42,19 +42,6 @@ struct Block {
 };
 
 // ------------------------------------------------------------- operands --
-// 16 bytes from memory straight to LDS: lane l's piece lands at lds + l.  In
-// assembly, so that the compiler does not make every read of LDS wait for the
-// loads in flight to other buffers; the waits are multiply's.  Nothing is
-// returned to registers, and the compiler keeps nothing in m0.
-__device__ __forceinline__ void to_lds(const void* p, u32x4* lds) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(RSE_LDS void*)lds);
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(at) : "memory");
-}
-// At most N of the wave's loads are still in flight.
-template <int N>
-__device__ __forceinline__ void loads_left() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
 // A block's operand of R rows (of the result) by KT<T> of the contraction, on
 // its way from memory to LDS, and read from there as matrix operands: 16 bytes a
 // lane, of row `lane % 32` the elements 8 s' + 4 (lane / 32) .. of step s in

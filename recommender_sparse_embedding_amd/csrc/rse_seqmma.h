@@ -223,6 +223,30 @@ __device__ __forceinline__ void store_four(uint16_t* p, f32x4 x) {
     *(RSE_GLOBAL u32x2*)p = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
 }
 
+// ------------------------------------------------------------ async copies --
+// 16 bytes (or 4) from memory straight to LDS: lane l's piece lands 16 l (4 l)
+// bytes past `lds`, the same of all lanes.  In assembly, so that the compiler does not make every read of
+// LDS wait for the loads in flight to other buffers; the waits are the
+// caller's.  Nothing is returned to registers, and the compiler keeps nothing in
+// m0.
+__device__ __forceinline__ uint32_t lds_address(const void* lds) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(RSE_LDS const void*)lds);
+}
+__device__ __forceinline__ void to_lds(const void* p, const void* lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds_address(lds)) : "memory");
+}
+__device__ __forceinline__ void to_lds4(const void* p, const void* lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(lds_address(lds)) : "memory");
+}
+// At most N of the wave's memory operations are still in flight.  The compiler
+// does not see this wait: for what it loads to registers itself it adds its own
+// where the value is first used, be it in a loop, unless none_left, which it
+// sees, comes before.
+template <int N>
+__device__ __forceinline__ void loads_left() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void none_left() { __builtin_amdgcn_s_waitcnt(0x0F70); }        // vmcnt(0), the others free
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // ---------------------------------------------------------------- buckets --
 // A wave's copy of one head's boundaries and bias (lane l: entries l and
 // 64 + l): a wave-uniform distance finds its bucket by two comparisons and
