@@ -18,12 +18,6 @@ using namespace rse_host;
 
 namespace {
 
-#ifndef FW3
-#define FW3 2
-#endif
-#ifndef FEWT
-#define FEWT 2
-#endif
 constexpr int CW = 4;                   // waves of a block
 
 // What the kernels know of the cache.
@@ -107,26 +101,29 @@ __device__ __forceinline__ int user_events(const SeqArgs& a, const PageArgs& p, 
 __device__ __forceinline__ bool find_work(const SeqArgs& a, const PageArgs& p, const Columns& cl, const Layout& lo, int tq, Work& w) {
     if (lo.list) {
         const Item& i = lo.list[blockIdx.x];
-        if (i.b < 0) return false;
-        w.b = i.b;
-        w.s = i.s;
-        w.had = i.had;
-        w.count = i.count;
-        w.tile = i.tile;
-        w.split = i.split;
-        w.parts = i.parts;
-        w.tiles = i.tiles;
-        w.per = i.per;
-        w.number = i.number;
-        w.heads(a, cl, (uint32_t)i.unit);
+        w.b = uniform(i.b);
+        if (w.b < 0) return false;
+        w.s = uniform(i.s);
+        w.had = uniform(i.had);
+        w.count = uniform(i.count);
+        w.tile = uniform(i.tile);
+        w.split = uniform(i.split);
+        w.parts = uniform(i.parts);
+        w.tiles = uniform(i.tiles);
+        w.per = uniform(i.per);
+        w.number = uniform(i.number);
+        w.heads(a, cl, (uint32_t)uniform(i.unit));
         return true;
     }
     const uint32_t item = blockIdx.x / lo.units, u = blockIdx.x - item * lo.units;
-    if (u == 0) {                               // every call checks the offsets once
-        for (int64_t i = (int64_t)item * blockDim.x + threadIdx.x; i < a.batch; i += (int64_t)lo.items * blockDim.x) {
-            const int64_t x = a.offsets[i], y = a.offsets[i + 1];
-            if (x > y || (i == 0 && x != 0) || (i == a.batch - 1 && y != a.n_events)) set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
-        }
+    // every call checks the offsets once (there are no fewer items than users);
+    // what is loaded for it arrives with what the block itself needs
+    const int64_t i = (int64_t)item * blockDim.x + threadIdx.x;
+    const bool check = u == 0 && i < a.batch;
+    int64_t x = 0, y = 0;
+    if (check) {
+        x = a.offsets[i];
+        y = a.offsets[i + 1];
     }
     int64_t t;
     if (lo.per_seq) {
@@ -142,6 +139,8 @@ __device__ __forceinline__ bool find_work(const SeqArgs& a, const PageArgs& p, c
     const int64_t end = uniform(e);
     w.had = uniform(n);
     t = uniform(t);
+    if (check && (x > y || (i == 0 && x != 0) || (i == a.batch - 1 && y != a.n_events)))
+        set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
     w.count = user_events(a, p, w.s, end, w.had, lane_id() == 0);
     if (t < 0 || t * tq >= w.count) return false;
     w.tile = (int)t;
@@ -154,7 +153,7 @@ __device__ __forceinline__ bool find_work(const SeqArgs& a, const PageArgs& p, c
 // The parts of the keys, by what the lengths on the device are: parts of
 // nearly equal length, as few tiles each as make about `want` parts of them all
 // (what the card runs at a time), but at least `least`, and a user's equal.
-// (Parts of max_len / n keys, with lengths up to it: 304 us for <T>, 8 users of
+// (Parts of max_len / 32 keys, with lengths up to it: 304 us for 205, 8 users of
 // up to 32768 events.)  One block; the lists of a user's units, parts and tiles, tiles
 // fastest, are dealt out so that an XCD gets neighbours, which read the same keys.
 constexpr int PLAN_THREADS = 1024, PLAN_USERS = 2048;
@@ -277,23 +276,96 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_chunk_plan(SeqArgs a, PageArgs
     }
 }
 
-// The tile's new events into their pages, by the threads of the blocks that
-// share them out by key/value head.
+// The tile's new events into their pages, by the block of the key/value head's
+// first query heads and first part.
 template <typename T, int D>
-__device__ __forceinline__ void store_events(const SeqArgs& a, const PageArgs& p, const Work& w, int64_t had, int first, int last,
+__device__ __forceinline__ void store_events(const SeqArgs& a, const PageArgs& p, const Work& w, int first, int last,
                                              const Rows<const T>& k, const Rows<const T>& v, T* kp, T* vp) {
     using TL = Tile<T, D>;
+    if (w.had < 0 || w.split != 0 || w.h0 != w.g * a.group) return;
     const int64_t row_elems = (int64_t)(a.n_heads / a.group) * D;
-    for (int t = threadIdx.x; t < (last - first) * TL::CH; t += CW * WAVE) {
+    for (int t = threadIdx.x; t < (last - first) * TL::CH; t += blockDim.x) {
         const int i = first + t / TL::CH, c = t % TL::CH;
-        const int64_t e = had + i, slot = slot_of(p, p.table[w.b * p.max_pages + (e >> p.shift)], e);
+        const int64_t e = w.had + i, page = p.table[w.b * p.max_pages + (e >> p.shift)];
+        const u32x4 kr = gload_u4(k.at(w.s + i, w.g) + c * TL::EPC), vr = gload_u4(v.at(w.s + i, w.g) + c * TL::EPC);
+        const int32_t at = a.pos[w.s + i];
+        __builtin_amdgcn_sched_barrier(0);      // one latency, not three
+        const int64_t slot = slot_of(p, page, e), to = slot * row_elems + w.g * D + c * TL::EPC;
         if (slot < 0) continue;
-        const int64_t at = slot * row_elems + w.g * D + c * TL::EPC;
-        gstore_u4(kp + at, gload_u4(k.at(w.s + i, w.g) + c * TL::EPC));
-        gstore_u4(vp + at, gload_u4(v.at(w.s + i, w.g) + c * TL::EPC));
-        if (w.g == 0 && c == 0) p.tp[slot] = a.pos[w.s + i];
+        gstore_u4(kp + to, kr);
+        gstore_u4(vp + to, vr);
+        if (w.g == 0 && c == 0) p.tp[slot] = at;
     }
 }
+
+// The operands of 16 rows of values and the probabilities of them: registers
+// 8 i .. 8 i + 7 of a lane (rows 16 i and on).  bf16: the probabilities as pairs
+// of values, the second the rounded remainder of the first.
+template <typename T, int D>
+struct Step;
+template <int D>
+struct Step<uint16_t, D> {
+    static constexpr int MMA = D / 16, READS = D / 16;
+    u32x4 v[D / 32], p[2];
+    __device__ __forceinline__ void load(const u32x4* tile, int r0) {
+        const int lane = lane_id(), h = lane >> 5, i = lane & 15;
+        const char* base = reinterpret_cast<const char*>(tile);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt) {
+            const int c = 4 * dt + 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);       // (as in OverRows)
+            s16x4 x[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int row = r0 + 8 * u + 4 * h + (i >> 2);
+                x[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (RSE_LDS s16x4*)(base + Tile<uint16_t, D>::chunk_at(row, c) * 16 + (i & 1) * 8));
+            }
+            v[dt].xy = __builtin_bit_cast(u32x2, x[0]);
+            v[dt].zw = __builtin_bit_cast(u32x2, x[1]);
+        }
+    }
+    __device__ __forceinline__ void take(const float (&x)[8]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            p[0][j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+            p[1][j] = pack_bf16(x[2 * j] - __uint_as_float(p[0][j] << 16), x[2 * j + 1] - __uint_as_float(p[0][j] & 0xFFFF0000u));
+        }
+    }
+    __device__ __forceinline__ void add(f32x16 (&o)[D / 32]) const {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt)
+                o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v[dt]), __builtin_bit_cast(bf16x8, p[t]),
+                                                                o[dt], 0, 0, 0);
+    }
+};
+template <int D>
+struct Step<float, D> {
+    static constexpr int MMA = D / 4, READS = D / 4;
+    float v[D / 32][8], p[8];
+    __device__ __forceinline__ void load(const u32x4* tile, int r0) {
+        const int lane = lane_id(), h = lane >> 5;
+        const float* f = reinterpret_cast<const float*>(tile);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int row = r0 + tile_row(r, h), d = 32 * dt + (lane & 31);
+                v[dt][r] = f[Tile<float, D>::chunk_at(row, d >> 2) * 4 + (d & 3)];
+            }
+    }
+    __device__ __forceinline__ void take(const float (&x)[8]) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) p[r] = x[r];
+    }
+    __device__ __forceinline__ void add(f32x16 (&o)[D / 32]) const {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+            for (int dt = 0; dt < D / 32; ++dt) o[dt] = __builtin_amdgcn_mfma_f32_32x32x2f32(v[dt][r], p[r], o[dt], 0, 0, 0);
+    }
+};
 
 // The softmax of a lane's column over the tiles of keys that went by, and the
 // sums of the values.
@@ -308,11 +380,14 @@ struct Online {
         m = l = 0.f;
         set = false;
     }
-    // x: logits less m, -infinity where not visible
-    __device__ __forceinline__ void add(f32x16& x, const u32x4* values, int r0) {
-        float top = x[0];
+    // x: logits less m of 32 N keys, -infinity where not visible
+    template <int N>
+    __device__ __forceinline__ void add(f32x16 (&x)[N], const u32x4* values) {
+        float top = x[0][0];
 #pragma unroll
-        for (int r = 1; r < 16; ++r) top = fmaxf(top, x[r]);
+        for (int u = 0; u < N; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, x[u][r]);
         top = fmaxf(top, other_half(top));
         const bool move = top > 8.f || (!set && top > -INFINITY);
         set |= top > -INFINITY;
@@ -321,15 +396,41 @@ struct Online {
             m += by;
             l = l == 0.f ? 0.f : l * r;         // nothing summed yet: 0, also where exp2 overflows
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] -= by;
+            for (int u = 0; u < N; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[u][i] -= by;
             const float ro = r < INFINITY ? r : 0.f;
 #pragma unroll
             for (int dt = 0; dt < D / 32; ++dt) o[dt] *= ro;
         }
+        // a step's products run while the next one's operands are formed (in the
+        // order that the compiler chose each pair of products waited for its own read)
+        Step<T, D> step[2];
+        auto form = [&](int i) {
+            float e[8];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) x[r] = __builtin_amdgcn_exp2f(x[r]);
-        l += sum_registers(x);
-        OverRows<T, D>::add(o, values, r0, x);
+            for (int r = 0; r < 8; ++r) e[r] = __builtin_amdgcn_exp2f(x[i / 2][8 * (i % 2) + r]);
+            l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+            step[i % 2].take(e);
+        };
+        step[0].load(values, 0);
+        form(0);
+#pragma unroll
+        for (int i = 0; i < 2 * N; ++i) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (i + 1 < 2 * N) step[(i + 1) % 2].load(values, 16 * (i + 1));
+            step[i % 2].add(o);
+            if (i + 1 < 2 * N) {
+                form(i + 1);
+                __builtin_amdgcn_sched_group_barrier(0x100, Step<T, D>::READS, 0);
+#pragma unroll
+                for (int j = 0; j < Step<T, D>::MMA; ++j) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
     }
     // the reference as a part leaves it: what saw nothing weighs nothing
     __device__ __forceinline__ float reference() const { return l == 0.f ? -INFINITY : m; }
@@ -347,10 +448,28 @@ __device__ __forceinline__ void hide_after(f32x16& x, int lim) {
 
 // The table of biases of a block's heads, in base 2, a row a head.
 __device__ __forceinline__ int bias_stride(int n_bounds) { return (n_bounds + 1) | 1; }
-__device__ __forceinline__ void load_bias(float* s_bias, const SeqArgs& a, const Work& w) {
-    const int nb = a.n_bounds + 1, st = bias_stride(a.n_bounds);
-    for (int t = threadIdx.x; t < w.nc * nb; t += CW * WAVE) s_bias[t / nb * st + t % nb] = bias2(a.bias[(w.h0 + t / nb) * nb + t % nb]);
-}
+// The block's bias and buckets, loaded well before they go to LDS.
+struct Early {
+    float bias;
+    int32_t bound;
+    uint32_t cell;
+    __device__ __forceinline__ void load(const SeqArgs& a, const Work& w) {
+        const int t = threadIdx.x;
+        bias = t < w.nc * (a.n_bounds + 1) ? a.bias[w.h0 * (a.n_bounds + 1) + t] : 0.f;
+        bound = t <= RSE_SEQ_MAX_BOUNDARIES ? a.hdr->bounds[t] : 0;
+        cell = t <= RSE_SEQ_MAX_BOUNDARIES ? reinterpret_cast<const uint32_t*>(a.hdr->cell)[t] : 0;
+    }
+    __device__ __forceinline__ void put(const SeqArgs& a, const Work& w, float* s_bias, LdsBuckets& buckets) const {
+        const int nb = a.n_bounds + 1, st = bias_stride(a.n_bounds), t = threadIdx.x;
+        if (t < w.nc * nb) s_bias[t / nb * st + t % nb] = bias2(bias);
+        for (int i = t + (int)blockDim.x; i < w.nc * nb; i += blockDim.x)
+            s_bias[i / nb * st + i % nb] = bias2(a.bias[w.h0 * nb + i]);
+        if (t <= RSE_SEQ_MAX_BOUNDARIES) {
+            buckets.bounds[t] = bound;
+            buckets.cell[t] = cell;
+        }
+    }
+};
 
 // What a column works on.
 template <typename T, int D>
@@ -372,6 +491,8 @@ struct Column {
         q.load(rows.at(w.s + i, head), lane_id() >> 5);
         if (a.scale < 0.f) q.negate();
         pos = a.pos[w.s + i];
+    }
+    __device__ __forceinline__ void loaded() {
         lo = half_min(pos);
         hi = half_max(pos);
     }
@@ -380,22 +501,33 @@ struct Column {
 // Few columns: all waves of a block have the same tile of columns and take
 // tiles of 32 keys in turn, each from memory to its own registers and LDS, so
 // that no wave waits for another; they are joined in LDS at the end.
-template <typename T, int D>
-constexpr int FEW_WAVES = D * sizeof(T) <= 128 ? FW3 : 1;
-
-template <typename T, int D>
-__global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(FEW_WAVES<T, D>))) void k_chunk_few(
+template <typename T, int D, int CW>
+__global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(D * sizeof(T) <= 128 ? 2 : 1))) void k_chunk_few(
     SeqArgs a, PageArgs p, Layout lo, Columns cl, Rows<const T> q, Rows<const T> k, Rows<const T> v, T* kp, T* vp, Rows<T> out,
     float* part_o, float* part_ml) {
     using TL = Tile<T, D>;
     constexpr int CH = TL::CH, ND = D / 32, NC = CH / 2;
     extern __shared__ float s_bias[];           // [cols][bias_stride]
-    __shared__ u32x4 s_mem[CW * 32 * CH > CW * 32 * D / 4 ? CW * 32 * CH : CW * 32 * D / 4];    // tiles of V, then the waves' sums
+    constexpr int SR = D + 4;                   // a column's sums: columns 16 bytes of banks apart
+    __shared__ u32x4 s_mem[CW * 32 * CH > CW * 32 * SR / 4 ? CW * 32 * CH : CW * 32 * SR / 4];  // tiles of V, then the waves' sums
     __shared__ LdsBuckets s_buckets;
     __shared__ u32x4 s_pairs[CW][WAVE];
     alignas(16) __shared__ int32_t s_pos[CW][32];       // (read by 16 bytes)
     __shared__ float s_ml[CW][2][32];
     const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), half = lane >> 5, col = lane & 31;
+    auto page_of = [&](int64_t b, int64_t t) -> int64_t {
+        const int64_t i = (t * 32 + col) >> p.shift;
+        return i < p.max_pages ? (int64_t)p.table[b * p.max_pages + i] : 0;
+    };
+    // Each load of a call waits some 2000 cycles, the first tiles' pages not for
+    // the lengths where the user is known without them.
+    const bool known = !lo.list && lo.per_seq;
+    int64_t pages[2];
+    if (known) {
+        const uint32_t b = blockIdx.x / lo.units % (uint32_t)a.batch;
+        pages[0] = page_of(b, w);
+        pages[1] = page_of(b, w + CW);
+    }
     Work wk;
     if (!find_work(a, p, cl, lo, cl.events, wk)) return;
     u32x4* tile = s_mem + w * 32 * CH;
@@ -409,21 +541,8 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(FEW_WAV
         t1 = t0 + wk.per < t1 ? t0 + wk.per : t1;
         if (t0 >= t1) return;                   // (the join knows)
     }
-    load_bias(s_bias, a, wk);
-    s_buckets.load(a.hdr);
-    if (had >= 0 && wk.split == 0 && wk.h0 == wk.g * a.group) store_events<T, D>(a, p, wk, had, first, last, k, v, kp, vp);
-    Column<T, D> c;
-    c.load(a, cl, wk, first, q);
-    LaneBuckets lb;
-    lb.load(a.hdr, s_bias + (c.head - wk.h0) * bias_stride(a.n_bounds), a.n_bounds);
-    __syncthreads();
-
     const int64_t row_elems = (int64_t)(a.n_heads / a.group) * D;
     const float c2 = fabsf(a.scale) * LOG2E;
-    auto page_of = [&](int64_t t) -> int64_t {
-        const int64_t e = t * 32 + col;
-        return t < t1 && e < had ? (int64_t)p.table[wk.b * p.max_pages + (e >> p.shift)] : 0;
-    };
     u32x4 rk[NC], rv[NC];
     int32_t rp = 0;
     bool see = false;
@@ -450,14 +569,29 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(FEW_WAV
             rv[i2] = gload_u4(vr + (2 * i2 + half) * TL::EPC);
         }
     };
+    // what the rows wait for comes first, and what else the block needs before them
+    int64_t t = t0 + w;
+    if (!known) {
+        pages[0] = page_of(wk.b, t);
+        pages[1] = page_of(wk.b, t + CW);
+    }
+    Early early;
+    early.load(a, wk);
+    Column<T, D> c;
+    c.load(a, cl, wk, first, q);
+    LaneBuckets lb;
+    lb.load(a.hdr, s_bias + (c.head - wk.h0) * bias_stride(a.n_bounds), a.n_bounds);
+    if (t < t1) load_rows(t, pages[0]);
+    int64_t page = pages[1];
+    early.put(a, wk, s_bias, s_buckets);
+    c.loaded();
+    store_events<T, D>(a, p, wk, first, last, k, v, kp, vp);
     Online<T, D> sm;
     sm.clear();
-    int64_t t = t0 + w;
-    int64_t page = page_of(t);
-    if (t < t1) load_rows(t, page);
-    page = page_of(t + CW);
+    __syncthreads();
     for (; t < t1; t += CW) {
-        f32x16 x = {};
+        f32x16 xs[1] = {};
+        f32x16& x = xs[0];
 #pragma unroll
         for (int i = 0; i < NC; ++i) x = mma_chunk<T>(rk[i], c.q.v[i], x);
 #pragma unroll
@@ -467,7 +601,7 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(FEW_WAV
         const int32_t range[2] = {half_min(rp), half_max(rp)};
         wave_lds_sync();
         if (t + CW < t1) load_rows(t + CW, page);
-        page = page_of(t + 2 * CW);
+        page = page_of(wk.b, t + 2 * CW);
         TileBuckets<true> tb;
         tb.set(lb, c.lo, c.hi, range);
         if (tb.many) {
@@ -481,7 +615,7 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(FEW_WAV
             for (int r = 0; r < 16; ++r) x[r] = (bits >> tile_row(r, 0)) & 1 ? x[r] : -INFINITY;
         }
         if (a.causal && t * 32 + 31 > had + first) hide_after(x, (int)(had - t * 32) + c.event - 4 * half);
-        sm.add(x, tile, 0);
+        sm.add(xs, tile);
         wave_lds_sync();                        // read before the next tile is stored
     }
     sm.l += other_half(sm.l);
@@ -491,21 +625,25 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(FEW_WAV
     }
     __syncthreads();                            // the V tiles are done with: their place takes the sums
     float* s_sum = reinterpret_cast<float*>(s_mem);
+    if (c.live) {
 #pragma unroll
-    for (int dt = 0; dt < ND; ++dt)
+        for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<f32x4*>(s_sum + (w * 32 + col) * D + 32 * dt + 8 * j + 4 * half) =
-                f32x4{sm.o[dt][4 * j], sm.o[dt][4 * j + 1], sm.o[dt][4 * j + 2], sm.o[dt][4 * j + 3]};
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<f32x4*>(s_sum + (w * 32 + col) * SR + 32 * dt + 8 * j + 4 * half) =
+                    f32x4{sm.o[dt][4 * j], sm.o[dt][4 * j + 1], sm.o[dt][4 * j + 2], sm.o[dt][4 * j + 3]};
+    }
     __syncthreads();
     for (int y = threadIdx.x; y < (last - first) * wk.nc * D; y += CW * WAVE) {
         const int cc = y / D, d = y % D;
         float M = -INFINITY, L = 0.f, O = 0.f;
+#pragma unroll
         for (int u = 0; u < CW; ++u) M = fmaxf(M, s_ml[u][0][cc]);
+#pragma unroll
         for (int u = 0; u < CW; ++u) {
             const float r = part_weight(s_ml[u][0][cc], M);
             L = __builtin_fmaf(s_ml[u][1][cc], r, L);
-            O = __builtin_fmaf(s_sum[(u * 32 + cc) * D + d], r, O);
+            O = __builtin_fmaf(s_sum[(u * 32 + cc) * SR + d], r, O);
         }
         const int64_t ev = wk.s + first + cc / wk.nc;
         const int head = wk.h0 + cc % wk.nc;
@@ -524,11 +662,17 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(FEW_WAV
 
 // Many columns: every wave has a tile of columns of its own, and the block
 // brings tiles of KT keys to LDS for them, NST - 1 tiles ahead and without
-// registers in between (with the next tile's rows in registers waves waited 57 % of
-// their time: 345 us for <T> on 8 users of up to 32768 events and 128 new ones).
+// registers in between (with the next tile's rows in registers, and those spilled:
+// 350 us for 192 on 8 users of up to 32768 events and 128 new ones, bf16 rows of 128).
+// 64 keys at a time in bf16 (32: 207 us there): one maximum and one question whether it
+// has moved, and one for the bias, for twice the products.  In fp32 32 (64: 180 us
+// for 139 on 24 users of up to 2048 events and 512 new ones, rows of 64).
+// Two waves share a SIMD, and their products and vector operations take turns
+// more than they overlap: 25 % of the cycles are products in bf16, 36 % in fp32.
 template <typename T, int D>
 struct Many {
-    static constexpr int RB = D * (int)sizeof(T), KT = RB == 64 ? 64 : 32, NST = RB <= 256 ? 4 : 3;
+    static constexpr int RB = D * (int)sizeof(T), KT = sizeof(T) == 2 ? 64 : 32;
+    static constexpr int NST = KT * RB <= 8192 ? 4 : sizeof(T) == 2 ? 2 : 3;       // (40 to 105 KiB: two blocks a CU, one of rows of 512 bytes)
     static constexpr int CH = Tile<T, D>::CH, NT = CW * WAVE, PER = KT * CH / NT;
     static constexpr int WAVES = RB <= 256 ? 2 : 1;         // that share a SIMD
     static constexpr int PAGES = 512;                       // of the table in LDS at a time
@@ -564,14 +708,16 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(Many<T,
         t1 = t0 + wk.per < t1 ? t0 + wk.per : t1;
         if (t0 >= t1) return;                   // (the join knows)
     }
-    load_bias(s_bias, a, wk);
-    s_buckets.load(a.hdr);
-    if (had >= 0 && wk.split == 0 && wk.h0 == wk.g * a.group) store_events<T, D>(a, p, wk, had, begin, past, k, v, kp, vp);
+    Early early;
+    early.load(a, wk);
     const int first = begin + w * cl.events;
     Column<T, D> c;
     c.load(a, cl, wk, first, q);
     LaneBuckets lb;
     lb.load(a.hdr, s_bias + (c.head - wk.h0) * bias_stride(a.n_bounds), a.n_bounds);
+    early.put(a, wk, s_bias, s_buckets);
+    c.loaded();
+    store_events<T, D>(a, p, wk, begin, past, k, v, kp, vp);
     const int64_t row_elems = (int64_t)(a.n_heads / a.group) * D;
     const float c2 = fabsf(a.scale) * LOG2E;
 
@@ -595,12 +741,10 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(Many<T,
         }
         __syncthreads();
     };
-    int64_t off_at[PER];                        // elements from a tile's first row to the thread's pieces
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int at = i * MY::NT + t, row = at / CH;
-        off_at[i] = row * row_elems + ((at % CH) ^ TL::swz(row)) * TL::EPC;
-    }
+    // where the thread's piece of a tile is; those of its other pieces are NT / CH rows
+    // apart, with the swizzle's term for the eighth row in odd ones of rows of 512 bytes
+    constexpr int ROWS = MY::NT / CH;
+    const uint32_t off_at = (uint32_t)(t / CH * (int)row_elems + ((t % CH) ^ TL::swz(t / CH)) * TL::EPC) * (uint32_t)sizeof(T);
     const bool in_page = p.shift >= (KT == 64 ? 6 : 5);         // a tile lies in one page
     auto send = [&](int64_t tile, int st) {
         if (tile * KT >= window_end) load_pages(tile * KT);
@@ -612,10 +756,11 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(Many<T,
                 const T *kt = kp + first_slot * row_elems + wk.g * D, *vt = vp + first_slot * row_elems + wk.g * D;
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    to_lds(kt + off_at[i], &s_k[st][i * MY::NT + w * WAVE]);
-                    to_lds(vt + off_at[i], &s_v[st][i * MY::NT + w * WAVE]);
+                    const uint32_t off = off_at ^ (uint32_t)(TL::swz(i * ROWS) * 16);
+                    to_lds(kt + i * ROWS * row_elems, off, &s_k[st][i * MY::NT + w * WAVE]);
+                    to_lds(vt + i * ROWS * row_elems, off, &s_v[st][i * MY::NT + w * WAVE]);
                 }
-                if (lane < KT) to_lds4(p.tp + first_slot + lane, s_pos[w][st]);
+                if (lane < KT) to_lds4(p.tp + first_slot, 4 * lane, s_pos[w][st]);
                 if (lane == 0) s_seen[w][st] = KT == 64 ? ~0ull : 0xFFFFFFFFull;
                 return;
             }
@@ -678,29 +823,53 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(Many<T,
     }
     for (int64_t tile = t0; tile < t1; ++tile) {
         next(tile);
+        const int64_t k0 = tile * KT;
+        const int32_t* pos = s_pos[w][st];
+        u32x4 rows[KT / 32][CH / 2];            // all on their way before the first is waited for
+        const int32_t rp = pos[lane % KT];
+#pragma unroll
+        for (int u = 0; u < KT / 32; ++u)
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) rows[u][i] = s_k[st][TL::chunk_at(32 * u + (lane & 31), 2 * i + half)];
+        __builtin_amdgcn_sched_barrier(0);
+        const int32_t low = half_min(rp), high = half_max(rp);
+        const int32_t l0 = __builtin_amdgcn_readlane(low, 0), l1 = __builtin_amdgcn_readlane(low, 32);
+        const int32_t h0 = __builtin_amdgcn_readlane(high, 0), h1 = __builtin_amdgcn_readlane(high, 32);
+        const int32_t range[2] = {l0 < l1 ? l0 : l1, h0 > h1 ? h0 : h1};
+        TileBuckets<true> tb;
+        tb.set(lb, c.lo, c.hi, range);
+        f32x16 z[KT / 32];
 #pragma unroll
         for (int u = 0; u < KT / 32; ++u) {
-            const int64_t k1 = tile * KT + 32 * u;
-            const int32_t* pos = s_pos[w][st] + 32 * u;
-            const int32_t rp = pos[lane & 31];
-            const int32_t range[2] = {half_min(rp), half_max(rp)};
-            TileBuckets<true> tb;
-            tb.set(lb, c.lo, c.hi, range);
-            f32x16 z = mma_rows<T, D>(s_k[st], 32 * u, c.q, f32x16{});
+            z[u] = f32x16{};
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) z[u] = mma_chunk<T>(rows[u][i], c.q.v[i], z[u]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < KT / 32; ++u) {
             if (tb.many) {
-                tb.find_pairs(s_pairs[w], 0, 1, s_buckets, a.n_bounds, a.cells, pos, c.pos);
+                tb.find_pairs(s_pairs[w], 0, 1, s_buckets, a.n_bounds, a.cells, pos + 32 * u, c.pos);
                 wave_lds_sync();
             }
-            z = tb.logits(z, c2, -sm.m, lb, s_pairs[w], lb.bias, pos, c.pos);
-            const uint32_t seen = __builtin_amdgcn_readfirstlane((uint32_t)(s_seen[w][st] >> (32 * u)));
-            if (seen != ~0u) {
-                const uint32_t bits = seen >> (4 * half);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) z[r] = (bits >> tile_row(r, 0)) & 1 ? z[r] : -INFINITY;
-            }
-            if (a.causal && k1 + 31 > had + first) hide_after(z, (int)(had - k1) + c.event - 4 * half);
-            sm.add(z, s_v[st], 32 * u);
+            z[u] = tb.logits(z[u], c2, -sm.m, lb, s_pairs[w], lb.bias, pos + 32 * u, c.pos);
+            if (tb.many) wave_lds_sync();       // read before the next are written
         }
+        const uint64_t seen = s_seen[w][st];
+        const uint32_t seen_lo = __builtin_amdgcn_readfirstlane((uint32_t)seen), seen_hi = __builtin_amdgcn_readfirstlane((uint32_t)(seen >> 32));
+        if ((KT == 64 ? seen_lo & seen_hi : seen_lo) != ~0u) {
+#pragma unroll
+            for (int u = 0; u < KT / 32; ++u) {
+                const uint32_t bits = (u ? seen_hi : seen_lo) >> (4 * half);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) z[u][r] = (bits >> tile_row(r, 0)) & 1 ? z[u][r] : -INFINITY;
+            }
+        }
+        if (a.causal && k0 + KT - 1 > had + first) {
+#pragma unroll
+            for (int u = 0; u < KT / 32; ++u) hide_after(z[u], (int)(had - k0) - 32 * u + c.event - 4 * half);
+        }
+        sm.add(z, s_v[st]);
         st = st == NST - 1 ? 0 : st + 1;
     }
     sm.l += other_half(sm.l);
@@ -759,15 +928,17 @@ __global__ __launch_bounds__(JT) void k_chunk_join(SeqArgs a, PageArgs p, Layout
 }
 
 // ------------------------------------------------------------------ host --
-#ifndef FWANT
-#define FWANT 512
-#endif
-#ifndef FROOM
-#define FROOM 512
-#endif
-#ifndef MWANT
-#define MWANT 1
-#endif
+// Blocks that run at a time, 2 a CU (1 with rows of 512 bytes).  Parts for twice
+// as many: 199 us for 192, and the join 16 for 11 (8 users of up to 32768 events).
+constexpr int ROOM = 512;
+// The few-columns kernel takes tiles of columns apart up to this many of a user:
+// the waves of a block share none of the loads, but wait for none of each other
+// (256 users of up to 1024 events, two tiles: 42 us for 62 with the other kernel).
+constexpr int FEW_TILES = 2;
+// Blocks up to which each has 8 waves (one user of 300 events: 11.0 us for 12.2);
+// with more, blocks of 4 overlap one's ends with the other's loop (256 users: 42 us for 58).
+constexpr int FEW_BLOCKS = 256;
+
 struct ChunkPlan {
     Columns cl;
     bool few;
@@ -784,14 +955,16 @@ ChunkPlan chunk_plan(const rse_seqattn* at, int64_t n_events, int64_t batch, int
     p.cl.cols = group < 32 ? group : 32;
     p.cl.blocks = (group + p.cl.cols - 1) / p.cl.cols;
     p.cl.events = 32 / p.cl.cols;
-    p.few = max_new <= FEWT * p.cl.events;
+    p.few = max_new <= FEW_TILES * p.cl.events;
     p.tq = p.few ? p.cl.events : CW * p.cl.events;
-    p.kt = p.few || row > 64 ? 32 : 64;
+    p.kt = p.few || at->dtype == RSE_F32 ? 32 : 64;
     p.grid = tile_grid(n_events, batch, max_new, p.tq);
     p.units = (int64_t)at->n_kv_heads * p.cl.blocks;
-    const int want = p.few ? FWANT : (row > 256 ? 256 : 512) * MWANT;
     p.least = 256 / p.kt;
-    p.want = max_len >= 512 && p.whole() < (p.few ? FROOM : PLAN_USERS) ? want : 0;
+    // Not for short histories, nor where there are blocks enough: the few-columns
+    // kernel's from ROOM on (256 users of up to 1024 events, 512 to 1024 blocks: 35 us for 42,
+    // but 17 for the plan and the join).
+    p.want = max_len >= 512 && p.whole() < (p.few ? ROOM : PLAN_USERS) ? (row > 256 ? ROOM / 2 : ROOM) : 0;
     return p;
 }
 
@@ -818,16 +991,22 @@ int run_chunk(const rse_seqcache* c, const SeqArgs& a, const PageArgs& pg, const
     if (p.blocks() > INT32_MAX) return RSE_ERR_UNSUPPORTED;
     const size_t lds = (size_t)p.cl.cols * ((a.n_bounds + 1) | 1) * sizeof(float);
     const Layout lo = {(uint32_t)p.units, (uint32_t)p.grid.items, (uint32_t)p.grid.per_seq, p.want ? ws.list : nullptr};
-    const dim3 grid((unsigned)p.blocks()), block(CW * WAVE);
+    const dim3 grid((unsigned)p.blocks());
     if (p.want)
         hipLaunchKernelGGL(k_chunk_plan, dim3(1), dim3(PLAN_THREADS), 0, s, a, pg, (int)p.units, p.tq, p.kt, p.least, p.want,
                            (int)p.blocks(), ws.list);
-    const auto run = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid, block, lds, s, a, pg, lo, p.cl, rows_view<const T>(q), rows_view<const T>(k),
+    const auto run = [&](auto kernel, int waves) {
+        hipLaunchKernelGGL(kernel, grid, dim3(waves * WAVE), lds, s, a, pg, lo, p.cl, rows_view<const T>(q), rows_view<const T>(k),
                            rows_view<const T>(v), static_cast<T*>(c->k), static_cast<T*>(c->v), rows_view<T>(out), ws.o, ws.ml);
     };
-    if (p.few) run(k_chunk_few<T, D>);
-    else run(k_chunk_many<T, D>);
+    if (p.few) {
+        if constexpr (D * sizeof(T) <= 128) {
+            if (p.blocks() <= FEW_BLOCKS) run(k_chunk_few<T, D, 8>, 8);
+            else run(k_chunk_few<T, D, 4>, 4);
+        } else {
+            run(k_chunk_few<T, D, 4>, 4);
+        }
+    } else run(k_chunk_many<T, D>, CW);
     if (p.want) {
         const int waves = p.few ? 1 : CW;
         hipLaunchKernelGGL((k_chunk_join<T, D>), dim3(grid.x, (unsigned)(waves * 32 * (D / 4) / JT)), dim3(JT), 0, s, a, pg, lo, p.cl,
@@ -873,8 +1052,9 @@ int seq_attention_chunk(const rse_seqattn* attn, rse_seqcache* cache, const rse_
     p.tp = cache->pos;
     p.max_pages = max_pages;
     p.n_pages = cache->n_pages;
-    p.max_len = max_len;
     p.shift = cache->page_shift;
+    p.max_len = max_len;
+    if (plan.want && max_pages > (INT64_C(1) << 36) >> p.shift && max_len > INT64_C(1) << 36) return RSE_ERR_UNSUPPORTED;      // tiles of keys in 32 bits
     return by_type(attn, [&](auto t, auto d) {
         return run_chunk<decltype(t), decltype(d)::value>(cache, a, p, plan, ws, q, k, v, out, as_stream(stream));
     });
