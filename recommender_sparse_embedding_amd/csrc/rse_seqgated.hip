@@ -365,15 +365,16 @@ struct GatedArgs {
     int32_t dim, hidden;
 };
 
-#ifndef INB
-#define INB Block<2, 4, 2, 2>
-#endif
 // Shapes, by the type's rate on the matrix cores.  bf16: a step of a block's
 // tile is 1024 cycles of products, 1152 of LDS reads and writes, 768 of the
 // vector memory path; two blocks a CU.  fp32 is 16 times as long in its
 // products, and small tiles fill the GPU more evenly.
 template <typename T>
-using InBlock = std::conditional_t<sizeof(T) == 2, INB, Block<1, 2, 2, 2>>;
+using InBlock = std::conditional_t<sizeof(T) == 2, Block<2, 4, 2, 2>, Block<1, 2, 2, 2>>;
+// bf16, where the large tiles would not give every CU one: 256 rows of 512 by
+// 1536 11.7 us for 6.8, 2048 rows (192 large tiles) 13.5 for 13.1; 4096 rows (384) 20.0 for 23.0.
+using FewBlock = Block<1, 2, 2, 2>;
+constexpr int CUS = 256;
 template <typename T>
 using OutBlock = std::conditional_t<sizeof(T) == 2, Block<2, 4, 2, 2>, Block<1, 1, 2, 2>>;
 template <typename B>
@@ -589,6 +590,15 @@ GatedWs gated_ws(int64_t n, int32_t dim, int32_t hidden, int32_t dtype, void* ba
     return w;
 }
 
+// f(block shape, blocks) of the projections
+template <typename T, typename F>
+int by_blocks(int64_t n, int32_t hidden, F f) {
+    const auto blocks = [&](auto b) { return up(n, decltype(b)::TQ) * up(hidden, decltype(b)::TP / 2); };
+    if constexpr (sizeof(T) == 2)
+        if (blocks(InBlock<T>()) < CUS) return f(FewBlock(), blocks(FewBlock()));
+    return f(InBlock<T>(), blocks(InBlock<T>()));
+}
+
 // f(T(), integral_constant<act>)
 template <typename F>
 int by_kind(int32_t dtype, int32_t act, F f) {
@@ -613,12 +623,13 @@ int seq_gated_linear_fwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const 
     return by_kind(dtype, act, [&](auto t, auto ac) -> int {
         using T = decltype(t);
         constexpr int ACT = decltype(ac)::value;
-        using B = InBlock<T>;
-        const int64_t blocks = up(n, B::TQ) * up(hidden, B::TP / 2);
-        if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
-        hipLaunchKernelGGL((k_gated<T, B, ACT, false>), dim3((unsigned)blocks), dim3(B::GT), 0, as_stream(stream), a, view<const T>(x),
-                           view<const T>(w_gate), view<const T>(w_up), Mat<const T>{nullptr, 0}, view<T>(out));
-        return launch_status();
+        return by_blocks<T>(n, hidden, [&](auto b, int64_t blocks) -> int {
+            using B = decltype(b);
+            if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+            hipLaunchKernelGGL((k_gated<T, B, ACT, false>), dim3((unsigned)blocks), dim3(B::GT), 0, as_stream(stream), a,
+                               view<const T>(x), view<const T>(w_gate), view<const T>(w_up), Mat<const T>{nullptr, 0}, view<T>(out));
+            return launch_status();
+        });
     });
 }
 

@@ -17,7 +17,7 @@ import torch
 
 from . import BF16, F32, SILU, _bytes, _ptr, lib
 from ._lib import RseSeqMat, check
-from .sequence import _PER16, _on, _size, _stream, _vector
+from .sequence import _PER16, _here, _on, _on_empty, _size, _stream, _vector
 
 _KIND = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -26,25 +26,36 @@ def _kind(x: torch.Tensor, name: str) -> int:
     kind = _KIND.get(x.dtype)
     if kind is None or not x.is_cuda or x.dim() != 2:
         raise TypeError(f"{name}: expected a fp32 or bf16 [n, width] CUDA tensor, got {x.dtype} {tuple(x.shape)} on {x.device}")
-    if x.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {x.device}, which is not the current device")
+    _here(x, name)
     return kind
+
+
+def _new(x: torch.Tensor, n: int, width: int, stream):
+    """A tensor of x's type for a result, and its description (a call of a few
+    rows takes as long here as on the GPU, so what is known is not looked at)."""
+    if stream is None:
+        t = x.new_empty((n, width))
+    else:
+        with torch.cuda.stream(stream):
+            t = x.new_empty((n, width))
+    return t, RseSeqMat(t.data_ptr(), width)
 
 
 def _mat(t: torch.Tensor, like: torch.Tensor, n: int, width: int, name: str, per: int = 1) -> RseSeqMat:
     """per: elements that address and stride are multiples of."""
-    if t.dtype != like.dtype or t.device != like.device:
+    if t.dtype != like.dtype or t.get_device() != like.get_device():
         raise TypeError(f"{name}: expected a {like.dtype} tensor on {like.device}, got {t.dtype} on {t.device}")
     if t.shape != (n, width):
         raise ValueError(f"{name}: expected shape ({n}, {width}), got {tuple(t.shape)}")
     row, one = t.stride()
     if n <= 1:                  # the stride of a dimension of one element is never used
         row = 0
-    if n and ((one != 1 and width > 1) or row % per or t.data_ptr() % (per * t.element_size())):
+    p = t.data_ptr()
+    if n and ((one != 1 and width > 1) or row % per or (per > 1 and p % 16)):
         raise ValueError(f"{name}: the last dimension must be contiguous"
                          + (", and the address and the row stride multiples of 16 bytes" if per > 1 else "")
                          + f" (strides {t.stride()})")
-    return RseSeqMat(t.data_ptr(), row)
+    return RseSeqMat(p, row)
 
 
 def _ref(m: RseSeqMat | None):
@@ -71,19 +82,21 @@ def seq_layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None, bias: torch
     bp = None if bias is None else _vector(bias, torch.float32, dim, "bias")
     if residual is None and sum_out is not None:
         raise ValueError("sum_out is given without a residual")
+    if out is None:
+        out, ym = _new(x, n, dim, stream)
+    else:
+        ym = _mat(out, x, n, dim, "out")
     rm = sm = None
-    with _on(stream):
-        y = torch.empty((n, dim), dtype=x.dtype, device=x.device) if out is None else out
-        if residual is not None:
-            rm = _mat(residual, x, n, dim, "residual")
-            if sum_out is None:
-                sum_out = torch.empty((n, dim), dtype=x.dtype, device=x.device)
+    if residual is not None:
+        rm = _mat(residual, x, n, dim, "residual")
+        if sum_out is None:
+            sum_out, sm = _new(x, n, dim, stream)
+        else:
             sm = _mat(sum_out, x, n, dim, "sum_out")
-        stats = torch.empty((n, 2), dtype=torch.float32, device=x.device) if for_backward else None
-    ym = _mat(y, x, n, dim, "out")
+    stats = _on_empty(stream, (n, 2), torch.float32, x.device) if for_backward else None
     check(lib.seq_layer_norm_fwd(_ref(xm), _ref(rm), _ref(sm), wp, bp, eps, n, dim, kind, _ref(ym), _ptr(stats),
                                  _stream(stream)), "seq_layer_norm_fwd")
-    return LayerNormOut(y, sum_out, stats)
+    return LayerNormOut(out, sum_out, stats)
 
 
 def seq_layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: torch.Tensor | None, stats: torch.Tensor,
@@ -99,14 +112,16 @@ def seq_layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: torch.Tensor |
     sp = _vector(stats, torch.float32, 2 * n, "stats")
     dsm = None if dsum is None else _mat(dsum, x, n, dim, "dsum")
     with _on(stream):
-        dx = torch.empty((n, dim), dtype=x.dtype, device=x.device) if out is None else out
         dw, db = (torch.empty(dim, dtype=torch.float32, device=x.device) for _ in range(2))
         ws = _bytes(_size(lib.rse_seq_layer_norm_bwd_workspace_size, "rse_seq_layer_norm_bwd_workspace_size", n, dim, kind),
                     x.device)
-    dxm = _mat(dx, x, n, dim, "out")
+    if out is None:
+        out, dxm = _new(x, n, dim, stream)
+    else:
+        dxm = _mat(out, x, n, dim, "out")
     check(lib.seq_layer_norm_bwd(_ref(xm), _ref(dym), wp, sp, _ref(dsm), n, dim, kind, _ref(dxm), _ptr(dw), _ptr(db),
                                  _ptr(ws), ws.numel(), _stream(stream)), "seq_layer_norm_bwd")
-    return dx, dw, db
+    return out, dw, db
 
 
 def _gated(x, w_gate, w_up):
@@ -125,10 +140,10 @@ def seq_gated_linear_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tens
     [hidden, dim] of one type; dim and hidden are multiples of 16 bytes.  act:
     SIGMOID, SILU or GELU."""
     kind, n, dim, hidden, per, mats = _gated(x, w_gate, w_up)
-    with _on(stream):
-        if out is None:
-            out = torch.empty((n, hidden), dtype=x.dtype, device=x.device)
-    o = _mat(out, x, n, hidden, "out", per)
+    if out is None:
+        out, o = _new(x, n, hidden, stream)
+    else:
+        o = _mat(out, x, n, hidden, "out", per)
     check(lib.seq_gated_linear_fwd(*map(_ref, mats), n, dim, hidden, kind, act, _ref(o), _stream(stream)),
           "seq_gated_linear_fwd")
     return out

@@ -38,6 +38,15 @@ def _stream(stream=None) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _here(t: torch.Tensor, name: str):
+    """t: a CUDA tensor (so that the runtime is up)."""
+    if t.get_device() != _current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+
+
 def _on(stream):
     """Allocations inside belong to `stream`."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
@@ -100,6 +109,7 @@ class SeqAttention:
               "rse_seqattn_create")
         self.handle = h
         self.step_bytes = (-1, -1, 0)            # the last step's batch, max_len and workspace size
+        self.chunk_bytes = (None, 0)             # the last chunk's sizes and workspace size
         self._finalizer = weakref.finalize(self, lib.rse_seqattn_destroy, h)
 
     @property
@@ -336,16 +346,25 @@ def seq_attention_chunk(attn: SeqAttention, cache: SeqCache, q: torch.Tensor, k:
     n = q.shape[0]
     dt, H, Hk, D = attn.torch_dtype, attn.n_heads, attn.n_kv_heads, attn.dim
     args = [_rows(q, dt, n, H, D, "q"), _rows(k, dt, n, Hk, D, "k"), _rows(v, dt, n, Hk, D, "v")]
+    _here(q, "q")
     b = _batch(attn, n, pos, bias, seq_offsets, None, max_new)
-    max_pages = _table(page_table, b.batch)
-    lens_p = _vector(lens, torch.int64, b.batch, "lens")
+    batch = b.batch
+    max_pages = _table(page_table, batch)
+    lens_p = _vector(lens, torch.int64, batch, "lens")
     most = max_pages * cache.page_size if max_len is None else int(max_len)
-    size = _size(lib.rse_seqattn_chunk_workspace_size, "rse_seqattn_chunk_workspace_size", attn.handle, n, b.batch,
-                 b.max_len, most)
+    shape = (n, batch, b.max_len, most)
+    known = attn.chunk_bytes
+    if known[0] == shape:
+        size = known[1]
+    else:
+        size = _size(lib.rse_seqattn_chunk_workspace_size, "rse_seqattn_chunk_workspace_size", attn.handle, *shape)
+        attn.chunk_bytes = (shape, size)
     if out is None:
         out = _on_empty(stream, (n, H, D), dt, q.device)
+        o = RseSeqRows(out.data_ptr(), H * D, D)
+    else:
+        o = _rows(out, dt, n, H, D, "out")
     ws = _on_empty(stream, size, torch.uint8, q.device) if size else None
-    o = _rows(out, dt, n, H, D, "out")
     byref = ctypes.byref
     check(lib.seq_attention_chunk(attn.handle, cache.handle, byref(b), byref(args[0]), byref(args[1]), byref(args[2]),
                                   page_table.data_ptr(), max_pages, lens_p, most, byref(o), _ptr(ws), size,
