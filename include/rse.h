@@ -743,6 +743,7 @@ int seq_attention_chunk(const rse_seqattn* attn, rse_seqcache* cache, const rse_
  * given type (RSE_F32 or RSE_BF16): the elements of a row are adjacent, the
  * distance between rows is free (a slice of a wider tensor; 0 or negative for
  * inputs too).  No two rows of an output overlap, else RSE_ERR_INVALID_ARG.
+ * An output overlaps no input and no other output but where a call says so.
  * These calls have no handle and no device-side errors; results are run-to-run
  * identical (no floating-point atomics).
  */
@@ -813,8 +814,9 @@ int rse_seq_gated_linear_bwd_workspace_size(int64_t n, int32_t dim, int32_t hidd
  *   dg = dout u act'(g),  du = dout act(g)
  *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
  * All gradients are of the rows' type and overwritten (the weights' with 0 for
- * n = 0).  With RSE_BF16, dg and du are rounded to bf16 before their products,
- * which are summed in fp32 and rounded once.
+ * n = 0).  dx may be x or dout (the same address and stride).  With RSE_BF16,
+ * dg and du are rounded to bf16 before their products, which are summed in
+ * fp32 and rounded once.
  */
 int seq_gated_linear_bwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const rse_seq_mat* w_up, const rse_seq_mat* dout,
                          int64_t n, int32_t dim, int32_t hidden, int32_t dtype, int32_t act, const rse_seq_mat* dx,

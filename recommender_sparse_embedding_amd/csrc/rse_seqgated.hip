@@ -8,7 +8,10 @@
 // All five are tiled matrix products on the matrix cores with fp32 sums.  The
 // backward forms g and u anew (4 dim operations a hidden element) instead of
 // reading them back in fp32 (8 bytes, and 8 to write): 0.9 ps against 3.3 ps at
-// dim 256.  dg and du pass through the workspace in the rows' type.
+// dim 256.  dg and du pass through the workspace in the rows' type: in bf16 they
+// are rounded once, as the operands of the matrix products that follow have to
+// be anyway (gradients 0.0023 from the float64 ones in relative 2-norm; 0.0017
+// with both in fp32 and plain products, whose own rounding to bf16 is that).
 #include "rse_seqmma.h"
 
 using namespace rse;
@@ -669,10 +672,11 @@ int seq_gated_linear_bwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const 
         if (n > 0) {
             hipLaunchKernelGGL((k_gated<T, BI, ACT, true>), dim3((unsigned)in_blocks), dim3(BI::GT), 0, s, a, view<const T>(x),
                                view<const T>(w_gate), view<const T>(w_up), view<const T>(dout), d);
-            hipLaunchKernelGGL((k_gated_dx<T, BO>), dim3((unsigned)dx_blocks), dim3(BO::GT), 0, s, a, dc, view<const T>(w_gate),
-                               view<const T>(w_up), view<T>(dx));
             hipLaunchKernelGGL((k_gated_dw<T, BO>), dim3((unsigned)dw_blocks), dim3(BO::GT), 0, s, a, dc, view<const T>(x), dp.rows,
                                ws.part);
+            // (after dW, which reads x: dx may be x)
+            hipLaunchKernelGGL((k_gated_dx<T, BO>), dim3((unsigned)dx_blocks), dim3(BO::GT), 0, s, a, dc, view<const T>(w_gate),
+                               view<const T>(w_up), view<T>(dx));
         }
         hipLaunchKernelGGL((k_gated_dw_join<T>), dim3(fill_blocks(2ll * hidden * dim, 4 * JT, 4096)), dim3(JT), 0, s, a, ws.part,
                            dp.splits, view<T>(dw_gate), view<T>(dw_up));

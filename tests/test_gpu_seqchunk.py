@@ -366,3 +366,104 @@ def test_chunk_repeats_are_identical(rse):
     u = Users(rse, [(1300, 70), (900, 5)], 4, 2, 64, BF16)
     a = u.call()
     assert all(torch.equal(u.call(), a) for _ in range(3))
+
+
+# Histories of unequal users, idle ones and ones without events among them, that
+# are split into parts (whose number follows the lengths on the device).
+PARTS = {"many": [(1500, 40), (0, 1), (-1, 3), (700, 0), (260, 33), (511, 1), (512, 64), (3, 70)],
+         "few": [(1300, 2), (-1, 1), (700, 3), (0, 2), (255, 1), (2000, 0)],
+         "one of many": [(2, 1)] * 30 + [(1800, 25)] + [(-1, 0)] * 5}
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [32, 64, 128])
+@pytest.mark.parametrize("users", PARTS)
+def test_chunk_parts_of_unequal_users(rse, users, D, dtype):
+    for causal in (True, False):
+        Users(rse, PARTS[users], 4, 2, D, dtype, causal=causal).check()
+
+
+@pytest.mark.parametrize("users", [[(900, 3), (600, 2)], [(900, 50), (600, 7)]])
+def test_chunk_not_finite_in_parts(rse, users):
+    """NaN in one part reaches its users' events, and a part that sees nothing
+    weighs nothing."""
+    for dtype in (F32, BF16):
+        u, clean = Users(rse, users, 4, 2, 32, dtype), Users(rse, users, 4, 2, 32, dtype)
+        ref, n = clean.call(), users[0][1]
+        u.cache.k[int(u.table[0, 20]), 5] = math.nan
+        got = u.call()
+        assert torch.all(torch.isnan(got[:n])) and torch.equal(got[n:], ref[n:])
+        far = Users(rse, users, 4, 2, 32, dtype, times="ones", bounds=(400,))
+        far.bias[:, 1] = -math.inf                              # keys further back than 400
+        far.check()
+        far.bias[:, :] = -math.inf
+        assert torch.all(far.call() == 0)
+
+
+def test_chunk_parts_follow_the_lengths(rse):
+    """A captured call whose lengths grow between replays, as a program adds the
+    events that it stored."""
+    for new in (3, 40):
+        users = [(600, new), (20, new), (100, new)]
+        u = Users(rse, users, 4, 2, 64, BF16, spare=40)
+        graph, most = torch.cuda.CUDAGraph(), u.most + 600
+        u.call(max_len=most)
+        torch.cuda.synchronize()
+        lens = u.lens.clone()
+        with torch.cuda.graph(graph):
+            out = u.call(max_len=most)
+        for step in (0, 1, 5, 2):
+            at = lens.clone()
+            at[1:] += 100 * step                                # (over pages of zeros and NaN: filled first)
+            for pool in u.cache_tensors():
+                pool.nan_to_num_(0) if pool.is_floating_point() else None
+            u.lens.copy_(at)
+            graph.replay()
+            torch.cuda.synchronize()
+            got = out.clone()
+            eager = u.call(max_len=most)
+            assert torch.equal(got, eager) and torch.all(torch.isfinite(got))
+        assert u.cache.status() == 0 and u.attn.status() == 0
+
+
+def test_chunk_long_table_windows(rse):
+    """A part over more pages than a block keeps of the table at a time: the
+    same keys in small and in large pages give the same bits."""
+    H = 256                                                     # all heads apart: too many blocks for parts
+    users = [(4300, 70)] + [(3, 66)] * 8                        # more than two tiles of 32 columns
+    small = Users(rse, users, H, H, 32, BF16, page=8)
+    large = Users(rse, users, H, H, 32, BF16, page=64)
+    for name in ("q", "k", "v", "pos", "bias"):
+        setattr(large, name, getattr(small, name))
+    for b, (had, _) in enumerate(users):
+        for pool, other in zip(large.cache_tensors(), small.cache_tensors()):
+            pool.view(-1, *pool.shape[2:])[_slots(large, b, had)] = other.view(-1, *other.shape[2:])[_slots(small, b, had)]
+    a, b = small.call(), large.call()
+    assert torch.equal(a, b) and torch.all(torch.isfinite(a))
+
+
+def _slots(u, b, n):
+    e = torch.arange(n, device="cuda")
+    return u.table[b].long()[e // u.page] * u.page + e % u.page
+
+
+@pytest.mark.parametrize("new", [3, 40])
+def test_chunk_bad_input_in_parts(rse, new):
+    """What is reported of calls without parts is of those with them."""
+    users = [(600, new), (700, new), (90, new)]
+    ref = Users(rse, users, 4, 2, 32, BF16).call()
+    for change, status, kept in ((lambda u: u.lens.__setitem__(1, 10**7), "cache", None),
+                                 (lambda u: u.table.__setitem__((1, 30), -1), "cache", None),
+                                 (lambda u: u.table.__setitem__((1, 30), 10**6), "cache", None),
+                                 (lambda u: u.off.__setitem__(2, new - 1), "attn", 7.0),
+                                 (lambda u: u.off.__setitem__(1, 10**9), "attn", 7.0),
+                                 (lambda u: u.off.copy_(torch.tensor([0, 3 * new, 0, 3 * new])), "attn", None)):
+        u = Users(rse, users, 4, 2, 32, BF16)
+        change(u)
+        out = torch.full_like(ref, 7.0)
+        u.call(out=out)
+        assert getattr(u, status).status() == -9
+        if status == "cache":
+            assert torch.equal(out[:new], ref[:new]) and torch.equal(out[2 * new:], ref[2 * new:])
+        if kept is not None:
+            assert torch.all(out[new:2 * new] == kept)
