@@ -501,8 +501,13 @@ struct Column {
 // Few columns: all waves of a block have the same tile of columns and take
 // tiles of 32 keys in turn, each from memory to its own registers and LDS, so
 // that no wave waits for another; they are joined in LDS at the end.
+// Bound by latency: a tile's rows are on their way while the last one's are
+// used, and what a tile waits is covered by the other waves of its SIMD.  Three, of
+// rows up to 128 bytes, though that spills some registers: 35.0 us for 42.2 with two on
+// 256 users of up to 1024 events and 16 new ones (1.9 TB/s; the longest users'
+// chains of nine tiles a wave end last).
 template <typename T, int D, int CW>
-__global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(D * sizeof(T) <= 128 ? 2 : 1))) void k_chunk_few(
+__global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(CW == 8 ? 2 : D * sizeof(T) <= 128 ? 3 : 1))) void k_chunk_few(
     SeqArgs a, PageArgs p, Layout lo, Columns cl, Rows<const T> q, Rows<const T> k, Rows<const T> v, T* kp, T* vp, Rows<T> out,
     float* part_o, float* part_ml) {
     using TL = Tile<T, D>;
@@ -515,14 +520,14 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(D * siz
     alignas(16) __shared__ int32_t s_pos[CW][32];       // (read by 16 bytes)
     __shared__ float s_ml[CW][2][32];
     const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE), half = lane >> 5, col = lane & 31;
-    auto page_of = [&](int64_t b, int64_t t) -> int64_t {
+    auto page_of = [&](int64_t b, int64_t t) -> int32_t {
         const int64_t i = (t * 32 + col) >> p.shift;
-        return i < p.max_pages ? (int64_t)p.table[b * p.max_pages + i] : 0;
+        return i < p.max_pages ? p.table[b * p.max_pages + i] : 0;
     };
     // Each load of a call waits some 2000 cycles, the first tiles' pages not for
     // the lengths where the user is known without them.
     const bool known = !lo.list && lo.per_seq;
-    int64_t pages[2];
+    int32_t pages[2];
     if (known) {
         const uint32_t b = blockIdx.x / lo.units % (uint32_t)a.batch;
         pages[0] = page_of(b, w);
@@ -546,7 +551,7 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(D * siz
     u32x4 rk[NC], rv[NC];
     int32_t rp = 0;
     bool see = false;
-    auto load_rows = [&](int64_t t, int64_t page) {
+    auto load_rows = [&](int64_t t, int32_t page) {
         const int64_t e = t * 32 + col;
         // a new event's rows, also (the last one's) for lanes past the end
         const int64_t i = wk.s + (e < had ? 0 : (e - had < wk.count ? e - had : wk.count - 1));
@@ -582,7 +587,7 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(D * siz
     LaneBuckets lb;
     lb.load(a.hdr, s_bias + (c.head - wk.h0) * bias_stride(a.n_bounds), a.n_bounds);
     if (t < t1) load_rows(t, pages[0]);
-    int64_t page = pages[1];
+    int32_t page = pages[1];
     early.put(a, wk, s_bias, s_buckets);
     c.loaded();
     store_events<T, D>(a, p, wk, first, last, k, v, kp, vp);
@@ -933,10 +938,10 @@ __global__ __launch_bounds__(JT) void k_chunk_join(SeqArgs a, PageArgs p, Layout
 constexpr int ROOM = 512;
 // The few-columns kernel takes tiles of columns apart up to this many of a user:
 // the waves of a block share none of the loads, but wait for none of each other
-// (256 users of up to 1024 events, two tiles: 42 us for 62 with the other kernel).
+// (256 users of up to 1024 events, two tiles: 35 us for 62 with the other kernel).
 constexpr int FEW_TILES = 2;
 // Blocks up to which each has 8 waves (one user of 300 events: 11.0 us for 12.2);
-// with more, blocks of 4 overlap one's ends with the other's loop (256 users: 42 us for 58).
+// with more, blocks of 4 overlap one's ends with the other's loop (256 users: 35 us for 58).
 constexpr int FEW_BLOCKS = 256;
 
 struct ChunkPlan {
@@ -962,7 +967,7 @@ ChunkPlan chunk_plan(const rse_seqattn* at, int64_t n_events, int64_t batch, int
     p.units = (int64_t)at->n_kv_heads * p.cl.blocks;
     p.least = 256 / p.kt;
     // Not for short histories, nor where there are blocks enough: the few-columns
-    // kernel's from ROOM on (256 users of up to 1024 events, 512 to 1024 blocks: 35 us for 42,
+    // kernel's from ROOM on (256 users of up to 1024 events, 512 to 1024 blocks: 33 us for 35,
     // but 17 for the plan and the join).
     p.want = max_len >= 512 && p.whole() < (p.few ? ROOM : PLAN_USERS) ? (row > 256 ? ROOM / 2 : ROOM) : 0;
     return p;
