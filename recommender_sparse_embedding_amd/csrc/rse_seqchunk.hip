@@ -933,8 +933,9 @@ __global__ __launch_bounds__(JT) void k_chunk_join(SeqArgs a, PageArgs p, Layout
 }
 
 // ------------------------------------------------------------------ host --
-// Blocks that run at a time, 2 a CU (1 with rows of 512 bytes).  Parts for twice
-// as many: 199 us for 192, and the join 16 for 11 (8 users of up to 32768 events).
+// Blocks that run at a time, 2 a CU (1 with rows of 512 bytes; 3 of few columns
+// with rows up to 128).  Parts for twice as many: 199 us for 192, and the join 16 for
+// 11 (8 users of up to 32768 events).
 constexpr int ROOM = 512;
 // The few-columns kernel takes tiles of columns apart up to this many of a user:
 // the waves of a block share none of the loads, but wait for none of each other
@@ -966,10 +967,13 @@ ChunkPlan chunk_plan(const rse_seqattn* at, int64_t n_events, int64_t batch, int
     p.grid = tile_grid(n_events, batch, max_new, p.tq);
     p.units = (int64_t)at->n_kv_heads * p.cl.blocks;
     p.least = 256 / p.kt;
-    // Not for short histories, nor where there are blocks enough: the few-columns
-    // kernel's from ROOM on (256 users of up to 1024 events, 512 to 1024 blocks: 33 us for 35,
-    // but 17 for the plan and the join).
-    p.want = max_len >= 512 && p.whole() < (p.few ? ROOM : PLAN_USERS) ? (row > 256 ? ROOM / 2 : ROOM) : 0;
+    // Not for short histories, nor where there are blocks enough; few columns
+    // with blocks for the CUs only where histories are long, as the plan and the join take
+    // 17 us.  Whole / in parts, 256 users of up to 1024, 4096, 8192 events (1024 blocks,
+    // bf16 rows of 64): 36 / 51, 102 / 95, 213 / 165; 128 of up to 4096 in fp32 (512): 170 / 152.
+    const int64_t from = p.few && p.whole() >= ROOM ? 4096 : 512;
+    if (max_len >= from && p.whole() < PLAN_USERS) p.want = p.few && row <= 128 ? 3 * ROOM / 2 : row > 256 ? ROOM / 2 : ROOM;
+    else p.want = 0;
     return p;
 }
 
