@@ -380,6 +380,8 @@ using FewBlock = Block<1, 2, 2, 2>;
 constexpr int CUS = 256;
 template <typename T>
 using OutBlock = std::conditional_t<sizeof(T) == 2, Block<2, 4, 2, 2>, Block<1, 1, 2, 2>>;
+// And of dx and dW in bf16 where large tiles are few (see dx_plan, dw_plan).
+using OutFew = Block<1, 1, 2, 2>;
 template <typename B>
 constexpr int SHARE = B::MQ * B::MP >= 8 ? 2 : 4;       // waves that share a SIMD
 template <typename B>
@@ -456,30 +458,35 @@ __global__ __launch_bounds__(B::GT) __attribute__((amdgpu_waves_per_eu(SHARE<B>)
     if constexpr (BWD) rows_to_memory<T, B::TQ, HT, B::GT>(lds + SIZE, out, r0, a.hidden + h0, a.n - r0, a.hidden - h0);
 }
 
-// dx = [dg du] [Wg; Wu].
+// dx = [dg du] [Wg; Wu]; where part is given, of part s of the contraction, the
+// indexes from s `len` on.
 template <typename T, typename B>
 __global__ __launch_bounds__(B::GT) __attribute__((amdgpu_waves_per_eu(SHARE<B>))) void k_gated_dx(GatedArgs a, Mat<const T> d,
                                                                                                 Mat<const T> wg, Mat<const T> wu,
-                                                                                                Mat<T> dx) {
+                                                                                                Mat<T> dx, int64_t len, float* part) {
     __shared__ u32x4 lds[NBUF * (B::TP + B::TQ) * KCH];
     const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE);
-    const uint32_t ct = (a.dim + B::TP - 1) / B::TP, tile = xcd_tile(blockIdx.x, gridDim.x);
-    const int64_t r0 = (int64_t)(tile / ct) * B::TQ, k_end = 2ll * a.hidden;
+    const uint32_t ct = (a.dim + B::TP - 1) / B::TP, rt = (uint32_t)((a.n + B::TQ - 1) / B::TQ);
+    uint32_t tile = xcd_tile(blockIdx.x, gridDim.x);
     const int c0 = (int)(tile % ct) * B::TP;
+    tile /= ct;
+    const int64_t r0 = (int64_t)(tile % rt) * B::TQ, s = tile / rt, k0 = s * len;
+    const int64_t k_end = k0 + len < 2ll * a.hidden ? k0 + len : 2ll * a.hidden;
     StackedRows<T, B::TP, B::GT> p;
     p.begin({wg.p + c0, wg.stride}, {wu.p + c0, wu.stride}, a.hidden, k_end, a.dim - c0);
     AlongRows<T, B::TQ, B::GT> q;
     q.begin([&](int r) { return d.row(r0 + r < a.n ? r0 + r : a.n - 1); }, k_end);
     f32x16 acc[B::MP][B::MQ] = {};
     const int pw = 32 * B::MP * (w % B::WP), qw = 32 * B::MQ * (w / B::WP);
-    multiply<T, B>(p, q, 0, k_end, [&](int j) { return pw + 32 * j; }, qw, acc, lds, w);
+    multiply<T, B>(p, q, k0, k_end, [&](int j) { return pw + 32 * j; }, qw, acc, lds, w);
 #pragma unroll
     for (int i = 0; i < B::MQ; ++i) {
-        const int64_t r = r0 + qw + 32 * i + (lane & 31);
+        const int64_t r = r0 + qw + 32 * i + (lane & 31), at = r < a.n ? r : 0;
 #pragma unroll
         for (int j = 0; j < B::MP; ++j) {
-            const int c = c0 + pw + 32 * j;
-            put_column(dx.row(r < a.n ? r : 0) + c, acc[j][i], r < a.n ? a.dim - c : 0);
+            const int c = c0 + pw + 32 * j, cols = r < a.n ? a.dim - c : 0;
+            if (part) put_column(part + (s * a.n + at) * a.dim + c, acc[j][i], cols);
+            else put_column(dx.row(at) + c, acc[j][i], cols);
         }
     }
 }
@@ -516,17 +523,19 @@ __global__ __launch_bounds__(B::GT) __attribute__((amdgpu_waves_per_eu(SHARE<B>)
     }
 }
 
-// The parts added, rounded once: four elements a thread.
+// The parts [splits][rows][dim] added, rounded once: four elements a thread.
+// Rows from `turn` on go to the second matrix.
 template <typename T>
-__global__ __launch_bounds__(JT) void k_gated_dw_join(GatedArgs a, const float* part, int splits, Mat<T> dwg, Mat<T> dwu) {
-    const int64_t size = 2ll * a.hidden * a.dim;
+__global__ __launch_bounds__(JT) void k_gated_join(const float* part, int splits, int64_t rows, int64_t turn, int32_t dim, Mat<T> m,
+                                                   Mat<T> m2) {
+    const int64_t size = rows * dim;
     for (int64_t t = 4 * ((int64_t)blockIdx.x * JT + threadIdx.x); t < size; t += 4ll * JT * gridDim.x) {
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
         for (int s = 0; s < splits; ++s) o += gload_f4(part + s * size + t);
-        const int64_t h = t / a.dim;
-        const int c = (int)(t - h * a.dim);
-        store_four((h < a.hidden ? dwg.row(h) : dwu.row(h - a.hidden)) + c, o);
+        const int64_t r = t / dim;
+        const int c = (int)(t - r * dim);
+        store_four((r < turn ? m.row(r) : m2.row(r - turn)) + c, o);
     }
 }
 
@@ -549,48 +558,75 @@ int gated_args(int64_t n, int32_t dim, int32_t hidden, int32_t dtype) {
     return RSE_OK;
 }
 
-// Parts of the events for dW, of whole steps and 512 events at least: as many
-// as make the rounds of blocks (SHARE a CU at once) fullest, the cost of adding a
-// part up taken as that of 64 events.
-struct DwPlan {
-    int splits;
-    int64_t rows;
-};
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+template <typename B>
+int64_t tiles(int64_t q, int64_t p) { return up(q, B::TQ) * up(p, B::TP); }
+
+// How dx and dW are formed: with large tiles or, where these are too few for the
+// CUs, small ones (of bf16), and in how many parts of the contraction.
+struct Plan {
+    bool few;
+    int splits;
+    int64_t len;                        // of a part
+};
+// dx: parts where the small tiles are few too, of eight steps at least, for two
+// blocks a CU (four: no faster).  3196 rows of 80 by 648 in fp32 42 us whole and 22
+// with the join; in bf16 500 of 256 by 1024 41 with large tiles and 8, 3196 of 512 by
+// 1368 56 and 32.
 template <typename T>
-int64_t dw_tiles(int32_t dim, int32_t hidden) { return up(dim, OutBlock<T>::TP) * up(2ll * hidden, OutBlock<T>::TQ); }
-DwPlan dw_plan(int64_t n, int32_t dim, int32_t hidden, int32_t dtype) {
-    const int64_t tiles = dtype == RSE_F32 ? dw_tiles<float>(dim, hidden) : dw_tiles<uint16_t>(dim, hidden);
-    const int64_t at_once = dtype == RSE_F32 ? AT_ONCE<OutBlock<float>> : AT_ONCE<OutBlock<uint16_t>>;
-    const int64_t most = (n + 511) / 512;
-    int64_t s = 1;
+Plan dx_plan(int64_t n, int32_t dim, int32_t hidden) {
+    Plan p = {tiles<OutBlock<T>>(n, dim) < CUS, 1, 2ll * hidden};
+    const int64_t blocks = tiles<OutFew>(n, dim), steps = up(2ll * hidden, KT<T>);
+    int64_t s = p.few && blocks > 0 ? 2 * CUS / blocks : 1;
+    if (s > steps / 8) s = steps / 8;
+    if (s > 1) {
+        p.len = up(steps, s) * KT<T>;
+        p.splits = (int)up(2ll * hidden, p.len);
+    }
+    return p;
+}
+
+// dW: parts of the events, of whole steps and 128 events at least: as many as
+// make the rounds of blocks (SHARE a CU at once) shortest, the time to add a part
+// up taken as that of an event for 24000 elements (413696 rows of 256 by 1024 in
+// 32 parts 14 us beside 459, 24571 of 1024 by 2736 in 5 22 beside 306).
+template <typename T>
+Plan dw_plan(int64_t n, int32_t dim, int32_t hidden) {
+    const int64_t most = up(n, 128) < 64 ? up(n, 128) : 64;
+    Plan p = {tiles<OutBlock<T>>(2ll * hidden, dim) * most < CUS, 1, 0};
+    const int64_t t = p.few ? tiles<OutFew>(2ll * hidden, dim) : tiles<OutBlock<T>>(2ll * hidden, dim);
+    const int64_t at_once = p.few ? AT_ONCE<OutFew> : AT_ONCE<OutBlock<T>>;
     double best = 0;
-    for (int64_t c = 1; c <= 64 && c <= most; ++c) {
-        const double cost = (double)(up(tiles * c, at_once)) * ((double)n / c + 64.0 * c);
+    for (int64_t c = 1; c <= most; ++c) {
+        const double cost = (double)up(t * c, at_once) * ((double)n / c) + c * (2.0 * hidden * dim / 24000);
         if (c == 1 || cost < best) {
             best = cost;
-            s = c;
+            p.splits = (int)c;
         }
     }
-    DwPlan p;
-    p.rows = ((n + s - 1) / s + 63) / 64 * 64;
-    p.splits = (int)(p.rows > 0 ? (n + p.rows - 1) / p.rows : 0);
+    p.len = up(up(n, p.splits), 64) * 64;
+    p.splits = (int)(n > 0 ? up(n, p.len) : 0);
     return p;
 }
 
 struct GatedWs {
     void* d;
-    float* part;
+    float *dw, *dx;                     // parts
     size_t bytes;
 };
-GatedWs gated_ws(int64_t n, int32_t dim, int32_t hidden, int32_t dtype, void* base) {
+template <typename T>
+GatedWs gated_ws(int64_t n, int32_t dim, int32_t hidden, void* base) {
     Carver c(base);
-    const size_t e = dtype == RSE_F32 ? 4 : 2;
+    const Plan x = dx_plan<T>(n, dim, hidden);
     GatedWs w;
-    w.d = c.take<char>((size_t)n * 2 * hidden * e);
-    w.part = c.take<float>((size_t)dw_plan(n, dim, hidden, dtype).splits * 2 * hidden * dim);
+    w.d = c.take<T>((size_t)n * 2 * hidden);
+    w.dw = c.take<float>((size_t)dw_plan<T>(n, dim, hidden).splits * 2 * hidden * dim);
+    w.dx = c.take<float>(x.splits > 1 ? (size_t)x.splits * n * dim : 0);
     w.bytes = c.size();
     return w;
+}
+GatedWs gated_ws(int64_t n, int32_t dim, int32_t hidden, int32_t dtype, void* base) {
+    return dtype == RSE_F32 ? gated_ws<float>(n, dim, hidden, base) : gated_ws<uint16_t>(n, dim, hidden, base);
 }
 
 // f(block shape, blocks) of the projections
@@ -656,30 +692,46 @@ int seq_gated_linear_bwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const 
     const GatedWs ws = gated_ws(n, dim, hidden, dtype, d_ws);
     if (ws_bytes < ws.bytes) return RSE_ERR_WORKSPACE;
     if (ws.bytes && (!d_ws || reinterpret_cast<uintptr_t>(d_ws) % 256)) return RSE_ERR_INVALID_ARG;
-    const DwPlan dp = dw_plan(n, dim, hidden, dtype);
     const GatedArgs a = {n, dim, hidden};
     hipStream_t s = as_stream(stream);
     return by_kind(dtype, act, [&](auto t, auto ac) -> int {
         using T = decltype(t);
         constexpr int ACT = decltype(ac)::value;
-        using BI = InBlock<T>;
-        using BO = OutBlock<T>;
-        const int64_t in_blocks = up(n, BI::TQ) * up(hidden, BI::TP / 2), dx_blocks = up(n, BO::TQ) * up(dim, BO::TP);
-        const int64_t dw_blocks = dp.splits * dw_tiles<T>(dim, hidden);
-        if (in_blocks > INT32_MAX || dx_blocks > INT32_MAX || dw_blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+        const Plan x_plan = dx_plan<T>(n, dim, hidden), w_plan = dw_plan<T>(n, dim, hidden);
         const Mat<T> d = {static_cast<T*>(ws.d), 2ll * hidden};
         const Mat<const T> dc = {d.p, d.stride};
         if (n > 0) {
-            hipLaunchKernelGGL((k_gated<T, BI, ACT, true>), dim3((unsigned)in_blocks), dim3(BI::GT), 0, s, a, view<const T>(x),
-                               view<const T>(w_gate), view<const T>(w_up), view<const T>(dout), d);
-            hipLaunchKernelGGL((k_gated_dw<T, BO>), dim3((unsigned)dw_blocks), dim3(BO::GT), 0, s, a, dc, view<const T>(x), dp.rows,
-                               ws.part);
+            int err = by_blocks<T>(n, hidden, [&](auto b, int64_t blocks) -> int {
+                using B = decltype(b);
+                if (blocks > INT32_MAX || (x_plan.few ? tiles<OutFew>(n, dim) : tiles<OutBlock<T>>(n, dim)) > INT32_MAX / 64)
+                    return RSE_ERR_UNSUPPORTED;
+                hipLaunchKernelGGL((k_gated<T, B, ACT, true>), dim3((unsigned)blocks), dim3(B::GT), 0, s, a, view<const T>(x),
+                                   view<const T>(w_gate), view<const T>(w_up), view<const T>(dout), d);
+                return launch_status();
+            });
+            if (err) return err;
+            const auto dw = [&](auto b) {
+                using B = decltype(b);
+                hipLaunchKernelGGL((k_gated_dw<T, B>), dim3((unsigned)(w_plan.splits * tiles<B>(2ll * hidden, dim))), dim3(B::GT), 0, s,
+                                   a, dc, view<const T>(x), w_plan.len, ws.dw);
+            };
+            const auto dx_of = [&](auto b) {
+                using B = decltype(b);
+                hipLaunchKernelGGL((k_gated_dx<T, B>), dim3((unsigned)(x_plan.splits * tiles<B>(n, dim))), dim3(B::GT), 0, s, a, dc,
+                                   view<const T>(w_gate), view<const T>(w_up), view<T>(dx), x_plan.len,
+                                   x_plan.splits > 1 ? ws.dx : nullptr);
+            };
+            if (w_plan.few) dw(OutFew());
+            else dw(OutBlock<T>());
             // (after dW, which reads x: dx may be x)
-            hipLaunchKernelGGL((k_gated_dx<T, BO>), dim3((unsigned)dx_blocks), dim3(BO::GT), 0, s, a, dc, view<const T>(w_gate),
-                               view<const T>(w_up), view<T>(dx));
+            if (x_plan.few) dx_of(OutFew());
+            else dx_of(OutBlock<T>());
+            if (x_plan.splits > 1)
+                hipLaunchKernelGGL((k_gated_join<T>), dim3(fill_blocks(n * dim, 4 * JT, 4096)), dim3(JT), 0, s, ws.dx, x_plan.splits, n,
+                                   n, dim, view<T>(dx), view<T>(dx));
         }
-        hipLaunchKernelGGL((k_gated_dw_join<T>), dim3(fill_blocks(2ll * hidden * dim, 4 * JT, 4096)), dim3(JT), 0, s, a, ws.part,
-                           dp.splits, view<T>(dw_gate), view<T>(dw_up));
+        hipLaunchKernelGGL((k_gated_join<T>), dim3(fill_blocks(2ll * hidden * dim, 4 * JT, 4096)), dim3(JT), 0, s, ws.dw, w_plan.splits,
+                           2ll * hidden, (int64_t)hidden, dim, view<T>(dw_gate), view<T>(dw_up));
         return launch_status();
     });
 }
