@@ -287,6 +287,51 @@ def test_gated_refusals(rse):
             bad()
 
 
+# Sizes whose tiles are enough for every CU, so that bf16 takes the large ones:
+# of the projections, dx and dW; of the projections alone; of dW alone.
+LARGE = [(16500, 264, 200), (5000, 24, 904), (130, 2056, 4104)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("n,dim,hidden", LARGE)
+def test_gated_large(rse, kind, n, dim, hidden):
+    _check_gated(rse, kind, *_gated_case(kind, n, dim, hidden), ACTS[n % 3])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_gated_large_strides_and_rows_apart(rse, kind):
+    """As above for views: what lies between the rows stays, and a row that is
+    not finite keeps to itself."""
+    n, dim, hidden = LARGE[0]
+    dt, g = DT[kind], _gen(8, n, 2)
+    x = _randn(g, n, dim + 24, dt=dt)[:, 16:16 + dim]
+    w = _randn(g, hidden, 2 * dim, dt=dt) * 0.1
+    wg, wu = w[:, :dim], w[:, dim:]
+    dout = _randn(g, n, hidden, dt=dt)
+    out = torch.full((n, hidden + 16), 7.0, dtype=dt, device="cuda")
+    dx = torch.full((n, dim + 16), 7.0, dtype=dt, device="cuda")
+    dw = torch.full((hidden, 2 * dim + 8), 7.0, dtype=dt, device="cuda")
+    rse.seq_gated_linear_fwd(x, wg, wu, out=out[:, 8:8 + hidden])
+    rse.seq_gated_linear_bwd(x, wg, wu, dout, grads=(dx[:, 8:8 + dim], dw[:, :dim], dw[:, dim:2 * dim]))
+    tight = [t.contiguous() for t in (x, wg, wu)]
+    ref, grads = rse.seq_gated_linear_fwd(*tight), rse.seq_gated_linear_bwd(*tight, dout)
+    assert torch.equal(out[:, 8:8 + hidden], ref) and torch.all(out[:, :8] == 7) and torch.all(out[:, 8 + hidden:] == 7)
+    assert torch.equal(dx[:, 8:8 + dim], grads[0]) and torch.all(dx[:, :8] == 7) and torch.all(dx[:, 8 + dim:] == 7)
+    assert torch.equal(dw[:, :dim], grads[1]) and torch.equal(dw[:, dim:2 * dim], grads[2]) and torch.all(dw[:, 2 * dim:] == 7)
+    bad = tight[0].clone()
+    bad[16499, 263] = float("nan")
+    assert torch.equal(rse.seq_gated_linear_fwd(bad, *tight[1:])[:-1], ref[:-1])
+    got = rse.seq_gated_linear_bwd(bad, *tight[1:], dout)[0]
+    assert torch.equal(got[:-1], grads[0][:-1]) and torch.all(torch.isnan(got[-1]))
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("n,dim", [(70_000, 8), (50_001, 20), (9000, 2050)])
+def test_norm_many_rows(rse, kind, n, dim):
+    """More rows than the blocks take at once."""
+    _check_norm(rse, kind, *_norm_case(rse, kind, n, dim, True))
+
+
 # ------------------------------------------------------ both, as they are used --
 def test_gradients_are_slopes(rse):
     """fp32 gradients against central differences of the oracle's forward."""
