@@ -368,10 +368,10 @@ struct GatedArgs {
     int32_t dim, hidden;
 };
 
-// Shapes, by the type's rate on the matrix cores.  bf16: a step of a block's
-// tile is 1024 cycles of products, 1152 of LDS reads and writes, 768 of the
-// vector memory path; two blocks a CU.  fp32 is 16 times as long in its
-// products, and small tiles fill the GPU more evenly.
+// Shapes, by the type's rate on the matrix cores.  bf16: a step of two blocks, which
+// share a CU, is 1024 cycles of products, 1152 of LDS reads and writes, 768 of the
+// vector memory path.  fp32 is 16 times as long in its products, and small tiles
+// fill the GPU more evenly.
 template <typename T>
 using InBlock = std::conditional_t<sizeof(T) == 2, Block<2, 4, 2, 2>, Block<1, 2, 2, 2>>;
 // bf16, where the large tiles would not give every CU one: 256 rows of 512 by

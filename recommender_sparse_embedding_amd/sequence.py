@@ -2,7 +2,8 @@
 
 ``SeqAttention`` is a layer's configuration (heads, type, causal or not,
 distance boundaries); ``SeqCache`` the paged keys, values and times of every
-user's history for serving.  Rows are [n_events, heads, dim] tensors whose
+user's history for serving, one new event a user (seq_attention_step) or
+several (seq_attention_chunk) at a time.  Rows are [n_events, heads, dim] tensors whose
 last dimension is contiguous; the other strides are free in steps of 16 bytes
 (views of a joint projection, for example); only inputs may overlap
 themselves (an expanded tensor).  Every call is ordered on the
