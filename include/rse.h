@@ -730,6 +730,8 @@ int rse_seqattn_chunk_workspace_size(const rse_seqattn* attn, int64_t n_events, 
  * in the attention handle's status, the sequences concerned are skipped and
  * their out is left as it was.  The lengths are not changed: the caller adds
  * the counts.
+ * Tables and max_len above 2^35 events both, or 2^31 users:
+ * RSE_ERR_UNSUPPORTED.
  */
 int seq_attention_chunk(const rse_seqattn* attn, rse_seqcache* cache, const rse_seq_batch* batch, const rse_seq_rows* q,
                         const rse_seq_rows* k, const rse_seq_rows* v, const int32_t* d_page_table, int32_t max_pages,

@@ -1042,6 +1042,9 @@ int seq_attention_chunk(const rse_seqattn* attn, rse_seqcache* cache, const rse_
     int rc = batch_ok(attn, batch);
     if (rc) return rc;
     if (!cache || max_pages < 0 || max_len < 0 || batch->d_key_off) return RSE_ERR_INVALID_ARG;
+    // users, and tiles of keys, are counted in 32 bits
+    const int64_t most = INT64_C(1) << 35;
+    if (batch->batch > INT32_MAX || (max_len > most && (int64_t)max_pages << cache->page_shift > most)) return RSE_ERR_UNSUPPORTED;
     if (attn->dim != cache->dim || attn->dtype != cache->dtype || attn->n_kv_heads != cache->n_kv_heads)
         return RSE_ERR_INVALID_ARG;
     if (batch->n_events == 0) return RSE_OK;
@@ -1063,7 +1066,6 @@ int seq_attention_chunk(const rse_seqattn* attn, rse_seqcache* cache, const rse_
     p.n_pages = cache->n_pages;
     p.shift = cache->page_shift;
     p.max_len = max_len;
-    if (plan.want && max_pages > (INT64_C(1) << 36) >> p.shift && max_len > INT64_C(1) << 36) return RSE_ERR_UNSUPPORTED;      // tiles of keys in 32 bits
     return by_type(attn, [&](auto t, auto d) {
         return run_chunk<decltype(t), decltype(d)::value>(cache, a, p, plan, ws, q, k, v, out, as_stream(stream));
     });
