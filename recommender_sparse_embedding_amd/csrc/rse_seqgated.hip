@@ -48,7 +48,7 @@ struct Block {
 // A block's operand of R rows (of the result) by KT<T> of the contraction, on
 // its way from memory to LDS, and read from there as matrix operands: 16 bytes a
 // lane, of row `lane % 32` the elements 8 s' + 4 (lane / 32) .. of step s in
-// fp32, 16 s + 8 (lane / 32) .. in bf16.  Thread t moves the pieces that stand at
+// fp32, 16 s + 8 (lane / 32) .. in bf16.  Thread t of GT moves the pieces that stand at
 // t, t + GT, ... in LDS.  Rows of the result past the end are doubles of an existing one
 // (their results are not stored); of a last, partial step the pieces past the
 // end are zeros, written through registers.
@@ -65,7 +65,7 @@ struct AlongRows {
         k_end = end;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = i * GT + threadIdx.x, r = t / KCH;
+            const int t = i * GT + threadIdx.x % GT, r = t / KCH;
             p[i] = row_at(r) + ((t % KCH) ^ TL::swz(r)) * EPC<T>;
         }
     }
@@ -76,7 +76,7 @@ struct AlongRows {
     __device__ __forceinline__ void partial(int64_t k0, u32x4* lds) const {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = i * GT + threadIdx.x;
+            const int t = i * GT + threadIdx.x % GT;
             const int64_t k = k0 + ((t % KCH) ^ TL::swz(t / KCH)) * EPC<T>;
             u32x4 x = {0, 0, 0, 0};
             if (k < k_end) x = gload_u4(p[i] + k0);
@@ -99,7 +99,7 @@ struct AcrossRows {
     int64_t k_end;
     int cols;                           // of the tile, that exist
     __device__ __forceinline__ const T* at(int64_t k0, int i) const {
-        const int t = i * GT + threadIdx.x, r = t / TL::CH, c = ((t % TL::CH) ^ TL::swz(r)) * EPC<T>;
+        const int t = i * GT + threadIdx.x % GT, r = t / TL::CH, c = ((t % TL::CH) ^ TL::swz(r)) * EPC<T>;
         return k_row(k0 + r) + (c < cols ? c : 0);
     }
     __device__ __forceinline__ void issue(int64_t k0, bool, u32x4* lds, int w) const {
@@ -109,7 +109,7 @@ struct AcrossRows {
     __device__ __forceinline__ void partial(int64_t k0, u32x4* lds) const {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = i * GT + threadIdx.x;
+            const int t = i * GT + threadIdx.x % GT;
             u32x4 x = {0, 0, 0, 0};
             if (k0 + t / TL::CH < k_end) x = gload_u4(at(k0, i));
             lds[t] = x;
@@ -167,7 +167,7 @@ struct StackedRows {
         k_end = end;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = i * GT + threadIdx.x, x = ((t % TL::CH) ^ TL::swz(t / TL::CH)) * EPC<T>;
+            const int t = i * GT + threadIdx.x % GT, x = ((t % TL::CH) ^ TL::swz(t / TL::CH)) * EPC<T>;
             c[i] = x < cols ? x : 0;
             p[i] = nullptr;
         }
@@ -177,7 +177,7 @@ struct StackedRows {
         const int64_t ahead = KT<T> * (k0 < turn ? m.stride : m2.stride);
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            if (anew) p[i] = row(k0 + (i * GT + (int)threadIdx.x) / TL::CH) + c[i];
+            if (anew) p[i] = row(k0 + (i * GT + (int)threadIdx.x % GT) / TL::CH) + c[i];
             else p[i] += ahead;
             to_lds(p[i], lds + i * GT + w * WAVE);
         }
@@ -185,7 +185,7 @@ struct StackedRows {
     __device__ __forceinline__ void partial(int64_t k0, u32x4* lds) const {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int t = i * GT + threadIdx.x;
+            const int t = i * GT + threadIdx.x % GT;
             const int64_t k = k0 + t / TL::CH;
             u32x4 x = {0, 0, 0, 0};
             if (k < k_end) x = gload_u4(row(k) + c[i]);
@@ -198,11 +198,12 @@ struct StackedRows {
 };
 
 // acc[j][i] += P rows p0(j) .. times Q rows q0 + 32 i .., over the contraction
-// from k0 to k1 (not empty).  One barrier a step: past it, the step's pieces have landed and
-// all waves are done with the buffer that the step after next is sent to.
+// from k0 to k1.  One barrier a step: past it, the step's pieces have landed and
+// all waves are done with the buffer that the step after next is sent to.  turns > 0:
+// that many barriers, for more groups of waves that have other parts of the contraction.
 template <typename T, typename B, typename P, typename Q, typename P0>
 __device__ __forceinline__ void multiply(P& p, Q& q, int64_t k0, int64_t k1, P0 p0, int q0, f32x16 (&acc)[B::MP][B::MQ],
-                                         u32x4* lds, int w) {
+                                         u32x4* lds, int w, int turns = 0) {
     constexpr int SIZE = (B::TP + B::TQ) * KCH;
     const int steps = (int)((k1 - k0 + KT<T> - 1) / KT<T>), full = (int)((k1 - k0) / KT<T>);
     auto send = [&](int i, int b) {
@@ -224,6 +225,7 @@ __device__ __forceinline__ void multiply(P& p, Q& q, int64_t k0, int64_t k1, P0 
         lds_barrier();
         send(i + 2, b == 0 ? 2 : b - 1);
         const u32x4 *lp = lds + b * SIZE, *lq = lp + B::TP * KCH;
+        if (turns == 0 || i < steps)
 #pragma unroll
         for (int s = 0; s < KCH / 2; ++s) {
             u32x4 a[B::MP], c[B::MQ];
@@ -237,7 +239,7 @@ __device__ __forceinline__ void multiply(P& p, Q& q, int64_t k0, int64_t k1, P0 
                 for (int u = 0; u < B::MQ; ++u) acc[j][u] = mma_chunk<T>(a[j], c[u], acc[j][u]);
         }
         b = b == 2 ? 0 : b + 1;
-    } while (++i < steps);
+    } while (++i < (turns ? turns : steps));
 }
 
 // A 32 by 32 tile of a lane's row as 16-byte pieces: piece(j) gives elements
@@ -377,6 +379,12 @@ using InBlock = std::conditional_t<sizeof(T) == 2, Block<2, 4, 2, 2>, Block<1, 2
 // bf16, where the large tiles would not give every CU one: 256 rows of 512 by
 // 1536 11.7 us for 6.8, 2048 rows (192 large tiles) 13.5 for 13.1; 4096 rows (384) 20.0 for 23.0.
 using FewBlock = Block<1, 2, 2, 2>;
+// fp32, whose products bound a CU: a wave a tile, and four of them a part of the
+// contraction each.  us, tiles of 64 by 64 / so: 46 rows of 792 by 320 32.5 / 12.6, 1011 of
+// 1496 by 304 59.8 / 34.1, 256 of 256 by 512 12.2 / 6.3.  (bf16, which waits for its loads
+// instead: 64 rows of 512 by 1536 6.5 / 5.6, but 1024 of 256 by 512 4.6 / 5.6.)
+using GroupBlock = Block<1, 2, 1, 1>;
+constexpr int GROUPS = 4;
 constexpr int CUS = 256;
 template <typename T>
 using OutBlock = std::conditional_t<sizeof(T) == 2, Block<2, 4, 2, 2>, Block<1, 1, 2, 2>>;
@@ -389,13 +397,15 @@ constexpr int AT_ONCE = 256 * SHARE<B> * 4 * WAVE / B::GT;      // blocks on the
 
 // out (BWD: dg beside du) of TQ rows by TP / 2 hidden elements: the tile's P
 // rows are TP / 2 rows of Wg, then the same ones of Wu, and a wave's
-// accumulators hold g and u of the same elements.
-template <typename T, typename B, int ACT, bool BWD>
-__global__ __launch_bounds__(B::GT) __attribute__((amdgpu_waves_per_eu(SHARE<B>))) void k_gated(
+// accumulators hold g and u of the same elements.  WK groups of waves have a part
+// of the contraction each.
+template <typename T, typename B, int WK, int ACT, bool BWD>
+__global__ __launch_bounds__((WK * B::GT)) __attribute__((amdgpu_waves_per_eu(WK > 1 ? 2 : SHARE<B>))) void k_gated(
     GatedArgs a, Mat<const T> x, Mat<const T> wg, Mat<const T> wu, Mat<const T> dout, Mat<T> out) {
     constexpr int HT = B::TP / 2, MH = B::MP / 2;
-    __shared__ u32x4 lds[NBUF * (B::TP + B::TQ) * KCH];
-    const int lane = lane_id(), w = uniform((int)threadIdx.x / WAVE);
+    constexpr int BUF = NBUF * (B::TP + B::TQ) * KCH;
+    __shared__ u32x4 lds[WK * BUF];
+    const int lane = lane_id(), group = uniform((int)threadIdx.x / B::GT), w = uniform((int)threadIdx.x % B::GT / WAVE);
     const uint32_t ht = (a.hidden + HT - 1) / HT, tile = xcd_tile(blockIdx.x, gridDim.x);
     const int64_t r0 = (int64_t)(tile / ht) * B::TQ;
     const int h0 = (int)(tile % ht) * HT;
@@ -409,7 +419,7 @@ __global__ __launch_bounds__(B::GT) __attribute__((amdgpu_waves_per_eu(SHARE<B>)
     f32x16 acc[B::MP][B::MQ] = {};
     const int hw = 32 * MH * (w % B::WP), qw = 32 * B::MQ * (w / B::WP);
     RawColumn<T> d[BWD ? MH : 1][B::MQ];
-    if constexpr (BWD)                          // on its way while the projections are formed
+    if (BWD && group == 0)                      // on its way while the projections are formed
 #pragma unroll
         for (int i = 0; i < B::MQ; ++i) {
             const int64_t r = r0 + qw + 32 * i + (lane & 31);
@@ -419,11 +429,38 @@ __global__ __launch_bounds__(B::GT) __attribute__((amdgpu_waves_per_eu(SHARE<B>)
                 d[j][i].load(dout.row(r < a.n ? r : 0) + h, r < a.n ? a.hidden - h : 0);
             }
         }
-    multiply<T, B>(p, q, 0, a.dim, [&](int j) { return hw + (j < MH ? 32 * j : HT + 32 * (j - MH)); }, qw, acc, lds, w);
+    const auto p_row = [&](int j) { return hw + (j < MH ? 32 * j : HT + 32 * (j - MH)); };
+    if constexpr (WK == 1) {
+        multiply<T, B>(p, q, 0, a.dim, p_row, qw, acc, lds, w);
+    } else {
+        const int turns = ((a.dim + KT<T> - 1) / KT<T> + WK - 1) / WK, k0 = group * turns * KT<T>, k1 = k0 + turns * KT<T>;
+        multiply<T, B>(p, q, k0, k1 < a.dim ? k1 : (k0 < a.dim ? a.dim : k0), p_row, qw, acc, lds + group * BUF, w, turns);
+        constexpr int NW = B::GT / WAVE, PART = B::MP * B::MQ * 4 * WAVE;       // a wave's sums
+        static_assert((WK - 1) * NW * PART <= WK * BUF, "sums in LDS");
+        lds_barrier();                          // all waves are done with the operands
+        if (group > 0) {
+#pragma unroll
+            for (int t = 0; t < B::MP * B::MQ * 4; ++t) {
+                const f32x16& x = acc[t / 4 / B::MQ][t / 4 % B::MQ];
+                const int e = 4 * (t % 4);
+                lds[((group - 1) * NW + w) * PART + t * WAVE + lane] =
+                    __builtin_bit_cast(u32x4, f32x4{x[e], x[e + 1], x[e + 2], x[e + 3]});
+            }
+        }
+        lds_barrier();
+        if (group > 0) return;
+        for (int o = 0; o < WK - 1; ++o)
+#pragma unroll
+            for (int t = 0; t < B::MP * B::MQ * 4; ++t) {
+                const f32x4 y = __builtin_bit_cast(f32x4, lds[(o * NW + w) * PART + t * WAVE + lane]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[t / 4 / B::MQ][t / 4 % B::MQ][4 * (t % 4) + e] += y[e];
+            }
+    }
     // by way of LDS, so that a store instruction writes whole lines (32 bytes of
     // 32 rows each ran at 2.8 TB/s)
     constexpr int SIZE = B::TQ * HT / EPC<T>;
-    static_assert((BWD ? 2 : 1) * SIZE <= NBUF * (B::TP + B::TQ) * KCH, "tiles of results in LDS");
+    static_assert((BWD ? 2 : 1) * SIZE <= WK * BUF, "tiles of results in LDS");
     lds_barrier();                              // all waves are done with the operands
 #pragma unroll
     for (int i = 0; i < B::MQ; ++i) {
@@ -629,13 +666,16 @@ GatedWs gated_ws(int64_t n, int32_t dim, int32_t hidden, int32_t dtype, void* ba
     return dtype == RSE_F32 ? gated_ws<float>(n, dim, hidden, base) : gated_ws<uint16_t>(n, dim, hidden, base);
 }
 
-// f(block shape, blocks) of the projections
+// f(block shape, integral_constant<groups of waves>, blocks) of the projections
 template <typename T, typename F>
-int by_blocks(int64_t n, int32_t hidden, F f) {
+int by_blocks(int64_t n, int32_t dim, int32_t hidden, F f) {
     const auto blocks = [&](auto b) { return up(n, decltype(b)::TQ) * up(hidden, decltype(b)::TP / 2); };
-    if constexpr (sizeof(T) == 2)
-        if (blocks(InBlock<T>()) < CUS) return f(FewBlock(), blocks(FewBlock()));
-    return f(InBlock<T>(), blocks(InBlock<T>()));
+    using One = std::integral_constant<int, 1>;
+    if (blocks(InBlock<T>()) < CUS) {
+        if constexpr (sizeof(T) == 2) return f(FewBlock(), One(), blocks(FewBlock()));
+        else if (up(dim, KT<T>) >= GROUPS) return f(GroupBlock(), std::integral_constant<int, GROUPS>(), blocks(GroupBlock()));
+    }
+    return f(InBlock<T>(), One(), blocks(InBlock<T>()));
 }
 
 // f(T(), integral_constant<act>)
@@ -662,10 +702,11 @@ int seq_gated_linear_fwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const 
     return by_kind(dtype, act, [&](auto t, auto ac) -> int {
         using T = decltype(t);
         constexpr int ACT = decltype(ac)::value;
-        return by_blocks<T>(n, hidden, [&](auto b, int64_t blocks) -> int {
+        return by_blocks<T>(n, dim, hidden, [&](auto b, auto g, int64_t blocks) -> int {
             using B = decltype(b);
+            constexpr int WK = decltype(g)::value;
             if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
-            hipLaunchKernelGGL((k_gated<T, B, ACT, false>), dim3((unsigned)blocks), dim3(B::GT), 0, as_stream(stream), a,
+            hipLaunchKernelGGL((k_gated<T, B, WK, ACT, false>), dim3((unsigned)blocks), dim3(WK * B::GT), 0, as_stream(stream), a,
                                view<const T>(x), view<const T>(w_gate), view<const T>(w_up), Mat<const T>{nullptr, 0}, view<T>(out));
             return launch_status();
         });
@@ -701,11 +742,12 @@ int seq_gated_linear_bwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const 
         const Mat<T> d = {static_cast<T*>(ws.d), 2ll * hidden};
         const Mat<const T> dc = {d.p, d.stride};
         if (n > 0) {
-            int err = by_blocks<T>(n, hidden, [&](auto b, int64_t blocks) -> int {
+            int err = by_blocks<T>(n, dim, hidden, [&](auto b, auto g, int64_t blocks) -> int {
                 using B = decltype(b);
+                constexpr int WK = decltype(g)::value;
                 if (blocks > INT32_MAX || (x_plan.few ? tiles<OutFew>(n, dim) : tiles<OutBlock<T>>(n, dim)) > INT32_MAX / 64)
                     return RSE_ERR_UNSUPPORTED;
-                hipLaunchKernelGGL((k_gated<T, B, ACT, true>), dim3((unsigned)blocks), dim3(B::GT), 0, s, a, view<const T>(x),
+                hipLaunchKernelGGL((k_gated<T, B, WK, ACT, true>), dim3((unsigned)blocks), dim3(WK * B::GT), 0, s, a, view<const T>(x),
                                    view<const T>(w_gate), view<const T>(w_up), view<const T>(dout), d);
                 return launch_status();
             });
