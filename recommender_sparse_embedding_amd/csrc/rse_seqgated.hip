@@ -14,6 +14,8 @@
 // with both in fp32 and plain products, whose own rounding to bf16 is that).
 #include "rse_seqmma.h"
 
+#include <tuple>
+
 using namespace rse;
 using namespace rse_host;
 
@@ -58,6 +60,7 @@ template <typename T, int R, int GT>
 struct AlongRows {
     using TL = Tile<T, KT<T>>;
     static constexpr int PER = R * KCH / GT;
+    static_assert(PER * GT == R * KCH, "a piece for every thread");
     const T* p[PER];
     int64_t k_end;
     template <typename F>
@@ -95,6 +98,7 @@ template <typename T, int R, int GT, typename F>
 struct AcrossRows {
     using TL = Tile<T, R>;
     static constexpr int PER = R * KCH / GT;
+    static_assert(PER * GT == R * KCH, "a piece for every thread");
     F k_row;
     int64_t k_end;
     int cols;                           // of the tile, that exist
@@ -149,6 +153,7 @@ template <typename T, int R, int GT>
 struct StackedRows {
     using TL = Tile<T, R>;
     static constexpr int PER = R * KCH / GT;
+    static_assert(PER * GT == R * KCH, "a piece for every thread");
     Mat<const T> m, m2;
     int64_t turn, k_end;
     const T* p[PER];                    // of the step sent last
@@ -379,6 +384,10 @@ using InBlock = std::conditional_t<sizeof(T) == 2, Block<2, 4, 2, 2>, Block<1, 2
 // bf16, where the large tiles would not give every CU one: 256 rows of 512 by
 // 1536 11.7 us for 6.8, 2048 rows (192 large tiles) 13.5 for 13.1; 4096 rows (384) 20.0 for 23.0.
 using FewBlock = Block<1, 2, 2, 2>;
+// bf16, where the large tiles' columns past the end cost more than the 15 % that
+// narrower ones do: forward of 100000 rows of 256 by 184 41.0 us for 32.7, backward 59.3 for
+// 45.8; by 64 25.7 for 18.1.
+using InNarrow = Block<2, 2, 2, 2>;
 // fp32, whose products bound a CU: a wave a tile, and four of them a part of the
 // contraction each.  us, tiles of 64 by 64 / so: 46 rows of 792 by 320 32.5 / 12.6, 1011 of
 // 1496 by 304 59.8 / 34.1, 256 of 256 by 512 12.2 / 6.3.  (bf16, which waits for its loads
@@ -386,14 +395,32 @@ using FewBlock = Block<1, 2, 2, 2>;
 using GroupBlock = Block<1, 2, 1, 1>;
 constexpr int GROUPS = 4;
 constexpr int CUS = 256;
-template <typename T>
-using OutBlock = std::conditional_t<sizeof(T) == 2, Block<2, 4, 2, 2>, Block<1, 1, 2, 2>>;
-// And of dx and dW in bf16 where large tiles are few (see dx_plan, dw_plan).
+// Waves that share a SIMD, by registers and by LDS, and blocks on the GPU at once.
+template <typename B>
+constexpr int BY_LDS = 160 * 1024 / (NBUF * (B::TP + B::TQ) * KB) * B::GT / (4 * WAVE);
+template <typename B>
+constexpr int SHARE = B::MQ * B::MP >= 8 ? 2 : BY_LDS<B> < 4 ? BY_LDS<B> : 4;
+template <typename B>
+constexpr int AT_ONCE = CUS * SHARE<B> * 4 * WAVE / B::GT;
+
+// Of dx and dW, whose P side is dim: shapes of a type, widest first, with the
+// time of a column of theirs relative to the first's; and a small one for where tiles
+// are few (see dx_plan, dw_plan).  us, dx of 100000 rows with 512 hidden elements,
+// bf16 of 256 / 128 / 64 columns: dim 32 67 / 46 / 33, 64 75 / 51 / 36, 128 74 / 55 /
+// 58, 320 136 / 117 / 120; fp32 of 64 / 32: dim 32 164 / 102, 144 401 / 363.
 using OutFew = Block<1, 1, 2, 2>;
-template <typename B>
-constexpr int SHARE = B::MQ * B::MP >= 8 ? 2 : 4;       // waves that share a SIMD
-template <typename B>
-constexpr int AT_ONCE = 256 * SHARE<B> * 4 * WAVE / B::GT;      // blocks on the GPU at once
+template <typename T>
+struct Out;
+template <>
+struct Out<uint16_t> {
+    using Shapes = std::tuple<Block<2, 4, 2, 2>, Block<2, 2, 2, 2>, Block<2, 2, 4, 1>>;
+    static constexpr double COST[] = {1.0, 1.15, 1.4};
+};
+template <>
+struct Out<float> {
+    using Shapes = std::tuple<Block<1, 1, 2, 2>, Block<1, 1, 2, 1>>;
+    static constexpr double COST[] = {1.0, 1.1};
+};
 
 // out (BWD: dg beside du) of TQ rows by TP / 2 hidden elements: the tile's P
 // rows are TP / 2 rows of Wg, then the same ones of Wu, and a wave's
@@ -599,22 +626,52 @@ int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 template <typename B>
 int64_t tiles(int64_t q, int64_t p) { return up(q, B::TQ) * up(p, B::TP); }
 
-// How dx and dW are formed: with large tiles or, where these are too few for the
-// CUs, small ones (of bf16), and in how many parts of the contraction.
+// How dx and dW are formed: by which of the type's shapes or, where its tiles
+// are too few for the CUs, by the small one, and in how many parts of the contraction.
 struct Plan {
-    bool few;
+    int shape;                          // -1: the small one
     int splits;
     int64_t len;                        // of a part
 };
+// f(the shape)
+template <typename T, int I = 0, typename F>
+int64_t by_shape(int shape, F f) {
+    using S = typename Out<T>::Shapes;
+    if (shape < 0) return f(OutFew());
+    if constexpr (I + 1 < (int)std::tuple_size_v<S>)
+        if (shape > I) return by_shape<T, I + 1>(shape, f);
+    return f(std::tuple_element_t<I, S>());
+}
+template <typename T>
+int64_t tiles_of(int shape, int64_t q, int64_t p) {
+    return by_shape<T>(shape, [&](auto b) { return tiles<decltype(b)>(q, p); });
+}
+// the shape that takes the least for its columns, those past dim included
+template <typename T>
+int shape_for(int32_t dim) {
+    int best = 0;
+    double least = 0;
+    for (int i = 0; i < (int)std::tuple_size_v<typename Out<T>::Shapes>; ++i) {
+        const double cost = Out<T>::COST[i] * by_shape<T>(i, [&](auto b) { return up(dim, decltype(b)::TP) * decltype(b)::TP; });
+        if (i == 0 || cost < least) {
+            least = cost;
+            best = i;
+        }
+    }
+    return best;
+}
+
 // dx: parts where the small tiles are few too, of eight steps at least, for two
 // blocks a CU (four: no faster).  3196 rows of 80 by 648 in fp32 42 us whole and 22
 // with the join; in bf16 500 of 256 by 1024 41 with large tiles and 8, 3196 of 512 by
 // 1368 56 and 32.
 template <typename T>
 Plan dx_plan(int64_t n, int32_t dim, int32_t hidden) {
-    Plan p = {tiles<OutBlock<T>>(n, dim) < CUS, 1, 2ll * hidden};
+    Plan p = {shape_for<T>(dim), 1, 2ll * hidden};
+    if (tiles_of<T>(p.shape, n, dim) >= CUS) return p;
+    p.shape = -1;
     const int64_t blocks = tiles<OutFew>(n, dim), steps = up(2ll * hidden, KT<T>);
-    int64_t s = p.few && blocks > 0 ? 2 * CUS / blocks : 1;
+    int64_t s = blocks > 0 ? 2 * CUS / blocks : 1;
     if (s > steps / 8) s = steps / 8;
     if (s > 1) {
         p.len = up(steps, s) * KT<T>;
@@ -624,15 +681,16 @@ Plan dx_plan(int64_t n, int32_t dim, int32_t hidden) {
 }
 
 // dW: parts of the events, of whole steps and 128 events at least: as many as
-// make the rounds of blocks (SHARE a CU at once) shortest, the time to add a part
+// make the rounds of blocks (AT_ONCE) shortest, the time to add a part
 // up taken as that of an event for 24000 elements (413696 rows of 256 by 1024 in
 // 32 parts 14 us beside 459, 24571 of 1024 by 2736 in 5 22 beside 306).
 template <typename T>
 Plan dw_plan(int64_t n, int32_t dim, int32_t hidden) {
     const int64_t most = up(n, 128) < 64 ? up(n, 128) : 64;
-    Plan p = {tiles<OutBlock<T>>(2ll * hidden, dim) * most < CUS, 1, 0};
-    const int64_t t = p.few ? tiles<OutFew>(2ll * hidden, dim) : tiles<OutBlock<T>>(2ll * hidden, dim);
-    const int64_t at_once = p.few ? AT_ONCE<OutFew> : AT_ONCE<OutBlock<T>>;
+    Plan p = {shape_for<T>(dim), 1, 0};
+    if (tiles_of<T>(p.shape, 2ll * hidden, dim) * most < CUS) p.shape = -1;
+    const int64_t t = tiles_of<T>(p.shape, 2ll * hidden, dim);
+    const int64_t at_once = by_shape<T>(p.shape, [](auto b) -> int64_t { return AT_ONCE<decltype(b)>; });
     double best = 0;
     for (int64_t c = 1; c <= most; ++c) {
         const double cost = (double)up(t * c, at_once) * ((double)n / c) + c * (2.0 * hidden * dim / 24000);
@@ -671,6 +729,8 @@ template <typename T, typename F>
 int by_blocks(int64_t n, int32_t dim, int32_t hidden, F f) {
     const auto blocks = [&](auto b) { return up(n, decltype(b)::TQ) * up(hidden, decltype(b)::TP / 2); };
     using One = std::integral_constant<int, 1>;
+    if constexpr (sizeof(T) == 2)
+        if (blocks(InBlock<T>()) >= CUS && up(hidden, 64) * 64 * 1.15 < up(hidden, 128) * 128) return f(InNarrow(), One(), blocks(InNarrow()));
     if (blocks(InBlock<T>()) < CUS) {
         if constexpr (sizeof(T) == 2) return f(FewBlock(), One(), blocks(FewBlock()));
         else if (up(dim, KT<T>) >= GROUPS) return f(GroupBlock(), std::integral_constant<int, GROUPS>(), blocks(GroupBlock()));
@@ -745,29 +805,27 @@ int seq_gated_linear_bwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const 
             int err = by_blocks<T>(n, dim, hidden, [&](auto b, auto g, int64_t blocks) -> int {
                 using B = decltype(b);
                 constexpr int WK = decltype(g)::value;
-                if (blocks > INT32_MAX || (x_plan.few ? tiles<OutFew>(n, dim) : tiles<OutBlock<T>>(n, dim)) > INT32_MAX / 64)
+                if (blocks > INT32_MAX || tiles_of<T>(x_plan.shape, n, dim) > INT32_MAX / 64)
                     return RSE_ERR_UNSUPPORTED;
                 hipLaunchKernelGGL((k_gated<T, B, WK, ACT, true>), dim3((unsigned)blocks), dim3(WK * B::GT), 0, s, a, view<const T>(x),
                                    view<const T>(w_gate), view<const T>(w_up), view<const T>(dout), d);
                 return launch_status();
             });
             if (err) return err;
-            const auto dw = [&](auto b) {
+            by_shape<T>(w_plan.shape, [&](auto b) -> int64_t {
                 using B = decltype(b);
                 hipLaunchKernelGGL((k_gated_dw<T, B>), dim3((unsigned)(w_plan.splits * tiles<B>(2ll * hidden, dim))), dim3(B::GT), 0, s,
                                    a, dc, view<const T>(x), w_plan.len, ws.dw);
-            };
-            const auto dx_of = [&](auto b) {
+                return 0;
+            });
+            // (after dW, which reads x: dx may be x)
+            by_shape<T>(x_plan.shape, [&](auto b) -> int64_t {
                 using B = decltype(b);
                 hipLaunchKernelGGL((k_gated_dx<T, B>), dim3((unsigned)(x_plan.splits * tiles<B>(n, dim))), dim3(B::GT), 0, s, a, dc,
                                    view<const T>(w_gate), view<const T>(w_up), view<T>(dx), x_plan.len,
                                    x_plan.splits > 1 ? ws.dx : nullptr);
-            };
-            if (w_plan.few) dw(OutFew());
-            else dw(OutBlock<T>());
-            // (after dW, which reads x: dx may be x)
-            if (x_plan.few) dx_of(OutFew());
-            else dx_of(OutBlock<T>());
+                return 0;
+            });
             if (x_plan.splits > 1)
                 hipLaunchKernelGGL((k_gated_join<T>), dim3(fill_blocks(n * dim, 4 * JT, 4096)), dim3(JT), 0, s, ws.dx, x_plan.splits, n,
                                    n, dim, view<T>(dx), view<T>(dx));

@@ -288,8 +288,9 @@ def test_gated_refusals(rse):
 
 
 # Sizes whose tiles are enough for every CU, so that bf16 takes the large ones:
-# of the projections, dx and dW; of the projections alone; of dW alone.
-LARGE = [(16500, 264, 200), (5000, 24, 904), (130, 2056, 4104)]
+# of the projections, dx and dW; of the projections alone; of dW alone; and the
+# narrow ones of all of them, by two widths.
+LARGE = [(16500, 264, 200), (5000, 24, 904), (130, 2056, 4104), (66000, 40, 64), (33000, 104, 184)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
