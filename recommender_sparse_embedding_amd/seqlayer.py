@@ -11,6 +11,7 @@ returns are allocated for that stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -60,6 +61,17 @@ def _mat(t: torch.Tensor, like: torch.Tensor, n: int, width: int, name: str, per
 
 def _ref(m: RseSeqMat | None):
     return None if m is None else ctypes.byref(m)
+
+
+# workspace sizes, by sizes alone
+@functools.lru_cache(maxsize=64)
+def _norm_bytes(n: int, dim: int, kind: int) -> int:
+    return _size(lib.rse_seq_layer_norm_bwd_workspace_size, "rse_seq_layer_norm_bwd_workspace_size", n, dim, kind)
+
+
+@functools.lru_cache(maxsize=64)
+def _gated_bytes(n: int, dim: int, hidden: int, kind: int) -> int:
+    return _size(lib.rse_seq_gated_linear_bwd_workspace_size, "rse_seq_gated_linear_bwd_workspace_size", n, dim, hidden, kind)
 
 
 class LayerNormOut(NamedTuple):
@@ -113,8 +125,7 @@ def seq_layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: torch.Tensor |
     dsm = None if dsum is None else _mat(dsum, x, n, dim, "dsum")
     with _on(stream):
         dw, db = (torch.empty(dim, dtype=torch.float32, device=x.device) for _ in range(2))
-        ws = _bytes(_size(lib.rse_seq_layer_norm_bwd_workspace_size, "rse_seq_layer_norm_bwd_workspace_size", n, dim, kind),
-                    x.device)
+        ws = _bytes(_norm_bytes(n, dim, kind), x.device)
     if out is None:
         out, dxm = _new(x, n, dim, stream)
     else:
@@ -160,8 +171,7 @@ def seq_gated_linear_bwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tens
     with _on(stream):
         if grads is None:
             grads = tuple(torch.empty(s, dtype=x.dtype, device=x.device) for s in shapes)
-        ws = _bytes(_size(lib.rse_seq_gated_linear_bwd_workspace_size, "rse_seq_gated_linear_bwd_workspace_size", n, dim,
-                          hidden, kind), x.device)
+        ws = _bytes(_gated_bytes(n, dim, hidden, kind), x.device)
     mats += [_mat(t, x, *s, name, per) for t, s, name in zip(grads, shapes, ("dx", "dw_gate", "dw_up"))]
     check(lib.seq_gated_linear_bwd(*map(_ref, mats[:4]), n, dim, hidden, kind, act, *map(_ref, mats[4:]), _ptr(ws), ws.numel(),
                                    _stream(stream)), "seq_gated_linear_bwd")
