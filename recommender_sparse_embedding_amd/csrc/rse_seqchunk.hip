@@ -672,14 +672,16 @@ __global__ __launch_bounds__(CW * 64) __attribute__((amdgpu_waves_per_eu(CW == 8
 // 64 keys at a time in bf16 (32: 207 us there): one maximum and one question whether it
 // has moved, and one for the bias, for twice the products.  In fp32 32 (64: 180 us
 // for 139 on 24 users of up to 2048 events and 512 new ones, rows of 64).
-// Two waves share a SIMD, and their products and vector operations take turns
+// Dims of 32 leave registers for three waves a SIMD: 95 users of up to 53 events and
+// 292 new ones, 32 heads on 4, bf16 121 us for 95; where histories are long no faster.
+// In general two waves share a SIMD, and their products and vector operations take turns
 // more than they overlap: 25 % of the cycles are products in bf16, 36 % in fp32.
 template <typename T, int D>
 struct Many {
     static constexpr int RB = D * (int)sizeof(T), KT = sizeof(T) == 2 ? 64 : 32;
     static constexpr int NST = KT * RB <= 8192 ? 4 : sizeof(T) == 2 ? 2 : 3;       // (40 to 105 KiB: two blocks a CU, one of rows of 512 bytes)
     static constexpr int CH = Tile<T, D>::CH, NT = CW * WAVE, PER = KT * CH / NT;
-    static constexpr int WAVES = RB <= 256 ? 2 : 1;         // that share a SIMD
+    static constexpr int WAVES = D == 32 ? 3 : RB <= 256 ? 2 : 1;       // that share a SIMD
     static constexpr int PAGES = 512;                       // of the table in LDS at a time
 };
 
