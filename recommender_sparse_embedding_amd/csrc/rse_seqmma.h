@@ -238,14 +238,17 @@ __device__ __forceinline__ void to_lds(const void* p, const void* lds) {
 __device__ __forceinline__ void to_lds4(const void* p, const void* lds) {
     asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(lds_address(lds)) : "memory");
 }
-// from `bytes` behind a place that the wave has in common
+// from `bytes` behind a place that the wave has in common.  A memory instruction
+// may read a scalar register five wait states after a vector one wrote it, as `from`
+// is, and the compiler does not count those inside the assembly: the move is one,
+// s_nop 3 four.
 __device__ __forceinline__ void to_lds(const void* base, uint32_t bytes, const void* lds) {
     const int64_t from = uniform((int64_t)(uintptr_t)base);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(bytes), "s"(from), "s"(lds_address(lds)) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(bytes), "s"(from), "s"(lds_address(lds)) : "memory");
 }
 __device__ __forceinline__ void to_lds4(const void* base, uint32_t bytes, const void* lds) {
     const int64_t from = uniform((int64_t)(uintptr_t)base);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(bytes), "s"(from), "s"(lds_address(lds)) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dword %0, %1" ::"v"(bytes), "s"(from), "s"(lds_address(lds)) : "memory");
 }
 // At most N of the wave's memory operations are still in flight.  The compiler
 // does not see this wait: for what it loads to registers itself it adds its own
