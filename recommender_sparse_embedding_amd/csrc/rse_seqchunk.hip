@@ -125,23 +125,23 @@ __device__ __forceinline__ bool find_work(const SeqArgs& a, const PageArgs& p, c
         x = a.offsets[i];
         y = a.offsets[i + 1];
     }
-    int64_t t;
+    int64_t t = 0;
     if (lo.per_seq) {
         const uint32_t n = (uint32_t)a.batch, first = item / n;
         w.b = item - first * n;
         t = first;
     } else {
         w.b = wave_last_le(a.batch, [&](int64_t x) { return a.offsets[x] / tq + x; }, (int64_t)item);
-        t = (int64_t)item - (a.offsets[w.b] / tq + w.b);
     }
     const int64_t s = a.offsets[w.b], e = a.offsets[w.b + 1], n = p.lens[w.b];
     w.s = uniform(s);
     const int64_t end = uniform(e);
     w.had = uniform(n);
-    t = uniform(t);
     if (check && (x > y || (i == 0 && x != 0) || (i == a.batch - 1 && y != a.n_events)))
         set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
     w.count = user_events(a, p, w.s, end, w.had, lane_id() == 0);
+    if (w.count <= 0) return false;             // (past this s is an event's number, and the products do not overflow)
+    if (!lo.per_seq) t = (int64_t)item - (w.s / tq + w.b);
     if (t < 0 || t * tq >= w.count) return false;
     w.tile = (int)t;
     w.split = 0;
