@@ -227,16 +227,19 @@ __device__ __forceinline__ void store_four(uint16_t* p, f32x4 x) {
 // 16 bytes (or 4) from memory straight to LDS: lane l's piece lands 16 l (4 l)
 // bytes past `lds`, the same of all lanes.  In assembly, so that the compiler does not make every read of
 // LDS wait for the loads in flight to other buffers; the waits are the
-// caller's.  Nothing is returned to registers, and the compiler keeps nothing in
-// m0.
+// caller's.  Nothing is returned to registers.  m0 is named as written (the compiler
+// may keep a value there from one use to the next; it warns that it does not save
+// registers of its own, which nothing here asks for).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ uint32_t lds_address(const void* lds) {
     return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(RSE_LDS const void*)lds);
 }
 __device__ __forceinline__ void to_lds(const void* p, const void* lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds_address(lds)) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds_address(lds)) : "memory", "m0");
 }
 __device__ __forceinline__ void to_lds4(const void* p, const void* lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(lds_address(lds)) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(lds_address(lds)) : "memory", "m0");
 }
 // from `bytes` behind a place that the wave has in common.  A memory instruction
 // may read a scalar register five wait states after a vector one wrote it, as `from`
@@ -244,12 +247,13 @@ __device__ __forceinline__ void to_lds4(const void* p, const void* lds) {
 // s_nop 3 four.
 __device__ __forceinline__ void to_lds(const void* base, uint32_t bytes, const void* lds) {
     const int64_t from = uniform((int64_t)(uintptr_t)base);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(bytes), "s"(from), "s"(lds_address(lds)) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(bytes), "s"(from), "s"(lds_address(lds)) : "memory", "m0");
 }
 __device__ __forceinline__ void to_lds4(const void* base, uint32_t bytes, const void* lds) {
     const int64_t from = uniform((int64_t)(uintptr_t)base);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dword %0, %1" ::"v"(bytes), "s"(from), "s"(lds_address(lds)) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dword %0, %1" ::"v"(bytes), "s"(from), "s"(lds_address(lds)) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // At most N of the wave's memory operations are still in flight.  The compiler
 // does not see this wait: for what it loads to registers itself it adds its own
 // where the value is first used, be it in a loop, unless none_left, which it

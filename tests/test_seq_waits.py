@@ -29,8 +29,22 @@ __global__ void by_four(const uint64_t* place, const uint32_t* bytes, uint32_t* 
 """
 
 
-@pytest.fixture(scope="module")
-def listing(tmp_path_factory):
+# a message's value passes through m0, as a copy's place in LDS does
+MESSAGES = """
+#include "rse_seqmma.h"
+__global__ void between(const uint64_t* place, uint32_t* out, int value) {
+    __shared__ rse::u32x4 lds[64];
+    const void* p = reinterpret_cast<const void*>(place[threadIdx.x]);
+    __builtin_amdgcn_s_sendmsg(1, value);
+    rse::to_lds(p, lds);
+    __builtin_amdgcn_s_sendmsg(1, value);
+    rse::loads_left<0>();
+    out[threadIdx.x] = lds[threadIdx.x][0];
+}
+"""
+
+
+def _listing(tmp_path, source):
     spec = importlib.util.spec_from_file_location("_rse_build_flags", os.path.join(PACKAGE, "build.py"))
     build = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(build)
@@ -38,8 +52,8 @@ def listing(tmp_path_factory):
         cc = build.hipcc()
     except RuntimeError as e:
         pytest.skip(str(e))
-    at = tmp_path_factory.mktemp("waits")
-    (at / "waits.hip").write_text(SOURCE)
+    at = tmp_path
+    (at / "waits.hip").write_text(source)
     r = subprocess.run([cc, *build.HIPCC_FLAGS, "-S", "--cuda-device-only", "-I", os.path.join(PACKAGE, "csrc"),
                         str(at / "waits.hip"), "-o", str(at / "waits.s")], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
@@ -60,10 +74,10 @@ def _scalars(operand):
     return {int(one[1])} if one else set(range(int(many[1]), int(many[2]) + 1)) if many else set()
 
 
-def test_scalar_addresses_wait_for_the_vector_instruction_that_wrote_them(listing):
+def test_scalar_addresses_wait_for_the_vector_instruction_that_wrote_them(tmp_path):
     """Five wait states from a vector instruction's write of a scalar register
     to a memory instruction that reads it."""
-    run = list(_instructions(listing))
+    run = list(_instructions(_listing(tmp_path, SOURCE)))
     loads = [i for i, (op, _) in enumerate(run) if op.startswith("global_load_lds")]
     assert len(loads) == 2
     for i in loads:
@@ -76,3 +90,12 @@ def test_scalar_addresses_wait_for_the_vector_instruction_that_wrote_them(listin
                 break
             waited += 1 + (int(args[0]) if op == "s_nop" else 0)
         assert written, "the address comes from a vector register"
+
+
+def test_m0_is_not_kept_over_a_copy(tmp_path):
+    """What the compiler put into m0 before a copy it puts there again behind it
+    (compiled only)."""
+    run = list(_instructions(_listing(tmp_path, MESSAGES)))
+    ops = [op if op != "s_mov_b32" else f"{op} {args[0]}" for op, args in run]
+    ops = [op for op in ops if op in ("s_mov_b32 m0", "s_sendmsg") or op.startswith("global_load_lds")]
+    assert ops == ["s_mov_b32 m0", "s_sendmsg", "s_mov_b32 m0", "global_load_lds_dwordx4", "s_mov_b32 m0", "s_sendmsg"]
