@@ -567,6 +567,9 @@ int dlrm_interaction_bwd(const float* d_dense, const float* d_pooled, const floa
  * products as pairs of bf16 values (2^-16 of each is lost); the bias gradient
  * is summed from the fp32 values.  No floating-point atomics are shared
  * between lanes: results are run-to-run identical.
+ * Any call of this and the next two sections returns RSE_ERR_UNSUPPORTED where
+ * its blocks are more than one launch holds: 2^32 threads, which are 2^24 tiles
+ * (of 32 to 128 events of a head, or of rows by columns) or users and heads.
  */
 #define RSE_SEQ_MAX_BOUNDARIES 127
 #define RSE_SEQ_MAX_HEADS 256

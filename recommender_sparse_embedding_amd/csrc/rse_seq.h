@@ -147,6 +147,9 @@ struct rse_seqcache {
 
 namespace rse_host {
 
+// A launch numbers its threads along an axis in 32 bits.
+inline bool launch_holds(int64_t blocks, int threads) { return blocks <= UINT32_MAX / threads; }
+
 // Rows of the handle's type: present, 16-byte aligned, strides in 16 bytes.
 inline bool rows_ok(const rse_seq_rows* r, int32_t dtype) {
     const int64_t e = dtype == RSE_F32 ? 4 : 2;

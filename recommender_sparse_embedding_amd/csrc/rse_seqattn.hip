@@ -248,7 +248,7 @@ int run_fwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, cons
     ShortGrid sg = {0, 0};
     if (KEEP == SAVE) sg = short_grid(a.batch, hblocks, a.max_len, SH::WAVES);
     const int64_t blocks = hblocks * (KEEP == SAVE ? sg.blocks : tg.items);
-    if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+    if (!launch_holds(blocks, SH::WAVES * WAVE)) return RSE_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)blocks), block(SH::WAVES * WAVE);
     if (sv.lse2)
         hipLaunchKernelGGL((k_attn_fwd<T, D, SH, KEEP>), grid, block, 0, s, a, tg, rows_view<const T>(q),

@@ -646,7 +646,7 @@ int run_bwd(const SeqArgs& a, const rse_seq_rows* q, const rse_seq_rows* k, cons
     const int64_t gblocks = IN_GROUP ? n_kv : (n_kv + KH - 1) / KH;
     const ShortGrid sg = short_grid(a.batch, gblocks, a.max_len, KS::WAVES);
     const int64_t blocks = gblocks * (brief ? sg.blocks : tk.items);
-    if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+    if (!launch_holds(blocks, KS::WAVES * WAVE)) return RSE_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)w.blocks, (a.n_heads + WH - 1) / WH), block(QS::WAVES * WAVE);
     const size_t lds = QS::WAVES * nb * cols * sizeof(float);
     if constexpr (brief)

@@ -717,7 +717,7 @@ int run_step(const rse_seqattn* at, const rse_seqcache* c, const StepArgs& a, co
     const size_t tiles = SW * 32 * D * sizeof(T), sums = (size_t)SW * p.cols * D * sizeof(float);
     const size_t lds = (tiles > sums ? tiles : sums) + (size_t)(a.n_bounds + 1) * p.cols * sizeof(float);
     const int64_t grid = a.batch * at->n_kv_heads * p.blocks * p.splits;
-    if (grid > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+    if (!launch_holds(grid, SW * WAVE) || (p.splits > 1 && !launch_holds(a.batch * a.n_heads, CB))) return RSE_ERR_UNSUPPORTED;
     const int few = std::is_same_v<T, float> && p.cols <= FEW_HEADS ? p.cols : 0;
     if constexpr (std::is_same_v<T, float>) {
         const auto run = [&](auto kernel, int heads) {

@@ -999,7 +999,7 @@ ChunkWs chunk_ws(const rse_seqattn* at, const ChunkPlan& p, void* base) {
 template <typename T, int D>
 int run_chunk(const rse_seqcache* c, const SeqArgs& a, const PageArgs& pg, const ChunkPlan& p, const ChunkWs& ws,
               const rse_seq_rows* q, const rse_seq_rows* k, const rse_seq_rows* v, const rse_seq_rows* out, hipStream_t s) {
-    if (p.blocks() > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+    if (!launch_holds(p.blocks(), CW * WAVE)) return RSE_ERR_UNSUPPORTED;
     const size_t lds = (size_t)p.cl.cols * ((a.n_bounds + 1) | 1) * sizeof(float);
     const Layout lo = {(uint32_t)p.units, (uint32_t)p.grid.items, (uint32_t)p.grid.per_seq, p.want ? ws.list : nullptr};
     const dim3 grid((unsigned)p.blocks());

@@ -704,6 +704,12 @@ Plan dw_plan(int64_t n, int32_t dim, int32_t hidden) {
     return p;
 }
 
+// whether a launch holds the plan's blocks
+template <typename T>
+bool plan_held(const Plan& p, int64_t q, int64_t c) {
+    return by_shape<T>(p.shape, [&](auto b) { return (int64_t)launch_holds(p.splits * tiles<decltype(b)>(q, c), decltype(b)::GT); });
+}
+
 struct GatedWs {
     void* d;
     float *dw, *dx;                     // parts
@@ -765,7 +771,7 @@ int seq_gated_linear_fwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const 
         return by_blocks<T>(n, dim, hidden, [&](auto b, auto g, int64_t blocks) -> int {
             using B = decltype(b);
             constexpr int WK = decltype(g)::value;
-            if (blocks > INT32_MAX) return RSE_ERR_UNSUPPORTED;
+            if (!launch_holds(blocks, WK * B::GT)) return RSE_ERR_UNSUPPORTED;
             hipLaunchKernelGGL((k_gated<T, B, WK, ACT, false>), dim3((unsigned)blocks), dim3(WK * B::GT), 0, as_stream(stream), a,
                                view<const T>(x), view<const T>(w_gate), view<const T>(w_up), Mat<const T>{nullptr, 0}, view<T>(out));
             return launch_status();
@@ -805,7 +811,7 @@ int seq_gated_linear_bwd(const rse_seq_mat* x, const rse_seq_mat* w_gate, const 
             int err = by_blocks<T>(n, dim, hidden, [&](auto b, auto g, int64_t blocks) -> int {
                 using B = decltype(b);
                 constexpr int WK = decltype(g)::value;
-                if (blocks > INT32_MAX || tiles_of<T>(x_plan.shape, n, dim) > INT32_MAX / 64)
+                if (!launch_holds(blocks, WK * B::GT) || !plan_held<T>(x_plan, n, dim) || !plan_held<T>(w_plan, 2ll * hidden, dim))
                     return RSE_ERR_UNSUPPORTED;
                 hipLaunchKernelGGL((k_gated<T, B, WK, ACT, true>), dim3((unsigned)blocks), dim3(WK * B::GT), 0, s, a, view<const T>(x),
                                    view<const T>(w_gate), view<const T>(w_up), view<const T>(dout), d);

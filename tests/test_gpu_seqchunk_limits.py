@@ -37,3 +37,26 @@ def test_offsets_at_the_ends_of_64_bits(rse, users, dtype):  # noqa: F811
             u.call(out=out)
             assert u.attn.status() == BAD, (at, value)
             _left_or_right(out, ref, (at, value))
+
+
+def test_more_blocks_than_a_launch_holds(rse):  # noqa: F811
+    """2^22 users of 4 heads are 2^24 blocks of 256 threads: refused by name, in
+    every call over users or events, and nothing is written."""
+    n, H, D = 1 << 22, 4, 32
+    attn = rse.SeqAttention(H, H, D, BF16)
+    row = torch.zeros((1, H, D), dtype=torch.bfloat16, device="cuda").expand(n, H, D)
+    out = torch.full((n, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    ints = torch.zeros(n, dtype=torch.int32, device="cuda")
+    off, lens = torch.arange(n + 1, device="cuda"), torch.zeros(n, dtype=torch.int64, device="cuda")
+    bias = torch.zeros((H, 1), device="cuda")
+    cache = rse.SeqCache.empty(4, 8, H, D)
+    saved = torch.empty(1 << 32, dtype=torch.uint8, device="cuda")
+    grads = [torch.empty_like(out) for _ in range(3)]
+    for call in (lambda: rse.seq_attention_chunk(attn, cache, row, row, row, ints, bias, off, ints.view(n, 1), lens, max_new=1, out=out),
+                 lambda: rse.seq_attention_step(attn, cache, row, row, row, ints, bias, ints.view(n, 1), lens, out=out),
+                 lambda: rse.seq_attention_fwd(attn, row, row, row, ints, bias, off, max_len=200, out=out),
+                 lambda: rse.seq_attention_bwd(attn, row, row, row, ints, bias, off, saved, row, max_len=200, grads=grads)):
+        with pytest.raises(rse.RseError, match="UNSUPPORTED"):
+            call()
+    assert torch.all(out == 7)
+    assert attn.status() == 0 and cache.status() == 0
