@@ -4,8 +4,8 @@ the gated feed-forward's projections of rse.h.
 Rows are [n, width] tensors whose last dimension is contiguous; the distance
 between rows is free (for the gated calls in steps of 16 bytes), so slices of
 wider tensors and expanded inputs will do.  Every call is ordered on the given
-stream (default: the current one) of the current device, and tensors it
-returns are allocated for that stream.
+stream (default: the current one) of the current device, where all its tensors
+are, and tensors it returns are allocated for that stream.
 """
 
 from __future__ import annotations
@@ -18,16 +18,16 @@ import torch
 
 from . import BF16, F32, SILU, _bytes, _ptr, lib
 from ._lib import RseSeqMat, check
-from .sequence import _PER16, _here, _on, _on_empty, _size, _stream, _vector
+from .sequence import _PER16, _beside, _here, _on, _on_empty, _size, _stream, _vector
 
 _KIND = {torch.float32: F32, torch.bfloat16: BF16}
 
 
-def _kind(x: torch.Tensor, name: str) -> int:
+def _kind(x: torch.Tensor, name: str, stream) -> int:
     kind = _KIND.get(x.dtype)
     if kind is None or not x.is_cuda or x.dim() != 2:
         raise TypeError(f"{name}: expected a fp32 or bf16 [n, width] CUDA tensor, got {x.dtype} {tuple(x.shape)} on {x.device}")
-    _here(x, name)
+    _here(x, name, stream)
     return kind
 
 
@@ -59,6 +59,14 @@ def _mat(t: torch.Tensor, like: torch.Tensor, n: int, width: int, name: str, per
     return RseSeqMat(p, row)
 
 
+def _floats(t: torch.Tensor | None, like: torch.Tensor, n: int, name: str):
+    if t is None:
+        return None
+    p = _vector(t, torch.float32, n, name)
+    _beside(t, like, name)
+    return p
+
+
 def _ref(m: RseSeqMat | None):
     return None if m is None else ctypes.byref(m)
 
@@ -87,11 +95,10 @@ def seq_layer_norm_fwd(x: torch.Tensor, weight: torch.Tensor | None, bias: torch
     it is stored (the stream that later layers and the backward read; sum_out:
     a tensor to write it to, x or residual for example).  weight, bias: fp32
     [dim] or None (1 and 0)."""
-    kind = _kind(x, "x")
+    kind = _kind(x, "x", stream)
     n, dim = x.shape
     xm = _mat(x, x, n, dim, "x")
-    wp = None if weight is None else _vector(weight, torch.float32, dim, "weight")
-    bp = None if bias is None else _vector(bias, torch.float32, dim, "bias")
+    wp, bp = _floats(weight, x, dim, "weight"), _floats(bias, x, dim, "bias")
     if residual is None and sum_out is not None:
         raise ValueError("sum_out is given without a residual")
     if out is None:
@@ -117,11 +124,10 @@ def seq_layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: torch.Tensor |
     were normalised (the forward's x, or its sum); stats: the forward's.  dsum:
     the gradient that reaches the sum by the stream; dx is then the gradient of
     x and of the residual.  dweight, dbias: fp32 [dim]."""
-    kind = _kind(x, "x")
+    kind = _kind(x, "x", stream)
     n, dim = x.shape
     xm, dym = _mat(x, x, n, dim, "x"), _mat(dy, x, n, dim, "dy")
-    wp = None if weight is None else _vector(weight, torch.float32, dim, "weight")
-    sp = _vector(stats, torch.float32, 2 * n, "stats")
+    wp, sp = _floats(weight, x, dim, "weight"), _floats(stats, x, 2 * n, "stats")
     dsm = None if dsum is None else _mat(dsum, x, n, dim, "dsum")
     with _on(stream):
         dw, db = (torch.empty(dim, dtype=torch.float32, device=x.device) for _ in range(2))
@@ -135,8 +141,8 @@ def seq_layer_norm_bwd(x: torch.Tensor, dy: torch.Tensor, weight: torch.Tensor |
     return out, dw, db
 
 
-def _gated(x, w_gate, w_up):
-    kind = _kind(x, "x")
+def _gated(x, w_gate, w_up, stream):
+    kind = _kind(x, "x", stream)
     n, dim = x.shape
     if w_gate.dim() != 2:
         raise ValueError(f"w_gate: expected [hidden, dim], got {tuple(w_gate.shape)}")
@@ -150,7 +156,7 @@ def seq_gated_linear_fwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tens
     """act(x w_gate^T) (x w_up^T) [n, hidden] for x [n, dim] and w_gate, w_up
     [hidden, dim] of one type; dim and hidden are multiples of 16 bytes.  act:
     SIGMOID, SILU or GELU."""
-    kind, n, dim, hidden, per, mats = _gated(x, w_gate, w_up)
+    kind, n, dim, hidden, per, mats = _gated(x, w_gate, w_up, stream)
     if out is None:
         out, o = _new(x, n, hidden, stream)
     else:
@@ -165,7 +171,7 @@ def seq_gated_linear_bwd(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tens
     """(dx, dw_gate, dw_up) for the upstream gradient dout [n, hidden]; the other
     arguments are the forward's, which leaves nothing else for this call.
     grads: tensors to write them to (halves of one joint gradient, for example)."""
-    kind, n, dim, hidden, per, mats = _gated(x, w_gate, w_up)
+    kind, n, dim, hidden, per, mats = _gated(x, w_gate, w_up, stream)
     mats.append(_mat(dout, x, n, hidden, "dout", per))
     shapes = ((n, dim), (hidden, dim), (hidden, dim))
     with _on(stream):

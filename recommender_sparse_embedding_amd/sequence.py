@@ -42,10 +42,18 @@ def _stream(stream=None) -> int:
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _here(t: torch.Tensor, name: str):
+def _here(t: torch.Tensor, name: str, stream=None):
     """t: a CUDA tensor (so that the runtime is up)."""
     if t.get_device() != _current_device():
         raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    if stream is not None and stream.device.index != t.get_device():
+        raise ValueError(f"the stream is of {stream.device}, {name} on {t.device}")
+
+
+def _beside(t: torch.Tensor, other: torch.Tensor, name: str):
+    """t: a CUDA tensor on other's device (a kernel would fault on another's memory)."""
+    if t.get_device() != other.get_device():
+        raise ValueError(f"{name} is on {t.device}, the rows on {other.device}")
 
 
 def _on(stream):
@@ -347,11 +355,14 @@ def seq_attention_chunk(attn: SeqAttention, cache: SeqCache, q: torch.Tensor, k:
     n = q.shape[0]
     dt, H, Hk, D = attn.torch_dtype, attn.n_heads, attn.n_kv_heads, attn.dim
     args = [_rows(q, dt, n, H, D, "q"), _rows(k, dt, n, Hk, D, "k"), _rows(v, dt, n, Hk, D, "v")]
-    _here(q, "q")
+    _here(q, "q", stream)
     b = _batch(attn, n, pos, bias, seq_offsets, None, max_new)
     batch = b.batch
     max_pages = _table(page_table, batch)
     lens_p = _vector(lens, torch.int64, batch, "lens")
+    for t, name in ((k, "k"), (v, "v"), (pos, "pos"), (bias, "bias"), (seq_offsets, "seq_offsets"), (page_table, "page_table"),
+                    (lens, "lens"), (cache.k, "cache"), (attn.mem, "attn")):
+        _beside(t, q, name)
     most = max_pages * cache.page_size if max_len is None else int(max_len)
     shape = (n, batch, b.max_len, most)
     known = attn.chunk_bytes
@@ -365,6 +376,7 @@ def seq_attention_chunk(attn: SeqAttention, cache: SeqCache, q: torch.Tensor, k:
         o = RseSeqRows(out.data_ptr(), H * D, D)
     else:
         o = _rows(out, dt, n, H, D, "out")
+        _beside(out, q, "out")
     ws = _on_empty(stream, size, torch.uint8, q.device) if size else None
     byref = ctypes.byref
     check(lib.seq_attention_chunk(attn.handle, cache.handle, byref(b), byref(args[0]), byref(args[1]), byref(args[2]),
