@@ -497,10 +497,10 @@ inline TileGrid tile_grid(int64_t n_events, int64_t batch, int64_t max_len, int 
     return {slots, 0};
 }
 
-// The item's sequence (number, first event, length) and tile; false if it is
-// idle.  backwards: items of a grid by tile index start from the last tile.
+// The item's sequence (first event, length) and tile; false if it is idle.
+// backwards: items of a grid by tile index start from the last tile.
 __device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, int64_t item, int tq, bool backwards,
-                                          int64_t& b, int64_t& s, int& len, int& tile, bool check) {
+                                          int64_t& s, int& len, int& tile, bool check) {
     if (check) {
         for (int64_t i = item * blockDim.x + threadIdx.x; i < a.batch; i += g.items * blockDim.x) {
             const int64_t x = a.offsets[i], y = a.offsets[i + 1];
@@ -508,7 +508,7 @@ __device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, i
                 set_status(&a.hdr->status, RSE_ERR_BAD_INPUT);
         }
     }
-    int64_t t;
+    int64_t b, t;
     if (g.per_seq) {
         t = item / a.batch;
         b = item - t * a.batch + t % a.batch;           // a sequence's tiles on different XCDs
@@ -529,11 +529,6 @@ __device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, i
     len = (int)(e - s);
     tile = (int)t;
     return true;
-}
-__device__ __forceinline__ bool find_tile(const SeqArgs& a, const TileGrid& g, int64_t item, int tq, bool backwards,
-                                          int64_t& s, int& len, int& tile, bool check) {
-    int64_t b;
-    return find_tile(a, g, item, tq, backwards, b, s, len, tile, check);
 }
 
 // The tiles a block works through, one after the other.  By sequence: block x
