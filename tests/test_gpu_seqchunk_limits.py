@@ -1,11 +1,13 @@
 """Attention of several new events per user at the limits of its arguments:
-offsets that no batch has, histories in more parts than the usual sizes make,
-calls that a launch does not hold."""
+offsets that no batch has, blocks that are more than the parts of the keys aim
+at, lengths that grow under a captured call, calls that a launch does not hold."""
 
 import numpy as np
 import pytest
 import torch
-from test_gpu_seqchunk import BF16, F32, Users, _np, rse  # noqa: F401  (rse: the fixture)
+from test_gpu_seqchunk import BF16, F32, KIND, Users, _np, rse  # noqa: F401  (rse: the fixture)
+
+from oracle import sequence as oseq
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +62,67 @@ def test_more_blocks_than_a_launch_holds(rse):  # noqa: F811
             call()
     assert torch.all(out == 7)
     assert attn.status() == 0 and cache.status() == 0
+
+
+# Histories in parts where the calls' own blocks, heads by tiles of new events, are
+# more than twice the parts aimed at (256 of fp32 rows of 128, else 512), and the
+# histories ragged: (users, cached at most, by which power of the user's number).
+CROWDED = {"all heads apart": (20, 400, 1, 16, 128, F32), "a few long ones": (100, 500, 4, 4, 128, F32),
+           "narrow rows": (150, 500, 3, 4, 32, BF16), "wide batch": (40, 1000, 1, 16, 64, BF16)}
+
+
+@pytest.mark.parametrize("case", CROWDED)
+def test_parts_of_crowded_calls(rse, case):  # noqa: F811
+    B, cached, power, H, D, dtype = CROWDED[case]
+    u = Users(rse, [(int(cached * ((i + 1) / B) ** power), 130) for i in range(B)], H, H, D, dtype)
+    assert u.most >= 512, "in parts"
+    u.check(out=torch.full_like(u.q, 7.0))
+
+
+def test_parts_of_crowded_calls_of_few_columns(rse):  # noqa: F811
+    """Two tiles of new events a user, histories past 4096 events: oracle of the
+    users of up to 1000, and of the longest one's last events."""
+    B, H, D = 150, 2, 128
+    users = [(int(4100 * ((i + 1) / B) ** 4), 64) for i in range(B)]
+    u = Users(rse, users, H, H, D, F32)
+    out = torch.full((B * 64, H, D), 7.0, device="cuda")
+    u.call(out=out)
+    assert u.attn.status() == 0 and u.cache.status() == 0
+    got, q = _np(out), _np(u.q)
+    assert np.all(np.isfinite(got)) and not np.any(np.all(got == 7.0, axis=(1, 2)))
+    for b, (k, v, t, n) in enumerate(u.hist):
+        if len(t) > 1000 and b < B - 1:
+            continue
+        at = slice(b * 64, (b + 1) * 64)
+        value, bound = oseq.chunk([(_np(k), _np(v), t.numpy(), n)], q[at], _np(u.bias), u.bounds, True, u.attn.scale, KIND[F32])
+        assert np.all(np.abs(got[at] - value) <= bound), b
+
+
+@pytest.mark.parametrize("new", [3, 40])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_replays_follow_the_lengths(rse, new, dtype):  # noqa: F811
+    """A captured call in parts whose lengths grow and shrink between replays,
+    each replay against the oracle of what the pages hold."""
+    u = Users(rse, [(600, new), (20, new), (100, new)], 4, 2, 64, dtype, spare=40)
+    for pool in u.cache_tensors()[:2]:
+        pool.nan_to_num_(0.5)
+    graph, most = torch.cuda.CUDAGraph(), u.most + 600
+    u.call(max_len=most)
+    torch.cuda.synchronize()
+    lens = u.lens.clone()
+    with torch.cuda.graph(graph):
+        out = u.call(max_len=most)
+    for step in (0, 1, 5, 2):
+        u.lens.copy_(lens)
+        u.lens[1:] += 100 * step
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        hist = []
+        for b, had in enumerate(u.lens.tolist()):
+            e = torch.arange(had + new, device="cuda")
+            at = u.table[b].long()[e // u.page], e % u.page
+            hist.append((*(_np(pool[at]) for pool in u.cache_tensors()[:2]), u.cache.pos[at].cpu().numpy(), new))
+        value, bound = oseq.chunk(hist, _np(u.q), _np(u.bias), u.bounds, True, u.attn.scale, KIND[dtype])
+        assert np.all(np.abs(_np(out) - value) <= bound), step
+    assert u.cache.status() == 0 and u.attn.status() == 0
