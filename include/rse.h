@@ -731,8 +731,9 @@ int rse_seqattn_chunk_workspace_size(const rse_seqattn* attn, int64_t n_events, 
  * page out of the pool: as in seq_attention_step, for the user's new events.
  * Malformed offsets, or more new events than batch->max_len: RSE_ERR_BAD_INPUT
  * in the attention handle's status, the sequences concerned are skipped and
- * their out is left as it was.  The lengths are not changed: the caller adds
- * the counts.
+ * their out is left as it was (of offsets that descend every sequence is
+ * concerned: any of them may be skipped, as others' ranges overlap its own).
+ * The lengths are not changed: the caller adds the counts.
  * Tables and max_len above 2^35 events both, or 2^31 users:
  * RSE_ERR_UNSUPPORTED.
  */

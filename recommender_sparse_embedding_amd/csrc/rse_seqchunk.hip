@@ -212,7 +212,9 @@ __global__ __launch_bounds__(PLAN_THREADS) void k_chunk_plan(SeqArgs a, PageArgs
 #pragma unroll
     for (int i = 0; i < NW; ++i) work += s_work[i];
     int items = 0, per = 1, mine = 0;
-    if (whole <= bound) {                       // only offsets that are wrong make more
+    // (only offsets that descend, of overlapping ranges, make more: status is set, and
+    // all are left out; those of a batch make at most bound - want)
+    if (whole <= bound) {
         // the least length that makes no more than `most` parts is from `per` to high
         const int most = want > whole + want / 2 ? want : whole + want / 2;
         int high = (int)(work * (1.f + 1e-5f) / (float)(most - whole)) + 1;

@@ -41,6 +41,27 @@ def test_offsets_at_the_ends_of_64_bits(rse, users, dtype):  # noqa: F811
             _left_or_right(out, ref, (at, value))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_ranges_that_overlap(rse, dtype):  # noqa: F811
+    """Offsets that go up and down between the ends, so that every other user has
+    all events: reported, and rows are left or written, never read past the ends;
+    where that makes more blocks than the parts' list holds, all are skipped."""
+    for cached, last in ((0, 1961), (600, 1961), (600, 200)):
+        users = [(0, 1)] * 39 + [(cached, last)]
+        n = sum(c for _, c in users)
+        u = Users(rse, users, 4, 4, 32, dtype, spare=n // 16 + 1)
+        u.off.copy_(torch.tensor([0, n] * 20 + [n]))
+        before = [t.clone() for t in u.cache_tensors()]
+        out = torch.full_like(u.q, 7.0)
+        u.call(out=out, max_new=n, max_len=cached + n)
+        torch.cuda.synchronize()
+        assert u.attn.status() == BAD and u.cache.status() == 0
+        assert torch.all(torch.isfinite(out))
+        if last > 1000:
+            assert torch.all(out == 7.0)
+            assert all(torch.equal(a.nan_to_num(), b.nan_to_num()) for a, b in zip(u.cache_tensors(), before))
+
+
 def test_more_blocks_than_a_launch_holds(rse):  # noqa: F811
     """2^22 users of 4 heads are 2^24 blocks of 256 threads: refused by name, in
     every call over users or events, and nothing is written."""
