@@ -147,3 +147,35 @@ def test_replays_follow_the_lengths(rse, new, dtype):  # noqa: F811
         value, bound = oseq.chunk(hist, _np(u.q), _np(u.bias), u.bounds, True, u.attn.scale, KIND[dtype])
         assert np.all(np.abs(_np(out) - value) <= bound), step
     assert u.cache.status() == 0 and u.attn.status() == 0
+
+
+@pytest.mark.parametrize("users", [[(40, 3), (0, 2)], [(40, 70), (0, 66)], [(900, 3)], [(900, 70)]])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bounds", [(5,), (-2**31 + 1, -7, 0, 2**31 - 1)])
+def test_times_at_the_ends_of_32_bits(rse, users, dtype, bounds):  # noqa: F811
+    """Distances saturate: times at both ends of int32, in cached and new events."""
+    u = Users(rse, users, 4, 2, 32, dtype, bounds=bounds)
+    g = np.random.default_rng(3)
+    at = np.array([-2**31, -2**31 + 1, -9, 0, 4, 2**31 - 2, 2**31 - 1])
+    first = 0
+    for b, (had, new) in enumerate(users):
+        k, v, t, n = u.hist[b]
+        t = torch.from_numpy(g.choice(at, had + new)).to(torch.int32)
+        u.hist[b] = (k, v, t, n)
+        e = torch.arange(had)
+        page = u.table[b].cpu().long()[e // u.page]
+        u.pos_pages[page, e % u.page] = t[:had]
+        u.cache.pos[page.cuda(), (e % u.page).cuda()] = t[:had].cuda()
+        u.pos[first:first + new] = t[had:].cuda()
+        first += new
+    u.check()
+
+
+@pytest.mark.parametrize("new", [3, 70])
+def test_tables_without_pages(rse, new):  # noqa: F811
+    """No history fits: reported, out is 0, nothing is stored; idle users are none."""
+    u = Users(rse, [(0, new), (-1, 2), (0, 1)], 4, 2, 32, BF16)
+    before = [t.clone() for t in u.cache_tensors()]
+    out = rse.seq_attention_chunk(u.attn, u.cache, u.q, u.k, u.v, u.pos, u.bias, u.off, u.table[:, :0].contiguous(), u.lens)
+    assert u.cache.status() == BAD and u.attn.status() == 0 and torch.all(out == 0)
+    assert all(torch.equal(a.nan_to_num(), b.nan_to_num()) for a, b in zip(u.cache_tensors(), before))
