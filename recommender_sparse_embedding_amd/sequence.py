@@ -360,9 +360,13 @@ def seq_attention_chunk(attn: SeqAttention, cache: SeqCache, q: torch.Tensor, k:
     batch = b.batch
     max_pages = _table(page_table, batch)
     lens_p = _vector(lens, torch.int64, batch, "lens")
-    for t, name in ((k, "k"), (v, "v"), (pos, "pos"), (bias, "bias"), (seq_offsets, "seq_offsets"), (page_table, "page_table"),
-                    (lens, "lens"), (cache.k, "cache"), (attn.mem, "attn")):
-        _beside(t, q, name)
+    # (one comparison where they agree: the names only when they do not)
+    if not (q.get_device() == k.get_device() == v.get_device() == pos.get_device() == bias.get_device()
+            == seq_offsets.get_device() == page_table.get_device() == lens.get_device() == cache.k.get_device()
+            == attn.mem.get_device()):
+        for t, name in ((k, "k"), (v, "v"), (pos, "pos"), (bias, "bias"), (seq_offsets, "seq_offsets"), (lens, "lens"),
+                        (page_table, "page_table"), (cache.k, "cache"), (attn.mem, "attn")):
+            _beside(t, q, name)
     most = max_pages * cache.page_size if max_len is None else int(max_len)
     shape = (n, batch, b.max_len, most)
     known = attn.chunk_bytes
